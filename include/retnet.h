@@ -357,6 +357,121 @@ RETNET_API retnet_status retnet_msr_layer(const void *x, const void *w_qkvg, con
                                           void *workspace, size_t workspace_bytes,
                                           retnet_stream_t stream);
 
+/* ---- Gated delta rule --------------------------------------------------
+ * The recurrence of retention with a decay of its own for every token and a
+ * write that replaces what the state already answers for a key.  Per
+ * (sequence, value head), row vectors q_t, k_t (dk) and v_t (dv), a log
+ * decay g_t, a write strength b_t and a float32 state S [dk, dv]:
+ *     S <- e^{g_t} S ;  x_t = b_t (v_t - k_t S) ;  S <- S + k_t^T x_t ;
+ *     o_t = scale q_t S.
+ *   q, k    device [batch, seqlen, key_heads, dk]; value head h uses key
+ *           head h / (heads / key_heads).  Used as given: bring k to length
+ *           one (or keep b_t |k_t|^2 below 2) for a recurrence that does not
+ *           grow.
+ *   v, out  device [batch, seqlen, heads, dv].
+ *   g, beta device [batch, seqlen, heads]: log decay (<= 0; -inf empties the
+ *           state) and write strength, of the shape's dtype as all the others.
+ *   lengths device int32 [batch] or NULL: sequence b has the tokens
+ *           t < lengths[b] (clamped to 0..seqlen).  The rows behind them are
+ *           not read, their rows of `out` are left as they were, and their
+ *           gradients are zero.
+ *   state   device float32 [batch, heads, dk, dv], as for retention.
+ * Sizes: batch, seqlen >= 0; 1 <= key_heads <= heads <= 256 with heads a
+ * multiple of key_heads; dk, dv in {64, 128, 256}; scale finite. */
+typedef struct retnet_delta_shape {
+    int batch;
+    int heads;       /* value heads */
+    int key_heads;   /* heads of q and k */
+    int seqlen;
+    int dk;
+    int dv;
+    retnet_dtype dtype;
+} retnet_delta_shape;
+
+/* Recurrent form: one decode step (seqlen = 1) or a run of tokens, with the
+ * state read and written once per call and updated in place.  A sequence of
+ * length 0 keeps its state.  Work grows with seqlen on CUDA cores; for long
+ * runs use retnet_delta_chunkwise.  out must not overlap the inputs.
+ * Errors: INVALID_ARG, UNSUPPORTED (dk/dv), CUDA. */
+RETNET_API retnet_status retnet_delta_recurrent(const void *q, const void *k, const void *v,
+                                                const void *g, const void *beta, float scale,
+                                                const int *lengths, float *state, void *out,
+                                                const retnet_delta_shape *shape,
+                                                retnet_stream_t stream);
+
+/* Prefill: all tokens of a batch, with an optional state before the first
+ * (NULL: zero) and after the last token (NULL: not wanted; may equal
+ * state_in).  RETNET_ALGO_SIMT runs the recurrent form; the tensor-core path
+ * works in chunks of 64 tokens, for bf16 with dk 64 or 128.  out must not
+ * overlap the inputs, the states or the workspace.
+ *   workspace  retnet_delta_workspace_size() bytes, 1024-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+RETNET_API retnet_status retnet_delta_workspace_size(const retnet_delta_shape *shape,
+                                                     retnet_algo algo, size_t *bytes);
+RETNET_API retnet_status retnet_delta_chunkwise(const void *q, const void *k, const void *v,
+                                                const void *g, const void *beta, float scale,
+                                                const int *lengths, void *out,
+                                                const retnet_delta_shape *shape,
+                                                const float *state_in, float *state_out,
+                                                retnet_algo algo, void *workspace,
+                                                size_t workspace_bytes, retnet_stream_t stream);
+
+/* Gradients of the prefill without initial state (as for retention): given
+ * d_out = dL/dout, writes dq, dk, dv, dg, dbeta, shaped and typed as q, k,
+ * v, g, beta; a key head's dq and dk are the sums over its value heads, in
+ * head order.  The gradients must not overlap the inputs or each other.
+ *   workspace  retnet_delta_backward_workspace_size() bytes, 1024-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+RETNET_API retnet_status retnet_delta_backward_workspace_size(const retnet_delta_shape *shape,
+                                                              retnet_algo algo, size_t *bytes);
+RETNET_API retnet_status retnet_delta_backward(const void *q, const void *k, const void *v,
+                                               const void *g, const void *beta,
+                                               const void *d_out, float scale,
+                                               const int *lengths, void *dq, void *dk, void *dv,
+                                               void *dg, void *dbeta,
+                                               const retnet_delta_shape *shape, retnet_algo algo,
+                                               void *workspace, size_t workspace_bytes,
+                                               retnet_stream_t stream);
+
+/* ---- Residual norm ------------------------------------------------------
+ * What stands between a layer and the next one, in one pass over rows of
+ * `hidden` channels: the norm behind the block, its gate, the residual and
+ * the norm before the next block.  With rms(a) = a / sqrt(mean(a^2) + eps):
+ *     z = post_norm ? rms(y) * post_weight : y
+ *     h = x + residual_scale * (gate ? swish(gate) z : z)
+ *     n = rms(h) * pre_weight            (of h before it is rounded to dtype)
+ *   x, y, gate, h, n  device [rows, hidden] of dtype; gate may be NULL.  h
+ *                     may equal x, and n may equal y; no other overlap.
+ *   post_weight, pre_weight  device float32 [hidden] (NULL = 1).
+ *   hidden  a multiple of 8, at most 16384.
+ * Backward: given dn and dh (NULL = 0), the gradients of n and h, writes dx,
+ * dy and dgate (needed exactly when there is a gate) and, where not NULL,
+ * dpost_weight (only with post_norm) and dpre_weight, float32 [hidden],
+ * summed over the rows in an order that does not change.  dx may equal dh
+ * and dy may equal dn; no other overlap.
+ *   workspace  retnet_residual_norm_backward_workspace_size() bytes,
+ *              256-byte aligned.
+ * Errors: INVALID_ARG, WORKSPACE, CUDA. */
+typedef struct retnet_block_norm {
+    const void *gate;
+    int post_norm;             /* 0 or 1 */
+    const float *post_weight;
+    const float *pre_weight;
+    float residual_scale;
+    float eps;
+} retnet_block_norm;
+RETNET_API retnet_status retnet_residual_norm(const void *x, const void *y,
+                                              const retnet_block_norm *norm, long long rows,
+                                              int hidden, retnet_dtype dtype, void *h, void *n,
+                                              retnet_stream_t stream);
+RETNET_API retnet_status retnet_residual_norm_backward_workspace_size(long long rows, int hidden,
+                                                                      size_t *bytes);
+RETNET_API retnet_status retnet_residual_norm_backward(
+    const void *x, const void *y, const void *dn, const void *dh, const retnet_block_norm *norm,
+    long long rows, int hidden, retnet_dtype dtype, void *dx, void *dy, void *dgate,
+    float *dpost_weight, float *dpre_weight, void *workspace, size_t workspace_bytes,
+    retnet_stream_t stream);
+
 /* Reads and clears the library's device-side error word on the current
  * device after synchronising `stream`.  Returns RETNET_OK when no kernel
  * reported a problem, RETNET_ERR_TIMEOUT when a bounded wait inside a

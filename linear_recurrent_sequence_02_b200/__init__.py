@@ -15,7 +15,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -32,6 +32,10 @@ __all__ = [
     "retnet_profiler_read", "ALGO_AUTO", "ALGO_SIMT", "ALGO_TENSOR", "LIB_PATH",
     "DEBUG_LIB_PATH", "using_library", "retnet_test_set_hooks",
     "retnet_linear", "retnet_msr_workspace_size", "retnet_msr_layer",
+    "retnet_delta_recurrent", "retnet_delta_workspace_size", "retnet_delta_chunkwise",
+    "retnet_delta_backward_workspace_size", "retnet_delta_backward",
+    "retnet_residual_norm", "retnet_residual_norm_backward_workspace_size",
+    "retnet_residual_norm_backward", "ResidualNormGrads",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libretnet.so")
@@ -59,6 +63,18 @@ class _Shape(ctypes.Structure):
 class _Gate(ctypes.Structure):
     _fields_ = [("g", ctypes.c_void_p), ("weight", ctypes.c_void_p),
                 ("bias", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class _DeltaShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("heads", ctypes.c_int), ("key_heads", ctypes.c_int),
+                ("seqlen", ctypes.c_int), ("dk", ctypes.c_int), ("dv", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
+
+
+class _BlockNorm(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("post_norm", ctypes.c_int),
+                ("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 _libs = {}
@@ -101,6 +117,19 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "retnet_msr_workspace_size": (i, [ctypes.POINTER(_Shape), i, i, ctypes.POINTER(sz)]),
         "retnet_msr_layer": (i, [vp, vp, vp, vp, i, vp, ctypes.POINTER(_Shape), i, ll, vp, vp,
                                  f, vp, vp, vp, sz, vp]),
+        "retnet_delta_recurrent": (i, [vp, vp, vp, vp, vp, f, vp, vp, vp,
+                                       ctypes.POINTER(_DeltaShape), vp]),
+        "retnet_delta_workspace_size": (i, [ctypes.POINTER(_DeltaShape), i, ctypes.POINTER(sz)]),
+        "retnet_delta_chunkwise": (i, [vp, vp, vp, vp, vp, f, vp, vp, ctypes.POINTER(_DeltaShape),
+                                       vp, vp, i, vp, sz, vp]),
+        "retnet_delta_backward_workspace_size": (i, [ctypes.POINTER(_DeltaShape), i,
+                                                     ctypes.POINTER(sz)]),
+        "retnet_delta_backward": (i, [vp, vp, vp, vp, vp, vp, f, vp, vp, vp, vp, vp, vp,
+                                      ctypes.POINTER(_DeltaShape), i, vp, sz, vp]),
+        "retnet_residual_norm": (i, [vp, vp, ctypes.POINTER(_BlockNorm), ll, i, i, vp, vp, vp]),
+        "retnet_residual_norm_backward_workspace_size": (i, [ll, i, ctypes.POINTER(sz)]),
+        "retnet_residual_norm_backward": (i, [vp, vp, vp, vp, ctypes.POINTER(_BlockNorm), ll, i, i,
+                                              vp, vp, vp, vp, vp, vp, sz, vp]),
         "retnet_check_device_errors": (i, [vp]),
         "retnet_profiler_enable": (i, [i]),
         "retnet_profiler_select": (i, [ctypes.c_char_p]),
@@ -532,6 +561,254 @@ def retnet_msr_layer(x: torch.Tensor, w_qkvg: torch.Tensor, w_o: torch.Tensor,
             _ptr(state_in), _ptr(state_out), _ptr(workspace), workspace.numel(), _stream(x))
     _check("retnet_msr_layer", st)
     return out
+
+
+# ------------------------------------------------------------------ gated delta rule
+def _one_device(x: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    for t in others:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"all tensors must be on {x.device}, got one on {t.device}")
+
+
+def _delta_shape(q, k, v, g, beta, lengths) -> _DeltaShape:
+    _dev(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, seqlen, key_heads, dk]")
+    B, n, Hk, dk = q.shape
+    _dev(k, "k", q.dtype, q.shape)
+    _dev(v, "v", q.dtype)
+    if v.dim() != 4 or tuple(v.shape[:2]) != (B, n):
+        raise ValueError(f"v must be [{B}, {n}, heads, dv], got {tuple(v.shape)}")
+    H, dv = v.shape[2:]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"heads ({H}) must be a multiple of key_heads ({Hk})")
+    _dev(g, "g", q.dtype, (B, n, H))
+    _dev(beta, "beta", q.dtype, (B, n, H))
+    _dev(lengths, "lengths", torch.int32, (B,))
+    _one_device(q, k, v, g, beta, lengths)
+    return _DeltaShape(B, H, Hk, n, dk, dv, _dtype_code(q))
+
+
+def _delta_scale(scale: Optional[float], dk: int) -> float:
+    return dk ** -0.5 if scale is None else float(scale)
+
+
+def retnet_delta_recurrent(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                           beta: torch.Tensor, state: torch.Tensor, *,
+                           scale: Optional[float] = None,
+                           lengths: Optional[torch.Tensor] = None,
+                           out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gated delta rule, recurrent form over q, k [batch, seqlen, key_heads, dk],
+    v [batch, seqlen, heads, dv], g (log decay) and beta [batch, seqlen, heads]:
+    for each token
+        state <- exp(g) state; x = beta (v - k state); state += k^T x; o = scale q state
+    with state float32 [batch, heads, dk, dv] updated in place (seqlen = 1 is
+    the decode step).  scale defaults to dk ** -0.5.  lengths (int32 [batch]):
+    sequence b has the tokens before lengths[b]; the rows behind them keep
+    what `out` held (zeros when it is made here).  Returns out
+    [batch, seqlen, heads, dv]."""
+    shape = _delta_shape(q, k, v, g, beta, lengths)
+    _dev(state, "state", torch.float32, (shape.batch, shape.heads, shape.dk, shape.dv))
+    out = _delta_out(v, lengths) if out is None else _dev(out, "out", q.dtype, v.shape)
+    _one_device(q, state, out)
+    with torch.cuda.device(q.device):
+        st = load_library().retnet_delta_recurrent(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _delta_scale(scale, shape.dk),
+            _ptr(lengths), _ptr(state), _ptr(out), ctypes.byref(shape), _stream(q))
+    _check("retnet_delta_recurrent", st)
+    return out
+
+
+def _delta_out(v: torch.Tensor, lengths: Optional[torch.Tensor]) -> torch.Tensor:
+    return torch.empty_like(v) if lengths is None else torch.zeros_like(v)
+
+
+def _delta_size(fn: str, batch, heads, key_heads, seqlen, dk, dv, dtype, algo) -> int:
+    shape = _DeltaShape(batch, heads, key_heads, seqlen, dk, dv,
+                        BF16 if dtype == torch.bfloat16 else F32)
+    n = ctypes.c_size_t(0)
+    _check(fn, getattr(load_library(), fn)(ctypes.byref(shape), _ALGOS[algo], ctypes.byref(n)))
+    return int(n.value)
+
+
+def retnet_delta_workspace_size(batch: int, heads: int, key_heads: int, seqlen: int, dk: int,
+                                dv: int, dtype: torch.dtype, algo="auto") -> int:
+    return _delta_size("retnet_delta_workspace_size", batch, heads, key_heads, seqlen, dk, dv,
+                       dtype, algo)
+
+
+def retnet_delta_backward_workspace_size(batch: int, heads: int, key_heads: int, seqlen: int,
+                                         dk: int, dv: int, dtype: torch.dtype, algo="auto") -> int:
+    return _delta_size("retnet_delta_backward_workspace_size", batch, heads, key_heads, seqlen,
+                       dk, dv, dtype, algo)
+
+
+def retnet_delta_chunkwise(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                           beta: torch.Tensor, *, scale: Optional[float] = None,
+                           lengths: Optional[torch.Tensor] = None,
+                           state_in: Optional[torch.Tensor] = None,
+                           state_out: Optional[torch.Tensor] = None, algo="auto",
+                           out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gated delta rule, prefill (tensors as for retnet_delta_recurrent).
+    state_in / state_out: float32 [batch, heads, dk, dv] states before the
+    first and after the last token.  `workspace` (uint8 CUDA tensor) is
+    allocated here when not supplied.  Returns out."""
+    shape = _delta_shape(q, k, v, g, beta, lengths)
+    sshape = (shape.batch, shape.heads, shape.dk, shape.dv)
+    _dev(state_in, "state_in", torch.float32, sshape)
+    _dev(state_out, "state_out", torch.float32, sshape)
+    out = _delta_out(v, lengths) if out is None else _dev(out, "out", q.dtype, v.shape)
+    if workspace is None:
+        workspace = retnet_workspace(
+            retnet_delta_workspace_size(shape.batch, shape.heads, shape.key_heads, shape.seqlen,
+                                        shape.dk, shape.dv, q.dtype, algo), q.device)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
+    _one_device(q, state_in, state_out, out, workspace)
+    with torch.cuda.device(q.device):
+        st = load_library().retnet_delta_chunkwise(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _delta_scale(scale, shape.dk),
+            _ptr(lengths), _ptr(out), ctypes.byref(shape), _ptr(state_in), _ptr(state_out),
+            _ALGOS[algo], _ptr(workspace), workspace.numel(), _stream(q))
+    _check("retnet_delta_chunkwise", st)
+    return out
+
+
+def retnet_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                          beta: torch.Tensor, d_out: torch.Tensor, *,
+                          scale: Optional[float] = None, lengths: Optional[torch.Tensor] = None,
+                          algo="auto", dq: Optional[torch.Tensor] = None,
+                          dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+                          dg: Optional[torch.Tensor] = None,
+                          dbeta: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None):
+    """Gradients (dq, dk, dv, dg, dbeta) of retnet_delta_chunkwise's out
+    (without initial state) given d_out = dL/dout; shapes as the inputs."""
+    shape = _delta_shape(q, k, v, g, beta, lengths)
+    _dev(d_out, "d_out", q.dtype, v.shape)
+    grads = []
+    for name, given, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dg", dg, g),
+                              ("dbeta", dbeta, beta)):
+        grads.append(torch.empty_like(like) if given is None else
+                     _dev(given, name, q.dtype, like.shape))
+    if workspace is None:
+        workspace = retnet_workspace(
+            retnet_delta_backward_workspace_size(shape.batch, shape.heads, shape.key_heads,
+                                                 shape.seqlen, shape.dk, shape.dv, q.dtype, algo),
+            q.device)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
+    _one_device(q, d_out, workspace, *grads)
+    with torch.cuda.device(q.device):
+        st = load_library().retnet_delta_backward(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(d_out),
+            _delta_scale(scale, shape.dk), _ptr(lengths), *(_ptr(t) for t in grads),
+            ctypes.byref(shape), _ALGOS[algo], _ptr(workspace), workspace.numel(), _stream(q))
+    _check("retnet_delta_backward", st)
+    return tuple(grads)
+
+
+# ------------------------------------------------------------------ residual norm
+class ResidualNormGrads(NamedTuple):
+    dx: torch.Tensor
+    dy: torch.Tensor
+    dgate: Optional[torch.Tensor]
+    dpost_weight: Optional[torch.Tensor]
+    dpre_weight: Optional[torch.Tensor]
+
+
+def _block_norm(x, y, gate, post_norm, post_weight, pre_weight, residual_scale, eps):
+    _dev(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., hidden]")
+    hidden = x.shape[-1]
+    _dev(y, "y", x.dtype, x.shape)
+    _dev(gate, "gate", x.dtype, x.shape)
+    if post_weight is not None and not post_norm:
+        raise ValueError("post_weight needs post_norm")
+    _dev(post_weight, "post_weight", torch.float32, (hidden,))
+    _dev(pre_weight, "pre_weight", torch.float32, (hidden,))
+    _one_device(x, y, gate, post_weight, pre_weight)
+    rows = x.numel() // hidden if x.numel() else 0
+    norm = _BlockNorm(None if gate is None else gate.data_ptr(), int(bool(post_norm)),
+                      None if post_weight is None else post_weight.data_ptr(),
+                      None if pre_weight is None else pre_weight.data_ptr(),
+                      float(residual_scale), float(eps))
+    return norm, rows, hidden
+
+
+def retnet_residual_norm(x: torch.Tensor, y: torch.Tensor, *, gate: Optional[torch.Tensor] = None,
+                         post_norm: bool = True, post_weight: Optional[torch.Tensor] = None,
+                         pre_weight: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                         eps: float = 1e-5, h: Optional[torch.Tensor] = None,
+                         n: Optional[torch.Tensor] = None):
+    """Norm behind a block, its gate, the residual and the norm before the
+    next block, for residual x, block output y and gate [..., hidden]:
+        z = rms(y) * post_weight (y when post_norm is False)
+        h = x + residual_scale * swish(gate) * z;  n = rms(h) * pre_weight
+    with float32 weights [hidden] (None: 1).  Returns (h, n); h may be x and
+    n may be y."""
+    norm, rows, hidden = _block_norm(x, y, gate, post_norm, post_weight, pre_weight,
+                                     residual_scale, eps)
+    h = torch.empty_like(x) if h is None else _dev(h, "h", x.dtype, x.shape)
+    n = torch.empty_like(x) if n is None else _dev(n, "n", x.dtype, x.shape)
+    _one_device(x, h, n)
+    with torch.cuda.device(x.device):
+        st = load_library().retnet_residual_norm(_ptr(x), _ptr(y), ctypes.byref(norm), rows,
+                                                 hidden, _dtype_code(x), _ptr(h), _ptr(n),
+                                                 _stream(x))
+    _check("retnet_residual_norm", st)
+    return h, n
+
+
+def retnet_residual_norm_backward_workspace_size(rows: int, hidden: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("retnet_residual_norm_backward_workspace_size",
+           load_library().retnet_residual_norm_backward_workspace_size(int(rows), int(hidden),
+                                                                       ctypes.byref(n)))
+    return int(n.value)
+
+
+def retnet_residual_norm_backward(x: torch.Tensor, y: torch.Tensor, dn: torch.Tensor,
+                                  dh: Optional[torch.Tensor] = None, *,
+                                  gate: Optional[torch.Tensor] = None, post_norm: bool = True,
+                                  post_weight: Optional[torch.Tensor] = None,
+                                  pre_weight: Optional[torch.Tensor] = None,
+                                  residual_scale: float = 1.0, eps: float = 1e-5,
+                                  dx: Optional[torch.Tensor] = None,
+                                  dy: Optional[torch.Tensor] = None,
+                                  dgate: Optional[torch.Tensor] = None,
+                                  workspace: Optional[torch.Tensor] = None) -> ResidualNormGrads:
+    """Gradients of retnet_residual_norm given dn and dh, the gradients of n
+    and h (dh None: 0).  dgate is None without a gate, and a weight's gradient
+    (float32 [hidden], summed over the rows) is None where the weight is."""
+    norm, rows, hidden = _block_norm(x, y, gate, post_norm, post_weight, pre_weight,
+                                     residual_scale, eps)
+    _dev(dn, "dn", x.dtype, x.shape)
+    _dev(dh, "dh", x.dtype, x.shape)
+    dx = torch.empty_like(x) if dx is None else _dev(dx, "dx", x.dtype, x.shape)
+    dy = torch.empty_like(x) if dy is None else _dev(dy, "dy", x.dtype, x.shape)
+    if gate is None:
+        if dgate is not None:
+            raise ValueError("dgate needs a gate")
+    else:
+        dgate = torch.empty_like(x) if dgate is None else _dev(dgate, "dgate", x.dtype, x.shape)
+    dpost = None if post_weight is None else torch.empty_like(post_weight)
+    dpre = None if pre_weight is None else torch.empty_like(pre_weight)
+    if workspace is None:
+        workspace = retnet_workspace(retnet_residual_norm_backward_workspace_size(rows, hidden),
+                                     x.device)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
+    _one_device(x, dn, dh, dx, dy, dgate, workspace)
+    with torch.cuda.device(x.device):
+        st = load_library().retnet_residual_norm_backward(
+            _ptr(x), _ptr(y), _ptr(dn), _ptr(dh), ctypes.byref(norm), rows, hidden,
+            _dtype_code(x), _ptr(dx), _ptr(dy), _ptr(dgate), _ptr(dpost), _ptr(dpre),
+            _ptr(workspace), workspace.numel(), _stream(x))
+    _check("retnet_residual_norm_backward", st)
+    return ResidualNormGrads(dx, dy, dgate, dpost, dpre)
 
 
 def retnet_check_device_errors(device=None) -> None:

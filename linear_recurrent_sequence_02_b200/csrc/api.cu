@@ -164,6 +164,51 @@ static FusedBackwardLayout fused_backward_layout(const retnet_shape *s, int chun
     return l;
 }
 
+// The gated delta rule's shape checks.
+static retnet_status check_delta_shape(const retnet_delta_shape *s) {
+    if (!s || s->batch < 0 || s->seqlen < 0 || s->heads < 1 || s->heads > kMaxHeads ||
+        s->key_heads < 1 || s->key_heads > s->heads || s->heads % s->key_heads ||
+        !dtype_ok(s->dtype) || s->dk <= 0 || s->dv <= 0)
+        return RETNET_ERR_INVALID_ARG;
+    if (!head_dim_ok(s->dk) || !head_dim_ok(s->dv)) return RETNET_ERR_UNSUPPORTED;
+    // a CTA per (sequence, head) and slab of columns or chunk of tokens
+    const long long bh = (long long)s->batch * s->heads;
+    const long long chunks = (s->seqlen + (long long)kDeltaChunk - 1) / kDeltaChunk;
+    if (bh * (chunks > 8 ? chunks : 8) > 0x7fffffffll) return RETNET_ERR_UNSUPPORTED;
+    return RETNET_OK;
+}
+static bool algo_ok(retnet_algo a) {
+    return a == RETNET_ALGO_AUTO || a == RETNET_ALGO_SIMT || a == RETNET_ALGO_TENSOR;
+}
+static DeltaArgs delta_args(const void *q, const void *k, const void *v, const void *g,
+                            const void *beta, float scale, const int *lengths,
+                            const retnet_delta_shape *s) {
+    DeltaArgs a = {};
+    a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta;
+    a.scale = scale; a.lengths = lengths;
+    a.batch = s->batch; a.heads = s->heads; a.key_heads = s->key_heads; a.seqlen = s->seqlen;
+    a.dk = s->dk; a.dv = s->dv; a.dtype = s->dtype;
+    return a;
+}
+static retnet_status check_delta_inputs(const DeltaArgs &a) {
+    if (!std::isfinite(a.scale) || !aligned16(a.lengths)) return RETNET_ERR_INVALID_ARG;
+    if ((long long)a.batch * a.seqlen == 0) return RETNET_OK;
+    for (const void *p : {a.q, a.k, a.v, a.g, a.beta})
+        if (!p || !aligned16(p)) return RETNET_ERR_INVALID_ARG;
+    return RETNET_OK;
+}
+static retnet_status check_block_norm(const retnet_block_norm *p, long long rows, int hidden,
+                                      retnet_dtype dtype) {
+    if (!p || rows < 0 || rows > 0x7fffffffll || hidden <= 0 || hidden % 8 || hidden > 16384 ||
+        !dtype_ok(dtype))
+        return RETNET_ERR_INVALID_ARG;
+    if ((p->post_norm != 0 && p->post_norm != 1) || !(p->eps >= 0.f) ||
+        !std::isfinite(p->residual_scale) || !aligned16(p->gate) || !aligned16(p->post_weight) ||
+        !aligned16(p->pre_weight))
+        return RETNET_ERR_INVALID_ARG;
+    return RETNET_OK;
+}
+
 }  // namespace retnet
 
 using namespace retnet;
@@ -523,6 +568,136 @@ retnet_status retnet_groupnorm_swish(const void *o, const void *g, const float *
         return RETNET_ERR_INVALID_ARG;
     RETNET_CUDA_TRY(launch_groupnorm_swish(o, g, weight, bias, eps, rows, heads, dv, dtype, y,
                                            (cudaStream_t)stream));
+    return RETNET_OK;
+}
+
+retnet_status retnet_delta_recurrent(const void *q, const void *k, const void *v, const void *g,
+                                     const void *beta, float scale, const int *lengths,
+                                     float *state, void *out, const retnet_delta_shape *shape,
+                                     retnet_stream_t stream) {
+    retnet_status st = check_delta_shape(shape);
+    if (st != RETNET_OK) return st;
+    DeltaArgs a = delta_args(q, k, v, g, beta, scale, lengths, shape);
+    st = check_delta_inputs(a);
+    if (st != RETNET_OK) return st;
+    if ((long long)a.batch * a.seqlen == 0) return RETNET_OK;
+    if (!state || !out || !aligned16(state) || !aligned16(out)) return RETNET_ERR_INVALID_ARG;
+    a.state_in = state; a.state_out = state; a.out = out;
+    RETNET_CUDA_TRY(launch_delta_recurrent(a, (cudaStream_t)stream));
+    return RETNET_OK;
+}
+
+retnet_status retnet_delta_workspace_size(const retnet_delta_shape *shape, retnet_algo algo,
+                                          size_t *bytes) {
+    if (!bytes || !algo_ok(algo)) return RETNET_ERR_INVALID_ARG;
+    retnet_status st = check_delta_shape(shape);
+    if (st != RETNET_OK) return st;
+    if (algo == RETNET_ALGO_TENSOR) return RETNET_ERR_UNSUPPORTED;
+    *bytes = 0;
+    return RETNET_OK;
+}
+
+retnet_status retnet_delta_chunkwise(const void *q, const void *k, const void *v, const void *g,
+                                     const void *beta, float scale, const int *lengths, void *out,
+                                     const retnet_delta_shape *shape, const float *state_in,
+                                     float *state_out, retnet_algo algo, void *workspace,
+                                     size_t workspace_bytes, retnet_stream_t stream) {
+    size_t need = 0;
+    retnet_status st = retnet_delta_workspace_size(shape, algo, &need);
+    if (st != RETNET_OK) return st;
+    DeltaArgs a = delta_args(q, k, v, g, beta, scale, lengths, shape);
+    st = check_delta_inputs(a);
+    if (st != RETNET_OK) return st;
+    const long long tokens = (long long)a.batch * a.seqlen;
+    if ((tokens > 0 && (!out || !aligned16(out))) || !aligned16(state_in) || !aligned16(state_out))
+        return RETNET_ERR_INVALID_ARG;
+    if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 1023u)))
+        return RETNET_ERR_WORKSPACE;
+    if (a.batch == 0 || (tokens == 0 && !state_out)) return RETNET_OK;
+    a.state_in = state_in; a.state_out = state_out; a.out = out;
+    RETNET_CUDA_TRY(launch_delta_recurrent(a, (cudaStream_t)stream));
+    return RETNET_OK;
+}
+
+retnet_status retnet_delta_backward_workspace_size(const retnet_delta_shape *shape,
+                                                   retnet_algo algo, size_t *bytes) {
+    if (!bytes || !algo_ok(algo)) return RETNET_ERR_INVALID_ARG;
+    retnet_status st = check_delta_shape(shape);
+    if (st != RETNET_OK) return st;
+    if (algo == RETNET_ALGO_TENSOR) return RETNET_ERR_UNSUPPORTED;
+    *bytes = delta_backward_simt_workspace(shape->batch, shape->heads, shape->key_heads,
+                                           shape->seqlen, shape->dk, shape->dv);
+    return RETNET_OK;
+}
+
+retnet_status retnet_delta_backward(const void *q, const void *k, const void *v, const void *g,
+                                    const void *beta, const void *d_out, float scale,
+                                    const int *lengths, void *dq, void *dk, void *dv, void *dg,
+                                    void *dbeta, const retnet_delta_shape *shape, retnet_algo algo,
+                                    void *workspace, size_t workspace_bytes,
+                                    retnet_stream_t stream) {
+    size_t need = 0;
+    retnet_status st = retnet_delta_backward_workspace_size(shape, algo, &need);
+    if (st != RETNET_OK) return st;
+    DeltaArgs a = delta_args(q, k, v, g, beta, scale, lengths, shape);
+    st = check_delta_inputs(a);
+    if (st != RETNET_OK) return st;
+    if ((long long)a.batch * a.seqlen == 0) return RETNET_OK;
+    for (const void *p : {d_out, (const void *)dq, (const void *)dk, (const void *)dv,
+                          (const void *)dg, (const void *)dbeta})
+        if (!p || !aligned16(p)) return RETNET_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 1023u))
+        return RETNET_ERR_WORKSPACE;
+    a.d_out = d_out;
+    a.dq = dq; a.dk_grad = dk; a.dv_grad = dv; a.dg = dg; a.dbeta = dbeta;
+    RETNET_CUDA_TRY(launch_delta_backward_simt(a, workspace, (cudaStream_t)stream));
+    return RETNET_OK;
+}
+
+retnet_status retnet_residual_norm(const void *x, const void *y, const retnet_block_norm *norm,
+                                   long long rows, int hidden, retnet_dtype dtype, void *h,
+                                   void *n, retnet_stream_t stream) {
+    retnet_status st = check_block_norm(norm, rows, hidden, dtype);
+    if (st != RETNET_OK) return st;
+    if (rows == 0) return RETNET_OK;
+    for (const void *p : {x, y, (const void *)h, (const void *)n})
+        if (!p || !aligned16(p)) return RETNET_ERR_INVALID_ARG;
+    RETNET_CUDA_TRY(launch_residual_norm(x, y, *norm, rows, hidden, dtype, h, n,
+                                         (cudaStream_t)stream));
+    return RETNET_OK;
+}
+
+retnet_status retnet_residual_norm_backward_workspace_size(long long rows, int hidden,
+                                                           size_t *bytes) {
+    if (!bytes || rows < 0 || rows > 0x7fffffffll || hidden <= 0 || hidden % 8 || hidden > 16384)
+        return RETNET_ERR_INVALID_ARG;
+    *bytes = residual_norm_backward_workspace(rows, hidden);
+    return RETNET_OK;
+}
+
+retnet_status retnet_residual_norm_backward(const void *x, const void *y, const void *dn,
+                                            const void *dh, const retnet_block_norm *norm,
+                                            long long rows, int hidden, retnet_dtype dtype,
+                                            void *dx, void *dy, void *dgate, float *dpost_weight,
+                                            float *dpre_weight, void *workspace,
+                                            size_t workspace_bytes, retnet_stream_t stream) {
+    retnet_status st = check_block_norm(norm, rows, hidden, dtype);
+    if (st != RETNET_OK) return st;
+    if ((dpost_weight && !norm->post_norm) || !aligned16(dpost_weight) || !aligned16(dpre_weight) ||
+        !aligned16(dh))
+        return RETNET_ERR_INVALID_ARG;
+    if (rows > 0) {
+        for (const void *p : {x, y, dn, (const void *)dx, (const void *)dy})
+            if (!p || !aligned16(p)) return RETNET_ERR_INVALID_ARG;
+        if ((norm->gate == nullptr) != (dgate == nullptr) || !aligned16(dgate))
+            return RETNET_ERR_INVALID_ARG;
+    }
+    const size_t need = residual_norm_backward_workspace(rows, hidden);
+    if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)))
+        return RETNET_ERR_WORKSPACE;
+    RETNET_CUDA_TRY(launch_residual_norm_backward(x, y, dn, dh, *norm, rows, hidden, dtype, dx, dy,
+                                                  dgate, dpost_weight, dpre_weight, workspace,
+                                                  (cudaStream_t)stream));
     return RETNET_OK;
 }
 

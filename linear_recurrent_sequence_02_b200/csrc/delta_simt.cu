@@ -1,0 +1,668 @@
+// Gated delta rule, token by token in float32, and its gradient.
+//
+// One kernel walks the tokens of a (sequence, head) with the state in
+// registers (the recurrent form); it serves the decode step, the float32
+// prefill, and the two sweeps of the float32 backward:
+//   forward   y = k S, z = q S of the state before the token;
+//             x = b (v - a y);  S <- a S + k^T x;  o = scale (a z + (q.k) x)
+//             with a = e^g.  Both products read the same state, so a token
+//             costs one reduction.
+//   reverse   D is the gradient of the state behind a token:
+//             r = k D + scale (k.q) do;  D <- a (D + scale q^T do - b k^T r).
+//             r is the gradient of x; dv = b r.
+// CTA (sequence, head, 32 columns of S) as in the retention step: 8 float4
+// column groups by 32 row lanes, the row lanes of a column reduced by
+// shuffles and then over the eight warps in shared memory.  A single token
+// is an HBM stream of 8 dk dv bytes a head; a long run is bound by the
+// latency of the chain product -> reduction -> update, token after token.
+#include <algorithm>
+
+#include "delta.cuh"
+
+namespace retnet {
+
+constexpr int kDeltaThreads = 256;
+constexpr int kDeltaCols = 32;                 // state columns per CTA
+constexpr int kDeltaGroups = kDeltaCols / 4;   // float4 column groups
+constexpr int kDeltaLanes = kDeltaThreads / kDeltaGroups;   // 32 row lanes
+constexpr int kDeltaStage = 8;                 // tokens staged in shared memory at a time
+
+enum DeltaSweep { kSweepForward, kSweepSave, kSweepReverse };
+
+template <typename T>
+__device__ __forceinline__ float4 load_f4(const T *p);
+template <>
+__device__ __forceinline__ float4 load_f4<float>(const float *p) {
+    return *reinterpret_cast<const float4 *>(p);
+}
+template <>
+__device__ __forceinline__ float4 load_f4<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    uint2 u = *reinterpret_cast<const uint2 *>(p);
+    float2 a = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&u.x));
+    float2 b = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&u.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store_f4(float *p, float4 v) {
+    *reinterpret_cast<float4 *>(p) = v;
+}
+__device__ __forceinline__ void store_f4(__nv_bfloat16 *p, float4 v) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2 *>(p) =
+        make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
+}
+__device__ __forceinline__ void fma4(float4 &a, float s, float4 v) {
+    a.x = fmaf(s, v.x, a.x); a.y = fmaf(s, v.y, a.y);
+    a.z = fmaf(s, v.z, a.z); a.w = fmaf(s, v.w, a.w);
+}
+__device__ __forceinline__ float4 scale4(float s, float4 v) {
+    return make_float4(s * v.x, s * v.y, s * v.z, s * v.w);
+}
+__device__ __forceinline__ void add4(float4 &a, float4 v) {
+    a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+}
+__device__ __forceinline__ void reduce_row_lanes(float4 &a) {
+#pragma unroll
+    for (int m = kDeltaGroups; m < 32; m <<= 1) {
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, m);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, m);
+        a.z += __shfl_xor_sync(0xffffffffu, a.z, m);
+        a.w += __shfl_xor_sync(0xffffffffu, a.w, m);
+    }
+}
+
+// v: the values (forward) or the output's gradient (reverse).
+// state_in / state_out may be the same (the recurrent form's update in place).
+// save: x (kSweepSave) or r (kSweepReverse), float32 [B, n, H, dv];
+// marks: the state before (D behind) every chunk of kDeltaChunk tokens,
+// float32 [B, H, chunks, dk, dv].
+template <typename T, int DK, DeltaSweep kSweep>
+__global__ void __launch_bounds__(kDeltaThreads)
+delta_tokens_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                    const T *__restrict__ g, const T *__restrict__ beta,
+                    const int *__restrict__ lengths, const float *state_in, float *state_out,
+                    T *__restrict__ out, float *__restrict__ save, float *__restrict__ marks,
+                    float scale, int heads, int key_heads, int tokens, int dv) {
+    constexpr int RPL = DK / kDeltaLanes;            // rows per thread: 2, 4 or 8
+    const int slabs = dv / kDeltaCols;
+    const int bh = blockIdx.x / slabs;
+    const int b = bh / heads, h = bh % heads;
+    const int col0 = (blockIdx.x % slabs) * kDeltaCols;
+    const int cg = threadIdx.x % kDeltaGroups, rl = threadIdx.x / kDeltaGroups;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int col = col0 + cg * 4;
+
+    __shared__ float qs[kDeltaStage][DK], ks[kDeltaStage][DK];
+    __shared__ float qk[kDeltaStage], al[kDeltaStage], be[kDeltaStage];
+    __shared__ float4 red[2][2][kDeltaThreads / 32][kDeltaGroups];
+
+    grid_dependency_wait();
+    const int n = delta_tokens_of(lengths, b, tokens);
+    const size_t sbase = (size_t)bh * DK * dv + col;
+    float4 s[RPL];
+#pragma unroll
+    for (int i = 0; i < RPL; ++i)
+        s[i] = state_in ? load_f4(state_in + sbase + (size_t)(rl + i * kDeltaLanes) * dv)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+
+    const size_t row0 = (size_t)b * tokens;
+    const int kh = h / (heads / key_heads);
+    const int nc = (tokens + kDeltaChunk - 1) / kDeltaChunk;
+    int flip = 0;
+    for (int g0 = 0; g0 < n; g0 += kDeltaStage) {
+        const int cnt = min(kDeltaStage, n - g0);
+        // stage slot u holds the u-th token of the walk: g0 + u, or n - 1 - (g0 + u)
+        float4 vv[kDeltaStage];
+#pragma unroll
+        for (int u = 0; u < kDeltaStage; ++u)
+            if (u < cnt) {
+                const int t = kSweep == kSweepReverse ? n - 1 - (g0 + u) : g0 + u;
+                vv[u] = load_f4(v + ((row0 + t) * heads + h) * (size_t)dv + col);
+            }
+        {   // warp u stages token u: q and k rows, q.k, the decay and the write strength
+            const int u = warp;
+            if (u < cnt) {
+                const int t = kSweep == kSweepReverse ? n - 1 - (g0 + u) : g0 + u;
+                const size_t o = ((row0 + t) * key_heads + kh) * (size_t)DK;
+                float dot = 0.f;
+#pragma unroll
+                for (int j = 0; j < DK / 32; ++j) {
+                    const float kv = to_f32(k[o + lane + 32 * j]);
+                    ks[u][lane + 32 * j] = kv;
+                    if (kSweep != kSweepSave) {
+                        const float qv = to_f32(q[o + lane + 32 * j]);
+                        qs[u][lane + 32 * j] = qv;
+                        dot = fmaf(qv, kv, dot);
+                    }
+                }
+#pragma unroll
+                for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+                if (lane == 0) {
+                    qk[u] = dot;
+                    al[u] = expf(to_f32(g[(row0 + t) * heads + h]));
+                    const float bt = to_f32(beta[(row0 + t) * heads + h]);
+                    be[u] = kSweep == kSweepSave ? nonzero_beta(bt) : bt;
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kDeltaStage; ++u) {
+            if (u < cnt) {
+                const int t = kSweep == kSweepReverse ? n - 1 - (g0 + u) : g0 + u;
+                if (kSweep != kSweepForward) {
+                    // a chunk's first token (its last, walking back)
+                    const bool mark = kSweep == kSweepSave
+                                          ? t % kDeltaChunk == 0
+                                          : t == n - 1 || t % kDeltaChunk == kDeltaChunk - 1;
+                    if (mark) {
+                        float *m = marks + ((size_t)bh * nc + t / kDeltaChunk) * DK * dv + col;
+#pragma unroll
+                        for (int i = 0; i < RPL; ++i)
+                            store_f4(m + (size_t)(rl + i * kDeltaLanes) * dv, s[i]);
+                    }
+                }
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
+#pragma unroll
+                for (int i = 0; i < RPL; ++i) {
+                    fma4(y, ks[u][rl + i * kDeltaLanes], s[i]);
+                    if (kSweep == kSweepForward) fma4(z, qs[u][rl + i * kDeltaLanes], s[i]);
+                }
+                reduce_row_lanes(y);
+                if (kSweep == kSweepForward) reduce_row_lanes(z);
+                if (lane < kDeltaGroups) {
+                    red[flip][0][warp][lane] = y;
+                    if (kSweep == kSweepForward) red[flip][1][warp][lane] = z;
+                }
+                __syncthreads();
+                y = red[flip][0][0][cg];
+#pragma unroll
+                for (int w = 1; w < kDeltaThreads / 32; ++w) add4(y, red[flip][0][w][cg]);
+                const float a = al[u], bt = be[u];
+                float4 x;
+                if (kSweep == kSweepReverse) {
+                    const float c = scale * qk[u];
+                    x = y;
+                    fma4(x, c, vv[u]);                            // r
+                    const float4 xb = scale4(-bt, x);
+#pragma unroll
+                    for (int i = 0; i < RPL; ++i) {
+                        const int rr = rl + i * kDeltaLanes;
+                        fma4(s[i], scale * qs[u][rr], vv[u]);
+                        fma4(s[i], ks[u][rr], xb);
+                        s[i] = scale4(a, s[i]);
+                    }
+                } else {
+                    x = vv[u];
+                    fma4(x, -a, y);
+                    x = scale4(bt, x);
+#pragma unroll
+                    for (int i = 0; i < RPL; ++i) {
+                        s[i] = scale4(a, s[i]);
+                        fma4(s[i], ks[u][rl + i * kDeltaLanes], x);
+                    }
+                }
+                const size_t vo = ((row0 + t) * heads + h) * (size_t)dv + col;
+                if (kSweep == kSweepForward) {
+                    if (warp == u % (kDeltaThreads / 32) && lane < kDeltaGroups) {
+                        z = red[flip][1][0][cg];
+#pragma unroll
+                        for (int w = 1; w < kDeltaThreads / 32; ++w) add4(z, red[flip][1][w][cg]);
+                        float4 o = scale4(a, z);
+                        fma4(o, qk[u], x);
+                        store_f4(out + vo, scale4(scale, o));
+                    }
+                } else if (rl == 0) {
+                    store_f4(save + vo, x);
+                }
+                flip ^= 1;
+            }
+        }
+        __syncthreads();               // the stage is rewritten
+    }
+    if (kSweep == kSweepForward && state_out && (n > 0 || state_out != state_in)) {
+#pragma unroll
+        for (int i = 0; i < RPL; ++i)
+            store_f4(state_out + sbase + (size_t)(rl + i * kDeltaLanes) * dv, s[i]);
+    }
+}
+
+// ------------------------------------------------------------------ gradients
+// One CTA per chunk of 64 tokens of a (sequence, head).  With X, R (the
+// gradients of X), the state S before the chunk and D (the gradient of the
+// state behind it), G the running sum of g inside the chunk:
+//   A_ij = scale (do_i . x_j) e^{G_i - G_j},  i >= j
+//   B_ij = -b_i (r_i . x_j) e^{G_i - G_j},    i > j
+//   dq = scale e^G (do S^T) + A K
+//   dk = e^{G_L - G} (X D^T) - b e^G (R S^T) + A^T Q + (B + B^T) K
+//   dv = b R,   dbeta = R . X / b
+// dg_t is the sum of everything that crosses token t, each term formed once
+// and added to the tokens it crosses: the pairs E = A (.) QK^T + B (.) KK^T
+// with j < t <= i (rows minus columns of E summed from t on: the same float
+// for both, so what does not cross cancels), what leaves S at i >= t, what
+// reaches D from j < t, and e^{G_L} <S, D>.
+constexpr int kGradThreads = 256;
+constexpr int kGradPad = 36;           // row stride of a 64 x 32 tile
+constexpr int kGradPadK = 68;          // row stride of a 64 x 64 tile
+
+struct DeltaGradSmem {
+    float A[64][kGradPadK], B[64][kGradPadK];
+    float Ks[64][kGradPadK], Qs[64][kGradPadK];
+    float X[64][kGradPad], R[64][kGradPad], O[64][kGradPad];
+    float S[64][kGradPad], D[64][kGradPad];
+    double G[64];                          // sums of g: their differences are taken
+    float beta[64], rowsum[64], colsum[64], inter[64], ahead[64], db[64];
+    float part[kGradThreads / 32];
+};
+
+// acc[4][4] += rows r0.. of a times rows c0.. of b over 32 columns
+__device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float (*a)[kGradPad],
+                                         const float (*b)[kGradPad], int r0, int c0) {
+#pragma unroll 2
+    for (int j = 0; j < 32; j += 4) {
+        float4 av[4], bv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) av[i] = *reinterpret_cast<const float4 *>(&a[r0 + 16 * i][j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bv[i] = *reinterpret_cast<const float4 *>(&b[c0 + 16 * i][j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+                acc[i][l] = fmaf(av[i].x, bv[l].x, acc[i][l]);
+                acc[i][l] = fmaf(av[i].y, bv[l].y, acc[i][l]);
+                acc[i][l] = fmaf(av[i].z, bv[l].z, acc[i][l]);
+                acc[i][l] = fmaf(av[i].w, bv[l].w, acc[i][l]);
+            }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads)
+delta_grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ d_out,
+                  const T *__restrict__ g, const T *__restrict__ beta,
+                  const int *__restrict__ lengths, const float *__restrict__ xs,
+                  const float *__restrict__ rs, const float *__restrict__ ss,
+                  const float *__restrict__ ds, T *dq, T *dk_, T *dv_, T *dg, T *dbeta,
+                  float *dq_wide, float *dk_wide, float scale, int heads, int key_heads,
+                  int tokens, int dk, int dv) {
+    extern __shared__ __align__(16) char raw[];
+    DeltaGradSmem &m = *reinterpret_cast<DeltaGradSmem *>(raw);
+    const int nc = (tokens + kDeltaChunk - 1) / kDeltaChunk;
+    const int bh = blockIdx.x / nc, c = blockIdx.x % nc;
+    const int b = bh / heads, h = bh % heads, kh = h / (heads / key_heads);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    grid_dependency_wait();
+    const int n = delta_tokens_of(lengths, b, tokens);
+    const int t0 = c * kDeltaChunk;
+    const int room = min(kDeltaChunk, tokens - t0);          // rows of the chunk
+    const int cnt = min(max(n - t0, 0), room);               // tokens of the sequence
+    const size_t row0 = (size_t)b * tokens + t0;
+    const bool shared_keys = heads != key_heads;
+
+    // rows behind the sequence have no gradient
+    for (int i = cnt + warp; i < room; i += kGradThreads / 32) {
+        T *v = dv_ + ((row0 + i) * heads + h) * (size_t)dv;
+        for (int j = lane; j < dv; j += 32) v[j] = from_f32<T>(0.f);
+        for (int j = lane; j < dk; j += 32) {
+            const size_t o = ((row0 + i) * (shared_keys ? heads : key_heads) + h) * (size_t)dk + j;
+            if (shared_keys) {
+                dq_wide[o] = 0.f;
+                dk_wide[o] = 0.f;
+            } else {
+                dq[o] = from_f32<T>(0.f);
+                dk_[o] = from_f32<T>(0.f);
+            }
+        }
+        if (lane == 0) {
+            dg[(row0 + i) * heads + h] = from_f32<T>(0.f);
+            dbeta[(row0 + i) * heads + h] = from_f32<T>(0.f);
+        }
+    }
+    if (cnt == 0) return;                                    // the whole CTA
+
+    if (tid < 64) {
+        m.beta[tid] = tid < cnt ? to_f32(beta[(row0 + tid) * heads + h]) : 0.f;
+        m.rowsum[tid] = m.colsum[tid] = m.inter[tid] = m.ahead[tid] = m.db[tid] = 0.f;
+    }
+    if (warp == 0) {
+        double a = lane < cnt ? log_decay(to_f32(g[(row0 + lane) * heads + h])) : 0.0;
+        double z = lane + 32 < cnt ? log_decay(to_f32(g[(row0 + lane + 32) * heads + h])) : 0.0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double ua = __shfl_up_sync(0xffffffffu, a, o);
+            const double uz = __shfl_up_sync(0xffffffffu, z, o);
+            if (lane >= o) {
+                a += ua;
+                z += uz;
+            }
+        }
+        m.G[lane] = a;
+        m.G[lane + 32] = z + __shfl_sync(0xffffffffu, a, 31);
+    }
+    __syncthreads();
+
+    auto load_rows = [&](float (*dst)[kGradPad], auto src, size_t stride, int rows) {
+        const int r = tid / 8, j = (tid % 8) * 4;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int rr = r + 32 * i;
+            const float4 x = rr < rows ? load_f4(src + (size_t)rr * stride + j)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4 *>(&dst[rr][j]) = x;
+        }
+    };
+    auto load_keys = [&](float (*dst)[kGradPadK], const T *src) {
+        const int r = tid / 16, j = (tid % 16) * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int rr = r + 16 * i;
+            const float4 x = rr < cnt ? load_f4(src + (size_t)rr * key_heads * dk + j)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4 *>(&dst[rr][j]) = x;
+        }
+    };
+    const size_t vrow = (row0 * heads + h) * (size_t)dv, vstep = (size_t)heads * dv;
+    const size_t krow = (row0 * key_heads + kh) * (size_t)dk;
+    const float *S0 = ss + ((size_t)bh * nc + c) * dk * dv, *D0 = ds + ((size_t)bh * nc + c) * dk * dv;
+    const int r0 = tid / 16, c0 = tid % 16;                  // rows r0 + 16 i, columns c0 + 16 l
+
+    // ---- the pairs of the chunk
+    float pa[4][4] = {}, pb[4][4] = {}, fq[4][4] = {}, fk[4][4] = {};
+    for (int j = 0; j < dv; j += 32) {
+        load_rows(m.X, xs + vrow + j, vstep, cnt);
+        load_rows(m.R, rs + vrow + j, vstep, cnt);
+        load_rows(m.O, d_out + vrow + j, vstep, cnt);
+        __syncthreads();
+        dot_tile(pa, m.O, m.X, r0, c0);
+        dot_tile(pb, m.R, m.X, r0, c0);
+        for (int i = warp; i < cnt; i += kGradThreads / 32) {
+            const float r = m.R[i][lane];
+            dv_[vrow + (size_t)i * vstep + j + lane] = from_f32<T>(m.beta[i] * r);
+            float d = r * m.X[i][lane];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+            if (lane == 0) m.db[i] += d;                     // one warp owns row i
+        }
+        __syncthreads();
+    }
+    for (int j = 0; j < dk; j += 32) {                       // through the X and R tiles
+        load_rows(m.X, k + krow + j, (size_t)key_heads * dk, cnt);
+        load_rows(m.R, q + krow + j, (size_t)key_heads * dk, cnt);
+        __syncthreads();
+        dot_tile(fq, m.R, m.X, r0, c0);
+        dot_tile(fk, m.X, m.X, r0, c0);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int ri = r0 + 16 * i;
+        float rsum = 0.f;
+#pragma unroll
+        for (int l = 0; l < 4; ++l) {
+            const int cj = c0 + 16 * l;
+            const float dec = ri >= cj && ri < cnt ? expf((float)(m.G[ri] - m.G[cj])) : 0.f;
+            const float va = scale * dec * pa[i][l];
+            const float vb = ri > cj ? -m.beta[ri] * dec * pb[i][l] : 0.f;
+            m.A[ri][cj] = va;
+            m.B[ri][cj] = vb;
+            fq[i][l] = ri == cj ? 0.f : fmaf(va, fq[i][l], vb * fk[i][l]);   // E off the diagonal
+            rsum += fq[i][l];
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) rsum += __shfl_xor_sync(0xffffffffu, rsum, o, 16);
+        if (c0 == 0) m.rowsum[ri] = rsum;
+    }
+    // columns of E through the (free) X, R tiles' space: 16 partial rows of 64
+    float *cols = &m.X[0][0];
+#pragma unroll
+    for (int l = 0; l < 4; ++l)
+        cols[r0 * 64 + c0 + 16 * l] = fq[0][l] + fq[1][l] + fq[2][l] + fq[3][l];
+    __syncthreads();
+    if (tid < 64) {
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a += cols[i * 64 + tid];
+        m.colsum[tid] = a;
+    }
+    __syncthreads();
+
+    // ---- through the states, 64 rows of S and D at a time
+    float sd = 0.f;
+    const double GL = m.G[cnt - 1];
+    for (int j0 = 0; j0 < dk; j0 += 64) {
+        float aq[4][4] = {}, ar[4][4] = {}, ax[4][4] = {};
+        load_keys(m.Ks, k + krow + j0);
+        load_keys(m.Qs, q + krow + j0);
+        for (int j = 0; j < dv; j += 32) {
+            load_rows(m.X, xs + vrow + j, vstep, cnt);
+            load_rows(m.R, rs + vrow + j, vstep, cnt);
+            load_rows(m.O, d_out + vrow + j, vstep, cnt);
+            load_rows(m.S, S0 + (size_t)j0 * dv + j, dv, 64);
+            load_rows(m.D, D0 + (size_t)j0 * dv + j, dv, 64);
+            __syncthreads();
+            dot_tile(aq, m.O, m.S, r0, c0);
+            dot_tile(ar, m.R, m.S, r0, c0);
+            dot_tile(ax, m.X, m.D, r0, c0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = tid + i * kGradThreads;
+                sd = fmaf(m.S[e / 32][e % 32], m.D[e / 32][e % 32], sd);
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int ri = r0 + 16 * i;
+            const float e = expf((float)m.G[ri]), rest = ri < cnt ? expf((float)(GL - m.G[ri])) : 0.f;
+            const float bt = m.beta[ri];
+            float inter = 0.f, ahead = 0.f;
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+                const int cj = c0 + 16 * l;
+                aq[i][l] *= scale * e;
+                ar[i][l] *= -bt * e;
+                ax[i][l] *= rest;
+                inter = fmaf(m.Qs[ri][cj], aq[i][l], inter);
+                inter = fmaf(m.Ks[ri][cj], ar[i][l], inter);
+                ahead = fmaf(m.Ks[ri][cj], ax[i][l], ahead);
+                ar[i][l] += ax[i][l];
+            }
+#pragma unroll
+            for (int o = 8; o; o >>= 1) {
+                inter += __shfl_xor_sync(0xffffffffu, inter, o, 16);
+                ahead += __shfl_xor_sync(0xffffffffu, ahead, o, 16);
+            }
+            if (c0 == 0) {
+                m.inter[ri] += inter;
+                m.ahead[ri] += ahead;
+            }
+        }
+        for (int t = 0; t < cnt; ++t) {                      // A K; A^T Q + (B + B^T) K
+            float kv[4], qv[4];
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+                kv[l] = m.Ks[t][c0 + 16 * l];
+                qv[l] = m.Qs[t][c0 + 16 * l];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int ri = r0 + 16 * i;
+                const float a = m.A[ri][t], at = m.A[t][ri], bb = m.B[ri][t] + m.B[t][ri];
+#pragma unroll
+                for (int l = 0; l < 4; ++l) {
+                    aq[i][l] = fmaf(a, kv[l], aq[i][l]);
+                    ar[i][l] = fmaf(at, qv[l], ar[i][l]);
+                    ar[i][l] = fmaf(bb, kv[l], ar[i][l]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int ri = r0 + 16 * i;
+            if (ri < cnt) {
+#pragma unroll
+                for (int l = 0; l < 4; ++l) {
+                    const int cj = j0 + c0 + 16 * l;
+                    if (shared_keys) {
+                        const size_t o = ((row0 + ri) * heads + h) * (size_t)dk + cj;
+                        dq_wide[o] = aq[i][l];
+                        dk_wide[o] = ar[i][l];
+                    } else {
+                        const size_t o = krow + (size_t)ri * key_heads * dk + cj;
+                        dq[o] = from_f32<T>(aq[i][l]);
+                        dk_[o] = from_f32<T>(ar[i][l]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
+    if (lane == 0) m.part[warp] = sd;
+    __syncthreads();
+    if (tid < cnt) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kGradThreads / 32; ++w) s += m.part[w];
+        s *= expf((float)GL);
+        for (int i = cnt - 1; i >= tid; --i) s += (m.rowsum[i] - m.colsum[i]) + m.inter[i];
+        for (int i = 0; i < tid; ++i) s += m.ahead[i];
+        dg[(row0 + tid) * heads + h] = from_f32<T>(s);
+        dbeta[(row0 + tid) * heads + h] = from_f32<T>(m.db[tid] / nonzero_beta(m.beta[tid]));
+    }
+}
+
+// dq, dk of a shared key head: the sum over its value heads, in head order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+delta_share_kernel(const float *__restrict__ dq_wide, const float *__restrict__ dk_wide, T *dq,
+                   T *dk_, long long vecs, int group, int dk) {
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;   // a float4 of (row, key head)
+    grid_dependency_wait();
+    if (i >= vecs) return;
+    const int per = dk / 4;
+    const long long rh = i / per;
+    const size_t src = (size_t)rh * group * dk + (i % per) * 4;
+    const float *from = blockIdx.y ? dk_wide : dq_wide;
+    float4 a = load_f4(from + src);
+    for (int w = 1; w < group; ++w) add4(a, load_f4(from + src + (size_t)w * dk));
+    store_f4((blockIdx.y ? dk_ : dq) + (size_t)i * 4, a);
+}
+
+// ------------------------------------------------------------------ launches
+template <typename T, int DK, DeltaSweep kSweep>
+static cudaError_t launch_sweep(const DeltaArgs &a, const void *v, const float *state_in,
+                                float *state_out, float *save, float *marks,
+                                cudaStream_t stream) {
+    const size_t grid = (size_t)a.batch * a.heads * (a.dv / kDeltaCols);
+    return launch_overlapped(delta_tokens_kernel<T, DK, kSweep>, dim3((unsigned)grid),
+                             dim3(kDeltaThreads), 0, stream, (const T *)a.q, (const T *)a.k,
+                             (const T *)v, (const T *)a.g, (const T *)a.beta, a.lengths, state_in,
+                             state_out, (T *)a.out, save, marks, a.scale, a.heads, a.key_heads,
+                             a.seqlen, a.dv);
+}
+template <DeltaSweep kSweep>
+static cudaError_t launch_sweep(const char *name, const DeltaArgs &a, const void *v,
+                                const float *state_in, float *state_out, float *save, float *marks,
+                                cudaStream_t stream) {
+    KernelTimer timer(name, stream);
+    count_launch();
+    const bool bf = a.dtype == RETNET_BF16;
+#define RETNET_SWEEP(DK)                                                                     \
+    return bf ? launch_sweep<__nv_bfloat16, DK, kSweep>(a, v, state_in, state_out, save,     \
+                                                        marks, stream)                       \
+              : launch_sweep<float, DK, kSweep>(a, v, state_in, state_out, save, marks, stream)
+    switch (a.dk) {
+        case 64: RETNET_SWEEP(64);
+        case 128: RETNET_SWEEP(128);
+    }
+    RETNET_SWEEP(256);
+#undef RETNET_SWEEP
+}
+
+cudaError_t launch_delta_recurrent(const DeltaArgs &a, cudaStream_t stream) {
+    return launch_sweep<kSweepForward>("delta_tokens", a, a.v, a.state_in, a.state_out, nullptr,
+                                       nullptr, stream);
+}
+
+static size_t up1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
+
+struct DeltaGradLayout {
+    size_t x, r, s, d, dq, dk, total;
+};
+static DeltaGradLayout grad_layout(int batch, int heads, int key_heads, int seqlen, int dk, int dv) {
+    const size_t rows = (size_t)batch * seqlen * heads;
+    const size_t nc = (seqlen + kDeltaChunk - 1) / kDeltaChunk;
+    const size_t rv = up1k(rows * dv * 4), rk = heads != key_heads ? up1k(rows * dk * 4) : 0;
+    const size_t st = up1k((size_t)batch * heads * nc * dk * dv * 4);
+    DeltaGradLayout l;
+    l.x = 0;
+    l.r = l.x + rv;
+    l.s = l.r + rv;
+    l.d = l.s + st;
+    l.dq = l.d + st;
+    l.dk = l.dq + rk;
+    l.total = l.dk + rk;
+    return l;
+}
+
+size_t delta_backward_simt_workspace(int batch, int heads, int key_heads, int seqlen, int dk,
+                                     int dv) {
+    return grad_layout(batch, heads, key_heads, seqlen, dk, dv).total;
+}
+
+template <typename T>
+static cudaError_t launch_grad(const DeltaArgs &a, const DeltaGradLayout &l, char *ws,
+                               cudaStream_t stream) {
+    const long long nc = (a.seqlen + kDeltaChunk - 1) / kDeltaChunk;
+    cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<T>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(DeltaGradSmem));
+    if (e != cudaSuccess) return e;
+    {
+        KernelTimer timer("delta_grad", stream);
+        count_launch();
+        e = launch_overlapped(
+            delta_grad_kernel<T>, dim3((unsigned)(nc * a.batch * a.heads)), dim3(kGradThreads),
+            sizeof(DeltaGradSmem), stream, (const T *)a.q, (const T *)a.k, (const T *)a.d_out,
+            (const T *)a.g, (const T *)a.beta, a.lengths, (const float *)(ws + l.x),
+            (const float *)(ws + l.r), (const float *)(ws + l.s), (const float *)(ws + l.d),
+            (T *)a.dq, (T *)a.dk_grad, (T *)a.dv_grad, (T *)a.dg, (T *)a.dbeta,
+            (float *)(ws + l.dq), (float *)(ws + l.dk), a.scale, a.heads, a.key_heads, a.seqlen,
+            a.dk, a.dv);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_delta_share(a, (const float *)(ws + l.dq), (const float *)(ws + l.dk), stream);
+}
+
+cudaError_t launch_delta_share(const DeltaArgs &a, const float *dq_wide, const float *dk_wide,
+                               cudaStream_t stream) {
+    if (a.heads == a.key_heads) return cudaSuccess;
+    const long long vecs = (long long)a.batch * a.seqlen * a.key_heads * a.dk / 4;
+    const dim3 grid((unsigned)((vecs + 255) / 256), 2);
+    KernelTimer timer("delta_share", stream);
+    count_launch();
+    if (a.dtype == RETNET_BF16)
+        return launch_overlapped(delta_share_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream,
+                                 dq_wide, dk_wide, (__nv_bfloat16 *)a.dq,
+                                 (__nv_bfloat16 *)a.dk_grad, vecs, a.heads / a.key_heads, a.dk);
+    return launch_overlapped(delta_share_kernel<float>, grid, dim3(256), 0, stream, dq_wide,
+                             dk_wide, (float *)a.dq, (float *)a.dk_grad, vecs,
+                             a.heads / a.key_heads, a.dk);
+}
+
+cudaError_t launch_delta_backward_simt(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
+    const DeltaGradLayout l = grad_layout(a.batch, a.heads, a.key_heads, a.seqlen, a.dk, a.dv);
+    char *ws = (char *)workspace;
+    cudaError_t e = launch_sweep<kSweepSave>("delta_forward_sweep", a, a.v, nullptr, nullptr,
+                                             (float *)(ws + l.x), (float *)(ws + l.s), stream);
+    if (e != cudaSuccess) return e;
+    e = launch_sweep<kSweepReverse>("delta_reverse_sweep", a, a.d_out, nullptr, nullptr,
+                                    (float *)(ws + l.r), (float *)(ws + l.d), stream);
+    if (e != cudaSuccess) return e;
+    return a.dtype == RETNET_BF16 ? launch_grad<__nv_bfloat16>(a, l, ws, stream)
+                                  : launch_grad<float>(a, l, ws, stream);
+}
+
+}  // namespace retnet

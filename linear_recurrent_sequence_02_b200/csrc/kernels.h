@@ -123,4 +123,39 @@ cudaError_t launch_gemm_bf16(const void *x, const void *w, void *const *outs, lo
                              int k, int n_split, cudaStream_t stream,
                              const char *timer_name = "gemm", const GemmFold *fold = nullptr);
 
+// residual_norm.cu ---------------------------------------------------------
+cudaError_t launch_residual_norm(const void *x, const void *y, const retnet_block_norm &p,
+                                 long long rows, int hidden, retnet_dtype dtype, void *h, void *n,
+                                 cudaStream_t stream);
+size_t residual_norm_backward_workspace(long long rows, int hidden);
+cudaError_t launch_residual_norm_backward(const void *x, const void *y, const void *dn,
+                                          const void *dh, const retnet_block_norm &p,
+                                          long long rows, int hidden, retnet_dtype dtype, void *dx,
+                                          void *dy, void *dgate, float *dpost, float *dpre,
+                                          void *workspace, cudaStream_t stream);
+
+// delta_simt.cu ------------------------------------------------------------
+constexpr int kDeltaChunk = 64;            // tokens per chunk of the gated delta rule
+struct DeltaArgs {
+    const void *q, *k, *v, *g, *beta;
+    const int *lengths;                    // may be null
+    const float *state_in;                 // may be null (zero)
+    float *state_out;                      // may be null
+    void *out;
+    const void *d_out;                     // backward only, with the gradients
+    void *dq, *dk_grad, *dv_grad, *dg, *dbeta;
+    float scale;
+    int batch, heads, key_heads, seqlen, dk, dv;
+    retnet_dtype dtype;
+};
+// Token by token, any supported shape: the recurrent form and the float32 prefill.
+cudaError_t launch_delta_recurrent(const DeltaArgs &a, cudaStream_t stream);
+size_t delta_backward_simt_workspace(int batch, int heads, int key_heads, int seqlen, int dk,
+                                     int dv);
+cudaError_t launch_delta_backward_simt(const DeltaArgs &a, void *workspace, cudaStream_t stream);
+// dq and dk of key heads shared by several value heads, from float32
+// [B, n, heads, dk] gradients per value head; nothing where none is shared.
+cudaError_t launch_delta_share(const DeltaArgs &a, const float *dq_wide, const float *dk_wide,
+                               cudaStream_t stream);
+
 }  // namespace retnet

@@ -21,3 +21,9 @@ from .retention import (  # noqa: F401
     linear,
     msr_layer,
 )
+from .delta import (  # noqa: F401,E402
+    delta_recurrent,
+    delta_backward,
+    residual_norm,
+    residual_norm_backward,
+)
