@@ -180,6 +180,10 @@ static retnet_status check_delta_shape(const retnet_delta_shape *s) {
 static bool algo_ok(retnet_algo a) {
     return a == RETNET_ALGO_AUTO || a == RETNET_ALGO_SIMT || a == RETNET_ALGO_TENSOR;
 }
+// Whether a call takes the tensor-core path.
+static bool delta_tensor(const retnet_delta_shape *s, retnet_algo algo) {
+    return algo != RETNET_ALGO_SIMT && delta_tc_shape_ok(s->dk, s->dv, s->dtype);
+}
 static DeltaArgs delta_args(const void *q, const void *k, const void *v, const void *g,
                             const void *beta, float scale, const int *lengths,
                             const retnet_delta_shape *s) {
@@ -592,8 +596,9 @@ retnet_status retnet_delta_workspace_size(const retnet_delta_shape *shape, retne
     if (!bytes || !algo_ok(algo)) return RETNET_ERR_INVALID_ARG;
     retnet_status st = check_delta_shape(shape);
     if (st != RETNET_OK) return st;
-    if (algo == RETNET_ALGO_TENSOR) return RETNET_ERR_UNSUPPORTED;
-    *bytes = 0;
+    const bool tensor = delta_tensor(shape, algo);
+    if (algo == RETNET_ALGO_TENSOR && !tensor) return RETNET_ERR_UNSUPPORTED;
+    *bytes = tensor ? delta_tc_workspace(shape->batch, shape->heads, shape->seqlen, shape->dk) : 0;
     return RETNET_OK;
 }
 
@@ -615,7 +620,10 @@ retnet_status retnet_delta_chunkwise(const void *q, const void *k, const void *v
         return RETNET_ERR_WORKSPACE;
     if (a.batch == 0 || (tokens == 0 && !state_out)) return RETNET_OK;
     a.state_in = state_in; a.state_out = state_out; a.out = out;
-    RETNET_CUDA_TRY(launch_delta_recurrent(a, (cudaStream_t)stream));
+    if (tokens > 0 && delta_tensor(shape, algo))
+        RETNET_CUDA_TRY(launch_delta_tc(a, workspace, (cudaStream_t)stream));
+    else
+        RETNET_CUDA_TRY(launch_delta_recurrent(a, (cudaStream_t)stream));
     return RETNET_OK;
 }
 

@@ -18,7 +18,7 @@ __device__ __forceinline__ int delta_tokens_of(const int *lengths, int b, int se
 // x is linear in b, and dbeta is (gradient of x) . x / b.  Where b is 0 the
 // backward takes a b of this size instead: x keeps all its digits, the
 // quotient is the limit, and what it writes to the state is nothing beside it.
-__device__ __forceinline__ float nonzero_beta(float b) { return fabsf(b) < 1e-20f ? 1e-20f : b; }
+__device__ __forceinline__ float nonzero_beta(float b) { return fabsf(b) < 1e-15f ? 1e-15f : b; }
 
 // g where sums of it are formed: e^g is 0 in float32 far above this bound,
 // and differences of sums stay finite when g is -inf.
