@@ -65,6 +65,11 @@ __device__ __forceinline__ void ldmatrix_x2_trans(uint32_t &r0, uint32_t &r1, co
                  : "=r"(r0), "=r"(r1)
                  : "r"(smem_u32(p)));
 }
+// One arrival for the warp (32 on one barrier are served one by one).
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 // Two bf16 parts of a pair: hi the rounding, lo the rounding of what it left.
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
     hi = pack_bf16x2(a, b);
@@ -341,22 +346,32 @@ delta_prep_kernel(DeltaPrepArgs a) {
 //   O^T  = S^T Q~^T                 (while the chain rounds X)
 //   Z^T  = Xs^T K                   [needs X]       -> chain: S = e^{G_L} S + Z
 //   O^T += X^T P^T                  (while the chain rounds S)
-// S itself stays in the chain's registers in float32.  With kSplit its
-// operand copies are two bf16 parts: X^T takes S_hi (W_hi + W_lo) + S_lo W_hi,
-// Z takes both parts of Xs against the exact K, so each product carries 16
-// bits (the lowest part's product, 2^-18, is left out) and the state keeps
-// float32 accuracy over the walk (measured 3e-6 after 8192 tokens); without
-// it S is only ever seen through bf16 outputs and one part is enough.
+// S and Z go 64 rows of S at a time, so that the chain's work on one piece
+// runs beside the MMAs of the other.  S itself stays in the chain's registers
+// in float32.  With kSplit its operand copies are two bf16 parts: X^T takes
+// S_hi (W_hi + W_lo) + S_lo W_hi, Z takes both parts of Xs against the exact
+// K, so each product carries 16 bits (the lowest parts' product, 2^-18, is
+// left out) and the state keeps float32 accuracy over the walk (measured
+// 3e-6 after 8192 tokens); without it S is only ever seen through bf16
+// outputs and one part is enough.
 constexpr int kScanThreads = 448;
-constexpr int kChain = 256;
+constexpr int kChainWarps = 8;
 
+struct DeltaScanBars {
+    uint64_t full[2], empty[2], s_ready[2], z_full[2], x_full, xs_ready, o_full, o_free, drain;
+    uint32_t tmem_slot;
+    int abort_flag;
+};
 template <int DK, bool kSplit>
 struct DeltaScanSmem {
     using Block = DeltaBlock<DK, kSplit>;
     static constexpr uint32_t kK = Block::kBytes;
     static constexpr uint32_t kV = kK + Block::kKB * kBox64;
     static constexpr uint32_t kStage = kV + 2 * kBox64;
-    static constexpr uint32_t kBytes = 2 * kStage + 1024;
+    static constexpr uint32_t kOut = 2 * kStage;          // 64 tokens x 128 channels
+    static constexpr uint32_t kBars = kOut + 2 * kBox64;
+    static constexpr uint32_t kBytes = kBars + 256;
+    static_assert(sizeof(DeltaScanBars) <= 256 && kBytes <= 227 * 1024, "shared memory");
 };
 // tensor memory columns
 template <int DK, bool kSplit>
@@ -386,47 +401,49 @@ struct DeltaScanArgs {
 template <int DK, bool kSplit, bool kOut, bool kSave>
 __global__ void __launch_bounds__(kScanThreads, 1)
 delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  DeltaScanArgs a) {
+                  const __grid_constant__ CUtensorMap tm_o, DeltaScanArgs a) {
     using Smem = DeltaScanSmem<DK, kSplit>;
     using Block = DeltaBlock<DK, kSplit>;
     using Tm = DeltaScanTmem<DK, kSplit>;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[2], empty[2], s_ready, x_full, xs_ready, z_full, o_full, o_free, drain;
-    __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
+    constexpr int kPieces = DK / 64;
+    // the only shared memory of the kernel, so it starts on its alignment
+    extern __shared__ __align__(1024) uint8_t smem[];
+    DeltaScanBars &bar = *reinterpret_cast<DeltaScanBars *>(smem + Smem::kBars);
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // warp-uniform as the compiler sees it
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int slabs = (a.dv + 127) / 128;
     const int bh = blockIdx.x / slabs, v0 = (blockIdx.x % slabs) * 128;
     const int b = bh / a.heads, h = bh % a.heads;
     unsigned *err = a.err;
+    int *abort_flag = &bar.abort_flag;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&bar.full[s], 1);
+            mbar_init(&bar.empty[s], 1);
+            mbar_init(&bar.s_ready[s], kChainWarps);
+            mbar_init(&bar.z_full[s], 1);
         }
-        mbar_init(&s_ready, kChain);
-        mbar_init(&x_full, 1);
-        mbar_init(&xs_ready, kChain);
-        mbar_init(&z_full, 1);
-        mbar_init(&o_full, 1);
-        mbar_init(&o_free, 128);
-        mbar_init(&drain, 1);
-        abort_flag = 0;
+        mbar_init(&bar.x_full, 1);
+        mbar_init(&bar.xs_ready, kChainWarps);
+        mbar_init(&bar.o_full, 1);
+        mbar_init(&bar.o_free, 4);
+        mbar_init(&bar.drain, 1);
+        bar.abort_flag = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
+        if (kOut) tma_prefetch_desc(&tm_o);
     }
     if (warp == 1) {
-        tmem_alloc(&tmem_slot, 512);
+        tmem_alloc(&bar.tmem_slot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = bar.tmem_slot;
     grid_dependency_wait();
     const int n = delta_tokens_of(a.lengths, b, a.tokens);
     const int nc = (n + kC - 1) / kC;
@@ -435,28 +452,30 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (warp == 0) {
         if (lane == 0) {
             const int kh = h / (a.heads / a.key_heads);
-            for (; it < nc && !abort_flag; ++it) {
+            for (; it < nc && !*(volatile int *)abort_flag; ++it) {
                 const int s = it & 1;
-                if (it >= 2 && !mbar_wait(&empty[s], ((it >> 1) - 1) & 1, &abort_flag, err)) break;
+                if (it >= 2 && !mbar_wait(&bar.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
                 uint8_t *st = smem + s * Smem::kStage;
-                mbar_expect_tx(&full[s], Smem::kStage);
+                mbar_expect_tx(&bar.full[s], Smem::kStage);
                 bulk_load(st, a.blocks + ((size_t)bh * a.nc + it) * Block::kBytes, Block::kBytes,
-                          &full[s]);
+                          &bar.full[s]);
                 for (int x = 0; x < DK / 64; ++x)
-                    tma_load_4d(st + Smem::kK + x * kBox64, &tm_k, &full[s], 64 * x, kh, it * kC, b);
+                    tma_load_4d(st + Smem::kK + x * kBox64, &tm_k, &bar.full[s], 64 * x, kh, it * kC, b);
                 for (int x = 0; x < 2; ++x)
-                    tma_load_4d(st + Smem::kV + x * kBox64, &tm_v, &full[s], v0 + 64 * x, h, it * kC, b);
+                    tma_load_4d(st + Smem::kV + x * kBox64, &tm_v, &bar.full[s], v0 + 64 * x, h, it * kC, b);
             }
         }
     } else if (warp == 1) {
         constexpr uint32_t id_tv = idesc_bf16(128, 64, 1, 0);   // A: V tile, v contiguous
         constexpr uint32_t id_x = idesc_bf16(128, 64, 0, 0);
-        constexpr uint32_t id_z = idesc_bf16(128, DK, 0, 1);    // B: K tile, k contiguous
+        constexpr uint32_t id_z = idesc_bf16(128, 64, 0, 1);    // B: K box, k contiguous
         for (int c = 0; c < nc; ++c) {
             const int s = c & 1;
             uint8_t *st = smem + s * Smem::kStage;
-            const uint32_t sb = smem_u32(st);
-            if (!warp_wait(&full[s], (c >> 1) & 1, &abort_flag, err)) break;
+            // K-major tiles and MN-major boxes; offsets are added >> 4
+            const uint64_t kmaj = smem_desc_sw128(smem_u32(st), 16, 1024);
+            const uint64_t mnmaj = smem_desc_sw128(smem_u32(st), kBox64, 1024);
+            if (!warp_spin_wait(&bar.full[s], (c >> 1) & 1, abort_flag, err)) break;
             const int cnt = n - c * kC;
             if (cnt < kC) {
                 // rows behind the sequence may hold anything: their products
@@ -470,105 +489,118 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 __syncwarp();
             }
             tc_fence_after();
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
-                    const uint64_t ad = smem_desc_sw128(sb + Smem::kV + ks * 2048, kBox64, 1024);
-                    mma_bf16(tmem + Tm::kX, ad, smem_desc_sw128(sb + Block::kT + ks * 32, 16, 1024), id_tv, ks > 0);
+                    const uint64_t ad = mnmaj + ((Smem::kV + ks * 2048) >> 4);
+                    mma_bf16(tmem + Tm::kX, ad, kmaj + ((Block::kT + ks * 32) >> 4), id_tv, ks > 0);
                     if (kSplit)
-                        mma_bf16(tmem + Tm::kX, ad, smem_desc_sw128(sb + Block::kTlo + ks * 32, 16, 1024), id_tv, 1);
+                        mma_bf16(tmem + Tm::kX, ad, kmaj + ((Block::kTlo + ks * 32) >> 4), id_tv, 1);
                 }
             }
-            if (!warp_wait(&s_ready, c & 1, &abort_flag, err)) break;
-            tc_fence_after();
-            if (lane == 0) {
+            __syncwarp();
+            bool ok = true;
 #pragma unroll
-                for (int ks = 0; ks < DK / 16; ++ks) {
-                    const uint32_t o = (ks / 4) * kBox64 + (ks % 4) * 32;
-                    const uint64_t w = smem_desc_sw128(sb + Block::kW + o, 16, 1024);
-                    mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kShi + 8 * ks, w, id_x, 1);
-                    if (kSplit) {
-                        mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kSlo + 8 * ks, w, id_x, 1);
-                        mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kShi + 8 * ks,
-                                    smem_desc_sw128(sb + Block::kWlo + o, 16, 1024), id_x, 1);
-                    }
-                }
-                mma_commit(&x_full);
-            }
-            if (kOut) {
-                if (c > 0 && !warp_wait(&o_free, (c - 1) & 1, &abort_flag, err)) break;
+            for (int p = 0; p < kPieces; ++p) {
+                ok = ok && warp_spin_wait(&bar.s_ready[p], c & 1, abort_flag, err);
+                if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4) {
+                        const int ks = 4 * p + k4;
+                        const uint32_t o = p * kBox64 + k4 * 32;
+                        const uint64_t w = kmaj + ((Block::kW + o) >> 4);
+                        mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kShi + 8 * ks, w, id_x, 1);
+                        if (kSplit) {
+                            mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kSlo + 8 * ks, w, id_x, 1);
+                            mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kShi + 8 * ks,
+                                        kmaj + ((Block::kWlo + o) >> 4), id_x, 1);
+                        }
+                    }
+                    if (p == kPieces - 1) mma_commit(&bar.x_full);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            if (kOut) {
+                if (c > 0 && !warp_spin_wait(&bar.o_free, (c - 1) & 1, abort_flag, err)) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < DK / 16; ++ks)
                         mma_bf16_ts(tmem + Tm::kO, tmem + Tm::kShi + 8 * ks,
-                                    smem_desc_sw128(sb + Block::kQ + (ks / 4) * kBox64 + (ks % 4) * 32, 16, 1024),
+                                    kmaj + ((Block::kQ + (ks / 4) * kBox64 + (ks % 4) * 32) >> 4),
                                     id_x, ks > 0);
                 }
+                __syncwarp();
             }
-            if (!warp_wait(&xs_ready, c & 1, &abort_flag, err)) break;
+            if (!warp_spin_wait(&bar.xs_ready, c & 1, abort_flag, err)) break;
             tc_fence_after();
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                    const uint64_t kd = smem_desc_sw128(sb + Smem::kK + ks * 2048, kBox64, 1024);
-                    mma_bf16_ts(tmem + Tm::kZ, tmem + Tm::kXs + 8 * ks, kd, id_z, ks > 0);
-                    if (kSplit) mma_bf16_ts(tmem + Tm::kZ, tmem + Tm::kXslo + 8 * ks, kd, id_z, 1);
+                for (int p = 0; p < kPieces; ++p) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint64_t kd = mnmaj + ((Smem::kK + p * kBox64 + ks * 2048) >> 4);
+                        mma_bf16_ts(tmem + Tm::kZ + 64 * p, tmem + Tm::kXs + 8 * ks, kd, id_z, ks > 0);
+                        if (kSplit)
+                            mma_bf16_ts(tmem + Tm::kZ + 64 * p, tmem + Tm::kXslo + 8 * ks, kd, id_z, 1);
+                    }
+                    mma_commit(&bar.z_full[p]);
                 }
-                mma_commit(&z_full);
                 if (kOut) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         mma_bf16_ts(tmem + Tm::kO, tmem + Tm::kXb + 8 * ks,
-                                    smem_desc_sw128(sb + Block::kP + ks * 32, 16, 1024), id_x, 1);
-                    mma_commit(&o_full);
+                                    kmaj + ((Block::kP + ks * 32) >> 4), id_x, 1);
+                    mma_commit(&bar.o_full);
                 }
-                mma_commit(&empty[s]);
+                mma_commit(&bar.empty[s]);
             }
             __syncwarp();
         }
     } else if (warp < 10) {
-        constexpr int kHalf = DK / 2;                      // k columns of this warpgroup
-        const int wg = (warp - 2) / 4;
+        const int wg = (warp - 2) / 4;                     // k columns 64 p + 32 wg ..
         const int v = v0 + 32 * (warp % 4) + lane;
         const bool live = v < a.dv;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
-        const size_t sbase = ((size_t)bh * DK + kHalf * wg) * a.dv + v;
-        float S[kHalf];
+        const size_t sbase = ((size_t)bh * DK + 32 * wg) * a.dv + v;
+        float S[kPieces][32];
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j)
-            S[j] = a.state_in && live ? a.state_in[sbase + (size_t)j * a.dv] : 0.f;
-        // S's operand copies, 32 columns at a time; c: the chunk that starts with it
-        auto put_state = [&](int c) {
+        for (int p = 0; p < kPieces; ++p)
 #pragma unroll
-            for (int p = 0; p < kHalf / 32; ++p) {
-                uint32_t hi[16], lo[16];
+            for (int j = 0; j < 32; ++j)
+                S[p][j] = a.state_in && live ? a.state_in[sbase + (size_t)(64 * p + j) * a.dv] : 0.f;
+        // the operand copies of a piece of S; c: the chunk that starts with it
+        auto put_state = [&](int p, int c) {
+            uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    if (kSplit) split_pair(S[32 * p + 2 * j], S[32 * p + 2 * j + 1], hi[j], lo[j]);
-                    else hi[j] = pack_bf16x2(S[32 * p + 2 * j], S[32 * p + 2 * j + 1]);
-                }
-                tmem_st16(tl + Tm::kShi + (kHalf * wg + 32 * p) / 2, hi);
-                if (kSplit) tmem_st16(tl + Tm::kSlo + (kHalf * wg + 32 * p) / 2, lo);
-                if (kSave && live && c < nc) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(
-                        a.s_save + (((size_t)bh * a.nc + c) * a.dv + v) * DK + kHalf * wg + 32 * p);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        dst[j] = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
-                }
+            for (int j = 0; j < 16; ++j) {
+                if (kSplit) split_pair(S[p][2 * j], S[p][2 * j + 1], hi[j], lo[j]);
+                else hi[j] = pack_bf16x2(S[p][2 * j], S[p][2 * j + 1]);
             }
+            tmem_st16(tl + Tm::kShi + 32 * p + 16 * wg, hi);
+            if (kSplit) tmem_st16(tl + Tm::kSlo + 32 * p + 16 * wg, lo);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&s_ready);
+            warp_arrive(&bar.s_ready[p]);
+            if (kSave && live && c < nc) {
+                uint4 *dst = reinterpret_cast<uint4 *>(
+                    a.s_save + (((size_t)bh * a.nc + c) * a.dv + v) * DK + 64 * p + 32 * wg);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    dst[j] = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
+            }
         };
-        put_state(0);
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) put_state(p, 0);
         for (int c = 0; c < nc; ++c) {
             const int s = c & 1;
             const float *hdr = reinterpret_cast<const float *>(smem + s * Smem::kStage + Block::kHdr);
-            if (!warp_wait(&full[s], (c >> 1) & 1, &abort_flag, err)) break;
+            if (!warp_spin_wait(&bar.full[s], (c >> 1) & 1, abort_flag, err)) break;
             const float eL = hdr[64];
-            if (!warp_wait(&x_full, c & 1, &abort_flag, err)) break;
+            if (!warp_spin_wait(&bar.x_full, c & 1, abort_flag, err)) break;
             tc_fence_after();
             {
                 uint32_t x[32], hi[16], lo[16], xb[16];
@@ -587,7 +619,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (kOut) tmem_st16(tl + Tm::kXb + 16 * wg, xb);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&xs_ready);
+                warp_arrive(&bar.xs_ready);
                 if (kSave && live) {
                     uint4 *dst = reinterpret_cast<uint4 *>(
                         a.x_save + (((size_t)bh * a.nc + c) * a.dv + v) * kC + 32 * wg);
@@ -596,55 +628,81 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         dst[j] = make_uint4(xb[4 * j], xb[4 * j + 1], xb[4 * j + 2], xb[4 * j + 3]);
                 }
             }
-            if (!warp_wait(&z_full, c & 1, &abort_flag, err)) break;
-            tc_fence_after();
+            bool ok = true;
 #pragma unroll
-            for (int p = 0; p < kHalf / 32; ++p) {
+            for (int p = 0; p < kPieces; ++p) {
+                ok = ok && warp_spin_wait(&bar.z_full[p], c & 1, abort_flag, err);
+                if (!ok) break;
+                tc_fence_after();
                 uint32_t z[32];
-                tmem_ld32(tl + Tm::kZ + kHalf * wg + 32 * p, z);
+                tmem_ld32(tl + Tm::kZ + 64 * p + 32 * wg, z);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    S[32 * p + j] = fmaf(eL, S[32 * p + j], __uint_as_float(z[j]));
+                    S[p][j] = fmaf(eL, S[p][j], __uint_as_float(z[j]));
+                put_state(p, c + 1);
             }
-            put_state(c + 1);
+            if (!ok) break;
         }
         if (a.state_out && live)
 #pragma unroll
-            for (int j = 0; j < kHalf; ++j) a.state_out[sbase + (size_t)j * a.dv] = S[j];
+            for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) a.state_out[sbase + (size_t)(64 * p + j) * a.dv] = S[p][j];
     } else if (kOut) {
-        const int v = v0 + 32 * (warp % 4) + lane;
-        const bool live = v < a.dv;
+        // O through shared memory, token rows of 64 channels (the swizzle of
+        // the copy out), so that global memory sees whole lines
+        const int col = 32 * (warp % 4) + lane, tid = threadIdx.x - 320;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
-        const size_t step = (size_t)a.heads * a.dv;
+        uint8_t *box = smem + Smem::kOut + (col / 64) * kBox64 + (col & 7) * 2;
         for (int c = 0; c < nc; ++c) {
-            if (!warp_wait(&o_full, c & 1, &abort_flag, err)) break;
+            if (!warp_spin_wait(&bar.o_full, c & 1, abort_flag, err)) break;
             tc_fence_after();
             uint32_t o[2][32];
             tmem_ld32(tl + Tm::kO, o[0]);
             tmem_ld32(tl + Tm::kO + 32, o[1]);
             tmem_wait_ld();
             tc_fence_before();
-            mbar_arrive(&o_free);
-            const int cnt = n - c * kC;
-            if (live) {
-                __nv_bfloat16 *dst = a.out + (((size_t)b * a.tokens + c * kC) * a.heads + h) * a.dv + v;
+            warp_arrive(&bar.o_free);
+            if (tid == 0) tma_store_wait_read();           // the last tile has left
+            named_barrier(1, 128);
 #pragma unroll
-                for (int i = 0; i < kC; ++i)
-                    if (i < cnt) dst[i * step] = __float2bfloat16_rn(__uint_as_float(o[i / 32][i % 32]));
+            for (int i = 0; i < kC; ++i)
+                *reinterpret_cast<__nv_bfloat16 *>(box + i * 128 + ((((col & 63) >> 3) ^ (i & 7)) << 4)) =
+                    __float2bfloat16_rn(__uint_as_float(o[i / 32][i % 32]));
+            const int cnt = n - c * kC;
+            if (cnt >= kC) fence_async_shared();
+            named_barrier(1, 128);
+            if (cnt >= kC) {
+                if (tid == 0) {
+                    for (int x = 0; x < 2; ++x)
+                        if (v0 + 64 * x < a.dv)
+                            tma_store_4d(&tm_o, smem + Smem::kOut + x * kBox64, v0 + 64 * x, h, c * kC, b);
+                    tma_store_commit();
+                }
+            } else {                                       // rows behind the sequence stay
+                for (int i = tid; i < cnt * 16; i += 128) {
+                    const int r = i / 16, ch = i % 16;
+                    if (v0 + ch * 8 < a.dv)
+                        *reinterpret_cast<uint4 *>(
+                            a.out + (((size_t)b * a.tokens + c * kC + r) * a.heads + h) * a.dv + v0 + ch * 8) =
+                            *reinterpret_cast<const uint4 *>(smem + Smem::kOut + (ch / 8) * kBox64 + r * 128 +
+                                                             (((ch & 7) ^ (r & 7)) << 4));
+                }
             }
         }
+        if (tid == 0) tma_store_wait_read();
     }
     tc_fence_before();
     __syncthreads();
     // After an abort, wait (bounded) for the copies still in flight before
     // shared memory goes away and for the MMAs before tensor memory is freed.
-    if (abort_flag && warp == 0 && lane == 0)
-        for (int j = max(0, it - 2); j < it; ++j) mbar_drain(&full[j & 1], (j >> 1) & 1, err);
+    if (*abort_flag && warp == 0 && lane == 0)
+        for (int j = max(0, it - 2); j < it; ++j) mbar_drain(&bar.full[j & 1], (j >> 1) & 1, err);
     if (warp == 1) {
-        if (abort_flag && lane == 0) {
-            mma_commit(&drain);
-            mbar_drain(&drain, 0, err);
+        if (*abort_flag && lane == 0) {
+            mma_commit(&bar.drain);
+            mbar_drain(&bar.drain, 0, err);
         }
         __syncwarp();
         tc_fence_after();
@@ -686,9 +744,10 @@ cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, __nv_
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Smem::kBytes);
     if (e != cudaSuccess) return e;
-    CUtensorMap tm_k, tm_v;
+    CUtensorMap tm_k, tm_v, tm_o;
     if (!token_map(&tm_k, a.k, a.batch, a.seqlen, a.key_heads, a.dk) ||
-        !token_map(&tm_v, a.v, a.batch, a.seqlen, a.heads, a.dv))
+        !token_map(&tm_v, a.v, a.batch, a.seqlen, a.heads, a.dv) ||
+        !token_map(&tm_o, kOut ? a.out : a.v, a.batch, a.seqlen, a.heads, a.dv))
         return cudaErrorInvalidValue;
     DeltaScanArgs s = {blocks, a.lengths, a.state_in, a.state_out, (__nv_bfloat16 *)a.out, x_save,
                        s_save, a.heads, a.key_heads, a.seqlen, nc, a.dv, device_error_word()};
@@ -697,7 +756,7 @@ cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, __nv_
     count_launch();
     return launch_overlapped(delta_scan_kernel<DK, kSplit, kOut, kSave>,
                              dim3((unsigned)(a.batch * a.heads * slabs)), dim3(kScanThreads),
-                             Smem::kBytes, stream, tm_k, tm_v, s);
+                             Smem::kBytes, stream, tm_k, tm_v, tm_o, s);
 }
 
 template <int DK, bool kSplit>

@@ -108,6 +108,27 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// As warp_wait, for waits of a few hundred cycles on a chain of hand-overs:
+// the warp polls at once and only then falls back to the suspending wait,
+// whose wake-up and clock reads cost as much as such a wait lasts.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool warp_spin_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                               unsigned *err) {
+    for (int i = 0; i < 256; ++i)
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    return warp_wait(bar, parity, abort, err);
+}
+
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)map) : "memory");
@@ -259,6 +280,17 @@ __device__ __forceinline__ void tmem_cp_128x256b(uint32_t taddr, uint64_t s_desc
 }
 __device__ __forceinline__ void tmem_wait_ld() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// One lane of a converged warp, chosen by the hardware.  tcgen05.mma issued
+// under this predicate takes its operands from uniform registers (about 10
+// cycles an instruction); under `lane == 0` the compiler cannot tell that one
+// thread issues and spends 175 (measured), more than a small MMA runs.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p));
+    return p != 0;
 }
 
 // ------------------------------------------------------------------ descriptors
