@@ -174,7 +174,8 @@ static retnet_status check_delta_shape(const retnet_delta_shape *s) {
     // a CTA per (sequence, head) and slab of columns or chunk of tokens
     const long long bh = (long long)s->batch * s->heads;
     const long long chunks = (s->seqlen + (long long)kDeltaChunk - 1) / kDeltaChunk;
-    if (bh * (chunks > 8 ? chunks : 8) > 0x7fffffffll) return RETNET_ERR_UNSUPPORTED;
+    // (and a row of the saved operands per value channel of each)
+    if (bh > 0x7fffffffll / 256 / (chunks > 0 ? chunks : 1)) return RETNET_ERR_UNSUPPORTED;
     return RETNET_OK;
 }
 static bool algo_ok(retnet_algo a) {
@@ -632,9 +633,10 @@ retnet_status retnet_delta_backward_workspace_size(const retnet_delta_shape *sha
     if (!bytes || !algo_ok(algo)) return RETNET_ERR_INVALID_ARG;
     retnet_status st = check_delta_shape(shape);
     if (st != RETNET_OK) return st;
-    if (algo == RETNET_ALGO_TENSOR) return RETNET_ERR_UNSUPPORTED;
-    *bytes = delta_backward_simt_workspace(shape->batch, shape->heads, shape->key_heads,
-                                           shape->seqlen, shape->dk, shape->dv);
+    const bool tensor = delta_tensor(shape, algo);
+    if (algo == RETNET_ALGO_TENSOR && !tensor) return RETNET_ERR_UNSUPPORTED;
+    *bytes = (tensor ? delta_backward_tc_workspace : delta_backward_simt_workspace)(
+        shape->batch, shape->heads, shape->key_heads, shape->seqlen, shape->dk, shape->dv);
     return RETNET_OK;
 }
 
@@ -658,7 +660,10 @@ retnet_status retnet_delta_backward(const void *q, const void *k, const void *v,
         return RETNET_ERR_WORKSPACE;
     a.d_out = d_out;
     a.dq = dq; a.dk_grad = dk; a.dv_grad = dv; a.dg = dg; a.dbeta = dbeta;
-    RETNET_CUDA_TRY(launch_delta_backward_simt(a, workspace, (cudaStream_t)stream));
+    if (delta_tensor(shape, algo))
+        RETNET_CUDA_TRY(launch_delta_backward_tc(a, workspace, (cudaStream_t)stream));
+    else
+        RETNET_CUDA_TRY(launch_delta_backward_simt(a, workspace, (cudaStream_t)stream));
     return RETNET_OK;
 }
 

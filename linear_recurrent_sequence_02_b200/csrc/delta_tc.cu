@@ -40,10 +40,11 @@ struct DeltaBlock {
     static constexpr uint32_t kTlo = kBox64;
     static constexpr uint32_t kW = kSplit ? 2 * kBox64 : kBox64;
     static constexpr uint32_t kWlo = kW + kKB * kBox64;
-    static constexpr uint32_t kQ = kSplit ? kWlo + kKB * kBox64 : kWlo;
+    // float rest[64] = e^{G_L - G}, then e^{G_L}; a walk without output stops here
+    static constexpr uint32_t kHdr = kSplit ? kWlo + kKB * kBox64 : kWlo;
+    static constexpr uint32_t kQ = kHdr + 1024;
     static constexpr uint32_t kP = kQ + kKB * kBox64;
-    static constexpr uint32_t kHdr = kP + kBox64;       // float rest[64] = e^{G_L - G}, then e^{G_L}
-    static constexpr uint32_t kBytes = kHdr + 1024;
+    static constexpr uint32_t kBytes = kP + kBox64;
 };
 
 // Byte offset of element (row, col) of a 64-row tile of boxes.
@@ -74,6 +75,28 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
     hi = pack_bf16x2(a, b);
     lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+}
+
+// Rows cnt.. of `boxes` 64-row boxes as zeros, by one warp.  Rows behind a
+// sequence may hold anything; the products that sum over tokens meet zeros
+// there on their other side, but 0 * NaN would not be 0.
+__device__ __forceinline__ void clear_rows(uint8_t *box, int boxes, int cnt, int lane) {
+    for (int i = lane; i < (kC - cnt) * 8; i += 32) {
+        const uint32_t o = (cnt + i / 8) * 128 + (i % 8) * 16;
+        for (int x = 0; x < boxes; ++x)
+            *reinterpret_cast<uint4 *>(box + x * kBox64 + o) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_shared();
+    __syncwarp();
+}
+// 64 tokens of a v channel's accumulator into a tile of token rows (two
+// boxes of 64 channels), bf16: col is the channel in the tile.
+__device__ __forceinline__ void put_channel(uint8_t *tile, int col, const uint32_t (&o)[2][32]) {
+    uint8_t *box = tile + (col / 64) * kBox64 + (col & 7) * 2;
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+        *reinterpret_cast<__nv_bfloat16 *>(box + i * 128 + ((((col & 63) >> 3) ^ (i & 7)) << 4)) =
+            __float2bfloat16_rn(__uint_as_float(o[i / 32][i % 32]));
 }
 
 // ------------------------------------------------------------------ prep
@@ -443,27 +466,33 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bar.tmem_slot;
+    // All 512 columns are this CTA's, so they start at address 0; as a
+    // constant it keeps the MMAs' operands out of general registers.
+    constexpr uint32_t tmem = 0;
     grid_dependency_wait();
     const int n = delta_tokens_of(a.lengths, b, a.tokens);
     const int nc = (n + kC - 1) / kC;
 
     int it = 0;                                            // chunks whose copies were issued
     if (warp == 0) {
-        if (lane == 0) {
-            const int kh = h / (a.heads / a.key_heads);
-            for (; it < nc && !*(volatile int *)abort_flag; ++it) {
-                const int s = it & 1;
-                if (it >= 2 && !mbar_wait(&bar.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
-                uint8_t *st = smem + s * Smem::kStage;
-                mbar_expect_tx(&bar.full[s], Smem::kStage);
-                bulk_load(st, a.blocks + ((size_t)bh * a.nc + it) * Block::kBytes, Block::kBytes,
-                          &bar.full[s]);
-                for (int x = 0; x < DK / 64; ++x)
-                    tma_load_4d(st + Smem::kK + x * kBox64, &tm_k, &bar.full[s], 64 * x, kh, it * kC, b);
+        const int kh = h / (a.heads / a.key_heads);
+        const uint8_t *blocks = a.blocks + (size_t)bh * a.nc * Block::kBytes;
+        for (; it < nc; ++it) {
+            const int s = it & 1;
+            if (it >= 2 && !warp_spin_wait(&bar.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
+            uint8_t *st = smem + s * Smem::kStage;
+            if (elect_one()) {
+                constexpr uint32_t kBlock = kOut ? Block::kBytes : Block::kQ;
+                mbar_expect_tx(&bar.full[s], kBlock + Smem::kStage - Smem::kK);
+                bulk_load(st, blocks + (size_t)it * Block::kBytes, kBlock, &bar.full[s]);
+#pragma unroll
                 for (int x = 0; x < 2; ++x)
                     tma_load_4d(st + Smem::kV + x * kBox64, &tm_v, &bar.full[s], v0 + 64 * x, h, it * kC, b);
+#pragma unroll
+                for (int x = 0; x < DK / 64; ++x)
+                    tma_load_4d(st + Smem::kK + x * kBox64, &tm_k, &bar.full[s], 64 * x, kh, it * kC, b);
             }
+            __syncwarp();
         }
     } else if (warp == 1) {
         constexpr uint32_t id_tv = idesc_bf16(128, 64, 1, 0);   // A: V tile, v contiguous
@@ -476,18 +505,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const uint64_t kmaj = smem_desc_sw128(smem_u32(st), 16, 1024);
             const uint64_t mnmaj = smem_desc_sw128(smem_u32(st), kBox64, 1024);
             if (!warp_spin_wait(&bar.full[s], (c >> 1) & 1, abort_flag, err)) break;
-            const int cnt = n - c * kC;
-            if (cnt < kC) {
-                // rows behind the sequence may hold anything: their products
-                // meet zeros in T^ and Xs, but 0 * NaN would not be 0
-                for (int i = lane; i < (kC - cnt) * 8; i += 32) {
-                    const uint32_t o = (cnt + i / 8) * 128 + (i % 8) * 16;
-                    for (uint32_t x = 0; x < DK / 64 + 2; ++x)
-                        *reinterpret_cast<uint4 *>(st + Smem::kK + x * kBox64 + o) = make_uint4(0, 0, 0, 0);
-                }
-                fence_async_shared();
-                __syncwarp();
-            }
+            if (n - c * kC < kC) clear_rows(st + Smem::kK, DK / 64 + 2, n - c * kC, lane);
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -654,7 +672,6 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         // the copy out), so that global memory sees whole lines
         const int col = 32 * (warp % 4) + lane, tid = threadIdx.x - 320;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
-        uint8_t *box = smem + Smem::kOut + (col / 64) * kBox64 + (col & 7) * 2;
         for (int c = 0; c < nc; ++c) {
             if (!warp_spin_wait(&bar.o_full, c & 1, abort_flag, err)) break;
             tc_fence_after();
@@ -666,10 +683,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             warp_arrive(&bar.o_free);
             if (tid == 0) tma_store_wait_read();           // the last tile has left
             named_barrier(1, 128);
-#pragma unroll
-            for (int i = 0; i < kC; ++i)
-                *reinterpret_cast<__nv_bfloat16 *>(box + i * 128 + ((((col & 63) >> 3) ^ (i & 7)) << 4)) =
-                    __float2bfloat16_rn(__uint_as_float(o[i / 32][i % 32]));
+            put_channel(smem + Smem::kOut, col, o);
             const int cnt = n - c * kC;
             if (cnt >= kC) fence_async_shared();
             named_barrier(1, 128);
@@ -703,6 +717,699 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (*abort_flag && lane == 0) {
             mma_commit(&bar.drain);
             mbar_drain(&bar.drain, 0, err);
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ reverse scan
+// The gradient's walk, last chunk first.  D is the gradient of the state
+// behind a chunk; with dO the output's gradient
+//   dX = P^T dO + diag(e^{G_L - G}) K D,   dV = T^^T dX,
+//   D <- e^{G_L} D + Q~^T dO - W^T dX,
+// transposed and laid out as in the forward walk (v channels as lanes, D in
+// the chain's registers in float32, its operand copy and dX rounded to bf16:
+// gradients leave in bf16).  Per chunk, in the order of the MMAs:
+//   Y1^T = dO^T P;  Y2^T = D^T K^T       [needs D]   -> chain: dX = Y1 + rest Y2
+//   Z^T  = dO^T Q~                       (while the chain rounds dX)
+//   Z^T += dX^T (-W)                     [needs dX]  -> chain: D = e^{G_L} D + Z
+//   dV^T = dX^T T^                       (while the chain rounds D)
+// D is kept for every chunk (d_save, as S^T in the forward walk).
+struct DeltaReverseBars {
+    uint64_t full[2], empty[2], d_ready[2], z_full[2], y_full, dx_ready, v_full, v_free, drain;
+    uint32_t tmem_slot;
+    int abort_flag;
+};
+
+struct DeltaReverseArgs {
+    const uint8_t *blocks;
+    const int *lengths;
+    __nv_bfloat16 *d_save;
+    int heads, key_heads, tokens, nc, dv;
+    unsigned *err;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(kScanThreads, 1)
+delta_reverse_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_do,
+                     const __grid_constant__ CUtensorMap tm_dv, DeltaReverseArgs a) {
+    using Smem = DeltaScanSmem<DK, false>;                // V's place holds dO, the output's dV
+    using Block = DeltaBlock<DK, false>;
+    constexpr int kPieces = DK / 64;
+    constexpr uint32_t kD = 0, kZ = DK / 2, kY1 = kZ + DK, kY2 = kY1 + 64, kDx = kY2 + 64, kDv = kDx + 32;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    DeltaReverseBars &bar = *reinterpret_cast<DeltaReverseBars *>(smem + Smem::kBars);
+    static_assert(sizeof(DeltaReverseBars) <= 256, "barriers");
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    const int slabs = (a.dv + 127) / 128;
+    const int bh = blockIdx.x / slabs, v0 = (blockIdx.x % slabs) * 128;
+    const int b = bh / a.heads, h = bh % a.heads;
+    unsigned *err = a.err;
+    int *abort_flag = &bar.abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar.full[s], 1);
+            mbar_init(&bar.empty[s], 1);
+            mbar_init(&bar.d_ready[s], kChainWarps);
+            mbar_init(&bar.z_full[s], 1);
+        }
+        mbar_init(&bar.y_full, 1);
+        mbar_init(&bar.dx_ready, kChainWarps);
+        mbar_init(&bar.v_full, 1);
+        mbar_init(&bar.v_free, 4);
+        mbar_init(&bar.drain, 1);
+        bar.abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_do);
+        tma_prefetch_desc(&tm_dv);
+    }
+    if (warp == 1) {
+        tmem_alloc(&bar.tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    constexpr uint32_t tmem = 0;                           // all 512 columns, as above
+    grid_dependency_wait();
+    const int n = delta_tokens_of(a.lengths, b, a.tokens);
+    const int nc = (n + kC - 1) / kC;
+
+    int it = 0;                                            // chunks whose copies were issued
+    if (warp == 0) {
+        const int kh = h / (a.heads / a.key_heads);
+        const uint8_t *blocks = a.blocks + (size_t)bh * a.nc * Block::kBytes;
+        for (; it < nc; ++it) {
+            const int s = it & 1, c = nc - 1 - it;
+            if (it >= 2 && !warp_spin_wait(&bar.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
+            uint8_t *st = smem + s * Smem::kStage;
+            if (elect_one()) {
+                mbar_expect_tx(&bar.full[s], Smem::kStage);
+                bulk_load(st, blocks + (size_t)c * Block::kBytes, Block::kBytes, &bar.full[s]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    tma_load_4d(st + Smem::kV + x * kBox64, &tm_do, &bar.full[s], v0 + 64 * x, h, c * kC, b);
+#pragma unroll
+                for (int x = 0; x < DK / 64; ++x)
+                    tma_load_4d(st + Smem::kK + x * kBox64, &tm_k, &bar.full[s], 64 * x, kh, c * kC, b);
+            }
+            __syncwarp();
+        }
+    } else if (warp == 1) {
+        constexpr uint32_t id_do = idesc_bf16(128, 64, 1, 1);   // A: dO tile, v contiguous
+        constexpr uint32_t id_k = idesc_bf16(128, 64, 0, 0);    // B: K tile, k contiguous
+        constexpr uint32_t id_w = idesc_bf16(128, 64, 0, 1);    // B: W, T^, columns contiguous
+        for (int u = 0; u < nc; ++u) {
+            const int s = u & 1, cnt = n - (nc - 1 - u) * kC;
+            uint8_t *st = smem + s * Smem::kStage;
+            const uint64_t kmaj = smem_desc_sw128(smem_u32(st), 16, 1024);
+            const uint64_t mnmaj = smem_desc_sw128(smem_u32(st), kBox64, 1024);
+            if (!warp_spin_wait(&bar.full[s], (u >> 1) & 1, abort_flag, err)) break;
+            if (cnt < kC) clear_rows(st + Smem::kK, DK / 64 + 2, cnt, lane);
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16(tmem + kY1, mnmaj + ((Smem::kV + ks * 2048) >> 4),
+                             mnmaj + ((Block::kP + ks * 2048) >> 4), id_do, ks > 0);
+            }
+            __syncwarp();
+            bool ok = true;
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                ok = ok && warp_spin_wait(&bar.d_ready[p], u & 1, abort_flag, err);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4)
+                        mma_bf16_ts(tmem + kY2, tmem + kD + 32 * p + 8 * k4,
+                                    kmaj + ((Smem::kK + p * kBox64 + k4 * 32) >> 4), id_k, p + k4 > 0);
+                    if (p == kPieces - 1) {
+                        mma_commit(&bar.y_full);
+#pragma unroll
+                        for (int q = 0; q < kPieces; ++q)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_bf16(tmem + kZ + 64 * q, mnmaj + ((Smem::kV + ks * 2048) >> 4),
+                                         mnmaj + ((Block::kQ + q * kBox64 + ks * 2048) >> 4), id_do, ks > 0);
+                    }
+                }
+                __syncwarp();
+            }
+            if (!ok || !warp_spin_wait(&bar.dx_ready, u & 1, abort_flag, err)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16_ts(tmem + kZ + 64 * p, tmem + kDx + 8 * ks,
+                                    mnmaj + ((Block::kW + p * kBox64 + ks * 2048) >> 4), id_w, 1);
+                    mma_commit(&bar.z_full[p]);
+                }
+            }
+            __syncwarp();
+            if (u > 0 && !warp_spin_wait(&bar.v_free, (u - 1) & 1, abort_flag, err)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16_ts(tmem + kDv, tmem + kDx + 8 * ks,
+                                mnmaj + ((Block::kT + ks * 2048) >> 4), id_w, ks > 0);
+                mma_commit(&bar.v_full);
+                mma_commit(&bar.empty[s]);
+            }
+            __syncwarp();
+        }
+    } else if (warp < 10) {
+        const int wg = (warp - 2) / 4;                     // k columns 64 p + 32 wg ..
+        const int v = v0 + 32 * (warp % 4) + lane;
+        const bool live = v < a.dv;
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
+        float D[kPieces][32] = {};
+        // the operand copy of a piece of D, kept for chunk c (the one in front of it)
+        auto put_grad = [&](int p, int c) {
+            uint32_t hi[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) hi[j] = pack_bf16x2(D[p][2 * j], D[p][2 * j + 1]);
+            tmem_st16(tl + kD + 32 * p + 16 * wg, hi);
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&bar.d_ready[p]);
+            if (live && c >= 0) {
+                uint4 *dst = reinterpret_cast<uint4 *>(
+                    a.d_save + (((size_t)bh * a.nc + c) * a.dv + v) * DK + 64 * p + 32 * wg);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    dst[j] = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
+            }
+        };
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) put_grad(p, nc - 1);
+        for (int u = 0; u < nc; ++u) {
+            const int s = u & 1;
+            const float *hdr = reinterpret_cast<const float *>(smem + s * Smem::kStage + Block::kHdr);
+            if (!warp_spin_wait(&bar.full[s], (u >> 1) & 1, abort_flag, err)) break;
+            const float eL = hdr[64];
+            if (!warp_spin_wait(&bar.y_full, u & 1, abort_flag, err)) break;
+            tc_fence_after();
+            {
+                uint32_t y1[32], y2[32], dx[16];
+                tmem_ld32(tl + kY1 + 32 * wg, y1);
+                tmem_ld32(tl + kY2 + 32 * wg, y2);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float2 r = *reinterpret_cast<const float2 *>(hdr + 32 * wg + 2 * j);
+                    dx[j] = pack_bf16x2(
+                        fmaf(r.x, __uint_as_float(y2[2 * j]), __uint_as_float(y1[2 * j])),
+                        fmaf(r.y, __uint_as_float(y2[2 * j + 1]), __uint_as_float(y1[2 * j + 1])));
+                }
+                tmem_st16(tl + kDx + 16 * wg, dx);
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(&bar.dx_ready);
+            }
+            bool ok = true;
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                ok = ok && warp_spin_wait(&bar.z_full[p], u & 1, abort_flag, err);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t z[32];
+                tmem_ld32(tl + kZ + 64 * p + 32 * wg, z);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) D[p][j] = fmaf(eL, D[p][j], __uint_as_float(z[j]));
+                put_grad(p, nc - 2 - u);
+            }
+            if (!ok) break;
+        }
+    } else {
+        const int col = 32 * (warp % 4) + lane, tid = threadIdx.x - 320;
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
+        for (int u = 0; u < nc; ++u) {
+            if (!warp_spin_wait(&bar.v_full, u & 1, abort_flag, err)) break;
+            tc_fence_after();
+            uint32_t o[2][32];
+            tmem_ld32(tl + kDv, o[0]);
+            tmem_ld32(tl + kDv + 32, o[1]);
+            tmem_wait_ld();
+            tc_fence_before();
+            warp_arrive(&bar.v_free);
+            if (tid == 0) tma_store_wait_read();
+            named_barrier(1, 128);
+            put_channel(smem + Smem::kOut, col, o);        // zeros behind the sequence
+            fence_async_shared();
+            named_barrier(1, 128);
+            if (tid == 0) {
+                for (int x = 0; x < 2; ++x)
+                    if (v0 + 64 * x < a.dv)
+                        tma_store_4d(&tm_dv, smem + Smem::kOut + x * kBox64, v0 + 64 * x, h,
+                                     (nc - 1 - u) * kC, b);
+                tma_store_commit();
+            }
+        }
+        if (tid == 0) tma_store_wait_read();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && warp == 0 && lane == 0)             // as in the forward walk
+        for (int j = max(0, it - 2); j < it; ++j) mbar_drain(&bar.full[j & 1], (j >> 1) & 1, err);
+    if (warp == 1) {
+        if (*abort_flag && lane == 0) {
+            mma_commit(&bar.drain);
+            mbar_drain(&bar.drain, 0, err);
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ gradients
+// dq, dk, dg and dbeta of a chunk from what the two walks left: X^T and S^T
+// (the state before the chunk), dV and D^T (the gradient of the state behind
+// it).  With dV = T^^T dX, which is b r of the float32 form (delta_simt.cu):
+//   A_ij = scale (do_i . x_j) e^{G_i - G_j}, i >= j;   B_ij = -(dv_i . x_j) e^{G_i - G_j}, i > j
+//   dq = scale e^G (dO S^T) + A K
+//   dk = -e^G (dV S^T) + e^{G_L - G} (X D^T) + A^T Q + (B + B^T) K
+//   dbeta = (dv . x) / b^2;  dg as in delta_simt.cu.
+// A chunk's 64 rows fill half of a tcgen05 tile, so two operands share one:
+// rows 0-63 belong to the queries (dO, Q, A), rows 64-127 to the keys
+// (dV, K, B), and a thread of the epilogue owns a row of dq or of dk:
+//   pair columns  [dO; dV] X^T and [Q; K] K^T        (64 each)
+//   C1 = [dO; dV] S^T,  C2 = [*; X] D^T              (summed over v, 64 at a time)
+//   C3 = [A; B] K,      C4 = [*; A^T] Q + [*; B^T] K (C4 where the pairs were)
+// (*: whatever precedes the operand in shared memory; those rows are not read.)
+constexpr int kGradTcThreads = 320;        // warps 0-7 rows, 8 copies, 9 MMAs
+
+struct DeltaGradTcBars {
+    uint64_t full[2], empty[2], keys, pair_full, ab_ready, c_full, drain;
+    uint32_t tmem_slot;
+    int abort_flag;
+    double G[kC];
+    float beta[kC], rest[kC];
+    float rowsum[2][2][kC];                // [queries, keys][column half]
+    float colsum[8][32];                   // by warp: its column half
+    float inter[2][2][kC], ahead[2][kC], db[kC], sd[8];
+};
+template <int DK>
+struct DeltaGradTcSmem {
+    static constexpr uint32_t kKB = DK / 64;
+    // keys: a Q and a K box by turns ([Q; K] is 128 rows of one operand, and
+    // each alone has its column blocks two boxes apart), then the tiles A, B
+    static constexpr uint32_t kQ = 0;
+    static constexpr uint32_t kK = kBox64;
+    static constexpr uint32_t kKeyStep = 2 * kBox64;
+    static constexpr uint32_t kA = 2 * kKB * kBox64;
+    static constexpr uint32_t kB = kA + kBox64;
+    static constexpr uint32_t kStage0 = kB + kBox64;
+    // a stage of 64 v channels: dO, dV, X^T, S^T, D^T
+    static constexpr uint32_t kDo = 0, kDv = kBox64, kX = 2 * kBox64, kS = 3 * kBox64;
+    static constexpr uint32_t kD = kS + kKB * kBox64;
+    static constexpr uint32_t kStage = kD + kKB * kBox64;
+    static constexpr uint32_t kBars = kStage0 + 2 * kStage;
+    static constexpr uint32_t kBytes = kBars + ((sizeof(DeltaGradTcBars) + 127) & ~127u);
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+    static_assert(2 * kKB * kBox64 <= kStage, "dq and dk leave through the first stage");
+};
+
+struct DeltaGradTcArgs {
+    const __nv_bfloat16 *g, *beta;
+    const int *lengths;
+    __nv_bfloat16 *dq, *dk_, *dv_, *dg, *dbeta;
+    float *dq_wide, *dk_wide;
+    float scale;
+    int heads, key_heads, tokens, nc, dv;
+    unsigned *err;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(kGradTcThreads, 1)
+delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dv,
+                     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_s,
+                     const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_dq,
+                     const __grid_constant__ CUtensorMap tm_dk, DeltaGradTcArgs a) {
+    using Smem = DeltaGradTcSmem<DK>;
+    constexpr int kKB = DK / 64;
+    constexpr uint32_t kPd = 0, kPk = 64, kC4 = 0, kC1 = 128, kC2 = kC1 + DK, kC3 = kC2 + DK;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    DeltaGradTcBars &m = *reinterpret_cast<DeltaGradTcBars *>(smem + Smem::kBars);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
+    const int bh = blockIdx.x / a.nc, c = blockIdx.x % a.nc;
+    const int b = bh / a.heads, h = bh % a.heads, kh = h / (a.heads / a.key_heads);
+    const bool shared_keys = a.heads != a.key_heads;
+    unsigned *err = a.err;
+    int *abort_flag = &m.abort_flag;
+
+    grid_dependency_wait();
+    const int n = delta_tokens_of(a.lengths, b, a.tokens);
+    const int t0 = c * kC;
+    const int room = min(kC, a.tokens - t0), cnt = min(kC, n - t0);
+    const size_t row0 = (size_t)b * a.tokens + t0;
+    if (cnt <= 0) {                                        // the whole CTA: no gradients here
+        for (int i = warp; i < room; i += kGradTcThreads / 32) {
+            const size_t r = (row0 + i) * a.heads + h;
+            for (int j = lane; j < a.dv; j += 32) a.dv_[r * a.dv + j] = from_f32<__nv_bfloat16>(0.f);
+            for (int j = lane; j < DK; j += 32) {
+                if (shared_keys) {
+                    a.dq_wide[r * DK + j] = 0.f;
+                    a.dk_wide[r * DK + j] = 0.f;
+                } else {
+                    a.dq[r * DK + j] = from_f32<__nv_bfloat16>(0.f);
+                    a.dk_[r * DK + j] = from_f32<__nv_bfloat16>(0.f);
+                }
+            }
+            if (lane == 0) {
+                a.dg[r] = from_f32<__nv_bfloat16>(0.f);
+                a.dbeta[r] = from_f32<__nv_bfloat16>(0.f);
+            }
+        }
+        return;
+    }
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&m.full[s], 1);
+            mbar_init(&m.empty[s], 9);                     // the MMAs and 8 warps
+        }
+        mbar_init(&m.keys, 1);
+        mbar_init(&m.pair_full, 1);
+        mbar_init(&m.ab_ready, 8);
+        mbar_init(&m.c_full, 1);
+        mbar_init(&m.drain, 1);
+        m.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(&m.tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == 0) {                                       // running sums of g
+        const size_t at = row0 * a.heads + h;
+        double lo = lane < cnt ? log_decay(to_f32(a.g[at + (size_t)lane * a.heads])) : 0.0;
+        double hi = lane + 32 < cnt ? log_decay(to_f32(a.g[at + (size_t)(lane + 32) * a.heads])) : 0.0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double ul = __shfl_up_sync(0xffffffffu, lo, o);
+            const double uh = __shfl_up_sync(0xffffffffu, hi, o);
+            if (lane >= o) {
+                lo += ul;
+                hi += uh;
+            }
+        }
+        hi += __shfl_sync(0xffffffffu, lo, 31);
+        const double GL = __shfl_sync(0xffffffffu, hi, 31);
+        m.G[lane] = lo;
+        m.G[lane + 32] = hi;
+        m.rest[lane] = expf((float)(GL - lo));
+        m.rest[lane + 32] = expf((float)(GL - hi));
+    } else if (warp == 1) {
+#pragma unroll
+        for (int i = lane; i < kC; i += 32)
+            m.beta[i] = i < cnt ? nonzero_beta(to_f32(a.beta[(row0 + i) * a.heads + h])) : 1.f;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    constexpr uint32_t tmem = 0;                           // all 512 columns, as above
+    const int nv = a.dv / 64;
+
+    int it = 0;
+    if (warp == 8) {
+        if (elect_one()) {
+            mbar_expect_tx(&m.keys, 2 * kKB * kBox64);
+#pragma unroll
+            for (int x = 0; x < kKB; ++x) {
+                tma_load_4d(smem + Smem::kQ + x * Smem::kKeyStep, &tm_q, &m.keys, 64 * x, kh, t0, b);
+                tma_load_4d(smem + Smem::kK + x * Smem::kKeyStep, &tm_k, &m.keys, 64 * x, kh, t0, b);
+            }
+        }
+        __syncwarp();
+        const int srow = (bh * a.nc + c) * a.dv;           // row of the saved tiles
+        for (; it < nv; ++it) {
+            const int s = it & 1;
+            if (it >= 2 && !warp_spin_wait(&m.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
+            uint8_t *st = smem + Smem::kStage0 + s * Smem::kStage;
+            if (elect_one()) {
+                mbar_expect_tx(&m.full[s], Smem::kStage);
+                tma_load_4d(st + Smem::kDo, &tm_do, &m.full[s], 64 * it, h, t0, b);
+                tma_load_4d(st + Smem::kDv, &tm_dv, &m.full[s], 64 * it, h, t0, b);
+                tma_load_2d(st + Smem::kX, &tm_x, &m.full[s], 0, srow + 64 * it);
+#pragma unroll
+                for (int x = 0; x < kKB; ++x) {
+                    tma_load_2d(st + Smem::kS + x * kBox64, &tm_s, &m.full[s], 64 * x, srow + 64 * it);
+                    tma_load_2d(st + Smem::kD + x * kBox64, &tm_d, &m.full[s], 64 * x, srow + 64 * it);
+                }
+            }
+            __syncwarp();
+        }
+    } else if (warp == 9) {
+        constexpr uint32_t id_kk = idesc_bf16(128, 64, 0, 0);
+        constexpr uint32_t id_px = idesc_bf16(128, 64, 0, 1);
+        constexpr uint32_t id_c1 = idesc_bf16(128, DK, 0, 1);
+        constexpr uint32_t id_c2 = idesc_bf16(128, DK, 1, 1);
+        const uint32_t base = smem_u32(smem);
+        const uint64_t kmaj = smem_desc_sw128(base, 16, 1024);
+        const uint64_t mnmaj = smem_desc_sw128(base, kBox64, 1024);
+        const uint64_t keymn = smem_desc_sw128(base, Smem::kKeyStep, 1024);
+        bool ok = warp_spin_wait(&m.keys, 0, abort_flag, err);
+        if (ok) {
+            if (cnt < kC) clear_rows(smem + Smem::kQ, 2 * kKB, cnt, lane);
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int x = 0; x < kKB; ++x)
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4) {
+                        const uint32_t o = x * Smem::kKeyStep + k4 * 32;
+                        mma_bf16(tmem + kPk, kmaj + ((Smem::kQ + o) >> 4), kmaj + ((Smem::kK + o) >> 4),
+                                 id_kk, x + k4 > 0);
+                    }
+            }
+            __syncwarp();
+        }
+        for (int i = 0; ok && i < nv; ++i) {
+            const int s = i & 1;
+            const uint32_t so = (Smem::kStage0 + s * Smem::kStage) >> 4;
+            const uint64_t kst = kmaj + so, mst = mnmaj + so;
+            ok = warp_spin_wait(&m.full[s], (i >> 1) & 1, abort_flag, err);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16(tmem + kPd, kst + ((Smem::kDo + ks * 32) >> 4),
+                             mst + ((Smem::kX + ks * 2048) >> 4), id_px, i + ks > 0);
+                if (i == nv - 1) mma_commit(&m.pair_full);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_bf16(tmem + kC1, kst + ((Smem::kDo + ks * 32) >> 4),
+                             mst + ((Smem::kS + ks * 2048) >> 4), id_c1, i + ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)             // dV fills the rows that are not read
+                    mma_bf16(tmem + kC2, mst + ((Smem::kDv + ks * 2048) >> 4),
+                             mst + ((Smem::kD + ks * 2048) >> 4), id_c2, i + ks > 0);
+                mma_commit(&m.empty[s]);
+            }
+            __syncwarp();
+        }
+        ok = ok && warp_spin_wait(&m.ab_ready, 0, abort_flag, err);
+        if (ok) {
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint64_t qb = keymn + ((Smem::kQ + ks * 2048) >> 4);
+                    const uint64_t kb = keymn + ((Smem::kK + ks * 2048) >> 4);
+                    mma_bf16(tmem + kC3, kmaj + ((Smem::kA + ks * 32) >> 4), kb, id_c1, ks > 0);
+                    // the box in front of A (of B) fills the rows that are not read
+                    mma_bf16(tmem + kC4, mnmaj + ((Smem::kA - kBox64 + ks * 2048) >> 4), qb, id_c2, ks > 0);
+                    mma_bf16(tmem + kC4, mnmaj + ((Smem::kA + ks * 2048) >> 4), kb, id_c2, 1);
+                }
+                mma_commit(&m.c_full);
+            }
+            __syncwarp();
+        }
+    } else {
+        const bool key = (warp & 2) != 0;                  // rows 64-127
+        const int hf = warp / 4, i = 32 * (warp & 1) + lane;
+        const bool in = i < cnt;
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
+        bool ok = true;
+        float sd = 0.f;                                    // this thread's part of <S, D>
+        for (int u = 0; ok && u < nv; ++u) {
+            const int s = u & 1;
+            ok = warp_spin_wait(&m.full[s], (u >> 1) & 1, abort_flag, err);
+            if (!ok) break;
+            const uint8_t *st = smem + Smem::kStage0 + s * Smem::kStage;
+#pragma unroll
+            for (int e = 0; e < 2 * kKB; ++e) {
+                const int o = (tid + 256 * e) * 16;        // both tiles have one layout
+                float sv[8], dv[8];
+                load8(reinterpret_cast<const __nv_bfloat16 *>(st + Smem::kS + o), sv);
+                load8(reinterpret_cast<const __nv_bfloat16 *>(st + Smem::kD + o), dv);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sd = fmaf(sv[j], dv[j], sd);
+            }
+            warp_arrive(&m.empty[s]);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
+        if (lane == 0) m.sd[warp] = sd;
+        ok = ok && warp_spin_wait(&m.keys, 0, abort_flag, err) &&
+             warp_spin_wait(&m.pair_full, 0, abort_flag, err);
+        if (ok) {                                          // A, B, and the sums of E
+            tc_fence_after();
+            uint32_t pd[32], pk[32];
+            tmem_ld32(tl + kPd + 32 * hf, pd);
+            tmem_ld32(tl + kPk + 32 * hf, pk);
+            tmem_wait_ld();
+            const double Gi = m.G[i];
+            float e[32], rs = 0.f;
+            uint8_t *tile = smem + (key ? Smem::kB : Smem::kA);
+#pragma unroll
+            for (int j8 = 0; j8 < 4; ++j8) {
+                float w[8];
+#pragma unroll
+                for (int jj = 0; jj < 8; ++jj) {
+                    const int jl = 8 * j8 + jj, j = 32 * hf + jl;
+                    const float p = __uint_as_float(pd[jl]);
+                    // a row behind the sequence may be NaN: chosen, not multiplied
+                    const bool on = in && (key ? i > j : i >= j);
+                    const float dec = on ? expf((float)(Gi - m.G[j])) : 0.f;
+                    w[jj] = on ? (key ? -p : a.scale * p) * dec : 0.f;
+                    e[jl] = on && i != j ? w[jj] * __uint_as_float(pk[jl]) : 0.f;
+                    rs += e[jl];
+                    if (key && i == j) m.db[i] = p;
+                }
+                store8(reinterpret_cast<__nv_bfloat16 *>(tile + tile_off(i, 32 * hf + 8 * j8)), w);
+            }
+            m.rowsum[key][hf][i] = rs;
+            // column sums over the warp's rows: halves swapped and added until
+            // a lane holds one column
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+#pragma unroll
+                for (int j = 0; j < o; ++j) {
+                    const float give = lane & o ? e[j] : e[j + o];
+                    const float keep = lane & o ? e[j + o] : e[j];
+                    e[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+            m.colsum[warp][lane] = e[0];
+            fence_async_shared();
+            tc_fence_before();
+            warp_arrive(&m.ab_ready);
+            ok = warp_spin_wait(&m.c_full, 0, abort_flag, err);
+        }
+        if (ok) {
+            tc_fence_after();
+            const float ei = expf((float)m.G[i]), f1 = key ? -ei : a.scale * ei, f2 = m.rest[i];
+            const uint8_t *mine = smem + (key ? Smem::kK : Smem::kQ);
+            uint8_t *leave = smem + Smem::kStage0 + (key ? kKB * kBox64 : 0);
+            float inter = 0.f, ahead = 0.f;
+            float *wide = (key ? a.dk_wide : a.dq_wide) + ((row0 + i) * a.heads + h) * (size_t)DK;
+#pragma unroll
+            for (int p = 0; p < kKB; ++p) {                // 32 of this half's columns
+                const int col = hf * (DK / 2) + 32 * p;
+                uint32_t c1[32], c3[32], c2[32];
+                tmem_ld32(tl + kC1 + col, c1);
+                tmem_ld32(tl + kC3 + col, c3);
+                if (key) tmem_ld32(tl + kC2 + col, c2);
+                tmem_wait_ld();
+                float r[32];
+#pragma unroll
+                for (int j8 = 0; j8 < 4; ++j8) {
+                    float own[8];
+                    load8(reinterpret_cast<const __nv_bfloat16 *>(
+                              mine + (col / 64) * Smem::kKeyStep + tile_off(i, (col & 63) + 8 * j8)), own);
+#pragma unroll
+                    for (int jj = 0; jj < 8; ++jj) {
+                        const int j = 8 * j8 + jj;
+                        const float z = f1 * __uint_as_float(c1[j]);
+                        inter = fmaf(own[jj], z, inter);
+                        r[j] = z + __uint_as_float(c3[j]);
+                        if (key) {
+                            const float x = f2 * __uint_as_float(c2[j]);
+                            ahead = fmaf(own[jj], x, ahead);
+                            r[j] += x;
+                        }
+                    }
+                }
+                if (key) {
+                    tmem_ld32(tl + kC4 + col, c1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] += __uint_as_float(c1[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = in ? r[j] : 0.f;
+                if (shared_keys) {
+                    if (i < room)
+#pragma unroll
+                        for (int j8 = 0; j8 < 4; ++j8) store8(wide + col + 8 * j8, &r[8 * j8]);
+                } else {
+#pragma unroll
+                    for (int j8 = 0; j8 < 4; ++j8)
+                        store8(reinterpret_cast<__nv_bfloat16 *>(leave + tile_off(i, col + 8 * j8)), &r[8 * j8]);
+                }
+            }
+            m.inter[key][hf][i] = in ? inter : 0.f;
+            if (key) m.ahead[hf][i] = in ? ahead : 0.f;
+            fence_async_shared();
+        }
+        named_barrier(1, 256);
+        if (ok) {
+            if (tid == 0 && !shared_keys) {
+#pragma unroll
+                for (int x = 0; x < kKB; ++x) {
+                    tma_store_4d(&tm_dq, smem + Smem::kStage0 + x * kBox64, 64 * x, kh, t0, b);
+                    tma_store_4d(&tm_dk, smem + Smem::kStage0 + (kKB + x) * kBox64, 64 * x, kh, t0, b);
+                }
+                tma_store_commit();
+            }
+            if (tid < kC) {
+                float t = m.inter[0][0][tid] + m.inter[0][1][tid] + m.inter[1][0][tid] + m.inter[1][1][tid];
+                t += m.rowsum[0][0][tid] + m.rowsum[0][1][tid] + m.rowsum[1][0][tid] + m.rowsum[1][1][tid];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) t -= m.colsum[4 * (tid / 32) + w][tid % 32];
+                m.rowsum[0][0][tid] = t;
+                m.ahead[0][tid] += m.ahead[1][tid];
+            }
+        }
+        named_barrier(1, 256);
+        if (ok && tid < room) {
+            float s = 0.f;
+            if (tid < cnt) {
+#pragma unroll
+                for (int w = 0; w < 8; ++w) s += m.sd[w];
+                s *= expf((float)m.G[kC - 1]);
+                for (int t = cnt - 1; t >= tid; --t) s += m.rowsum[0][0][t];
+                for (int t = 0; t < tid; ++t) s += m.ahead[0][t];
+            }
+            const size_t r = (row0 + tid) * a.heads + h;
+            a.dg[r] = from_f32<__nv_bfloat16>(s);
+            a.dbeta[r] = from_f32<__nv_bfloat16>(tid < cnt ? m.db[tid] / (m.beta[tid] * m.beta[tid]) : 0.f);
+        }
+        if (tid == 0) tma_store_wait_read();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && warp == 8 && lane == 0) {           // as in the walks
+        mbar_drain(&m.keys, 0, err);
+        for (int j = max(0, it - 2); j < it; ++j) mbar_drain(&m.full[j & 1], (j >> 1) & 1, err);
+    }
+    if (warp == 9) {
+        if (*abort_flag && lane == 0) {
+            mma_commit(&m.drain);
+            mbar_drain(&m.drain, 0, err);
         }
         __syncwarp();
         tc_fence_after();
@@ -759,6 +1466,90 @@ cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, __nv_
                              Smem::kBytes, stream, tm_k, tm_v, tm_o, s);
 }
 
+// Map of [rows, cols] in boxes of 64 x 64.
+bool row_map(CUtensorMap *tm, const void *p, long long rows, int cols) {
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t str[1] = {(cuuint64_t)cols * 2};
+    cuuint32_t box[2] = {64, 64};
+    return make_tensor_map_bf16(tm, p, 2, dims, str, box);
+}
+
+size_t up1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
+
+struct DeltaTcGradLayout {
+    size_t blocks, x, s, d, dq, dk, total;
+};
+DeltaTcGradLayout tc_grad_layout(int batch, int heads, int key_heads, int seqlen, int dk, int dv) {
+    const size_t chunks = (size_t)batch * heads * ((seqlen + kC - 1) / kC);
+    const size_t wide = heads != key_heads ? up1k((size_t)batch * seqlen * heads * dk * 4) : 0;
+    DeltaTcGradLayout l;
+    l.blocks = 0;
+    l.x = chunks * (dk == 64 ? DeltaBlock<64, false>::kBytes : DeltaBlock<128, false>::kBytes);
+    l.s = l.x + chunks * dv * kC * 2;
+    l.d = l.s + chunks * dv * dk * 2;
+    l.dq = l.d + chunks * dv * dk * 2;
+    l.dk = l.dq + wide;
+    l.total = l.dk + wide;
+    return l;
+}
+
+template <int DK>
+cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
+    const int nc = (a.seqlen + kC - 1) / kC, slabs = (a.dv + 127) / 128;
+    const long long bh = (long long)a.batch * a.heads, vrows = bh * nc * a.dv;
+    const DeltaTcGradLayout l = tc_grad_layout(a.batch, a.heads, a.key_heads, a.seqlen, a.dk, a.dv);
+    uint8_t *ws = (uint8_t *)workspace;
+    __nv_bfloat16 *xs = (__nv_bfloat16 *)(ws + l.x), *ss = (__nv_bfloat16 *)(ws + l.s),
+                  *ds = (__nv_bfloat16 *)(ws + l.d);
+    float *dq_wide = (float *)(ws + l.dq), *dk_wide = (float *)(ws + l.dk);
+    cudaError_t e = launch_prep<DK, false>(a, nc, ws + l.blocks, true, stream);
+    if (e != cudaSuccess) return e;
+    e = launch_scan<DK, false, false, true>(a, nc, ws + l.blocks, xs, ss, stream);
+    if (e != cudaSuccess) return e;
+
+    CUtensorMap tm_q, tm_k, tm_do, tm_dv, tm_x, tm_s, tm_d, tm_dq, tm_dk;
+    if (!token_map(&tm_q, a.q, a.batch, a.seqlen, a.key_heads, DK) ||
+        !token_map(&tm_k, a.k, a.batch, a.seqlen, a.key_heads, DK) ||
+        !token_map(&tm_do, a.d_out, a.batch, a.seqlen, a.heads, a.dv) ||
+        !token_map(&tm_dv, a.dv_grad, a.batch, a.seqlen, a.heads, a.dv) ||
+        !token_map(&tm_dq, a.dq, a.batch, a.seqlen, a.key_heads, DK) ||
+        !token_map(&tm_dk, a.dk_grad, a.batch, a.seqlen, a.key_heads, DK) ||
+        !row_map(&tm_x, xs, vrows, kC) || !row_map(&tm_s, ss, vrows, DK) ||
+        !row_map(&tm_d, ds, vrows, DK))
+        return cudaErrorInvalidValue;
+    {
+        using Smem = DeltaScanSmem<DK, false>;
+        e = cudaFuncSetAttribute(delta_reverse_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)Smem::kBytes);
+        if (e != cudaSuccess) return e;
+        DeltaReverseArgs r = {ws + l.blocks, a.lengths, ds, a.heads, a.key_heads, a.seqlen, nc, a.dv,
+                              device_error_word()};
+        KernelTimer timer("delta_reverse", stream);
+        count_launch();
+        e = launch_overlapped(delta_reverse_kernel<DK>, dim3((unsigned)(bh * slabs)),
+                              dim3(kScanThreads), Smem::kBytes, stream, tm_k, tm_do, tm_dv, r);
+        if (e != cudaSuccess) return e;
+    }
+    {
+        using Smem = DeltaGradTcSmem<DK>;
+        e = cudaFuncSetAttribute(delta_grad_tc_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)Smem::kBytes);
+        if (e != cudaSuccess) return e;
+        DeltaGradTcArgs g = {(const __nv_bfloat16 *)a.g, (const __nv_bfloat16 *)a.beta, a.lengths,
+                             (__nv_bfloat16 *)a.dq, (__nv_bfloat16 *)a.dk_grad,
+                             (__nv_bfloat16 *)a.dv_grad, (__nv_bfloat16 *)a.dg,
+                             (__nv_bfloat16 *)a.dbeta, dq_wide, dk_wide, a.scale, a.heads,
+                             a.key_heads, a.seqlen, nc, a.dv, device_error_word()};
+        KernelTimer timer("delta_grad_tc", stream);
+        count_launch();
+        e = launch_overlapped(delta_grad_tc_kernel<DK>, dim3((unsigned)(bh * nc)),
+                              dim3(kGradTcThreads), Smem::kBytes, stream, tm_q, tm_k, tm_do, tm_dv,
+                              tm_x, tm_s, tm_d, tm_dq, tm_dk, g);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_delta_share(a, dq_wide, dk_wide, stream);
+}
+
 template <int DK, bool kSplit>
 cudaError_t launch_forward(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
     const int nc = (a.seqlen + kC - 1) / kC;
@@ -769,6 +1560,15 @@ cudaError_t launch_forward(const DeltaArgs &a, void *workspace, cudaStream_t str
 }
 
 }  // namespace
+
+size_t delta_backward_tc_workspace(int batch, int heads, int key_heads, int seqlen, int dk, int dv) {
+    return tc_grad_layout(batch, heads, key_heads, seqlen, dk, dv).total;
+}
+
+cudaError_t launch_delta_backward_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
+    return a.dk == 64 ? launch_backward<64>(a, workspace, stream)
+                      : launch_backward<128>(a, workspace, stream);
+}
 
 bool delta_tc_shape_ok(int dk, int dv, retnet_dtype dtype) {
     return dtype == RETNET_BF16 && (dk == 64 || dk == 128) && dv >= 64;

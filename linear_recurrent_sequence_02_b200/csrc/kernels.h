@@ -157,6 +157,8 @@ cudaError_t launch_delta_backward_simt(const DeltaArgs &a, void *workspace, cuda
 bool delta_tc_shape_ok(int dk, int dv, retnet_dtype dtype);
 size_t delta_tc_workspace(int batch, int heads, int seqlen, int dk);
 cudaError_t launch_delta_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream);
+size_t delta_backward_tc_workspace(int batch, int heads, int key_heads, int seqlen, int dk, int dv);
+cudaError_t launch_delta_backward_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream);
 // dq and dk of key heads shared by several value heads, from float32
 // [B, n, heads, dk] gradients per value head; nothing where none is shared.
 cudaError_t launch_delta_share(const DeltaArgs &a, const float *dq_wide, const float *dk_wide,

