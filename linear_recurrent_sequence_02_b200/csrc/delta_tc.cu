@@ -99,6 +99,22 @@ __device__ __forceinline__ void put_channel(uint8_t *tile, int col, const uint32
             __float2bfloat16_rn(__uint_as_float(o[i / 32][i % 32]));
 }
 
+// What the walks keep for the gradients (X^T, S^T, D^T: a row of `cols`
+// values per v channel and chunk) lies as [chunk][block of 64 channels][group
+// of 8 columns][channel][8]: a warp, whose lanes are channels, writes 512
+// consecutive bytes at a time, and a block is one copy and, as it is, an
+// MN-major operand without swizzle (columns by channels).  Offset, in
+// elements, of 8 columns of channel v.
+__device__ __forceinline__ size_t kept_off(size_t chunk, int dv, int v, int cols, int col) {
+    return ((chunk * (dv / 64) + v / 64) * (cols / 8) + col / 8) * 512 + (v % 64) * 8;
+}
+__device__ __forceinline__ void keep_row(__nv_bfloat16 *kept, size_t chunk, int dv, int v, int cols,
+                                         int col, const uint32_t (&x)[16]) {
+    uint4 *dst = reinterpret_cast<uint4 *>(kept + kept_off(chunk, dv, v, cols, col));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dst[64 * j] = make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+}
+
 // ------------------------------------------------------------------ prep
 // One CTA of four warps per chunk of a (sequence, value head): the two
 // products by mma.sync (a 64 x 64 x dk product has too few rows to fill a
@@ -416,7 +432,7 @@ struct DeltaScanArgs {
     const float *state_in;
     float *state_out;
     __nv_bfloat16 *out;
-    __nv_bfloat16 *x_save, *s_save;        // kSave: X^T [.., dv, 64], S^T [.., dv, DK] per chunk
+    __nv_bfloat16 *x_save, *s_save;        // kSave: X^T, S^T of every chunk (keep_row)
     int heads, key_heads, tokens, nc, dv;
     unsigned *err;
 };
@@ -603,13 +619,8 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&bar.s_ready[p]);
-            if (kSave && live && c < nc) {
-                uint4 *dst = reinterpret_cast<uint4 *>(
-                    a.s_save + (((size_t)bh * a.nc + c) * a.dv + v) * DK + 64 * p + 32 * wg);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    dst[j] = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
-            }
+            if (kSave && live && c < nc)
+                keep_row(a.s_save, (size_t)bh * a.nc + c, a.dv, v, DK, 64 * p + 32 * wg, hi);
         };
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) put_state(p, 0);
@@ -638,13 +649,8 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(&bar.xs_ready);
-                if (kSave && live) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(
-                        a.x_save + (((size_t)bh * a.nc + c) * a.dv + v) * kC + 32 * wg);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        dst[j] = make_uint4(xb[4 * j], xb[4 * j + 1], xb[4 * j + 2], xb[4 * j + 3]);
-                }
+                if (kSave && live)
+                    keep_row(a.x_save, (size_t)bh * a.nc + c, a.dv, v, kC, 32 * wg, xb);
             }
             bool ok = true;
 #pragma unroll
@@ -738,7 +744,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 //   dV^T = dX^T T^                       (while the chain rounds D)
 // D is kept for every chunk (d_save, as S^T in the forward walk).
 struct DeltaReverseBars {
-    uint64_t full[2], empty[2], d_ready[2], z_full[2], y_full, dx_ready, v_full, v_free, drain;
+    uint64_t full[2], empty[2], d_ready[2], z_full[2], y_full, dx_ready, lo_ready, v_full, v_free, drain;
     uint32_t tmem_slot;
     int abort_flag;
 };
@@ -758,7 +764,8 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     using Smem = DeltaScanSmem<DK, false>;                // V's place holds dO, the output's dV
     using Block = DeltaBlock<DK, false>;
     constexpr int kPieces = DK / 64;
-    constexpr uint32_t kD = 0, kZ = DK / 2, kY1 = kZ + DK, kY2 = kY1 + 64, kDx = kY2 + 64, kDv = kDx + 32;
+    constexpr uint32_t kD = 0, kZ = DK / 2, kY1 = kZ + DK, kY2 = kY1 + 64, kDx = kY2 + 64, kDxlo = kDx + 32, kDv = kDxlo + 32;
+    static_assert(kDv + 64 <= 512, "tensor memory");
     extern __shared__ __align__(1024) uint8_t smem[];
     DeltaReverseBars &bar = *reinterpret_cast<DeltaReverseBars *>(smem + Smem::kBars);
     static_assert(sizeof(DeltaReverseBars) <= 256, "barriers");
@@ -779,6 +786,7 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
         mbar_init(&bar.y_full, 1);
         mbar_init(&bar.dx_ready, kChainWarps);
+        mbar_init(&bar.lo_ready, kChainWarps);
         mbar_init(&bar.v_full, 1);
         mbar_init(&bar.v_free, 4);
         mbar_init(&bar.drain, 1);
@@ -876,12 +884,15 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             }
             __syncwarp();
             if (u > 0 && !warp_spin_wait(&bar.v_free, (u - 1) & 1, abort_flag, err)) break;
+            if (!warp_spin_wait(&bar.lo_ready, u & 1, abort_flag, err)) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16_ts(tmem + kDv, tmem + kDx + 8 * ks,
-                                mnmaj + ((Block::kT + ks * 2048) >> 4), id_w, ks > 0);
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint64_t td = mnmaj + ((Block::kT + ks * 2048) >> 4);
+                    mma_bf16_ts(tmem + kDv, tmem + kDx + 8 * ks, td, id_w, ks > 0);
+                    mma_bf16_ts(tmem + kDv, tmem + kDxlo + 8 * ks, td, id_w, 1);
+                }
                 mma_commit(&bar.v_full);
                 mma_commit(&bar.empty[s]);
             }
@@ -902,13 +913,8 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&bar.d_ready[p]);
-            if (live && c >= 0) {
-                uint4 *dst = reinterpret_cast<uint4 *>(
-                    a.d_save + (((size_t)bh * a.nc + c) * a.dv + v) * DK + 64 * p + 32 * wg);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    dst[j] = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
-            }
+            if (live && c >= 0)
+                keep_row(a.d_save, (size_t)bh * a.nc + c, a.dv, v, DK, 64 * p + 32 * wg, hi);
         };
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) put_grad(p, nc - 1);
@@ -920,21 +926,25 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             if (!warp_spin_wait(&bar.y_full, u & 1, abort_flag, err)) break;
             tc_fence_after();
             {
-                uint32_t y1[32], y2[32], dx[16];
+                uint32_t y1[32], y2[32], dx[16], lo[16];
                 tmem_ld32(tl + kY1 + 32 * wg, y1);
                 tmem_ld32(tl + kY2 + 32 * wg, y2);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float2 r = *reinterpret_cast<const float2 *>(hdr + 32 * wg + 2 * j);
-                    dx[j] = pack_bf16x2(
-                        fmaf(r.x, __uint_as_float(y2[2 * j]), __uint_as_float(y1[2 * j])),
-                        fmaf(r.y, __uint_as_float(y2[2 * j + 1]), __uint_as_float(y1[2 * j + 1])));
+                    split_pair(fmaf(r.x, __uint_as_float(y2[2 * j]), __uint_as_float(y1[2 * j])),
+                               fmaf(r.y, __uint_as_float(y2[2 * j + 1]), __uint_as_float(y1[2 * j + 1])),
+                               dx[j], lo[j]);
                 }
                 tmem_st16(tl + kDx + 16 * wg, dx);
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(&bar.dx_ready);
+                tmem_st16(tl + kDxlo + 16 * wg, lo);
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(&bar.lo_ready);
             }
             bool ok = true;
 #pragma unroll
@@ -1042,7 +1052,7 @@ struct DeltaGradTcSmem {
 };
 
 struct DeltaGradTcArgs {
-    const __nv_bfloat16 *g, *beta;
+    const __nv_bfloat16 *g, *beta, *x, *s, *d;             // X^T, S^T, D^T of every chunk
     const int *lengths;
     __nv_bfloat16 *dq, *dk_, *dv_, *dg, *dbeta;
     float *dq_wide, *dk_wide;
@@ -1055,8 +1065,7 @@ template <int DK>
 __global__ void __launch_bounds__(kGradTcThreads, 1)
 delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dv,
-                     const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_s,
-                     const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_dq,
+                     const __grid_constant__ CUtensorMap tm_dq,
                      const __grid_constant__ CUtensorMap tm_dk, DeltaGradTcArgs a) {
     using Smem = DeltaGradTcSmem<DK>;
     constexpr int kKB = DK / 64;
@@ -1153,7 +1162,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             }
         }
         __syncwarp();
-        const int srow = (bh * a.nc + c) * a.dv;           // row of the saved tiles
+        const size_t first = (size_t)blockIdx.x * nv;      // block of 64 channels
         for (; it < nv; ++it) {
             const int s = it & 1;
             if (it >= 2 && !warp_spin_wait(&m.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
@@ -1162,12 +1171,9 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 mbar_expect_tx(&m.full[s], Smem::kStage);
                 tma_load_4d(st + Smem::kDo, &tm_do, &m.full[s], 64 * it, h, t0, b);
                 tma_load_4d(st + Smem::kDv, &tm_dv, &m.full[s], 64 * it, h, t0, b);
-                tma_load_2d(st + Smem::kX, &tm_x, &m.full[s], 0, srow + 64 * it);
-#pragma unroll
-                for (int x = 0; x < kKB; ++x) {
-                    tma_load_2d(st + Smem::kS + x * kBox64, &tm_s, &m.full[s], 64 * x, srow + 64 * it);
-                    tma_load_2d(st + Smem::kD + x * kBox64, &tm_d, &m.full[s], 64 * x, srow + 64 * it);
-                }
+                bulk_load(st + Smem::kX, a.x + (first + it) * (64 * kC), kBox64, &m.full[s]);
+                bulk_load(st + Smem::kS, a.s + (first + it) * (64 * DK), kKB * kBox64, &m.full[s]);
+                bulk_load(st + Smem::kD, a.d + (first + it) * (64 * DK), kKB * kBox64, &m.full[s]);
             }
             __syncwarp();
         }
@@ -1180,6 +1186,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const uint64_t kmaj = smem_desc_sw128(base, 16, 1024);
         const uint64_t mnmaj = smem_desc_sw128(base, kBox64, 1024);
         const uint64_t keymn = smem_desc_sw128(base, Smem::kKeyStep, 1024);
+        const uint64_t plain = smem_desc_plain(base, 128, 1024);   // X^T, S^T, D^T blocks
         bool ok = warp_spin_wait(&m.keys, 0, abort_flag, err);
         if (ok) {
             if (cnt < kC) clear_rows(smem + Smem::kQ, 2 * kKB, cnt, lane);
@@ -1199,7 +1206,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         for (int i = 0; ok && i < nv; ++i) {
             const int s = i & 1;
             const uint32_t so = (Smem::kStage0 + s * Smem::kStage) >> 4;
-            const uint64_t kst = kmaj + so, mst = mnmaj + so;
+            const uint64_t kst = kmaj + so, kept = plain + so;
             ok = warp_spin_wait(&m.full[s], (i >> 1) & 1, abort_flag, err);
             if (!ok) break;
             tc_fence_after();
@@ -1207,16 +1214,16 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
                     mma_bf16(tmem + kPd, kst + ((Smem::kDo + ks * 32) >> 4),
-                             mst + ((Smem::kX + ks * 2048) >> 4), id_px, i + ks > 0);
+                             kept + ((Smem::kX + ks * 256) >> 4), id_px, i + ks > 0);
                 if (i == nv - 1) mma_commit(&m.pair_full);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
                     mma_bf16(tmem + kC1, kst + ((Smem::kDo + ks * 32) >> 4),
-                             mst + ((Smem::kS + ks * 2048) >> 4), id_c1, i + ks > 0);
+                             kept + ((Smem::kS + ks * 256) >> 4), id_c1, i + ks > 0);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)             // dV fills the rows that are not read
-                    mma_bf16(tmem + kC2, mst + ((Smem::kDv + ks * 2048) >> 4),
-                             mst + ((Smem::kD + ks * 2048) >> 4), id_c2, i + ks > 0);
+                    mma_bf16(tmem + kC2, kept + ((Smem::kDv + ks * 256) >> 4),
+                             kept + ((Smem::kD + ks * 256) >> 4), id_c2, i + ks > 0);
                 mma_commit(&m.empty[s]);
             }
             __syncwarp();
@@ -1466,14 +1473,6 @@ cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, __nv_
                              Smem::kBytes, stream, tm_k, tm_v, tm_o, s);
 }
 
-// Map of [rows, cols] in boxes of 64 x 64.
-bool row_map(CUtensorMap *tm, const void *p, long long rows, int cols) {
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t str[1] = {(cuuint64_t)cols * 2};
-    cuuint32_t box[2] = {64, 64};
-    return make_tensor_map_bf16(tm, p, 2, dims, str, box);
-}
-
 size_t up1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
 
 struct DeltaTcGradLayout {
@@ -1496,7 +1495,7 @@ DeltaTcGradLayout tc_grad_layout(int batch, int heads, int key_heads, int seqlen
 template <int DK>
 cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
     const int nc = (a.seqlen + kC - 1) / kC, slabs = (a.dv + 127) / 128;
-    const long long bh = (long long)a.batch * a.heads, vrows = bh * nc * a.dv;
+    const long long bh = (long long)a.batch * a.heads;
     const DeltaTcGradLayout l = tc_grad_layout(a.batch, a.heads, a.key_heads, a.seqlen, a.dk, a.dv);
     uint8_t *ws = (uint8_t *)workspace;
     __nv_bfloat16 *xs = (__nv_bfloat16 *)(ws + l.x), *ss = (__nv_bfloat16 *)(ws + l.s),
@@ -1507,15 +1506,13 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
     e = launch_scan<DK, false, false, true>(a, nc, ws + l.blocks, xs, ss, stream);
     if (e != cudaSuccess) return e;
 
-    CUtensorMap tm_q, tm_k, tm_do, tm_dv, tm_x, tm_s, tm_d, tm_dq, tm_dk;
+    CUtensorMap tm_q, tm_k, tm_do, tm_dv, tm_dq, tm_dk;
     if (!token_map(&tm_q, a.q, a.batch, a.seqlen, a.key_heads, DK) ||
         !token_map(&tm_k, a.k, a.batch, a.seqlen, a.key_heads, DK) ||
         !token_map(&tm_do, a.d_out, a.batch, a.seqlen, a.heads, a.dv) ||
         !token_map(&tm_dv, a.dv_grad, a.batch, a.seqlen, a.heads, a.dv) ||
         !token_map(&tm_dq, a.dq, a.batch, a.seqlen, a.key_heads, DK) ||
-        !token_map(&tm_dk, a.dk_grad, a.batch, a.seqlen, a.key_heads, DK) ||
-        !row_map(&tm_x, xs, vrows, kC) || !row_map(&tm_s, ss, vrows, DK) ||
-        !row_map(&tm_d, ds, vrows, DK))
+        !token_map(&tm_dk, a.dk_grad, a.batch, a.seqlen, a.key_heads, DK))
         return cudaErrorInvalidValue;
     {
         using Smem = DeltaScanSmem<DK, false>;
@@ -1535,7 +1532,7 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
         e = cudaFuncSetAttribute(delta_grad_tc_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Smem::kBytes);
         if (e != cudaSuccess) return e;
-        DeltaGradTcArgs g = {(const __nv_bfloat16 *)a.g, (const __nv_bfloat16 *)a.beta, a.lengths,
+        DeltaGradTcArgs g = {(const __nv_bfloat16 *)a.g, (const __nv_bfloat16 *)a.beta, xs, ss, ds, a.lengths,
                              (__nv_bfloat16 *)a.dq, (__nv_bfloat16 *)a.dk_grad,
                              (__nv_bfloat16 *)a.dv_grad, (__nv_bfloat16 *)a.dg,
                              (__nv_bfloat16 *)a.dbeta, dq_wide, dk_wide, a.scale, a.heads,
@@ -1544,7 +1541,7 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
         count_launch();
         e = launch_overlapped(delta_grad_tc_kernel<DK>, dim3((unsigned)(bh * nc)),
                               dim3(kGradTcThreads), Smem::kBytes, stream, tm_q, tm_k, tm_do, tm_dv,
-                              tm_x, tm_s, tm_d, tm_dq, tm_dk, g);
+                              tm_dq, tm_dk, g);
         if (e != cudaSuccess) return e;
     }
     return launch_delta_share(a, dq_wide, dk_wide, stream);
