@@ -61,11 +61,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void ldmatrix_x2_trans(uint32_t &r0, uint32_t &r1, const void *p) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
-                 : "=r"(r0), "=r"(r1)
-                 : "r"(smem_u32(p)));
-}
 // One arrival for the warp (32 on one barrier are served one by one).
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     __syncwarp();
@@ -116,20 +111,26 @@ __device__ __forceinline__ void keep_row(__nv_bfloat16 *kept, size_t chunk, int 
 }
 
 // ------------------------------------------------------------------ prep
-// One CTA of four warps per chunk of a (sequence, value head): the two
-// products by mma.sync (a 64 x 64 x dk product has too few rows to fill a
-// tcgen05 tile, and a grid of thousands of chunks hides its latency), the
-// inverse in float32: two 32 x 32 triangles by substitution, a column a
-// lane, then the square below them by two products.
-constexpr int kPrepThreads = 128;
+// One CTA of eight warps per chunk of a (sequence, value head): the products
+// by mma.sync (a 64 x 64 x dk product has too few rows to fill a tcgen05
+// tile, and a grid of thousands of chunks hides its latency), the inverse in
+// float32: four 16 x 16 triangles by substitution, a column a lane, then the
+// squares below them by products, 16 and then 32 rows at a time.
+// The chunk's block is put together in shared memory, K and Q first where W
+// and Q~ replace them, and leaves by one copy.
+// Decays e^{G_i - G_j}: of rows and columns in different 16-row blocks as
+// e^{G_i - G_r} e^{G_r - G_j} with r the row before the block of i, so that
+// both factors are at most 1 and 160 exponentials replace 2000.
+constexpr int kPrepThreads = 256;
 constexpr int kMPad = 68;
 
-template <int DK>
+template <int DK, bool kSplit>
 struct DeltaPrepSmem {
-    __nv_bfloat16 K[kC][DK + 8], Q[kC][DK + 8];
-    float M[kC][kMPad], T[kC][kMPad];
+    uint8_t block[DeltaBlock<DK, kSplit>::kBytes];
+    float M[kC][kMPad];                    // M, then T in its place
     double G[kC];
-    float beta[kC], e[kC];
+    float beta[kC], e[kC], in[kC];         // e^G; e^{G_i - G_r}
+    float across[3][kC];                   // [block - 1][j]: e^{G_r - G_j}
 };
 
 struct DeltaPrepArgs {
@@ -140,12 +141,61 @@ struct DeltaPrepArgs {
     int heads, key_heads, tokens, nc, backward;
 };
 
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p)));
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p)));
+}
+
+// An 8-column tile of sign A B for 16 rows of A (both kMPad wide, K columns
+// deep) by one warp, in three tf32 products (x = hi + lo, lo lo left out:
+// 2^-22), to C.
+template <int K>
+__device__ __forceinline__ void square_tile(const float *A, const float *B, float *C, float sign,
+                                            int lane) {
+    const int gr = lane / 4, tq = lane % 4;
+    float acc[4] = {};
+    auto part = [](float x, uint32_t &hi, uint32_t &lo) {
+        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+    };
+    auto mma = [&acc](const uint32_t (&x)[4], const uint32_t (&y)[2]) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
+            : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(y[0]), "r"(y[1]));
+    };
+#pragma unroll
+    for (int k = 0; k < K; k += 8) {
+        uint32_t ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            part(A[(gr + 8 * (e & 1)) * kMPad + k + tq + 4 * (e >> 1)], ah[e], al[e]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) part(B[(k + tq + 4 * e) * kMPad + gr], bh[e], bl[e]);
+        mma(ah, bh);
+        mma(ah, bl);
+        mma(al, bh);
+    }
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+        *reinterpret_cast<float2 *>(&C[(gr + 8 * hf) * kMPad + 2 * tq]) =
+            make_float2(sign * acc[2 * hf], sign * acc[2 * hf + 1]);
+}
+
 template <int DK, bool kSplit>
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, kSplit ? 2 : 3)
 delta_prep_kernel(DeltaPrepArgs a) {
     using Block = DeltaBlock<DK, kSplit>;
-    extern __shared__ __align__(16) uint8_t raw[];
-    DeltaPrepSmem<DK> &m = *reinterpret_cast<DeltaPrepSmem<DK> *>(raw);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    DeltaPrepSmem<DK, kSplit> &m = *reinterpret_cast<DeltaPrepSmem<DK, kSplit> *>(smem);
+    uint8_t *Kt = m.block + Block::kW, *Qt = m.block + Block::kQ;
     const int bh = blockIdx.x / a.nc, c = blockIdx.x % a.nc;
     const int b = bh / a.heads, h = bh % a.heads, kh = h / (a.heads / a.key_heads);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -155,63 +205,76 @@ delta_prep_kernel(DeltaPrepArgs a) {
     const int cnt = min(kC, n - c * kC);
     if (cnt <= 0) return;                                  // the whole CTA
     const size_t row0 = (size_t)b * a.tokens + c * kC;
-    uint8_t *out = a.blocks + (size_t)blockIdx.x * Block::kBytes;
 
     {   // K and Q, rows behind the sequence as zeros
-        constexpr int kVecs = DK / 8;
+        constexpr int kVecs = DK / 8, kEach = kC * kVecs / kPrepThreads;
         const size_t step = (size_t)a.key_heads * DK;
         const __nv_bfloat16 *ks = a.k + (row0 * a.key_heads + kh) * (size_t)DK;
         const __nv_bfloat16 *qs = a.q + (row0 * a.key_heads + kh) * (size_t)DK;
-#pragma unroll 4
-        for (int i = tid; i < kC * kVecs; i += kPrepThreads) {
-            const int r = i / kVecs, j = (i % kVecs) * 8;
-            uint4 kv = make_uint4(0, 0, 0, 0), qv = kv;
+        uint4 kv[kEach], qv[kEach];
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+            const int i = tid + u * kPrepThreads, r = i / kVecs, j = (i % kVecs) * 8;
+            kv[u] = qv[u] = make_uint4(0, 0, 0, 0);
             if (r < cnt) {
-                kv = *reinterpret_cast<const uint4 *>(ks + r * step + j);
-                qv = *reinterpret_cast<const uint4 *>(qs + r * step + j);
-            }
-            *reinterpret_cast<uint4 *>(&m.K[r][j]) = kv;
-            *reinterpret_cast<uint4 *>(&m.Q[r][j]) = qv;
-        }
-    }
-    if (warp == 0) {                                       // running sums of g
-        const size_t at = row0 * a.heads + h;
-        double lo = lane < cnt ? log_decay(to_f32(a.g[at + (size_t)lane * a.heads])) : 0.0;
-        double hi = lane + 32 < cnt ? log_decay(to_f32(a.g[at + (size_t)(lane + 32) * a.heads])) : 0.0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double ul = __shfl_up_sync(0xffffffffu, lo, o);
-            const double uh = __shfl_up_sync(0xffffffffu, hi, o);
-            if (lane >= o) {
-                lo += ul;
-                hi += uh;
+                kv[u] = *reinterpret_cast<const uint4 *>(ks + r * step + j);
+                qv[u] = *reinterpret_cast<const uint4 *>(qs + r * step + j);
             }
         }
-        hi += __shfl_sync(0xffffffffu, lo, 31);
-        const double GL = __shfl_sync(0xffffffffu, hi, 31);
-        m.G[lane] = lo;
-        m.G[lane + 32] = hi;
-        m.e[lane] = expf((float)lo);
-        m.e[lane + 32] = expf((float)hi);
-        float *hdr = reinterpret_cast<float *>(out + Block::kHdr);
-        hdr[lane] = expf((float)(GL - lo));
-        hdr[lane + 32] = expf((float)(GL - hi));
-        if (lane == 0) hdr[64] = expf((float)GL);
-    } else if (warp == 1) {
+        if (warp == 0) {                                   // running sums of g
+            const size_t at = row0 * a.heads + h;
+            double lo = lane < cnt ? log_decay(to_f32(a.g[at + (size_t)lane * a.heads])) : 0.0;
+            double hi = lane + 32 < cnt ? log_decay(to_f32(a.g[at + (size_t)(lane + 32) * a.heads])) : 0.0;
 #pragma unroll
-        for (int i = lane; i < kC; i += 32) {
-            float bt = 0.f;
-            if (i < cnt) {
-                bt = to_f32(a.beta[(row0 + i) * a.heads + h]);
-                if (a.backward) bt = nonzero_beta(bt);
+            for (int o = 1; o < 32; o <<= 1) {
+                const double ul = __shfl_up_sync(0xffffffffu, lo, o);
+                const double uh = __shfl_up_sync(0xffffffffu, hi, o);
+                if (lane >= o) {
+                    lo += ul;
+                    hi += uh;
+                }
             }
-            m.beta[i] = bt;
+            m.G[lane] = lo;
+            m.G[lane + 32] = hi + __shfl_sync(0xffffffffu, lo, 31);
+        } else if (warp == 1) {
+#pragma unroll
+            for (int i = lane; i < kC; i += 32) {
+                float bt = 0.f;
+                if (i < cnt) {
+                    bt = to_f32(a.beta[(row0 + i) * a.heads + h]);
+                    if (a.backward) bt = nonzero_beta(bt);
+                }
+                m.beta[i] = bt;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+            const int i = tid + u * kPrepThreads, r = i / kVecs, j = (i % kVecs) * 8;
+            *reinterpret_cast<uint4 *>(Kt + tile_off(r, j)) = kv[u];
+            *reinterpret_cast<uint4 *>(Qt + tile_off(r, j)) = qv[u];
         }
     }
     __syncthreads();
+    if (tid < 64) {
+        const int r = (tid & ~15) - 1;
+        m.e[tid] = expf((float)m.G[tid]);
+        m.in[tid] = expf((float)(m.G[tid] - (r < 0 ? 0.0 : m.G[r])));
+    } else if (tid < 128) {
+        float *hdr = reinterpret_cast<float *>(m.block + Block::kHdr);
+        hdr[tid - 64] = expf((float)(m.G[kC - 1] - m.G[tid - 64]));
+        if (tid == 64) hdr[64] = expf((float)m.G[kC - 1]);
+    } else if (tid < 224) {                                // 16, 32 and 48 columns
+        const int t = tid - 128, blk = t < 16 ? 1 : t < 48 ? 2 : 3;
+        const int j = t - (blk == 1 ? 0 : blk == 2 ? 16 : 48);
+        m.across[blk - 1][j] = expf((float)(m.G[16 * blk - 1] - m.G[j]));
+    }
+    __syncthreads();
 
-    // rows 16 rb .. of (a row-major operand) times the rows of K, up to the diagonal
-    auto gram = [&](float (&acc)[8][4], const __nv_bfloat16 (*A)[DK + 8], int rb) {
+    {   // warps 0-3: M from K K^T, warps 4-7: P from Q K^T; 16 rows each, up to the diagonal
+        const int rb = warp & 3;
+        const bool isP = warp >= 4;
+        const uint8_t *At = isP ? Qt : Kt;
+        float acc[8][4];
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
@@ -219,39 +282,49 @@ delta_prep_kernel(DeltaPrepArgs a) {
 #pragma unroll
         for (int k0 = 0; k0 < DK; k0 += 16) {
             uint32_t av[4];
-            const int r = 16 * rb + gr;
-            av[0] = *reinterpret_cast<const uint32_t *>(&A[r][k0 + 2 * tq]);
-            av[1] = *reinterpret_cast<const uint32_t *>(&A[r + 8][k0 + 2 * tq]);
-            av[2] = *reinterpret_cast<const uint32_t *>(&A[r][k0 + 2 * tq + 8]);
-            av[3] = *reinterpret_cast<const uint32_t *>(&A[r + 8][k0 + 2 * tq + 8]);
+            ldmatrix_x4(av, At + tile_off(16 * rb + (lane & 15), k0 + 8 * (lane >> 4)));
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
-                if (t < 2 * rb + 2) {
-                    const uint32_t b0 = *reinterpret_cast<const uint32_t *>(&m.K[8 * t + gr][k0 + 2 * tq]);
-                    const uint32_t b1 = *reinterpret_cast<const uint32_t *>(&m.K[8 * t + gr][k0 + 2 * tq + 8]);
-                    mma16816(acc[t], av, b0, b1);
+            for (int t2 = 0; t2 < 4; ++t2)
+                if (t2 <= rb) {
+                    uint32_t bv[4];
+                    ldmatrix_x4(bv, Kt + tile_off(16 * t2 + (lane & 7) + ((lane >> 4) << 3),
+                                                  k0 + 8 * ((lane >> 3) & 1)));
+                    mma16816(acc[2 * t2], av, bv[0], bv[1]);
+                    mma16816(acc[2 * t2 + 1], av, bv[2], bv[3]);
                 }
         }
-    };
-    {   // M: warp w the rows 16 w ..
-        float acc[8][4];
-        gram(acc, m.K, warp);
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int hf = 0; hf < 2; ++hf) {
+            const int i = 16 * rb + gr + 8 * hf;
+            const double Gi = m.G[i];
+            const float f = (isP ? a.scale : m.beta[i]), far = f * m.in[i];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 16 * warp + gr + (e >= 2 ? 8 : 0), j = 8 * t + 2 * tq + (e & 1);
-                m.M[i][j] = i > j ? acc[t][e] * m.beta[i] * expf((float)(m.G[i] - m.G[j])) : 0.f;
+            for (int t = 0; t < 8; ++t) {
+                const int j = 8 * t + 2 * tq;
+                float w[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float x = acc[t][2 * hf + e];
+                    if (t / 2 < rb) w[e] = x * far * m.across[rb - 1][j + e];
+                    else if (t / 2 == rb)
+                        w[e] = i > j + e || (isP && i == j + e) ? x * f * expf((float)(Gi - m.G[j + e])) : 0.f;
+                    else w[e] = 0.f;
+                }
+                if (isP)
+                    *reinterpret_cast<uint32_t *>(m.block + Block::kP + tile_off(i, j)) = pack_bf16x2(w[0], w[1]);
+                else
+                    *reinterpret_cast<float2 *>(&m.M[i][j]) = make_float2(w[0], w[1]);
             }
+        }
     }
     __syncthreads();
-    if (warp < 2) {
-        // lane's column of the inverse of triangle `warp`
-        const int o = 32 * warp;
-        float x[32];
+    if (warp < 4) {
+        // lane's column of the inverse of triangle `warp` (lanes 16.. repeat them)
+        const int o = 16 * warp, col = lane & 15;
+        float x[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
+        for (int i = 0; i < 16; ++i) {
+            float s0 = i == col ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
             for (int j = 0; j < i; ++j) {
                 const float mv = m.M[o + i][o + j];
@@ -259,120 +332,102 @@ delta_prep_kernel(DeltaPrepArgs a) {
                 else s0 = fmaf(-mv, x[j], s0);
             }
             x[i] = s0 + s1;
-            m.T[o + i][o + lane] = x[i];
         }
-        if (warp == 0)                                     // the square above them
+        __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) m.T[i][32 + lane] = 0.f;
-    } else {
-        // P and Q~: warps 2, 3 take row blocks {0, 3} and {1, 2}
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int rb = u ? (warp == 2 ? 3 : 2) : warp - 2;
-            float acc[8][4];
-            gram(acc, m.Q, rb);
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int i = 16 * rb + gr + 8 * hf, j = 8 * t + 2 * tq;
-                    const float p0 = i >= j ? a.scale * acc[t][2 * hf] * expf((float)(m.G[i] - m.G[j])) : 0.f;
-                    const float p1 = i >= j + 1 ? a.scale * acc[t][2 * hf + 1] * expf((float)(m.G[i] - m.G[j + 1])) : 0.f;
-                    *reinterpret_cast<uint32_t *>(out + Block::kP + tile_off(i, j)) = pack_bf16x2(p0, p1);
-                }
-            constexpr int kVecs = DK / 8;
+        for (int i = 0; i < 16; ++i) m.M[o + i][o + col] = x[i];
+    } else {                                               // Q~ where Q was
+        constexpr int kVecs = DK / 8;
 #pragma unroll 2
-            for (int i = lane; i < 16 * kVecs; i += 32) {
-                const int r = 16 * rb + i / kVecs, j = (i % kVecs) * 8;
-                float qv[8];
-                load8(&m.Q[r][j], qv);
-                const float s = a.scale * m.e[r];
+        for (int i = tid - 128; i < kC * kVecs; i += 128) {
+            const int r = i / kVecs, j = (i % kVecs) * 8;
+            __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(Qt + tile_off(r, j));
+            float qv[8];
+            load8(p, qv);
+            const float s = a.scale * m.e[r];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) qv[e] *= s;
-                store8(reinterpret_cast<__nv_bfloat16 *>(out + Block::kQ + tile_off(r, j)), qv);
-            }
+            for (int e = 0; e < 8; ++e) qv[e] *= s;
+            store8(p, qv);
         }
     }
     __syncthreads();
-    // T_10 = -T_11 (M_10 T_00): the inner product into M's free upper square
+    // T_10 = -T_11 (M_10 T_00), for the two pairs of triangles of 16 rows and
+    // then for those of 32; the inner product goes to the square of M above
+    // the diagonal of 32, which is not read otherwise
     {
-        const int r = tid / 8 * 2, cc = (tid % 8) * 4;      // 2 x 4 outputs a thread
-        float s[2][4] = {};
-#pragma unroll 4
-        for (int j = 0; j < 32; ++j) {
-            const float4 t = *reinterpret_cast<const float4 *>(&m.T[j][cc]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float mv = m.M[32 + r + i][j];
-                s[i][0] = fmaf(mv, t.x, s[i][0]); s[i][1] = fmaf(mv, t.y, s[i][1]);
-                s[i][2] = fmaf(mv, t.z, s[i][2]); s[i][3] = fmaf(mv, t.w, s[i][3]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float4 *>(&m.M[r + i][32 + cc]) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+        const int o = 32 * (warp & 1), t8 = 8 * ((warp >> 1) & 1);     // warps 0-3
+        if (warp < 4) square_tile<16>(&m.M[o + 16][o], &m.M[o][o + t8], &m.M[o / 2][32 + t8], 1.f, lane);
         __syncthreads();
-        float u[2][4] = {};
-#pragma unroll 4
-        for (int j = 0; j < 32; ++j) {
-            const float4 t = *reinterpret_cast<const float4 *>(&m.M[j][32 + cc]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float tv = m.T[32 + r + i][32 + j];
-                u[i][0] = fmaf(-tv, t.x, u[i][0]); u[i][1] = fmaf(-tv, t.y, u[i][1]);
-                u[i][2] = fmaf(-tv, t.z, u[i][2]); u[i][3] = fmaf(-tv, t.w, u[i][3]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float4 *>(&m.T[32 + r + i][cc]) = make_float4(u[i][0], u[i][1], u[i][2], u[i][3]);
+        if (warp < 4)
+            square_tile<16>(&m.M[o + 16][o + 16], &m.M[o / 2][32 + t8], &m.M[o + 16][o + t8], -1.f, lane);
+        __syncthreads();
+        const int r = 16 * (warp & 1), c8 = 8 * (warp >> 1);           // a tile a warp
+        square_tile<32>(&m.M[32 + r][0], &m.M[0][c8], &m.M[r][32 + c8], 1.f, lane);
+        __syncthreads();
+        square_tile<32>(&m.M[32 + r][32], &m.M[0][32 + c8], &m.M[32 + r][c8], -1.f, lane);
+        __syncthreads();
     }
-    __syncthreads();
-    // T^ = T diag(b) in its tiles; W = T^ diag(e^G) K in two parts of T^, K being exact
+    // T^ = T diag(b) in its tiles; W = T^ diag(e^G) K in two parts of T^, K
+    // being exact: warp w the rows 16 (w % 4) and a half of the columns
     {
-        const int r = 16 * warp + gr;
-        float acc[DK / 8][4] = {};
+        constexpr int kTiles = DK / 16;                    // of 8 columns
+        const int rb = warp & 3, half = warp >> 2, r = 16 * rb + gr;
+        float acc[kTiles][4] = {};
 #pragma unroll
         for (int j0 = 0; j0 < kC; j0 += 16) {
-            if (j0 <= 16 * warp) {
+            if (j0 <= 16 * rb) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = r + (e & 1) * 8, j = j0 + 2 * tq + (e >> 1) * 8;
-                    const float2 t = *reinterpret_cast<const float2 *>(&m.T[i][j]);
-                    const float t0 = t.x * m.beta[j], t1 = t.y * m.beta[j + 1];
-                    uint32_t th, tl;
-                    split_pair(t0, t1, th, tl);
-                    *reinterpret_cast<uint32_t *>(out + Block::kT + tile_off(i, j)) = th;
-                    if (kSplit) *reinterpret_cast<uint32_t *>(out + Block::kTlo + tile_off(i, j)) = tl;
-                    split_pair(-t0 * m.e[j], -t1 * m.e[j + 1], hi[e], lo[e]);
+                    const float2 t = *reinterpret_cast<const float2 *>(&m.M[i][j]);
+                    const float2 bt = *reinterpret_cast<const float2 *>(&m.beta[j]);
+                    const float2 ej = *reinterpret_cast<const float2 *>(&m.e[j]);
+                    const float t0 = t.x * bt.x, t1 = t.y * bt.y;
+                    if (half == 0) {
+                        uint32_t th, tl;
+                        split_pair(t0, t1, th, tl);
+                        *reinterpret_cast<uint32_t *>(m.block + Block::kT + tile_off(i, j)) = th;
+                        if (kSplit) *reinterpret_cast<uint32_t *>(m.block + Block::kTlo + tile_off(i, j)) = tl;
+                    }
+                    split_pair(-t0 * ej.x, -t1 * ej.y, hi[e], lo[e]);
                 }
 #pragma unroll
-                for (int t = 0; t < DK / 8; ++t) {
-                    uint32_t b0, b1;
-                    ldmatrix_x2_trans(b0, b1, &m.K[j0 + (lane & 15)][8 * t]);
-                    mma16816(acc[t], hi, b0, b1);
-                    mma16816(acc[t], lo, b0, b1);
+                for (int t = 0; t < kTiles; t += 2) {
+                    uint32_t bv[4];
+                    ldmatrix_x4_trans(bv, Kt + tile_off(j0 + (lane & 15), half * (DK / 2) + 8 * t + 8 * (lane >> 4)));
+                    mma16816(acc[t], hi, bv[0], bv[1]);
+                    mma16816(acc[t], lo, bv[0], bv[1]);
+                    mma16816(acc[t + 1], hi, bv[2], bv[3]);
+                    mma16816(acc[t + 1], lo, bv[2], bv[3]);
                 }
-            } else {
+            } else if (half == 0) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = r + (e & 1) * 8, j = j0 + 2 * tq + (e >> 1) * 8;
-                    *reinterpret_cast<uint32_t *>(out + Block::kT + tile_off(i, j)) = 0u;
-                    if (kSplit) *reinterpret_cast<uint32_t *>(out + Block::kTlo + tile_off(i, j)) = 0u;
+                    const uint32_t o = tile_off(r + (e & 1) * 8, j0 + 2 * tq + (e >> 1) * 8);
+                    *reinterpret_cast<uint32_t *>(m.block + Block::kT + o) = 0u;
+                    if (kSplit) *reinterpret_cast<uint32_t *>(m.block + Block::kTlo + o) = 0u;
                 }
             }
         }
+        __syncthreads();                                   // K has been read
 #pragma unroll
-        for (int t = 0; t < DK / 8; ++t)
+        for (int t = 0; t < kTiles; ++t)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t o = tile_off(r + 8 * hf, 8 * t + 2 * tq);
+                const uint32_t o = tile_off(r + 8 * hf, half * (DK / 2) + 8 * t + 2 * tq);
                 uint32_t wh, wl;
                 split_pair(acc[t][2 * hf], acc[t][2 * hf + 1], wh, wl);
-                *reinterpret_cast<uint32_t *>(out + Block::kW + o) = wh;
-                if (kSplit) *reinterpret_cast<uint32_t *>(out + Block::kWlo + o) = wl;
+                *reinterpret_cast<uint32_t *>(m.block + Block::kW + o) = wh;
+                if (kSplit) *reinterpret_cast<uint32_t *>(m.block + Block::kWlo + o) = wl;
             }
+    }
+    fence_async_shared();
+    __syncthreads();
+    if (tid == 0) {
+        bulk_store(a.blocks + (size_t)blockIdx.x * Block::kBytes, m.block, Block::kBytes);
+        tma_store_commit();
+        tma_store_wait_read();
     }
 }
 
@@ -1438,7 +1493,7 @@ cudaError_t launch_prep(const DeltaArgs &a, int nc, uint8_t *blocks, bool backwa
                         cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel<DK, kSplit>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(DeltaPrepSmem<DK>));
+                                         (int)sizeof(DeltaPrepSmem<DK, kSplit>));
     if (e != cudaSuccess) return e;
     DeltaPrepArgs p = {(const __nv_bfloat16 *)a.q, (const __nv_bfloat16 *)a.k,
                        (const __nv_bfloat16 *)a.g, (const __nv_bfloat16 *)a.beta, a.lengths,
@@ -1447,7 +1502,7 @@ cudaError_t launch_prep(const DeltaArgs &a, int nc, uint8_t *blocks, bool backwa
     count_launch();
     return launch_overlapped(delta_prep_kernel<DK, kSplit>,
                              dim3((unsigned)((long long)a.batch * a.heads * nc)), dim3(kPrepThreads),
-                             sizeof(DeltaPrepSmem<DK>), stream, p);
+                             sizeof(DeltaPrepSmem<DK, kSplit>), stream, p);
 }
 
 template <int DK, bool kSplit, bool kOut, bool kSave>

@@ -158,6 +158,13 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         "r"(smem_u32(bar))
         : "memory");
 }
+// Contiguous copy shared -> global, same rules.
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                     (uint64_t)__cvta_generic_to_global(dst)),
+                 "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
 // TMA tile store shared -> global (rows outside the tensor are dropped);
 // the start coordinate must not be negative.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *src, int c0,
