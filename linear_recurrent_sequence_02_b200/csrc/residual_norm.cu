@@ -10,16 +10,15 @@
 //   dy  = r_y (u - y^ mean(u y^)),       u = dz post.
 // Every row is read once and written once: an HBM stream of 5 tensors
 // forward (x, y, g; h, n) and 8 backward (x, y, g, dh, dn; dx, dy, dg).  A
-// row stays in the registers of the threads that own it (two vectors of 8
-// channels each at most), so the two (three) sums over the row cost
+// row stays in the registers of the threads that own it (a vector of 8
+// channels each, two above 8192), so the two (three) sums over the row cost
 // shuffles and one barrier each and nothing is read twice; h is formed from
 // x, y and g again in the backward, which reads no more than a stored h would.
 #include "kernels.h"
 
 namespace retnet {
 
-constexpr int kNormVecs = 2;               // vectors of 8 channels per thread
-constexpr int kNormWarpRows = 4;           // rows per CTA where a warp owns a row
+constexpr int kNormWarpRows = 8;           // rows per CTA where a warp owns a row
 
 struct NormArgs {
     const void *x, *y, *gate, *dh, *dn;
@@ -54,12 +53,74 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float (*red)[N]) {
     }
 }
 
-// The fast exponential and quotient (a few 2^-22 relative, and 0 where the
+// The fast exponential and reciprocal (a few 2^-22 relative, and 0 where the
 // exponential overflows): with the exact ones the arithmetic of a gated row
-// takes about as long as its traffic.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// takes longer than its traffic.
+__device__ __forceinline__ float sigmoid(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
+    return r;
+}
 
-template <typename T, int TPR>
+// 8 channels as they lie in memory: rows stay packed until they are used, or
+// a row's registers would leave too few warps to hide its loads.
+template <typename T>
+struct Packed;
+template <>
+struct Packed<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    // 16-byte pieces `stride` apart
+    __device__ __forceinline__ void load(const uint8_t *p, int) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ float2 at(int e) const {    // channels 2 e, 2 e + 1
+        const uint32_t w = e == 0 ? u.x : e == 1 ? u.y : e == 2 ? u.z : u.w;
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+};
+template <>
+struct Packed<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void load(const uint8_t *p, int stride) {
+        a = *reinterpret_cast<const float4 *>(p);
+        b = *reinterpret_cast<const float4 *>(p + stride);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ float2 at(int e) const {
+        const float4 &v = e < 2 ? a : b;
+        return e & 1 ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
+    }
+};
+__device__ __forceinline__ void store8(float *p, const float2 (&v)[4]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float2 (&v)[4]) {
+    uint4 u;
+    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __float22bfloat162_rn(v[i]);
+    *reinterpret_cast<uint4 *>(p) = u;
+}
+// A weight's 8 channels (1 where there is none).
+__device__ __forceinline__ void load_weight(const float *w, int c, float2 (&o)[4]) {
+    if (w) {
+        const float4 *p = reinterpret_cast<const float4 *>(w + c * 8);
+        const float4 a = p[0], b = p[1];
+        o[0] = make_float2(a.x, a.y); o[1] = make_float2(a.z, a.w);
+        o[2] = make_float2(b.x, b.y); o[3] = make_float2(b.z, b.w);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = make_float2(1.f, 1.f);
+    }
+}
+__device__ __forceinline__ float2 sigmoid2(float2 x) { return make_float2(sigmoid(x.x), sigmoid(x.y)); }
+
+template <typename T, int TPR, int kVecs>
 __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarpRows : TPR)
 residual_norm_kernel(NormArgs a) {
     constexpr int kRows = TPR == 32 ? kNormWarpRows : 1;
@@ -69,62 +130,64 @@ residual_norm_kernel(NormArgs a) {
     grid_dependency_wait();
     if (row >= a.rows) return;             // a whole warp, or no thread of a CTA
     const size_t base = (size_t)row * a.hidden;
-    const T *x = (const T *)a.x + base, *y = (const T *)a.y + base;
-    const T *g = a.gate ? (const T *)a.gate + base : nullptr;
+    const bool gated = a.gate != nullptr;
     const int vecs = a.hidden / 8;
 
-    float xv[kNormVecs][8], yv[kNormVecs][8], gv[kNormVecs][8];
+    Packed<T> xp[kVecs], yp[kVecs], gp[kVecs];
 #pragma unroll
-    for (int i = 0; i < kNormVecs; ++i) {
+    for (int i = 0; i < kVecs; ++i) {
         const int c = lane + i * TPR;
         if (c < vecs) {
-            load8(y + c * 8, yv[i]);
-            load8(x + c * 8, xv[i]);
-            if (g) load8(g + c * 8, gv[i]);
+            yp[i].load((const T *)a.y + base + c * 8);
+            xp[i].load((const T *)a.x + base + c * 8);
+            if (gated) gp[i].load((const T *)a.gate + base + c * 8);
         } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) xv[i][e] = yv[i][e] = gv[i][e] = 0.f;
+            yp[i].zero();
+            xp[i].zero();
+            gp[i].zero();
         }
     }
     float ry = 1.f;
     if (a.post_norm) {
-        float s[1] = {0.f};
+        float2 q = both(0.f);
 #pragma unroll
-        for (int i = 0; i < kNormVecs; ++i)
+        for (int i = 0; i < kVecs; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[0] = fmaf(yv[i][e], yv[i][e], s[0]);
+            for (int e = 0; e < 4; ++e) q = fma2(yp[i].at(e), yp[i].at(e), q);
+        float s[1] = {q.x + q.y};
         row_sum<TPR>(s, red[0]);
         ry = rsqrtf(s[0] / (float)a.hidden + a.eps);
     }
-    float s[1] = {0.f};
+    float2 q = both(0.f), h[kVecs][4];
+    const float *post = a.post_norm ? a.post : nullptr;
 #pragma unroll
-    for (int i = 0; i < kNormVecs; ++i) {
+    for (int i = 0; i < kVecs; ++i) {
         const int c = lane + i * TPR;
         if (c < vecs) {
-            float w[8];
-            if (a.post_norm && a.post) load8(a.post + c * 8, w);
+            float2 w[4];
+            load_weight(post, c, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float z = yv[i][e] * ry;
-                if (a.post_norm && a.post) z *= w[e];
-                if (g) z *= gv[i][e] * sigmoid(gv[i][e]);
-                xv[i][e] = fmaf(a.scale, z, xv[i][e]);
-                s[0] = fmaf(xv[i][e], xv[i][e], s[0]);
+            for (int e = 0; e < 4; ++e) {
+                float2 z = mul2(mul2(yp[i].at(e), both(ry)), w[e]);
+                if (gated) z = mul2(z, mul2(gp[i].at(e), sigmoid2(gp[i].at(e))));
+                h[i][e] = fma2(both(a.scale), z, xp[i].at(e));
+                q = fma2(h[i][e], h[i][e], q);
             }
+            store8((T *)a.h + base + c * 8, h[i]);
         }
     }
+    float s[1] = {q.x + q.y};
     row_sum<TPR>(s, red[1]);
     const float rh = rsqrtf(s[0] / (float)a.hidden + a.eps);
 #pragma unroll
-    for (int i = 0; i < kNormVecs; ++i) {
+    for (int i = 0; i < kVecs; ++i) {
         const int c = lane + i * TPR;
         if (c < vecs) {
-            store8((T *)a.h + base + c * 8, xv[i]);
-            float w[8];
-            if (a.pre) load8(a.pre + c * 8, w);
+            float2 w[4];
+            load_weight(a.pre, c, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) xv[i][e] *= a.pre ? rh * w[e] : rh;
-            store8((T *)a.n + base + c * 8, xv[i]);
+            for (int e = 0; e < 4; ++e) h[i][e] = mul2(h[i][e], mul2(both(rh), w[e]));
+            store8((T *)a.n + base + c * 8, h[i]);
         }
     }
 }
@@ -132,130 +195,168 @@ residual_norm_kernel(NormArgs a) {
 // A CTA takes rows blockIdx.x, + gridDim.x, ... and keeps the weights'
 // gradients of its channels in registers until the end, so they cost one
 // partial row a CTA instead of an atomic a channel and row, and their order
-// does not change from run to run.
-template <typename T, int TPR>
-__global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarpRows : TPR)
+// does not change from run to run.  With kAhead every thread copies its
+// vectors of the next row to shared memory while it works on this one (8192 x
+// 4096 bf16: 157 us without, 116 with), and reads them again in each pass
+// instead of holding them; without (rows too long for two in shared memory)
+// they come from global memory as they are needed.
+template <typename T, int TPR, int kVecs, bool kAhead>
+__global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarpRows : TPR, TPR <= 256 ? 512 / (TPR == 32 ? 256 : TPR) : 1)
 residual_norm_backward_kernel(NormArgs a) {
+    enum { kX, kY, kGate, kDn, kDh, kTensors };
+    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int kVecBytes = 8 * sizeof(T), kThreads = TPR == 32 ? 32 * kNormWarpRows : TPR;
     constexpr int kRows = TPR == 32 ? kNormWarpRows : 1;
     __shared__ float red1[2][TPR / 32][1], red2[2][TPR / 32][2], red3[2][TPR / 32][1];
     const int lane = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
     const long long first = (long long)blockIdx.x * kRows + (TPR == 32 ? threadIdx.x >> 5 : 0);
     const int vecs = a.hidden / 8;
-    const bool gated = a.gate != nullptr, weighted = a.post_norm && a.post;
+    const bool gated = a.gate != nullptr;
+    const float *post = a.post_norm ? a.post : nullptr;
     const float inv = 1.f / (float)a.hidden;
-    float apost[kNormVecs][8] = {}, apre[kNormVecs][8] = {};
+    float2 apost[kVecs][4] = {}, apre[kVecs][4] = {};
     grid_dependency_wait();
 
-    int turn = 0;                          // alternating slots of the sums
-    for (long long row = first; row < a.rows; row += (long long)gridDim.x * kRows, turn ^= 1) {
-        const size_t base = (size_t)row * a.hidden;
-        float xv[kNormVecs][8], yv[kNormVecs][8], gv[kNormVecs][8], tv[kNormVecs][8];
-        float dv[kNormVecs][8];
+    const T *from[kTensors] = {(const T *)a.x, (const T *)a.y, (const T *)a.gate, (const T *)a.dn,
+                               (const T *)a.dh};
+    const long long step = (long long)gridDim.x * kRows;
+    // this thread's vector i of a tensor in slot `turn`; 16-byte pieces of the
+    // CTA's threads side by side
+    auto place = [&](int turn, int t, int i, int half) {
+        return smem + ((((turn * kTensors + t) * kVecs + i) * (kVecBytes / 16) + half) * kThreads + threadIdx.x) * 16;
+    };
+    auto fetch = [&](long long row, int turn) {
+        if (kAhead && row < a.rows)
 #pragma unroll
-        for (int i = 0; i < kNormVecs; ++i) {
-            const int c = lane + i * TPR;
-            if (c < vecs) {
-                const size_t o = base + c * 8;
-                load8((const T *)a.y + o, yv[i]);
-                load8((const T *)a.x + o, xv[i]);
-                if (gated) load8((const T *)a.gate + o, gv[i]);
-                load8((const T *)a.dn + o, tv[i]);
-                if (a.dh) load8((const T *)a.dh + o, dv[i]);
-            }
-        }
+            for (int t = 0; t < kTensors; ++t)
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i)
+                    if (from[t] && lane + i * TPR < vecs)
+#pragma unroll
+                        for (int half = 0; half < kVecBytes / 16; ++half)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                             (uint32_t)__cvta_generic_to_shared(place(turn, t, i, half))),
+                                         "l"((const char *)(from[t] + (size_t)row * a.hidden + (lane + i * TPR) * 8) + 16 * half)
+                                         : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int turn = 0;                          // alternating slots
+    fetch(first, 0);
+    for (long long row = first; row < a.rows; row += step, turn ^= 1) {
+        const size_t base = (size_t)row * a.hidden;
+        fetch(row + step, turn ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        auto get = [&](int t, int i) {
+            Packed<T> v;
+            if (kAhead) v.load(place(turn, t, i, 0), 16 * kThreads);
+            else v.load(from[t] + base + (lane + i * TPR) * 8);
+            return v;
+        };
         float ry = 1.f;
         if (a.post_norm) {
-            float s[1] = {0.f};
+            float2 q = both(0.f);
 #pragma unroll
-            for (int i = 0; i < kNormVecs; ++i)
-                if (lane + i * TPR < vecs)
+            for (int i = 0; i < kVecs; ++i)
+                if (lane + i * TPR < vecs) {
+                    const Packed<T> y = get(kY, i);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) s[0] = fmaf(yv[i][e], yv[i][e], s[0]);
+                    for (int e = 0; e < 4; ++e) q = fma2(y.at(e), y.at(e), q);
+                }
+            float s[1] = {q.x + q.y};
             row_sum<TPR>(s, red1[turn]);
             ry = rsqrtf(s[0] * inv + a.eps);
         }
         // h, and the sums of h^2 and (dn pre) h
-        float s2[2] = {0.f, 0.f};
+        float2 q0 = both(0.f), q1 = q0, h[kVecs][4], sg[kVecs][4];
 #pragma unroll
-        for (int i = 0; i < kNormVecs; ++i) {
+        for (int i = 0; i < kVecs; ++i) {
             const int c = lane + i * TPR;
             if (c < vecs) {
-                float w[8], p[8];
-                if (weighted) load8(a.post + c * 8, w);
-                if (a.pre) load8(a.pre + c * 8, p);
+                float2 w[4], p[4];
+                load_weight(post, c, w);
+                load_weight(a.pre, c, p);
+                const Packed<T> x = get(kX, i), y = get(kY, i), dn = get(kDn, i);
+                Packed<T> g;
+                if (gated) g = get(kGate, i);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    yv[i][e] *= ry;                       // y^
-                    float z = weighted ? yv[i][e] * w[e] : yv[i][e];
-                    if (gated) z *= gv[i][e] * sigmoid(gv[i][e]);
-                    xv[i][e] = fmaf(a.scale, z, xv[i][e]);
-                    const float t = a.pre ? tv[i][e] * p[e] : tv[i][e];
-                    s2[0] = fmaf(xv[i][e], xv[i][e], s2[0]);
-                    s2[1] = fmaf(t, xv[i][e], s2[1]);
+                for (int e = 0; e < 4; ++e) {
+                    float2 z = mul2(mul2(y.at(e), both(ry)), w[e]);
+                    if (gated) {
+                        sg[i][e] = sigmoid2(g.at(e));
+                        z = mul2(z, mul2(g.at(e), sg[i][e]));
+                    }
+                    h[i][e] = fma2(both(a.scale), z, x.at(e));
+                    q0 = fma2(h[i][e], h[i][e], q0);
+                    q1 = fma2(mul2(dn.at(e), p[e]), h[i][e], q1);
                 }
             }
         }
+        float s2[2] = {q0.x + q0.y, q1.x + q1.y};
         row_sum<TPR>(s2, red2[turn]);
         const float rh = rsqrtf(s2[0] * inv + a.eps);
         const float mh = s2[1] * rh * inv;                // mean(t h^)
-        float s3[1] = {0.f};
+        float2 q3 = both(0.f);
 #pragma unroll
-        for (int i = 0; i < kNormVecs; ++i) {
+        for (int i = 0; i < kVecs; ++i) {
             const int c = lane + i * TPR;
             if (c < vecs) {
-                float w[8], p[8];
-                if (weighted) load8(a.post + c * 8, w);
-                if (a.pre) load8(a.pre + c * 8, p);
-                float dg[8];
+                float2 w[4], p[4], dg[4], dx[4];
+                load_weight(post, c, w);
+                load_weight(a.pre, c, p);
+                const Packed<T> y = get(kY, i), dn = get(kDn, i);
+                Packed<T> g, dh;
+                if (gated) g = get(kGate, i);
+                if (a.dh) dh = get(kDh, i);
+                else dh.zero();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float hh = xv[i][e] * rh;       // h^
-                    apre[i][e] = fmaf(tv[i][e], hh, apre[i][e]);
-                    const float t = a.pre ? tv[i][e] * p[e] : tv[i][e];
-                    float d = rh * (t - hh * mh);
-                    if (a.dh) d += dv[i][e];
-                    dv[i][e] = d;                         // dx
-                    float dz = a.scale * d;
+                for (int e = 0; e < 4; ++e) {
+                    const float2 hh = mul2(h[i][e], both(rh));     // h^
+                    const float2 yh = mul2(y.at(e), both(ry));     // y^
+                    apre[i][e] = fma2(dn.at(e), hh, apre[i][e]);
+                    dx[e] = fma2(both(rh), fma2(hh, both(-mh), mul2(dn.at(e), p[e])), dh.at(e));
+                    float2 dz = mul2(both(a.scale), dx[e]);
                     if (gated) {
-                        const float sg = sigmoid(gv[i][e]), sw = gv[i][e] * sg;
-                        const float z = weighted ? yv[i][e] * w[e] : yv[i][e];
-                        dg[e] = dz * z * fmaf(sw, 1.f - sg, sg);
-                        dz *= sw;
+                        const float2 sw = mul2(g.at(e), sg[i][e]);
+                        // swish' = sg + sw (1 - sg)
+                        const float2 ds = add2(fma2(sw, mul2(sg[i][e], both(-1.f)), sw), sg[i][e]);
+                        dg[e] = mul2(mul2(dz, mul2(yh, w[e])), ds);
+                        dz = mul2(dz, sw);
                     }
-                    apost[i][e] = fmaf(dz, yv[i][e], apost[i][e]);
-                    const float u = weighted ? dz * w[e] : dz;
-                    tv[i][e] = u;
-                    s3[0] = fmaf(u, yv[i][e], s3[0]);
+                    apost[i][e] = fma2(dz, yh, apost[i][e]);
+                    h[i][e] = mul2(dz, w[e]);                      // u
+                    q3 = fma2(h[i][e], yh, q3);
                 }
-                store8((T *)a.dx + base + c * 8, dv[i]);
+                store8((T *)a.dx + base + c * 8, dx);
                 if (gated) store8((T *)a.dgate + base + c * 8, dg);
             }
         }
         float my = 0.f;
         if (a.post_norm) {
+            float s3[1] = {q3.x + q3.y};
             row_sum<TPR>(s3, red3[turn]);
             my = s3[0] * inv;                             // mean(u y^)
         }
 #pragma unroll
-        for (int i = 0; i < kNormVecs; ++i) {
+        for (int i = 0; i < kVecs; ++i) {
             const int c = lane + i * TPR;
             if (c < vecs) {
-                float o[8];
+                if (a.post_norm) {
+                    const Packed<T> y = get(kY, i);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    o[e] = a.post_norm ? ry * (tv[i][e] - yv[i][e] * my) : tv[i][e];
-                store8((T *)a.dy + base + c * 8, o);
+                    for (int e = 0; e < 4; ++e)
+                        h[i][e] = mul2(both(ry), fma2(y.at(e), both(-ry * my), h[i][e]));
+                }
+                store8((T *)a.dy + base + c * 8, h[i]);
             }
         }
     }
     // this CTA's (this warp's) partial sums over its rows
-    const long long part = first;          // < gridDim.x * kRows
 #pragma unroll
-    for (int i = 0; i < kNormVecs; ++i) {
+    for (int i = 0; i < kVecs; ++i) {
         const int c = lane + i * TPR;
         if (c < vecs) {
-            if (a.part_post) store8(a.part_post + (size_t)part * a.hidden + c * 8, apost[i]);
-            if (a.part_pre) store8(a.part_pre + (size_t)part * a.hidden + c * 8, apre[i]);
+            if (a.part_post) store8(a.part_post + (size_t)first * a.hidden + c * 8, apost[i]);
+            if (a.part_pre) store8(a.part_pre + (size_t)first * a.hidden + c * 8, apre[i]);
         }
     }
 }
@@ -284,55 +385,68 @@ norm_weight_sum_kernel(const float *part_post, const float *part_pre, float *dpo
     }
 }
 
-// Threads per row: two vectors of 8 channels a thread at most.
-static int norm_threads(int hidden) {
-    if (hidden <= 512) return 32;
-    if (hidden <= 2048) return 128;
-    if (hidden <= 4096) return 256;
-    return hidden <= 8192 ? 512 : 1024;
+// Threads per row, each with up to `vecs` vectors of 8 channels.
+static int norm_threads(int hidden, int vecs) {
+    int t = 32;
+    while (t < 1024 && hidden > 8 * vecs * t) t *= 2;
+    return t;
 }
+static int rows_per_cta(int tpr) { return tpr == 32 ? kNormWarpRows : 1; }
+constexpr int kForwardVecs = 4, kBackwardVecs = 2;
 
-// CTAs of the backward: as many as are resident on 148 SMs at 64 registers a
-// thread, and no more than there are rows for.
+// CTAs of the backward: as many as are resident on 148 SMs, and no more than
+// there are rows for.
 static long long norm_backward_grid(long long rows, int hidden) {
-    const int tpr = norm_threads(hidden);
-    const int per_cta = tpr == 32 ? kNormWarpRows : 1;
-    const int threads = tpr == 32 ? 32 * kNormWarpRows : tpr;
-    const long long resident = 148ll * (1024 / threads);
+    const int tpr = norm_threads(hidden, kBackwardVecs), per_cta = rows_per_cta(tpr);
+    const long long resident = 148ll * (tpr <= 256 ? 512 / (tpr == 32 ? 256 : tpr) : 1);
     const long long want = (rows + per_cta - 1) / per_cta;
     return want < resident ? want : resident;
 }
-
+static long long norm_backward_parts(long long rows, int hidden) {
+    return norm_backward_grid(rows, hidden) * rows_per_cta(norm_threads(hidden, kBackwardVecs));
+}
 size_t residual_norm_backward_workspace(long long rows, int hidden) {
-    const int per_cta = norm_threads(hidden) == 32 ? kNormWarpRows : 1;
-    return (size_t)norm_backward_grid(rows, hidden) * per_cta * hidden * 2 * sizeof(float);
+    return (size_t)norm_backward_parts(rows, hidden) * hidden * 2 * sizeof(float);
 }
 
 template <typename T>
 static cudaError_t launch_forward(const NormArgs &a, cudaStream_t stream) {
-    const int tpr = norm_threads(a.hidden);
-    const long long grid = tpr == 32 ? (a.rows + kNormWarpRows - 1) / kNormWarpRows : a.rows;
-    const dim3 g((unsigned)grid), b(tpr == 32 ? 32 * kNormWarpRows : tpr);
+    constexpr int V = kForwardVecs;
+    const int tpr = norm_threads(a.hidden, V), per_cta = rows_per_cta(tpr);
+    const dim3 g((unsigned)((a.rows + per_cta - 1) / per_cta)), b(tpr * per_cta);
     switch (tpr) {
-        case 32: return launch_overlapped(residual_norm_kernel<T, 32>, g, b, 0, stream, a);
-        case 128: return launch_overlapped(residual_norm_kernel<T, 128>, g, b, 0, stream, a);
-        case 256: return launch_overlapped(residual_norm_kernel<T, 256>, g, b, 0, stream, a);
-        case 512: return launch_overlapped(residual_norm_kernel<T, 512>, g, b, 0, stream, a);
+        case 32: return launch_overlapped(residual_norm_kernel<T, 32, V>, g, b, 0, stream, a);
+        case 64: return launch_overlapped(residual_norm_kernel<T, 64, V>, g, b, 0, stream, a);
+        case 128: return launch_overlapped(residual_norm_kernel<T, 128, V>, g, b, 0, stream, a);
+        case 256: return launch_overlapped(residual_norm_kernel<T, 256, V>, g, b, 0, stream, a);
     }
-    return launch_overlapped(residual_norm_kernel<T, 1024>, g, b, 0, stream, a);
+    return launch_overlapped(residual_norm_kernel<T, 512, V>, g, b, 0, stream, a);
+}
+
+template <typename T, int TPR>
+static cudaError_t launch_backward_tpr(const NormArgs &a, unsigned grid, cudaStream_t stream) {
+    constexpr int V = kBackwardVecs, kThreads = TPR == 32 ? 32 * kNormWarpRows : TPR;
+    // two rows of five tensors; two CTAs of 256 threads share an SM's 227 KB
+    constexpr int kBytes = 2 * 5 * V * 8 * (int)sizeof(T) * kThreads;
+    constexpr bool kAhead = kBytes <= 220 * 1024;
+    auto kernel = residual_norm_backward_kernel<T, TPR, V, kAhead>;
+    if (kAhead) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_overlapped(kernel, dim3(grid), dim3(kThreads), kAhead ? kBytes : 0, stream, a);
 }
 
 template <typename T>
 static cudaError_t launch_backward(const NormArgs &a, unsigned grid, cudaStream_t stream) {
-    const int tpr = norm_threads(a.hidden);
-    const dim3 g(grid), b(tpr == 32 ? 32 * kNormWarpRows : tpr);
-    switch (tpr) {
-        case 32: return launch_overlapped(residual_norm_backward_kernel<T, 32>, g, b, 0, stream, a);
-        case 128: return launch_overlapped(residual_norm_backward_kernel<T, 128>, g, b, 0, stream, a);
-        case 256: return launch_overlapped(residual_norm_backward_kernel<T, 256>, g, b, 0, stream, a);
-        case 512: return launch_overlapped(residual_norm_backward_kernel<T, 512>, g, b, 0, stream, a);
+    switch (norm_threads(a.hidden, kBackwardVecs)) {
+        case 32: return launch_backward_tpr<T, 32>(a, grid, stream);
+        case 64: return launch_backward_tpr<T, 64>(a, grid, stream);
+        case 128: return launch_backward_tpr<T, 128>(a, grid, stream);
+        case 256: return launch_backward_tpr<T, 256>(a, grid, stream);
+        case 512: return launch_backward_tpr<T, 512>(a, grid, stream);
     }
-    return launch_overlapped(residual_norm_backward_kernel<T, 1024>, g, b, 0, stream, a);
+    return launch_backward_tpr<T, 1024>(a, grid, stream);
 }
 
 static NormArgs norm_args(const retnet_block_norm &p, long long rows, int hidden) {
@@ -366,7 +480,7 @@ cudaError_t launch_residual_norm_backward(const void *x, const void *y, const vo
                                           void *dy, void *dgate, float *dpost, float *dpre,
                                           void *workspace, cudaStream_t stream) {
     const long long grid = norm_backward_grid(rows, hidden);
-    const int parts = (int)grid * (norm_threads(hidden) == 32 ? kNormWarpRows : 1);
+    const int parts = (int)norm_backward_parts(rows, hidden);
     float *part_post = (float *)workspace;
     float *part_pre = part_post + (size_t)parts * hidden;
     if (rows > 0) {
