@@ -19,7 +19,8 @@
 // accumulator.  Nothing but the prepared tiles, K and V goes through shared
 // memory, all of it by bulk copies one chunk ahead.
 #include "delta.cuh"
-#include "sm100.cuh"
+#include "pairs.cuh"
+#include "sm100_chain.cuh"
 
 namespace retnet {
 namespace {

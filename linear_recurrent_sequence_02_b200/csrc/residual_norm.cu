@@ -15,6 +15,7 @@
 // shuffles and one barrier each and nothing is read twice; h is formed from
 // x, y and g again in the backward, which reads no more than a stored h would.
 #include "kernels.h"
+#include "pairs.cuh"
 
 namespace retnet {
 
