@@ -624,7 +624,7 @@ retnet_status retnet_delta_chunkwise(const void *q, const void *k, const void *v
     if (tokens > 0 && delta_tensor(shape, algo))
         RETNET_CUDA_TRY(launch_delta_tc(a, workspace, (cudaStream_t)stream));
     else
-        RETNET_CUDA_TRY(launch_delta_recurrent(a, (cudaStream_t)stream));
+        RETNET_CUDA_TRY(launch_delta_walk(a, (cudaStream_t)stream));
     return RETNET_OK;
 }
 

@@ -1,8 +1,5 @@
 // Gated delta rule, token by token in float32, and its gradient.
 //
-// One kernel walks the tokens of a (sequence, head) with the state in
-// registers (the recurrent form); it serves the decode step, the float32
-// prefill, and the two sweeps of the float32 backward:
 //   forward   y = k S, z = q S of the state before the token;
 //             x = b (v - a y);  S <- a S + k^T x;  o = scale (a z + (q.k) x)
 //             with a = e^g.  Both products read the same state, so a token
@@ -10,13 +7,18 @@
 //   reverse   D is the gradient of the state behind a token:
 //             r = k D + scale (k.q) do;  D <- a (D + scale q^T do - b k^T r).
 //             r is the gradient of x; dv = b r.
-// CTA (sequence, head, 32 columns of S) as in the retention step: 8 float4
-// column groups by 32 row lanes, the row lanes of a column reduced by
-// shuffles and then over the eight warps in shared memory.  A single token
-// is an HBM stream of 8 dk dv bytes a head; a long run is bound by the
-// latency of the chain product -> reduction -> update, token after token.
-#include <algorithm>
-
+// Three kernels hold S in registers in float32:
+//   delta_step_kernel    one token (decode): an HBM stream of 8 dk dv bytes a
+//     head.  CTA (sequence, head, 32 columns) as in the retention step: 8
+//     float4 column groups by 32 row lanes, a column's row lanes reduced by
+//     shuffles and then over the eight warps in shared memory.
+//   delta_tokens_kernel  a few tokens, with the same arithmetic in the same
+//     order, so that a run equals its single steps bit for bit.
+//   delta_walk_kernel    long runs (the float32 prefill and the two sweeps of
+//     the float32 backward), bound by the latency of the chain product ->
+//     reduction -> update from token to token: a warp owns 4 columns and all
+//     rows, so that the chain is nine shuffles and no barrier (1000 tokens of
+//     128 x 64: 650 us in slabs of 32 columns, 190 us so).
 #include "delta.cuh"
 
 namespace retnet {
@@ -70,26 +72,92 @@ __device__ __forceinline__ void reduce_row_lanes(float4 &a) {
     }
 }
 
-// v: the values (forward) or the output's gradient (reverse).
-// state_in / state_out may be the same (the recurrent form's update in place).
-// save: x (kSweepSave) or r (kSweepReverse), float32 [B, n, H, dv];
-// marks: the state before (D behind) every chunk of kDeltaChunk tokens,
-// float32 [B, H, chunks, dk, dv].
-template <typename T, int DK, DeltaSweep kSweep>
+// ---- the arithmetic of a token that the step and the run of tokens share
+// (explicit fused operations: nothing is contracted differently in the two)
+
+// q and k rows (of row krow of their tensors), q.k, the decay and the write
+// strength (of element row), by one warp.
+template <typename T, int DK>
+__device__ __forceinline__ void stage_token(const T *q, const T *k, const T *g, const T *beta,
+                                            size_t krow, size_t row, int lane, float *qs, float *ks,
+                                            float &qk, float &al, float &be) {
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < DK / 32; ++j) {
+        const float kv = to_f32(k[krow * DK + lane + 32 * j]);
+        const float qv = to_f32(q[krow * DK + lane + 32 * j]);
+        ks[lane + 32 * j] = kv;
+        qs[lane + 32 * j] = qv;
+        dot = fmaf(qv, kv, dot);
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+    if (lane == 0) {
+        qk = dot;
+        al = expf(to_f32(g[row]));
+        be = to_f32(beta[row]);
+    }
+}
+// This warp's part of y = k S and z = q S.
+template <int RPL>
+__device__ __forceinline__ void token_products(const float4 (&s)[RPL], const float *qs,
+                                               const float *ks, int rl, int lane, float4 *ry,
+                                               float4 *rz) {
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
+#pragma unroll
+    for (int i = 0; i < RPL; ++i) {
+        fma4(y, ks[rl + i * kDeltaLanes], s[i]);
+        fma4(z, qs[rl + i * kDeltaLanes], s[i]);
+    }
+    reduce_row_lanes(y);
+    reduce_row_lanes(z);
+    if (lane < kDeltaGroups) {
+        ry[lane] = y;
+        rz[lane] = z;
+    }
+}
+// x, and S <- a S + k^T x.
+template <int RPL>
+__device__ __forceinline__ float4 token_update(float4 (&s)[RPL], const float *ks, int rl,
+                                               const float4 (*red)[kDeltaGroups], int cg, float4 v,
+                                               float a, float b) {
+    float4 y = red[0][cg];
+#pragma unroll
+    for (int w = 1; w < kDeltaThreads / 32; ++w) add4(y, red[w][cg]);
+    float4 x = v;
+    fma4(x, -a, y);
+    x = scale4(b, x);
+#pragma unroll
+    for (int i = 0; i < RPL; ++i) {
+        s[i] = scale4(a, s[i]);
+        fma4(s[i], ks[rl + i * kDeltaLanes], x);
+    }
+    return x;
+}
+__device__ __forceinline__ float4 token_output(const float4 (*red)[kDeltaGroups], int cg, float4 x,
+                                               float a, float qk, float scale) {
+    float4 z = red[0][cg];
+#pragma unroll
+    for (int w = 1; w < kDeltaThreads / 32; ++w) add4(z, red[w][cg]);
+    float4 o = scale4(a, z);
+    fma4(o, qk, x);
+    return scale4(scale, o);
+}
+
+// v [batch, tokens, heads, dv]; the state is updated in place.
+template <typename T, int DK>
 __global__ void __launch_bounds__(kDeltaThreads)
 delta_tokens_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
                     const T *__restrict__ g, const T *__restrict__ beta,
-                    const int *__restrict__ lengths, const float *state_in, float *state_out,
-                    T *__restrict__ out, float *__restrict__ save, float *__restrict__ marks,
+                    const int *__restrict__ lengths, float *state, T *__restrict__ out,
                     float scale, int heads, int key_heads, int tokens, int dv) {
     constexpr int RPL = DK / kDeltaLanes;            // rows per thread: 2, 4 or 8
     const int slabs = dv / kDeltaCols;
     const int bh = blockIdx.x / slabs;
     const int b = bh / heads, h = bh % heads;
-    const int col0 = (blockIdx.x % slabs) * kDeltaCols;
     const int cg = threadIdx.x % kDeltaGroups, rl = threadIdx.x / kDeltaGroups;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int col = col0 + cg * 4;
+    const int col = (blockIdx.x % slabs) * kDeltaCols + cg * 4;
 
     __shared__ float qs[kDeltaStage][DK], ks[kDeltaStage][DK];
     __shared__ float qk[kDeltaStage], al[kDeltaStage], be[kDeltaStage];
@@ -97,132 +165,224 @@ delta_tokens_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *_
 
     grid_dependency_wait();
     const int n = delta_tokens_of(lengths, b, tokens);
-    const size_t sbase = (size_t)bh * DK * dv + col;
+    if (n == 0) return;                              // the whole CTA
+    float *S = state + (size_t)bh * DK * dv + col;
     float4 s[RPL];
 #pragma unroll
-    for (int i = 0; i < RPL; ++i)
-        s[i] = state_in ? load_f4(state_in + sbase + (size_t)(rl + i * kDeltaLanes) * dv)
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < RPL; ++i) s[i] = load_f4(S + (size_t)(rl + i * kDeltaLanes) * dv);
 
     const size_t row0 = (size_t)b * tokens;
     const int kh = h / (heads / key_heads);
-    const int nc = (tokens + kDeltaChunk - 1) / kDeltaChunk;
     int flip = 0;
     for (int g0 = 0; g0 < n; g0 += kDeltaStage) {
         const int cnt = min(kDeltaStage, n - g0);
-        // stage slot u holds the u-th token of the walk: g0 + u, or n - 1 - (g0 + u)
         float4 vv[kDeltaStage];
 #pragma unroll
         for (int u = 0; u < kDeltaStage; ++u)
-            if (u < cnt) {
-                const int t = kSweep == kSweepReverse ? n - 1 - (g0 + u) : g0 + u;
-                vv[u] = load_f4(v + ((row0 + t) * heads + h) * (size_t)dv + col);
-            }
-        {   // warp u stages token u: q and k rows, q.k, the decay and the write strength
-            const int u = warp;
-            if (u < cnt) {
-                const int t = kSweep == kSweepReverse ? n - 1 - (g0 + u) : g0 + u;
-                const size_t o = ((row0 + t) * key_heads + kh) * (size_t)DK;
-                float dot = 0.f;
-#pragma unroll
-                for (int j = 0; j < DK / 32; ++j) {
-                    const float kv = to_f32(k[o + lane + 32 * j]);
-                    ks[u][lane + 32 * j] = kv;
-                    if (kSweep != kSweepSave) {
-                        const float qv = to_f32(q[o + lane + 32 * j]);
-                        qs[u][lane + 32 * j] = qv;
-                        dot = fmaf(qv, kv, dot);
-                    }
-                }
-#pragma unroll
-                for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-                if (lane == 0) {
-                    qk[u] = dot;
-                    al[u] = expf(to_f32(g[(row0 + t) * heads + h]));
-                    const float bt = to_f32(beta[(row0 + t) * heads + h]);
-                    be[u] = kSweep == kSweepSave ? nonzero_beta(bt) : bt;
-                }
-            }
-        }
+            if (u < cnt) vv[u] = load_f4(v + ((row0 + g0 + u) * heads + h) * (size_t)dv + col);
+        if (warp < cnt)                              // warp u stages token u
+            stage_token<T, DK>(q, k, g, beta, (row0 + g0 + warp) * key_heads + kh,
+                               (row0 + g0 + warp) * heads + h, lane, qs[warp], ks[warp], qk[warp],
+                               al[warp], be[warp]);
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < kDeltaStage; ++u) {
             if (u < cnt) {
-                const int t = kSweep == kSweepReverse ? n - 1 - (g0 + u) : g0 + u;
-                if (kSweep != kSweepForward) {
-                    // a chunk's first token (its last, walking back)
-                    const bool mark = kSweep == kSweepSave
-                                          ? t % kDeltaChunk == 0
-                                          : t == n - 1 || t % kDeltaChunk == kDeltaChunk - 1;
-                    if (mark) {
-                        float *m = marks + ((size_t)bh * nc + t / kDeltaChunk) * DK * dv + col;
-#pragma unroll
-                        for (int i = 0; i < RPL; ++i)
-                            store_f4(m + (size_t)(rl + i * kDeltaLanes) * dv, s[i]);
-                    }
-                }
-                float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
-#pragma unroll
-                for (int i = 0; i < RPL; ++i) {
-                    fma4(y, ks[u][rl + i * kDeltaLanes], s[i]);
-                    if (kSweep == kSweepForward) fma4(z, qs[u][rl + i * kDeltaLanes], s[i]);
-                }
-                reduce_row_lanes(y);
-                if (kSweep == kSweepForward) reduce_row_lanes(z);
-                if (lane < kDeltaGroups) {
-                    red[flip][0][warp][lane] = y;
-                    if (kSweep == kSweepForward) red[flip][1][warp][lane] = z;
-                }
+                token_products<RPL>(s, qs[u], ks[u], rl, lane, red[flip][0][warp], red[flip][1][warp]);
                 __syncthreads();
-                y = red[flip][0][0][cg];
-#pragma unroll
-                for (int w = 1; w < kDeltaThreads / 32; ++w) add4(y, red[flip][0][w][cg]);
-                const float a = al[u], bt = be[u];
-                float4 x;
-                if (kSweep == kSweepReverse) {
-                    const float c = scale * qk[u];
-                    x = y;
-                    fma4(x, c, vv[u]);                            // r
-                    const float4 xb = scale4(-bt, x);
-#pragma unroll
-                    for (int i = 0; i < RPL; ++i) {
-                        const int rr = rl + i * kDeltaLanes;
-                        fma4(s[i], scale * qs[u][rr], vv[u]);
-                        fma4(s[i], ks[u][rr], xb);
-                        s[i] = scale4(a, s[i]);
-                    }
-                } else {
-                    x = vv[u];
-                    fma4(x, -a, y);
-                    x = scale4(bt, x);
-#pragma unroll
-                    for (int i = 0; i < RPL; ++i) {
-                        s[i] = scale4(a, s[i]);
-                        fma4(s[i], ks[u][rl + i * kDeltaLanes], x);
-                    }
-                }
-                const size_t vo = ((row0 + t) * heads + h) * (size_t)dv + col;
-                if (kSweep == kSweepForward) {
-                    if (warp == u % (kDeltaThreads / 32) && lane < kDeltaGroups) {
-                        z = red[flip][1][0][cg];
-#pragma unroll
-                        for (int w = 1; w < kDeltaThreads / 32; ++w) add4(z, red[flip][1][w][cg]);
-                        float4 o = scale4(a, z);
-                        fma4(o, qk[u], x);
-                        store_f4(out + vo, scale4(scale, o));
-                    }
-                } else if (rl == 0) {
-                    store_f4(save + vo, x);
-                }
+                const float a = al[u];
+                const float4 x = token_update<RPL>(s, ks[u], rl, red[flip][0], cg, vv[u], a, be[u]);
+                if (warp == u && lane < kDeltaGroups)
+                    store_f4(out + ((row0 + g0 + u) * heads + h) * (size_t)dv + col,
+                             token_output(red[flip][1], cg, x, a, qk[u], scale));
                 flip ^= 1;
             }
         }
-        __syncthreads();               // the stage is rewritten
+        __syncthreads();                             // the stage is rewritten
     }
-    if (kSweep == kSweepForward && state_out && (n > 0 || state_out != state_in)) {
 #pragma unroll
-        for (int i = 0; i < RPL; ++i)
-            store_f4(state_out + sbase + (size_t)(rl + i * kDeltaLanes) * dv, s[i]);
+    for (int i = 0; i < RPL; ++i) store_f4(S + (size_t)(rl + i * kDeltaLanes) * dv, s[i]);
+}
+
+// One token; q, k [batch, key_heads, DK], v, out [batch, heads, dv].  64
+// registers a thread keep four CTAs and 4 * 128 DK bytes of state in flight
+// on an SM.
+template <typename T, int DK>
+__global__ void __launch_bounds__(kDeltaThreads, 4)
+delta_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                  const T *__restrict__ g, const T *__restrict__ beta,
+                  const int *__restrict__ lengths, float *state, T *__restrict__ out, float scale,
+                  int heads, int key_heads, int dv) {
+    constexpr int RPL = DK / kDeltaLanes;
+    const int slabs = dv / kDeltaCols;
+    const int bh = blockIdx.x / slabs;
+    const int b = bh / heads, h = bh % heads;
+    const int cg = threadIdx.x % kDeltaGroups, rl = threadIdx.x / kDeltaGroups;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int col = (blockIdx.x % slabs) * kDeltaCols + cg * 4;
+
+    __shared__ float qs[DK], ks[DK], qk, al, be;
+    __shared__ float4 red[2][kDeltaThreads / 32][kDeltaGroups];
+
+    grid_dependency_wait();
+    if (lengths && lengths[b] < 1) return;           // the whole CTA
+    float *S = state + (size_t)bh * DK * dv + col;
+    float4 s[RPL];
+#pragma unroll
+    for (int i = 0; i < RPL; ++i) s[i] = load_f4(S + (size_t)(rl + i * kDeltaLanes) * dv);
+    const float4 vv = load_f4(v + (size_t)bh * dv + col);
+    if (warp == 0)
+        stage_token<T, DK>(q, k, g, beta, (size_t)b * key_heads + h / (heads / key_heads), bh, lane,
+                           qs, ks, qk, al, be);
+    __syncthreads();
+    token_products<RPL>(s, qs, ks, rl, lane, red[0][warp], red[1][warp]);
+    __syncthreads();
+    const float a = al;
+    const float4 x = token_update<RPL>(s, ks, rl, red[0], cg, vv, a, be);
+#pragma unroll
+    for (int i = 0; i < RPL; ++i) store_f4(S + (size_t)(rl + i * kDeltaLanes) * dv, s[i]);
+    if (warp == 0 && lane < kDeltaGroups)
+        store_f4(out + (size_t)bh * dv + col, token_output(red[1], cg, x, a, qk, scale));
+}
+
+// v: the values (forward) or the output's gradient (reverse).  state_in and
+// state_out may be missing and may be the same.
+// save: x (kSweepSave) or r (kSweepReverse), float32 [B, n, H, dv];
+// marks: the state before (D behind) every chunk of kDeltaChunk tokens,
+// float32 [B, H, chunks, dk, dv].
+constexpr int kWalkWarps = 4, kWalkCols = 4;         // columns per warp
+constexpr int kWalkAhead = 4;                        // tokens loaded ahead
+
+template <typename T, int DK, DeltaSweep kSweep>
+__global__ void __launch_bounds__(32 * kWalkWarps)
+delta_walk_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                  const T *__restrict__ g, const T *__restrict__ beta,
+                  const int *__restrict__ lengths, const float *state_in, float *state_out,
+                  T *__restrict__ out, float *__restrict__ save, float *__restrict__ marks,
+                  float scale, int heads, int key_heads, int tokens, int dv) {
+    constexpr int RPL = DK / 32;                     // rows lane, lane + 32, ...
+    constexpr bool kFwd = kSweep == kSweepForward, kRev = kSweep == kSweepReverse;
+    const int slabs = dv / (kWalkWarps * kWalkCols);
+    const int bh = blockIdx.x / slabs;
+    const int b = bh / heads, h = bh % heads, kh = h / (heads / key_heads);
+    const int lane = threadIdx.x % 32;
+    const int col = (blockIdx.x % slabs) * (kWalkWarps * kWalkCols) + (threadIdx.x / 32) * kWalkCols;
+
+    grid_dependency_wait();
+    const int n = delta_tokens_of(lengths, b, tokens);
+    const int nc = (tokens + kDeltaChunk - 1) / kDeltaChunk;
+    const size_t row0 = (size_t)b * tokens, sbase = (size_t)bh * DK * dv + col;
+    float4 s[RPL];
+#pragma unroll
+    for (int i = 0; i < RPL; ++i)
+        s[i] = state_in ? load_f4(state_in + sbase + (size_t)(lane + 32 * i) * dv)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+
+    struct Token {
+        float k[RPL], q[RPL], g, b, qk;
+        float4 v;
+    } ahead[kWalkAhead];
+    auto load = [&](Token &w, int step) {            // the step-th token of the walk
+        if (step >= n) return;
+        const size_t t = row0 + (kRev ? n - 1 - step : step);
+        const size_t o = (t * key_heads + kh) * (size_t)DK + lane;
+#pragma unroll
+        for (int i = 0; i < RPL; ++i) {
+            w.k[i] = to_f32(k[o + 32 * i]);
+            w.q[i] = kSweep == kSweepSave ? 0.f : to_f32(q[o + 32 * i]);
+        }
+        w.v = load_f4(v + (t * heads + h) * (size_t)dv + col);
+        w.g = to_f32(g[t * heads + h]);
+        w.b = to_f32(beta[t * heads + h]);
+    };
+    auto dot = [&](Token &w) {                       // q.k, off the chain
+        if (kSweep == kSweepSave) return;
+        float d = 0.f;
+#pragma unroll
+        for (int i = 0; i < RPL; ++i) d = fmaf(w.q[i], w.k[i], d);
+#pragma unroll
+        for (int m = 16; m; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+        w.qk = d;
+    };
+#pragma unroll
+    for (int u = 0; u < kWalkAhead; ++u) load(ahead[u], u);
+    for (int s0 = 0; s0 < n; s0 += kWalkAhead) {
+#pragma unroll
+        for (int u = 0; u < kWalkAhead; ++u) {
+            const int step = s0 + u;
+            if (step >= n) break;
+            Token w = ahead[u];
+            load(ahead[u], step + kWalkAhead);
+            dot(w);
+            const int t = kRev ? n - 1 - step : step;
+            if (!kFwd && (kRev ? step == 0 || t % kDeltaChunk == kDeltaChunk - 1 : t % kDeltaChunk == 0)) {
+                float *m = marks + ((size_t)bh * nc + t / kDeltaChunk) * DK * dv + col;
+#pragma unroll
+                for (int i = 0; i < RPL; ++i) store_f4(m + (size_t)(lane + 32 * i) * dv, s[i]);
+            }
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
+#pragma unroll
+            for (int i = 0; i < RPL; ++i) {
+                fma4(y, w.k[i], s[i]);
+                if (kFwd) fma4(z, w.q[i], s[i]);
+            }
+            // sums over the lanes: a lane gives away the half of the values
+            // that it does not keep, so that it ends with one
+            float e0, e1;
+            if (kFwd) {                              // lanes 0-15 y, 16-31 z
+                const bool up = lane & 16;
+                y.x = (up ? z.x : y.x) + __shfl_xor_sync(0xffffffffu, up ? y.x : z.x, 16);
+                y.y = (up ? z.y : y.y) + __shfl_xor_sync(0xffffffffu, up ? y.y : z.y, 16);
+                y.z = (up ? z.z : y.z) + __shfl_xor_sync(0xffffffffu, up ? y.z : z.z, 16);
+                y.w = (up ? z.w : y.w) + __shfl_xor_sync(0xffffffffu, up ? y.w : z.w, 16);
+            }
+            const bool far = lane & 8, odd = lane & 4;
+            e0 = (far ? y.z : y.x) + __shfl_xor_sync(0xffffffffu, far ? y.x : y.z, 8);
+            e1 = (far ? y.w : y.y) + __shfl_xor_sync(0xffffffffu, far ? y.y : y.w, 8);
+            e0 = (odd ? e1 : e0) + __shfl_xor_sync(0xffffffffu, odd ? e0 : e1, 4);
+            if (!kFwd) e0 += __shfl_xor_sync(0xffffffffu, e0, 16);
+            e0 += __shfl_xor_sync(0xffffffffu, e0, 2);
+            e0 += __shfl_xor_sync(0xffffffffu, e0, 1);
+            y.x = __shfl_sync(0xffffffffu, e0, 0);
+            y.y = __shfl_sync(0xffffffffu, e0, 4);
+            y.z = __shfl_sync(0xffffffffu, e0, 8);
+            y.w = __shfl_sync(0xffffffffu, e0, 12);
+            const float a = expf(w.g), bt = kSweep == kSweepSave ? nonzero_beta(w.b) : w.b;
+            float4 x;
+            if (kRev) {
+                x = y;
+                fma4(x, scale * w.qk, w.v);                        // r
+                const float4 xb = scale4(-bt, x);
+#pragma unroll
+                for (int i = 0; i < RPL; ++i) {
+                    fma4(s[i], scale * w.q[i], w.v);
+                    fma4(s[i], w.k[i], xb);
+                    s[i] = scale4(a, s[i]);
+                }
+            } else {
+                x = w.v;
+                fma4(x, -a, y);
+                x = scale4(bt, x);
+#pragma unroll
+                for (int i = 0; i < RPL; ++i) {
+                    s[i] = scale4(a, s[i]);
+                    fma4(s[i], w.k[i], x);
+                }
+            }
+            const size_t vo = ((row0 + t) * heads + h) * (size_t)dv + col;
+            if (kFwd) {
+                // lanes 16, 20, 24, 28 hold z of columns 0 .. 3
+                const float xe = far ? (odd ? x.w : x.z) : (odd ? x.y : x.x);
+                if ((lane & 19) == 16)
+                    out[vo + (lane - 16) / 4] = from_f32<T>(scale * fmaf(w.qk, xe, a * e0));
+            } else if (lane == 0) {
+                store_f4(save + vo, x);
+            }
+        }
+    }
+    if (kFwd && state_out && (n > 0 || state_out != state_in)) {
+#pragma unroll
+        for (int i = 0; i < RPL; ++i) store_f4(state_out + sbase + (size_t)(lane + 32 * i) * dv, s[i]);
     }
 }
 
@@ -552,38 +712,57 @@ delta_share_kernel(const float *__restrict__ dq_wide, const float *__restrict__ 
 
 // ------------------------------------------------------------------ launches
 template <typename T, int DK, DeltaSweep kSweep>
-static cudaError_t launch_sweep(const DeltaArgs &a, const void *v, const float *state_in,
-                                float *state_out, float *save, float *marks,
-                                cudaStream_t stream) {
-    const size_t grid = (size_t)a.batch * a.heads * (a.dv / kDeltaCols);
-    return launch_overlapped(delta_tokens_kernel<T, DK, kSweep>, dim3((unsigned)grid),
-                             dim3(kDeltaThreads), 0, stream, (const T *)a.q, (const T *)a.k,
-                             (const T *)v, (const T *)a.g, (const T *)a.beta, a.lengths, state_in,
-                             state_out, (T *)a.out, save, marks, a.scale, a.heads, a.key_heads,
-                             a.seqlen, a.dv);
+static cudaError_t launch_walk(const DeltaArgs &a, const void *v, float *save, float *marks,
+                               cudaStream_t stream) {
+    const size_t grid = (size_t)a.batch * a.heads * (a.dv / (kWalkWarps * kWalkCols));
+    return launch_overlapped(delta_walk_kernel<T, DK, kSweep>, dim3((unsigned)grid),
+                             dim3(32 * kWalkWarps), 0, stream, (const T *)a.q, (const T *)a.k,
+                             (const T *)v, (const T *)a.g, (const T *)a.beta, a.lengths,
+                             a.state_in, a.state_out, (T *)a.out, save, marks, a.scale, a.heads,
+                             a.key_heads, a.seqlen, a.dv);
 }
+template <typename T, int DK>
+static cudaError_t launch_tokens(const DeltaArgs &a, cudaStream_t stream) {
+    const dim3 grid((unsigned)((size_t)a.batch * a.heads * (a.dv / kDeltaCols)));
+    if (a.seqlen == 1)
+        return launch_overlapped(delta_step_kernel<T, DK>, grid, dim3(kDeltaThreads), 0, stream,
+                                 (const T *)a.q, (const T *)a.k, (const T *)a.v, (const T *)a.g,
+                                 (const T *)a.beta, a.lengths, a.state_out, (T *)a.out, a.scale,
+                                 a.heads, a.key_heads, a.dv);
+    return launch_overlapped(delta_tokens_kernel<T, DK>, grid, dim3(kDeltaThreads), 0, stream,
+                             (const T *)a.q, (const T *)a.k, (const T *)a.v, (const T *)a.g,
+                             (const T *)a.beta, a.lengths, a.state_out, (T *)a.out, a.scale,
+                             a.heads, a.key_heads, a.seqlen, a.dv);
+}
+
+#define RETNET_DELTA_CASES(CALL, ...)                                            \
+    if (a.dtype == RETNET_BF16) switch (a.dk) {                                  \
+            case 64: return CALL<__nv_bfloat16, 64 __VA_ARGS__;                  \
+            case 128: return CALL<__nv_bfloat16, 128 __VA_ARGS__;                \
+            default: return CALL<__nv_bfloat16, 256 __VA_ARGS__;                 \
+        }                                                                        \
+    switch (a.dk) {                                                              \
+        case 64: return CALL<float, 64 __VA_ARGS__;                              \
+        case 128: return CALL<float, 128 __VA_ARGS__;                            \
+        default: return CALL<float, 256 __VA_ARGS__;                             \
+    }
+
 template <DeltaSweep kSweep>
-static cudaError_t launch_sweep(const char *name, const DeltaArgs &a, const void *v,
-                                const float *state_in, float *state_out, float *save, float *marks,
-                                cudaStream_t stream) {
+static cudaError_t launch_sweep(const char *name, const DeltaArgs &a, const void *v, float *save,
+                                float *marks, cudaStream_t stream) {
     KernelTimer timer(name, stream);
     count_launch();
-    const bool bf = a.dtype == RETNET_BF16;
-#define RETNET_SWEEP(DK)                                                                     \
-    return bf ? launch_sweep<__nv_bfloat16, DK, kSweep>(a, v, state_in, state_out, save,     \
-                                                        marks, stream)                       \
-              : launch_sweep<float, DK, kSweep>(a, v, state_in, state_out, save, marks, stream)
-    switch (a.dk) {
-        case 64: RETNET_SWEEP(64);
-        case 128: RETNET_SWEEP(128);
-    }
-    RETNET_SWEEP(256);
-#undef RETNET_SWEEP
+    RETNET_DELTA_CASES(launch_walk, , kSweep>(a, v, save, marks, stream))
 }
 
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, cudaStream_t stream) {
-    return launch_sweep<kSweepForward>("delta_tokens", a, a.v, a.state_in, a.state_out, nullptr,
-                                       nullptr, stream);
+    KernelTimer timer(a.seqlen == 1 ? "delta_step" : "delta_tokens", stream);
+    count_launch();
+    RETNET_DELTA_CASES(launch_tokens, >(a, stream))
+}
+
+cudaError_t launch_delta_walk(const DeltaArgs &a, cudaStream_t stream) {
+    return launch_sweep<kSweepForward>("delta_walk", a, a.v, nullptr, nullptr, stream);
 }
 
 static size_t up1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
@@ -655,11 +834,11 @@ cudaError_t launch_delta_share(const DeltaArgs &a, const float *dq_wide, const f
 cudaError_t launch_delta_backward_simt(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
     const DeltaGradLayout l = grad_layout(a.batch, a.heads, a.key_heads, a.seqlen, a.dk, a.dv);
     char *ws = (char *)workspace;
-    cudaError_t e = launch_sweep<kSweepSave>("delta_forward_sweep", a, a.v, nullptr, nullptr,
-                                             (float *)(ws + l.x), (float *)(ws + l.s), stream);
+    cudaError_t e = launch_sweep<kSweepSave>("delta_forward_sweep", a, a.v, (float *)(ws + l.x),
+                                             (float *)(ws + l.s), stream);
     if (e != cudaSuccess) return e;
-    e = launch_sweep<kSweepReverse>("delta_reverse_sweep", a, a.d_out, nullptr, nullptr,
-                                    (float *)(ws + l.r), (float *)(ws + l.d), stream);
+    e = launch_sweep<kSweepReverse>("delta_reverse_sweep", a, a.d_out, (float *)(ws + l.r),
+                                    (float *)(ws + l.d), stream);
     if (e != cudaSuccess) return e;
     return a.dtype == RETNET_BF16 ? launch_grad<__nv_bfloat16>(a, l, ws, stream)
                                   : launch_grad<float>(a, l, ws, stream);

@@ -148,8 +148,10 @@ struct DeltaArgs {
     int batch, heads, key_heads, seqlen, dk, dv;
     retnet_dtype dtype;
 };
-// Token by token, any supported shape: the recurrent form and the float32 prefill.
+// Token by token, any supported shape: the recurrent form, state_in and
+// state_out the same and seqlen > 0; and the prefill.
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, cudaStream_t stream);
+cudaError_t launch_delta_walk(const DeltaArgs &a, cudaStream_t stream);
 size_t delta_backward_simt_workspace(int batch, int heads, int key_heads, int seqlen, int dk,
                                      int dv);
 cudaError_t launch_delta_backward_simt(const DeltaArgs &a, void *workspace, cudaStream_t stream);
