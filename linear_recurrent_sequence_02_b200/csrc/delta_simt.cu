@@ -75,23 +75,29 @@ __device__ __forceinline__ void reduce_row_lanes(float4 &a) {
 // ---- the arithmetic of a token that the step and the run of tokens share
 // (explicit fused operations: nothing is contracted differently in the two)
 
+// q.k by one warp.
+template <int DK, typename R>
+__device__ __forceinline__ float token_dot(const R *q, const R *k, int lane) {
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < DK / 32; ++j) dot = fmaf(to_f32(q[lane + 32 * j]), to_f32(k[lane + 32 * j]), dot);
+#pragma unroll
+    for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+    return dot;
+}
 // q and k rows (of row krow of their tensors), q.k, the decay and the write
 // strength (of element row), by one warp.
 template <typename T, int DK>
 __device__ __forceinline__ void stage_token(const T *q, const T *k, const T *g, const T *beta,
                                             size_t krow, size_t row, int lane, float *qs, float *ks,
                                             float &qk, float &al, float &be) {
-    float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < DK / 32; ++j) {
-        const float kv = to_f32(k[krow * DK + lane + 32 * j]);
-        const float qv = to_f32(q[krow * DK + lane + 32 * j]);
-        ks[lane + 32 * j] = kv;
-        qs[lane + 32 * j] = qv;
-        dot = fmaf(qv, kv, dot);
+        ks[lane + 32 * j] = to_f32(k[krow * DK + lane + 32 * j]);
+        qs[lane + 32 * j] = to_f32(q[krow * DK + lane + 32 * j]);
     }
-#pragma unroll
-    for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+    __syncwarp();
+    const float dot = token_dot<DK>(qs, ks, lane);
     if (lane == 0) {
         qk = dot;
         al = expf(to_f32(g[row]));
@@ -99,15 +105,14 @@ __device__ __forceinline__ void stage_token(const T *q, const T *k, const T *g, 
     }
 }
 // This warp's part of y = k S and z = q S.
-template <int RPL>
-__device__ __forceinline__ void token_products(const float4 (&s)[RPL], const float *qs,
-                                               const float *ks, int rl, int lane, float4 *ry,
-                                               float4 *rz) {
+template <int RPL, typename R>
+__device__ __forceinline__ void token_products(const float4 (&s)[RPL], const R *qs, const R *ks,
+                                               int rl, int lane, float4 *ry, float4 *rz) {
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
 #pragma unroll
     for (int i = 0; i < RPL; ++i) {
-        fma4(y, ks[rl + i * kDeltaLanes], s[i]);
-        fma4(z, qs[rl + i * kDeltaLanes], s[i]);
+        fma4(y, to_f32(ks[rl + i * kDeltaLanes]), s[i]);
+        fma4(z, to_f32(qs[rl + i * kDeltaLanes]), s[i]);
     }
     reduce_row_lanes(y);
     reduce_row_lanes(z);
@@ -117,8 +122,8 @@ __device__ __forceinline__ void token_products(const float4 (&s)[RPL], const flo
     }
 }
 // x, and S <- a S + k^T x.
-template <int RPL>
-__device__ __forceinline__ float4 token_update(float4 (&s)[RPL], const float *ks, int rl,
+template <int RPL, typename R>
+__device__ __forceinline__ float4 token_update(float4 (&s)[RPL], const R *ks, int rl,
                                                const float4 (*red)[kDeltaGroups], int cg, float4 v,
                                                float a, float b) {
     float4 y = red[0][cg];
@@ -130,7 +135,7 @@ __device__ __forceinline__ float4 token_update(float4 (&s)[RPL], const float *ks
 #pragma unroll
     for (int i = 0; i < RPL; ++i) {
         s[i] = scale4(a, s[i]);
-        fma4(s[i], ks[rl + i * kDeltaLanes], x);
+        fma4(s[i], to_f32(ks[rl + i * kDeltaLanes]), x);
     }
     return x;
 }
@@ -204,45 +209,113 @@ delta_tokens_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *_
     for (int i = 0; i < RPL; ++i) store_f4(S + (size_t)(rl + i * kDeltaLanes) * dv, s[i]);
 }
 
-// One token; q, k [batch, key_heads, DK], v, out [batch, heads, dv].  64
-// registers a thread keep four CTAs and 4 * 128 DK bytes of state in flight
-// on an SM.
+// One token; q, k [batch, key_heads, DK], v, out [batch, heads, dv].
+// Persistent: a CTA takes every gridDim.x-th (sequence, head, 32 columns) and
+// copies the states, q, k and v of the next ones to shared memory while it
+// works on this one (a CTA for each, its loads waited for, spent two thirds
+// of its time at barriers behind them: 128 sequences, 16 heads of 256, 258 us
+// against 196 us so).  The state's slots are a thread's own.
 template <typename T, int DK>
-__global__ void __launch_bounds__(kDeltaThreads, 4)
+struct DeltaStepSmem {
+    static constexpr int RPL = DK / kDeltaLanes;
+    struct Stage {
+        float4 s[RPL][kDeltaThreads];
+        T q[DK], k[DK], v[kDeltaCols];
+    };
+    static constexpr int kStages = DK == 256 ? 2 : 4;                // three CTAs share an SM's 227 KB
+    Stage stage[kStages];
+    float4 red[2][kDeltaThreads / 32][kDeltaGroups];
+    float qk;
+};
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+template <typename T, int DK>
+__global__ void __launch_bounds__(kDeltaThreads, 3)
 delta_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
                   const T *__restrict__ g, const T *__restrict__ beta,
                   const int *__restrict__ lengths, float *state, T *__restrict__ out, float scale,
-                  int heads, int key_heads, int dv) {
-    constexpr int RPL = DK / kDeltaLanes;
-    const int slabs = dv / kDeltaCols;
-    const int bh = blockIdx.x / slabs;
-    const int b = bh / heads, h = bh % heads;
+                  int heads, int key_heads, int dv, int items) {
+    using Smem = DeltaStepSmem<T, DK>;
+    constexpr int RPL = Smem::RPL, S = Smem::kStages;
+    constexpr int kRowCopies = DK * (int)sizeof(T) / 16;             // of a q or k row
+    constexpr int kVCopies = kDeltaCols * (int)sizeof(T) / 16;
+    static_assert(128 + kRowCopies + kVCopies <= kDeltaThreads, "threads for the copies");
+    extern __shared__ __align__(16) char raw[];
+    Smem &m = *reinterpret_cast<Smem *>(raw);
+    const int slabs = dv / kDeltaCols, group = heads / key_heads;
     const int cg = threadIdx.x % kDeltaGroups, rl = threadIdx.x / kDeltaGroups;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int col = (blockIdx.x % slabs) * kDeltaCols + cg * 4;
-
-    __shared__ float qs[DK], ks[DK], qk, al, be;
-    __shared__ float4 red[2][kDeltaThreads / 32][kDeltaGroups];
 
     grid_dependency_wait();
-    if (lengths && lengths[b] < 1) return;           // the whole CTA
-    float *S = state + (size_t)bh * DK * dv + col;
-    float4 s[RPL];
+    auto place = [&](int item, int &bh, int &col) {
+        bh = item / slabs;
+        col = (item % slabs) * kDeltaCols + cg * 4;
+    };
+    auto fetch = [&](int item, typename Smem::Stage &st) {
+        if (item < items) {
+            int bh, col;
+            place(item, bh, col);
+            const float *src = state + (size_t)bh * DK * dv + col;
 #pragma unroll
-    for (int i = 0; i < RPL; ++i) s[i] = load_f4(S + (size_t)(rl + i * kDeltaLanes) * dv);
-    const float4 vv = load_f4(v + (size_t)bh * dv + col);
-    if (warp == 0)
-        stage_token<T, DK>(q, k, g, beta, (size_t)b * key_heads + h / (heads / key_heads), bh, lane,
-                           qs, ks, qk, al, be);
-    __syncthreads();
-    token_products<RPL>(s, qs, ks, rl, lane, red[0][warp], red[1][warp]);
-    __syncthreads();
-    const float a = al;
-    const float4 x = token_update<RPL>(s, ks, rl, red[0], cg, vv, a, be);
+            for (int i = 0; i < RPL; ++i)
+                copy16(&st.s[i][threadIdx.x], src + (size_t)(rl + i * kDeltaLanes) * dv);
+            const size_t row = (size_t)(bh / heads) * key_heads + (bh % heads) / group;
+            if (threadIdx.x < kRowCopies)
+                copy16((char *)st.q + 16 * threadIdx.x, (const char *)(q + row * DK) + 16 * threadIdx.x);
+            else if (threadIdx.x - 128 < kRowCopies && threadIdx.x >= 128)
+                copy16((char *)st.k + 16 * (threadIdx.x - 128), (const char *)(k + row * DK) + 16 * (threadIdx.x - 128));
+            else if (threadIdx.x >= kDeltaThreads - kVCopies) {
+                const int c = threadIdx.x - (kDeltaThreads - kVCopies);
+                copy16((char *)st.v + 16 * c, (const char *)(v + (size_t)bh * dv + col - cg * 4) + 16 * c);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // decay, write strength and whether the sequence goes on, one item ahead
+    float gn = 0.f, bn = 0.f;
+    bool on = true;
+    auto gates = [&](int item) {
+        if (item >= items) return;
+        const int bh = item / slabs;
+        gn = to_f32(g[bh]);
+        bn = to_f32(beta[bh]);
+        on = !lengths || lengths[bh / heads] > 0;
+    };
 #pragma unroll
-    for (int i = 0; i < RPL; ++i) store_f4(S + (size_t)(rl + i * kDeltaLanes) * dv, s[i]);
-    if (warp == 0 && lane < kDeltaGroups)
-        store_f4(out + (size_t)bh * dv + col, token_output(red[1], cg, x, a, qk, scale));
+    for (int u = 0; u < S - 1; ++u) fetch(blockIdx.x + u * gridDim.x, m.stage[u]);
+    gates(blockIdx.x);
+    int slot = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        __syncthreads();                             // q, k of all threads; the last slot is free
+        fetch(item + (S - 1) * gridDim.x, m.stage[(slot + S - 1) % S]);
+        typename Smem::Stage &st = m.stage[slot];
+        slot = (slot + 1) % S;
+        const float a = expf(gn), bt = bn;
+        const bool live = on;
+        gates(item + gridDim.x);
+        if (!live) continue;                         // the whole CTA
+        int bh, col;
+        place(item, bh, col);
+        float4 s[RPL];
+#pragma unroll
+        for (int i = 0; i < RPL; ++i) s[i] = st.s[i][threadIdx.x];
+        token_products<RPL>(s, st.q, st.k, rl, lane, m.red[0][warp], m.red[1][warp]);
+        if (warp == 0) {
+            const float dot = token_dot<DK>(st.q, st.k, lane);
+            if (lane == 0) m.qk = dot;
+        }
+        __syncthreads();
+        const float4 x = token_update<RPL>(s, st.k, rl, m.red[0], cg,
+                                           load_f4(&st.v[4 * cg]), a, bt);
+        float *dst = state + (size_t)bh * DK * dv + col;
+#pragma unroll
+        for (int i = 0; i < RPL; ++i) store_f4(dst + (size_t)(rl + i * kDeltaLanes) * dv, s[i]);
+        if (warp == 0 && lane < kDeltaGroups)
+            store_f4(out + (size_t)bh * dv + col, token_output(m.red[1], cg, x, a, m.qk, scale));
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // v: the values (forward) or the output's gradient (reverse).  state_in and
@@ -724,11 +797,18 @@ static cudaError_t launch_walk(const DeltaArgs &a, const void *v, float *save, f
 template <typename T, int DK>
 static cudaError_t launch_tokens(const DeltaArgs &a, cudaStream_t stream) {
     const dim3 grid((unsigned)((size_t)a.batch * a.heads * (a.dv / kDeltaCols)));
-    if (a.seqlen == 1)
-        return launch_overlapped(delta_step_kernel<T, DK>, grid, dim3(kDeltaThreads), 0, stream,
-                                 (const T *)a.q, (const T *)a.k, (const T *)a.v, (const T *)a.g,
-                                 (const T *)a.beta, a.lengths, a.state_out, (T *)a.out, a.scale,
-                                 a.heads, a.key_heads, a.dv);
+    if (a.seqlen == 1) {
+        constexpr int kBytes = (int)sizeof(DeltaStepSmem<T, DK>);
+        cudaError_t e = cudaFuncSetAttribute(delta_step_kernel<T, DK>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+        if (e != cudaSuccess) return e;
+        const unsigned resident = 148 * 3;
+        return launch_overlapped(delta_step_kernel<T, DK>, dim3(grid.x < resident ? grid.x : resident),
+                                 dim3(kDeltaThreads), kBytes, stream, (const T *)a.q,
+                                 (const T *)a.k, (const T *)a.v, (const T *)a.g, (const T *)a.beta,
+                                 a.lengths, a.state_out, (T *)a.out, a.scale, a.heads,
+                                 a.key_heads, a.dv, (int)grid.x);
+    }
     return launch_overlapped(delta_tokens_kernel<T, DK>, grid, dim3(kDeltaThreads), 0, stream,
                              (const T *)a.q, (const T *)a.k, (const T *)a.v, (const T *)a.g,
                              (const T *)a.beta, a.lengths, a.state_out, (T *)a.out, a.scale,
