@@ -494,9 +494,9 @@ struct DeltaScanArgs {
 };
 
 template <int DK, bool kSplit, bool kOut, bool kSave>
-__global__ void __launch_bounds__(kScanThreads, 1)
-delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_o, DeltaScanArgs a) {
+__device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                                             const CUtensorMap &tm_o, const DeltaScanArgs &a,
+                                             int cta) {
     using Smem = DeltaScanSmem<DK, kSplit>;
     using Block = DeltaBlock<DK, kSplit>;
     using Tm = DeltaScanTmem<DK, kSplit>;
@@ -508,7 +508,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     // warp-uniform as the compiler sees it
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int slabs = (a.dv + 127) / 128;
-    const int bh = blockIdx.x / slabs, v0 = (blockIdx.x % slabs) * 128;
+    const int bh = cta / slabs, v0 = (cta % slabs) * 128;
     const int b = bh / a.heads, h = bh % a.heads;
     unsigned *err = a.err;
     int *abort_flag = &bar.abort_flag;
@@ -786,6 +786,13 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     }
 }
 
+template <int DK, bool kSplit>
+__global__ void __launch_bounds__(kScanThreads, 1)
+delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ CUtensorMap tm_o, DeltaScanArgs a) {
+    forward_walk<DK, kSplit, true, false>(tm_k, tm_v, tm_o, a, blockIdx.x);
+}
+
 // ------------------------------------------------------------------ reverse scan
 // The gradient's walk, last chunk first.  D is the gradient of the state
 // behind a chunk; with dO the output's gradient
@@ -814,9 +821,9 @@ struct DeltaReverseArgs {
 };
 
 template <int DK>
-__global__ void __launch_bounds__(kScanThreads, 1)
-delta_reverse_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_do,
-                     const __grid_constant__ CUtensorMap tm_dv, DeltaReverseArgs a) {
+__device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUtensorMap &tm_do,
+                                             const CUtensorMap &tm_dv, const DeltaReverseArgs &a,
+                                             int cta) {
     using Smem = DeltaScanSmem<DK, false>;                // V's place holds dO, the output's dV
     using Block = DeltaBlock<DK, false>;
     constexpr int kPieces = DK / 64;
@@ -828,7 +835,7 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int slabs = (a.dv + 127) / 128;
-    const int bh = blockIdx.x / slabs, v0 = (blockIdx.x % slabs) * 128;
+    const int bh = cta / slabs, v0 = (cta % slabs) * 128;
     const int b = bh / a.heads, h = bh % a.heads;
     unsigned *err = a.err;
     int *abort_flag = &bar.abort_flag;
@@ -1057,6 +1064,19 @@ delta_reverse_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// The backward's two walks.  Neither needs the other, and each has a CTA per
+// (sequence, head) and 128 channels only, so they share a launch: the first
+// half of the CTAs walks forward and keeps X^T and S^T, the second back.
+template <int DK>
+__global__ void __launch_bounds__(kScanThreads, 1)
+delta_walks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dv,
+                   DeltaScanArgs f, DeltaReverseArgs r) {
+    const int half = gridDim.x / 2;
+    if ((int)blockIdx.x < half) forward_walk<DK, false, false, true>(tm_k, tm_v, tm_v, f, blockIdx.x);
+    else reverse_walk<DK>(tm_k, tm_do, tm_dv, r, blockIdx.x - half);
 }
 
 // ------------------------------------------------------------------ gradients
@@ -1506,25 +1526,24 @@ cudaError_t launch_prep(const DeltaArgs &a, int nc, uint8_t *blocks, bool backwa
                              sizeof(DeltaPrepSmem<DK, kSplit>), stream, p);
 }
 
-template <int DK, bool kSplit, bool kOut, bool kSave>
-cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, __nv_bfloat16 *x_save,
-                        __nv_bfloat16 *s_save, cudaStream_t stream) {
+template <int DK, bool kSplit>
+cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, cudaStream_t stream) {
     using Smem = DeltaScanSmem<DK, kSplit>;
-    cudaError_t e = cudaFuncSetAttribute(delta_scan_kernel<DK, kSplit, kOut, kSave>,
+    cudaError_t e = cudaFuncSetAttribute(delta_scan_kernel<DK, kSplit>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Smem::kBytes);
     if (e != cudaSuccess) return e;
     CUtensorMap tm_k, tm_v, tm_o;
     if (!token_map(&tm_k, a.k, a.batch, a.seqlen, a.key_heads, a.dk) ||
         !token_map(&tm_v, a.v, a.batch, a.seqlen, a.heads, a.dv) ||
-        !token_map(&tm_o, kOut ? a.out : a.v, a.batch, a.seqlen, a.heads, a.dv))
+        !token_map(&tm_o, a.out, a.batch, a.seqlen, a.heads, a.dv))
         return cudaErrorInvalidValue;
-    DeltaScanArgs s = {blocks, a.lengths, a.state_in, a.state_out, (__nv_bfloat16 *)a.out, x_save,
-                       s_save, a.heads, a.key_heads, a.seqlen, nc, a.dv, device_error_word()};
+    DeltaScanArgs s = {blocks, a.lengths, a.state_in, a.state_out, (__nv_bfloat16 *)a.out, nullptr,
+                       nullptr, a.heads, a.key_heads, a.seqlen, nc, a.dv, device_error_word()};
     const int slabs = (a.dv + 127) / 128;
     KernelTimer timer("delta_scan", stream);
     count_launch();
-    return launch_overlapped(delta_scan_kernel<DK, kSplit, kOut, kSave>,
+    return launch_overlapped(delta_scan_kernel<DK, kSplit>,
                              dim3((unsigned)(a.batch * a.heads * slabs)), dim3(kScanThreads),
                              Smem::kBytes, stream, tm_k, tm_v, tm_o, s);
 }
@@ -1559,12 +1578,10 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
     float *dq_wide = (float *)(ws + l.dq), *dk_wide = (float *)(ws + l.dk);
     cudaError_t e = launch_prep<DK, false>(a, nc, ws + l.blocks, true, stream);
     if (e != cudaSuccess) return e;
-    e = launch_scan<DK, false, false, true>(a, nc, ws + l.blocks, xs, ss, stream);
-    if (e != cudaSuccess) return e;
-
-    CUtensorMap tm_q, tm_k, tm_do, tm_dv, tm_dq, tm_dk;
+    CUtensorMap tm_q, tm_k, tm_v, tm_do, tm_dv, tm_dq, tm_dk;
     if (!token_map(&tm_q, a.q, a.batch, a.seqlen, a.key_heads, DK) ||
         !token_map(&tm_k, a.k, a.batch, a.seqlen, a.key_heads, DK) ||
+        !token_map(&tm_v, a.v, a.batch, a.seqlen, a.heads, a.dv) ||
         !token_map(&tm_do, a.d_out, a.batch, a.seqlen, a.heads, a.dv) ||
         !token_map(&tm_dv, a.dv_grad, a.batch, a.seqlen, a.heads, a.dv) ||
         !token_map(&tm_dq, a.dq, a.batch, a.seqlen, a.key_heads, DK) ||
@@ -1572,15 +1589,17 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
         return cudaErrorInvalidValue;
     {
         using Smem = DeltaScanSmem<DK, false>;
-        e = cudaFuncSetAttribute(delta_reverse_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(delta_walks_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Smem::kBytes);
         if (e != cudaSuccess) return e;
+        DeltaScanArgs f = {ws + l.blocks, a.lengths, nullptr, nullptr, nullptr, xs, ss, a.heads,
+                           a.key_heads, a.seqlen, nc, a.dv, device_error_word()};
         DeltaReverseArgs r = {ws + l.blocks, a.lengths, ds, a.heads, a.key_heads, a.seqlen, nc, a.dv,
                               device_error_word()};
-        KernelTimer timer("delta_reverse", stream);
+        KernelTimer timer("delta_walks", stream);
         count_launch();
-        e = launch_overlapped(delta_reverse_kernel<DK>, dim3((unsigned)(bh * slabs)),
-                              dim3(kScanThreads), Smem::kBytes, stream, tm_k, tm_do, tm_dv, r);
+        e = launch_overlapped(delta_walks_kernel<DK>, dim3((unsigned)(2 * bh * slabs)),
+                              dim3(kScanThreads), Smem::kBytes, stream, tm_k, tm_v, tm_do, tm_dv, f, r);
         if (e != cudaSuccess) return e;
     }
     {
@@ -1608,8 +1627,7 @@ cudaError_t launch_forward(const DeltaArgs &a, void *workspace, cudaStream_t str
     const int nc = (a.seqlen + kC - 1) / kC;
     cudaError_t e = launch_prep<DK, kSplit>(a, nc, (uint8_t *)workspace, false, stream);
     if (e != cudaSuccess) return e;
-    return launch_scan<DK, kSplit, true, false>(a, nc, (const uint8_t *)workspace, nullptr, nullptr,
-                                                stream);
+    return launch_scan<DK, kSplit>(a, nc, (const uint8_t *)workspace, stream);
 }
 
 }  // namespace
