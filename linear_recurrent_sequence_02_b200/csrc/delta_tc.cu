@@ -68,9 +68,17 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 // Two bf16 parts of a pair: hi the rounding, lo the rounding of what it left.
+__device__ __forceinline__ void split_pair(float2 x, uint32_t &hi, uint32_t &lo) {
+    hi = pack_bf16x2(x.x, x.y);
+    const float2 left = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)),
+                             both(-1.f), x);
+    lo = pack_bf16x2(left.x, left.y);
+}
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16x2(a, b);
-    lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+    split_pair(make_float2(a, b), hi, lo);
+}
+__device__ __forceinline__ float2 as_pair(uint32_t a, uint32_t b) {
+    return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
 
 // Rows cnt.. of `boxes` 64-row boxes as zeros, by one warp.  Rows behind a
@@ -656,19 +664,21 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
         const bool live = v < a.dv;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
         const size_t sbase = ((size_t)bh * DK + 32 * wg) * a.dv + v;
-        float S[kPieces][32];
+        float2 S[kPieces][16];
 #pragma unroll
         for (int p = 0; p < kPieces; ++p)
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                S[p][j] = a.state_in && live ? a.state_in[sbase + (size_t)(64 * p + j) * a.dv] : 0.f;
+            for (int j = 0; j < 16; ++j) {
+                const float *src = a.state_in + sbase + (size_t)(64 * p + 2 * j) * a.dv;
+                S[p][j] = a.state_in && live ? make_float2(src[0], src[a.dv]) : both(0.f);
+            }
         // the operand copies of a piece of S; c: the chunk that starts with it
         auto put_state = [&](int p, int c) {
             uint32_t hi[16], lo[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                if (kSplit) split_pair(S[p][2 * j], S[p][2 * j + 1], hi[j], lo[j]);
-                else hi[j] = pack_bf16x2(S[p][2 * j], S[p][2 * j + 1]);
+                if (kSplit) split_pair(S[p][j], hi[j], lo[j]);
+                else hi[j] = pack_bf16x2(S[p][j].x, S[p][j].y);
             }
             tmem_st16(tl + Tm::kShi + 32 * p + 16 * wg, hi);
             if (kSplit) tmem_st16(tl + Tm::kSlo + 32 * p + 16 * wg, lo);
@@ -694,10 +704,10 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float2 r = *reinterpret_cast<const float2 *>(hdr + 32 * wg + 2 * j);
-                    const float x0 = __uint_as_float(x[2 * j]), x1 = __uint_as_float(x[2 * j + 1]);
-                    if (kSplit) split_pair(x0 * r.x, x1 * r.y, hi[j], lo[j]);
-                    else hi[j] = pack_bf16x2(x0 * r.x, x1 * r.y);
-                    if (kOut || kSave) xb[j] = pack_bf16x2(x0, x1);
+                    const float2 xv = as_pair(x[2 * j], x[2 * j + 1]), xr = mul2(xv, r);
+                    if (kSplit) split_pair(xr, hi[j], lo[j]);
+                    else hi[j] = pack_bf16x2(xr.x, xr.y);
+                    if (kOut || kSave) xb[j] = pack_bf16x2(xv.x, xv.y);
                 }
                 tmem_st16(tl + Tm::kXs + 16 * wg, hi);
                 if (kSplit) tmem_st16(tl + Tm::kXslo + 16 * wg, lo);
@@ -718,8 +728,8 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                 tmem_ld32(tl + Tm::kZ + 64 * p + 32 * wg, z);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    S[p][j] = fmaf(eL, S[p][j], __uint_as_float(z[j]));
+                for (int j = 0; j < 16; ++j)
+                    S[p][j] = fma2(both(eL), S[p][j], as_pair(z[2 * j], z[2 * j + 1]));
                 put_state(p, c + 1);
             }
             if (!ok) break;
@@ -728,23 +738,29 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
 #pragma unroll
             for (int p = 0; p < kPieces; ++p)
 #pragma unroll
-                for (int j = 0; j < 32; ++j) a.state_out[sbase + (size_t)(64 * p + j) * a.dv] = S[p][j];
+                for (int j = 0; j < 16; ++j) {
+                    float *dst = a.state_out + sbase + (size_t)(64 * p + 2 * j) * a.dv;
+                    dst[0] = S[p][j].x;
+                    dst[a.dv] = S[p][j].y;
+                }
     } else if (kOut) {
         // O through shared memory, token rows of 64 channels (the swizzle of
         // the copy out), so that global memory sees whole lines
         const int col = 32 * (warp % 4) + lane, tid = threadIdx.x - 320;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
         for (int c = 0; c < nc; ++c) {
-            if (!warp_spin_wait(&bar.o_full, c & 1, abort_flag, err)) break;
-            tc_fence_after();
+            const bool ok = warp_spin_wait(&bar.o_full, c & 1, abort_flag, err);
             uint32_t o[2][32];
-            tmem_ld32(tl + Tm::kO, o[0]);
-            tmem_ld32(tl + Tm::kO + 32, o[1]);
-            tmem_wait_ld();
-            tc_fence_before();
-            warp_arrive(&bar.o_free);
+            if (ok) {
+                tc_fence_after();
+                tmem_ld32(tl + Tm::kO, o[0]);
+                tmem_ld32(tl + Tm::kO + 32, o[1]);
+                tmem_wait_ld();
+                tc_fence_before();
+                warp_arrive(&bar.o_free);
+            }
             if (tid == 0) tma_store_wait_read();           // the last tile has left
-            named_barrier(1, 128);
+            if (named_barrier_or(1, 128, !ok)) break;
             put_channel(smem + Smem::kOut, col, o);
             const int cnt = n - c * kC;
             if (cnt >= kC) fence_async_shared();
@@ -966,12 +982,12 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
         const int v = v0 + 32 * (warp % 4) + lane;
         const bool live = v < a.dv;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
-        float D[kPieces][32] = {};
+        float2 D[kPieces][16] = {};
         // the operand copy of a piece of D, kept for chunk c (the one in front of it)
         auto put_grad = [&](int p, int c) {
             uint32_t hi[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) hi[j] = pack_bf16x2(D[p][2 * j], D[p][2 * j + 1]);
+            for (int j = 0; j < 16; ++j) hi[j] = pack_bf16x2(D[p][j].x, D[p][j].y);
             tmem_st16(tl + kD + 32 * p + 16 * wg, hi);
             tmem_wait_st();
             tc_fence_before();
@@ -996,8 +1012,7 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float2 r = *reinterpret_cast<const float2 *>(hdr + 32 * wg + 2 * j);
-                    split_pair(fmaf(r.x, __uint_as_float(y2[2 * j]), __uint_as_float(y1[2 * j])),
-                               fmaf(r.y, __uint_as_float(y2[2 * j + 1]), __uint_as_float(y1[2 * j + 1])),
+                    split_pair(fma2(r, as_pair(y2[2 * j], y2[2 * j + 1]), as_pair(y1[2 * j], y1[2 * j + 1])),
                                dx[j], lo[j]);
                 }
                 tmem_st16(tl + kDx + 16 * wg, dx);
@@ -1019,7 +1034,8 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
                 tmem_ld32(tl + kZ + 64 * p + 32 * wg, z);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) D[p][j] = fmaf(eL, D[p][j], __uint_as_float(z[j]));
+                for (int j = 0; j < 16; ++j)
+                    D[p][j] = fma2(both(eL), D[p][j], as_pair(z[2 * j], z[2 * j + 1]));
                 put_grad(p, nc - 2 - u);
             }
             if (!ok) break;
@@ -1028,16 +1044,18 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
         const int col = 32 * (warp % 4) + lane, tid = threadIdx.x - 320;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
         for (int u = 0; u < nc; ++u) {
-            if (!warp_spin_wait(&bar.v_full, u & 1, abort_flag, err)) break;
-            tc_fence_after();
+            const bool ok = warp_spin_wait(&bar.v_full, u & 1, abort_flag, err);
             uint32_t o[2][32];
-            tmem_ld32(tl + kDv, o[0]);
-            tmem_ld32(tl + kDv + 32, o[1]);
-            tmem_wait_ld();
-            tc_fence_before();
-            warp_arrive(&bar.v_free);
+            if (ok) {
+                tc_fence_after();
+                tmem_ld32(tl + kDv, o[0]);
+                tmem_ld32(tl + kDv + 32, o[1]);
+                tmem_wait_ld();
+                tc_fence_before();
+                warp_arrive(&bar.v_free);
+            }
             if (tid == 0) tma_store_wait_read();
-            named_barrier(1, 128);
+            if (named_barrier_or(1, 128, !ok)) break;
             put_channel(smem + Smem::kOut, col, o);        // zeros behind the sequence
             fence_async_shared();
             named_barrier(1, 128);
@@ -1094,27 +1112,32 @@ delta_walks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 //   C1 = [dO; dV] S^T,  C2 = [*; X] D^T              (summed over v, 64 at a time)
 //   C3 = [A; B] K,      C4 = [*; A^T] Q + [*; B^T] K (C4 where the pairs were)
 // (*: whatever precedes the operand in shared memory; those rows are not read.)
+// Persistent, a CTA an SM: the copies of the next chunk run beside the pairs
+// and the epilogue of this one (a CTA a chunk, 2048 chunks of 128 x 128: 175
+// us, persistent 98 us).
 constexpr int kGradTcThreads = 320;        // warps 0-7 rows, 8 copies, 9 MMAs
 
 struct DeltaGradTcBars {
-    uint64_t full[2], empty[2], keys, pair_full, ab_ready, c_full, drain;
+    uint64_t full[2], empty[2], keys[2], keys_free[2], pair_full, ab_ready, c_full, acc_free, drain;
     uint32_t tmem_slot;
     int abort_flag;
     double G[kC];
     float beta[kC], rest[kC];
     float rowsum[2][2][kC];                // [queries, keys][column half]
     float colsum[8][32];                   // by warp: its column half
-    float inter[2][2][kC], ahead[2][kC], db[kC], sd[8];
+    float inter[2][2][kC], ahead[2][kC], total[kC], front[kC], db[kC], sd[8];
 };
 template <int DK>
 struct DeltaGradTcSmem {
     static constexpr uint32_t kKB = DK / 64;
-    // keys: a Q and a K box by turns ([Q; K] is 128 rows of one operand, and
-    // each alone has its column blocks two boxes apart), then the tiles A, B
+    // two buffers of keys: a Q and a K box by turns ([Q; K] is 128 rows of one
+    // operand, and each alone has its column blocks two boxes apart; dq and dk
+    // leave from where a thread read its row of them), then the tiles A, B
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kK = kBox64;
     static constexpr uint32_t kKeyStep = 2 * kBox64;
-    static constexpr uint32_t kA = 2 * kKB * kBox64;
+    static constexpr uint32_t kKeys = 2 * kKB * kBox64;
+    static constexpr uint32_t kA = 2 * kKeys;
     static constexpr uint32_t kB = kA + kBox64;
     static constexpr uint32_t kStage0 = kB + kBox64;
     // a stage of 64 v channels: dO, dV, X^T, S^T, D^T
@@ -1124,7 +1147,6 @@ struct DeltaGradTcSmem {
     static constexpr uint32_t kBars = kStage0 + 2 * kStage;
     static constexpr uint32_t kBytes = kBars + ((sizeof(DeltaGradTcBars) + 127) & ~127u);
     static_assert(kBytes <= 227 * 1024, "shared memory");
-    static_assert(2 * kKB * kBox64 <= kStage, "dq and dk leave through the first stage");
 };
 
 struct DeltaGradTcArgs {
@@ -1133,7 +1155,7 @@ struct DeltaGradTcArgs {
     __nv_bfloat16 *dq, *dk_, *dv_, *dg, *dbeta;
     float *dq_wide, *dk_wide;
     float scale;
-    int heads, key_heads, tokens, nc, dv;
+    int heads, key_heads, tokens, nc, dv, items;
     unsigned *err;
 };
 
@@ -1149,46 +1171,22 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     extern __shared__ __align__(1024) uint8_t smem[];
     DeltaGradTcBars &m = *reinterpret_cast<DeltaGradTcBars *>(smem + Smem::kBars);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
-    const int bh = blockIdx.x / a.nc, c = blockIdx.x % a.nc;
-    const int b = bh / a.heads, h = bh % a.heads, kh = h / (a.heads / a.key_heads);
     const bool shared_keys = a.heads != a.key_heads;
+    const int nv = a.dv / 64;
     unsigned *err = a.err;
     int *abort_flag = &m.abort_flag;
 
-    grid_dependency_wait();
-    const int n = delta_tokens_of(a.lengths, b, a.tokens);
-    const int t0 = c * kC;
-    const int room = min(kC, a.tokens - t0), cnt = min(kC, n - t0);
-    const size_t row0 = (size_t)b * a.tokens + t0;
-    if (cnt <= 0) {                                        // the whole CTA: no gradients here
-        for (int i = warp; i < room; i += kGradTcThreads / 32) {
-            const size_t r = (row0 + i) * a.heads + h;
-            for (int j = lane; j < a.dv; j += 32) a.dv_[r * a.dv + j] = from_f32<__nv_bfloat16>(0.f);
-            for (int j = lane; j < DK; j += 32) {
-                if (shared_keys) {
-                    a.dq_wide[r * DK + j] = 0.f;
-                    a.dk_wide[r * DK + j] = 0.f;
-                } else {
-                    a.dq[r * DK + j] = from_f32<__nv_bfloat16>(0.f);
-                    a.dk_[r * DK + j] = from_f32<__nv_bfloat16>(0.f);
-                }
-            }
-            if (lane == 0) {
-                a.dg[r] = from_f32<__nv_bfloat16>(0.f);
-                a.dbeta[r] = from_f32<__nv_bfloat16>(0.f);
-            }
-        }
-        return;
-    }
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&m.full[s], 1);
             mbar_init(&m.empty[s], 9);                     // the MMAs and 8 warps
+            mbar_init(&m.keys[s], 1);
+            mbar_init(&m.keys_free[s], 1);
         }
-        mbar_init(&m.keys, 1);
         mbar_init(&m.pair_full, 1);
         mbar_init(&m.ab_ready, 8);
         mbar_init(&m.c_full, 1);
+        mbar_init(&m.acc_free, 8);
         mbar_init(&m.drain, 1);
         m.abort_flag = 0;
         fence_barrier_init();
@@ -1197,61 +1195,63 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         tmem_alloc(&m.tmem_slot, 512);
         tmem_relinquish();
     }
-    if (warp == 0) {                                       // running sums of g
-        const size_t at = row0 * a.heads + h;
-        double lo = lane < cnt ? log_decay(to_f32(a.g[at + (size_t)lane * a.heads])) : 0.0;
-        double hi = lane + 32 < cnt ? log_decay(to_f32(a.g[at + (size_t)(lane + 32) * a.heads])) : 0.0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double ul = __shfl_up_sync(0xffffffffu, lo, o);
-            const double uh = __shfl_up_sync(0xffffffffu, hi, o);
-            if (lane >= o) {
-                lo += ul;
-                hi += uh;
-            }
-        }
-        hi += __shfl_sync(0xffffffffu, lo, 31);
-        const double GL = __shfl_sync(0xffffffffu, hi, 31);
-        m.G[lane] = lo;
-        m.G[lane + 32] = hi;
-        m.rest[lane] = expf((float)(GL - lo));
-        m.rest[lane + 32] = expf((float)(GL - hi));
-    } else if (warp == 1) {
-#pragma unroll
-        for (int i = lane; i < kC; i += 32)
-            m.beta[i] = i < cnt ? nonzero_beta(to_f32(a.beta[(row0 + i) * a.heads + h])) : 1.f;
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     constexpr uint32_t tmem = 0;                           // all 512 columns, as above
-    const int nv = a.dv / 64;
+    grid_dependency_wait();
 
-    int it = 0;
+    // the chunk of an item, and how many of its tokens belong to the sequence
+    struct Item {
+        int bh, b, h, kh, t0, cnt;
+    };
+    auto item_of = [&](int i) {
+        Item w;
+        w.bh = i / a.nc;
+        w.b = w.bh / a.heads;
+        w.h = w.bh % a.heads;
+        w.kh = w.h / (a.heads / a.key_heads);
+        w.t0 = (i % a.nc) * kC;
+        w.cnt = min(kC, delta_tokens_of(a.lengths, w.b, a.tokens) - w.t0);
+        return w;
+    };
+
+    int it = 0, kit = 0;                                   // stages and keys issued
     if (warp == 8) {
-        if (elect_one()) {
-            mbar_expect_tx(&m.keys, 2 * kKB * kBox64);
-#pragma unroll
-            for (int x = 0; x < kKB; ++x) {
-                tma_load_4d(smem + Smem::kQ + x * Smem::kKeyStep, &tm_q, &m.keys, 64 * x, kh, t0, b);
-                tma_load_4d(smem + Smem::kK + x * Smem::kKeyStep, &tm_k, &m.keys, 64 * x, kh, t0, b);
-            }
-        }
-        __syncwarp();
-        const size_t first = (size_t)blockIdx.x * nv;      // block of 64 channels
-        for (; it < nv; ++it) {
-            const int s = it & 1;
-            if (it >= 2 && !warp_spin_wait(&m.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
-            uint8_t *st = smem + Smem::kStage0 + s * Smem::kStage;
+        bool ok = true;
+        for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+            const Item w = item_of(i);
+            if (w.cnt <= 0) continue;
+            const int kb = kit & 1;
+            if (kit >= 2) ok = warp_spin_wait(&m.keys_free[kb], ((kit >> 1) - 1) & 1, abort_flag, err);
+            if (!ok) break;
             if (elect_one()) {
-                mbar_expect_tx(&m.full[s], Smem::kStage);
-                tma_load_4d(st + Smem::kDo, &tm_do, &m.full[s], 64 * it, h, t0, b);
-                tma_load_4d(st + Smem::kDv, &tm_dv, &m.full[s], 64 * it, h, t0, b);
-                bulk_load(st + Smem::kX, a.x + (first + it) * (64 * kC), kBox64, &m.full[s]);
-                bulk_load(st + Smem::kS, a.s + (first + it) * (64 * DK), kKB * kBox64, &m.full[s]);
-                bulk_load(st + Smem::kD, a.d + (first + it) * (64 * DK), kKB * kBox64, &m.full[s]);
+                uint8_t *ks = smem + kb * Smem::kKeys;
+                mbar_expect_tx(&m.keys[kb], Smem::kKeys);
+#pragma unroll
+                for (int x = 0; x < kKB; ++x) {
+                    tma_load_4d(ks + Smem::kQ + x * Smem::kKeyStep, &tm_q, &m.keys[kb], 64 * x, w.kh, w.t0, w.b);
+                    tma_load_4d(ks + Smem::kK + x * Smem::kKeyStep, &tm_k, &m.keys[kb], 64 * x, w.kh, w.t0, w.b);
+                }
             }
             __syncwarp();
+            ++kit;
+            const size_t first = (size_t)i * nv;           // block of 64 channels
+            for (int u = 0; u < nv; ++u, ++it) {
+                const int s = it & 1;
+                if (it >= 2) ok = warp_spin_wait(&m.empty[s], ((it >> 1) - 1) & 1, abort_flag, err);
+                if (!ok) break;
+                uint8_t *st = smem + Smem::kStage0 + s * Smem::kStage;
+                if (elect_one()) {
+                    mbar_expect_tx(&m.full[s], Smem::kStage);
+                    tma_load_4d(st + Smem::kDo, &tm_do, &m.full[s], 64 * u, w.h, w.t0, w.b);
+                    tma_load_4d(st + Smem::kDv, &tm_dv, &m.full[s], 64 * u, w.h, w.t0, w.b);
+                    bulk_load(st + Smem::kX, a.x + (first + u) * (64 * kC), kBox64, &m.full[s]);
+                    bulk_load(st + Smem::kS, a.s + (first + u) * (64 * DK), kKB * kBox64, &m.full[s]);
+                    bulk_load(st + Smem::kD, a.d + (first + u) * (64 * DK), kKB * kBox64, &m.full[s]);
+                }
+                __syncwarp();
+            }
         }
     } else if (warp == 9) {
         constexpr uint32_t id_kk = idesc_bf16(128, 64, 0, 0);
@@ -1259,13 +1259,20 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         constexpr uint32_t id_c1 = idesc_bf16(128, DK, 0, 1);
         constexpr uint32_t id_c2 = idesc_bf16(128, DK, 1, 1);
         const uint32_t base = smem_u32(smem);
-        const uint64_t kmaj = smem_desc_sw128(base, 16, 1024);
-        const uint64_t mnmaj = smem_desc_sw128(base, kBox64, 1024);
-        const uint64_t keymn = smem_desc_sw128(base, Smem::kKeyStep, 1024);
         const uint64_t plain = smem_desc_plain(base, 128, 1024);   // X^T, S^T, D^T blocks
-        bool ok = warp_spin_wait(&m.keys, 0, abort_flag, err);
-        if (ok) {
-            if (cnt < kC) clear_rows(smem + Smem::kQ, 2 * kKB, cnt, lane);
+        const uint64_t akm = smem_desc_sw128(base, 16, 1024), amn = smem_desc_sw128(base, kBox64, 1024);
+        int g = 0, n = 0;                                  // stages and items so far
+        bool ok = true;
+        for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+            const Item w = item_of(i);
+            if (w.cnt <= 0) continue;
+            const uint32_t ko = (n & 1) * Smem::kKeys;
+            const uint64_t kmaj = akm + (ko >> 4);
+            const uint64_t keymn = smem_desc_sw128(base + ko, Smem::kKeyStep, 1024);
+            ok = warp_spin_wait(&m.keys[n & 1], (n >> 1) & 1, abort_flag, err);
+            if (ok && w.cnt < kC) clear_rows(smem + ko + Smem::kQ, 2 * kKB, w.cnt, lane);
+            if (ok && n > 0) ok = warp_spin_wait(&m.acc_free, (n - 1) & 1, abort_flag, err);
+            if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -1278,215 +1285,290 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     }
             }
             __syncwarp();
-        }
-        for (int i = 0; ok && i < nv; ++i) {
-            const int s = i & 1;
-            const uint32_t so = (Smem::kStage0 + s * Smem::kStage) >> 4;
-            const uint64_t kst = kmaj + so, kept = plain + so;
-            ok = warp_spin_wait(&m.full[s], (i >> 1) & 1, abort_flag, err);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
+            for (int u = 0; u < nv; ++u, ++g) {
+                const int s = g & 1;
+                const uint32_t so = (Smem::kStage0 + s * Smem::kStage) >> 4;
+                const uint64_t kst = akm + so, kept = plain + so;
+                ok = warp_spin_wait(&m.full[s], (g >> 1) & 1, abort_flag, err);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16(tmem + kPd, kst + ((Smem::kDo + ks * 32) >> 4),
-                             kept + ((Smem::kX + ks * 256) >> 4), id_px, i + ks > 0);
-                if (i == nv - 1) mma_commit(&m.pair_full);
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16(tmem + kPd, kst + ((Smem::kDo + ks * 32) >> 4),
+                                 kept + ((Smem::kX + ks * 256) >> 4), id_px, u + ks > 0);
+                    if (u == nv - 1) mma_commit(&m.pair_full);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16(tmem + kC1, kst + ((Smem::kDo + ks * 32) >> 4),
-                             kept + ((Smem::kS + ks * 256) >> 4), id_c1, i + ks > 0);
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16(tmem + kC1, kst + ((Smem::kDo + ks * 32) >> 4),
+                                 kept + ((Smem::kS + ks * 256) >> 4), id_c1, u + ks > 0);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)             // dV fills the rows that are not read
-                    mma_bf16(tmem + kC2, kept + ((Smem::kDv + ks * 256) >> 4),
-                             kept + ((Smem::kD + ks * 256) >> 4), id_c2, i + ks > 0);
-                mma_commit(&m.empty[s]);
+                    for (int ks = 0; ks < 4; ++ks)         // dV fills the rows that are not read
+                        mma_bf16(tmem + kC2, kept + ((Smem::kDv + ks * 256) >> 4),
+                                 kept + ((Smem::kD + ks * 256) >> 4), id_c2, u + ks > 0);
+                    mma_commit(&m.empty[s]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
-        }
-        ok = ok && warp_spin_wait(&m.ab_ready, 0, abort_flag, err);
-        if (ok) {
+            ok = ok && warp_spin_wait(&m.ab_ready, n & 1, abort_flag, err);
+            if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
                     const uint64_t qb = keymn + ((Smem::kQ + ks * 2048) >> 4);
                     const uint64_t kb = keymn + ((Smem::kK + ks * 2048) >> 4);
-                    mma_bf16(tmem + kC3, kmaj + ((Smem::kA + ks * 32) >> 4), kb, id_c1, ks > 0);
+                    mma_bf16(tmem + kC3, akm + ((Smem::kA + ks * 32) >> 4), kb, id_c1, ks > 0);
                     // the box in front of A (of B) fills the rows that are not read
-                    mma_bf16(tmem + kC4, mnmaj + ((Smem::kA - kBox64 + ks * 2048) >> 4), qb, id_c2, ks > 0);
-                    mma_bf16(tmem + kC4, mnmaj + ((Smem::kA + ks * 2048) >> 4), kb, id_c2, 1);
+                    mma_bf16(tmem + kC4, amn + ((Smem::kA - kBox64 + ks * 2048) >> 4), qb, id_c2, ks > 0);
+                    mma_bf16(tmem + kC4, amn + ((Smem::kA + ks * 2048) >> 4), kb, id_c2, 1);
                 }
                 mma_commit(&m.c_full);
             }
             __syncwarp();
+            ++n;
         }
     } else {
         const bool key = (warp & 2) != 0;                  // rows 64-127
         const int hf = warp / 4, i = 32 * (warp & 1) + lane;
-        const bool in = i < cnt;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
+        int g = 0, n = 0;
         bool ok = true;
-        float sd = 0.f;                                    // this thread's part of <S, D>
-        for (int u = 0; ok && u < nv; ++u) {
-            const int s = u & 1;
-            ok = warp_spin_wait(&m.full[s], (u >> 1) & 1, abort_flag, err);
-            if (!ok) break;
-            const uint8_t *st = smem + Smem::kStage0 + s * Smem::kStage;
-#pragma unroll
-            for (int e = 0; e < 2 * kKB; ++e) {
-                const int o = (tid + 256 * e) * 16;        // both tiles have one layout
-                float sv[8], dv[8];
-                load8(reinterpret_cast<const __nv_bfloat16 *>(st + Smem::kS + o), sv);
-                load8(reinterpret_cast<const __nv_bfloat16 *>(st + Smem::kD + o), dv);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sd = fmaf(sv[j], dv[j], sd);
-            }
-            warp_arrive(&m.empty[s]);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
-        if (lane == 0) m.sd[warp] = sd;
-        ok = ok && warp_spin_wait(&m.keys, 0, abort_flag, err) &&
-             warp_spin_wait(&m.pair_full, 0, abort_flag, err);
-        if (ok) {                                          // A, B, and the sums of E
-            tc_fence_after();
-            uint32_t pd[32], pk[32];
-            tmem_ld32(tl + kPd + 32 * hf, pd);
-            tmem_ld32(tl + kPk + 32 * hf, pk);
-            tmem_wait_ld();
-            const double Gi = m.G[i];
-            float e[32], rs = 0.f;
-            uint8_t *tile = smem + (key ? Smem::kB : Smem::kA);
-#pragma unroll
-            for (int j8 = 0; j8 < 4; ++j8) {
-                float w[8];
-#pragma unroll
-                for (int jj = 0; jj < 8; ++jj) {
-                    const int jl = 8 * j8 + jj, j = 32 * hf + jl;
-                    const float p = __uint_as_float(pd[jl]);
-                    // a row behind the sequence may be NaN: chosen, not multiplied
-                    const bool on = in && (key ? i > j : i >= j);
-                    const float dec = on ? expf((float)(Gi - m.G[j])) : 0.f;
-                    w[jj] = on ? (key ? -p : a.scale * p) * dec : 0.f;
-                    e[jl] = on && i != j ? w[jj] * __uint_as_float(pk[jl]) : 0.f;
-                    rs += e[jl];
-                    if (key && i == j) m.db[i] = p;
-                }
-                store8(reinterpret_cast<__nv_bfloat16 *>(tile + tile_off(i, 32 * hf + 8 * j8)), w);
-            }
-            m.rowsum[key][hf][i] = rs;
-            // column sums over the warp's rows: halves swapped and added until
-            // a lane holds one column
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-#pragma unroll
-                for (int j = 0; j < o; ++j) {
-                    const float give = lane & o ? e[j] : e[j + o];
-                    const float keep = lane & o ? e[j + o] : e[j];
-                    e[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                }
-            m.colsum[warp][lane] = e[0];
-            fence_async_shared();
-            tc_fence_before();
-            warp_arrive(&m.ab_ready);
-            ok = warp_spin_wait(&m.c_full, 0, abort_flag, err);
-        }
-        if (ok) {
-            tc_fence_after();
-            const float ei = expf((float)m.G[i]), f1 = key ? -ei : a.scale * ei, f2 = m.rest[i];
-            const uint8_t *mine = smem + (key ? Smem::kK : Smem::kQ);
-            uint8_t *leave = smem + Smem::kStage0 + (key ? kKB * kBox64 : 0);
-            float inter = 0.f, ahead = 0.f;
-            float *wide = (key ? a.dk_wide : a.dq_wide) + ((row0 + i) * a.heads + h) * (size_t)DK;
-#pragma unroll
-            for (int p = 0; p < kKB; ++p) {                // 32 of this half's columns
-                const int col = hf * (DK / 2) + 32 * p;
-                uint32_t c1[32], c3[32], c2[32];
-                tmem_ld32(tl + kC1 + col, c1);
-                tmem_ld32(tl + kC3 + col, c3);
-                if (key) tmem_ld32(tl + kC2 + col, c2);
-                tmem_wait_ld();
-                float r[32];
-#pragma unroll
-                for (int j8 = 0; j8 < 4; ++j8) {
-                    float own[8];
-                    load8(reinterpret_cast<const __nv_bfloat16 *>(
-                              mine + (col / 64) * Smem::kKeyStep + tile_off(i, (col & 63) + 8 * j8)), own);
-#pragma unroll
-                    for (int jj = 0; jj < 8; ++jj) {
-                        const int j = 8 * j8 + jj;
-                        const float z = f1 * __uint_as_float(c1[j]);
-                        inter = fmaf(own[jj], z, inter);
-                        r[j] = z + __uint_as_float(c3[j]);
-                        if (key) {
-                            const float x = f2 * __uint_as_float(c2[j]);
-                            ahead = fmaf(own[jj], x, ahead);
-                            r[j] += x;
+        // warp 0: decays, warp 1: write strengths, loaded an item ahead
+        float lo = 0.f, hi = 0.f;
+        auto gates = [&](int item) {
+            if (warp > 1 || item >= a.items) return;
+            const Item w = item_of(item);
+            const size_t at = ((size_t)w.b * a.tokens + w.t0) * a.heads + w.h;
+            const __nv_bfloat16 *src = warp == 0 ? a.g : a.beta;
+            lo = lane < w.cnt ? to_f32(src[at + (size_t)lane * a.heads]) : 0.f;
+            hi = lane + 32 < w.cnt ? to_f32(src[at + (size_t)(lane + 32) * a.heads]) : 0.f;
+        };
+        gates(blockIdx.x);
+        for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
+            const Item w = item_of(item);
+            const int cnt = w.cnt, room = min(kC, a.tokens - w.t0);
+            const size_t row0 = (size_t)w.b * a.tokens + w.t0;
+            if (cnt <= 0) {                                // no gradients here
+                for (int r8 = warp; r8 < room; r8 += 8) {
+                    const size_t r = (row0 + r8) * a.heads + w.h;
+                    for (int j = lane; j < a.dv; j += 32) a.dv_[r * a.dv + j] = from_f32<__nv_bfloat16>(0.f);
+                    for (int j = lane; j < DK; j += 32) {
+                        if (shared_keys) {
+                            a.dq_wide[r * DK + j] = 0.f;
+                            a.dk_wide[r * DK + j] = 0.f;
+                        } else {
+                            a.dq[r * DK + j] = from_f32<__nv_bfloat16>(0.f);
+                            a.dk_[r * DK + j] = from_f32<__nv_bfloat16>(0.f);
                         }
                     }
+                    if (lane == 0) {
+                        a.dg[r] = from_f32<__nv_bfloat16>(0.f);
+                        a.dbeta[r] = from_f32<__nv_bfloat16>(0.f);
+                    }
                 }
-                if (key) {
-                    tmem_ld32(tl + kC4 + col, c1);
+                gates(item + gridDim.x);
+                continue;
+            }
+            if (warp < 2) named_barrier(2, 64);            // both have read the last item's
+            if (warp == 0) {                               // running sums of g
+                double l = log_decay(lo), u = log_decay(hi);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double ul = __shfl_up_sync(0xffffffffu, l, o);
+                    const double uu = __shfl_up_sync(0xffffffffu, u, o);
+                    if (lane >= o) {
+                        l += ul;
+                        u += uu;
+                    }
+                }
+                u += __shfl_sync(0xffffffffu, l, 31);
+                const double GL = __shfl_sync(0xffffffffu, u, 31);
+                m.G[lane] = l;
+                m.G[lane + 32] = u;
+                m.rest[lane] = expf((float)(GL - l));
+                m.rest[lane + 32] = expf((float)(GL - u));
+            } else if (warp == 1) {
+                m.beta[lane] = lane < cnt ? nonzero_beta(lo) : 1.f;
+                m.beta[lane + 32] = lane + 32 < cnt ? nonzero_beta(hi) : 1.f;
+            }
+            gates(item + gridDim.x);
+            named_barrier(1, 256);                         // and the last item's sums are read
+            const bool in = i < cnt;
+            const int kb = n & 1;
+            uint8_t *ks = smem + kb * Smem::kKeys;
+            float sd = 0.f;                                // this thread's part of <S, D>
+            for (int u = 0; ok && u < nv; ++u, ++g) {
+                const int s = g & 1;
+                ok = warp_spin_wait(&m.full[s], (g >> 1) & 1, abort_flag, err);
+                if (!ok) break;
+                const uint8_t *st = smem + Smem::kStage0 + s * Smem::kStage;
+#pragma unroll
+                for (int e = 0; e < 2 * kKB; ++e) {
+                    const int o = (tid + 256 * e) * 16;    // both tiles have one layout
+                    float sv[8], dv[8];
+                    load8(reinterpret_cast<const __nv_bfloat16 *>(st + Smem::kS + o), sv);
+                    load8(reinterpret_cast<const __nv_bfloat16 *>(st + Smem::kD + o), dv);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sd = fmaf(sv[j], dv[j], sd);
+                }
+                warp_arrive(&m.empty[s]);
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
+            if (lane == 0) m.sd[warp] = sd;
+            ok = ok && warp_spin_wait(&m.keys[kb], (n >> 1) & 1, abort_flag, err) &&
+                 warp_spin_wait(&m.pair_full, n & 1, abort_flag, err);
+            if (ok) {                                      // A, B, and the sums of E
+                tc_fence_after();
+                uint32_t pd[32], pk[32];
+                tmem_ld32(tl + kPd + 32 * hf, pd);
+                tmem_ld32(tl + kPk + 32 * hf, pk);
+                tmem_wait_ld();
+                const double Gi = m.G[i];
+                float e[32], rs = 0.f;
+                uint8_t *tile = smem + (key ? Smem::kB : Smem::kA);
+#pragma unroll
+                for (int j8 = 0; j8 < 4; ++j8) {
+                    float w8[8];
+#pragma unroll
+                    for (int jj = 0; jj < 8; ++jj) {
+                        const int jl = 8 * j8 + jj, j = 32 * hf + jl;
+                        const float p = __uint_as_float(pd[jl]);
+                        // a row behind the sequence may be NaN: chosen, not multiplied
+                        const bool on = in && (key ? i > j : i >= j);
+                        const float dec = on ? expf((float)(Gi - m.G[j])) : 0.f;
+                        w8[jj] = on ? (key ? -p : a.scale * p) * dec : 0.f;
+                        e[jl] = on && i != j ? w8[jj] * __uint_as_float(pk[jl]) : 0.f;
+                        rs += e[jl];
+                        if (key && i == j) m.db[i] = p;
+                    }
+                    store8(reinterpret_cast<__nv_bfloat16 *>(tile + tile_off(i, 32 * hf + 8 * j8)), w8);
+                }
+                fence_async_shared();
+                tc_fence_before();
+                warp_arrive(&m.ab_ready);
+                m.rowsum[key][hf][i] = rs;
+                // column sums over the warp's rows: halves swapped and added
+                // until a lane holds one column
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+#pragma unroll
+                    for (int j = 0; j < o; ++j) {
+                        const float give = lane & o ? e[j] : e[j + o];
+                        const float keep = lane & o ? e[j + o] : e[j];
+                        e[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
+                m.colsum[warp][lane] = e[0];
+                // the last item's dq and dk have left their keys
+                if (tid == 0 && n > 0) {
+                    tma_store_wait_read();
+                    mbar_arrive(&m.keys_free[kb ^ 1]);
+                }
+                ok = warp_spin_wait(&m.c_full, n & 1, abort_flag, err);
+            }
+            if (ok) {
+                tc_fence_after();
+                const float ei = expf((float)m.G[i]), f1 = key ? -ei : a.scale * ei, f2 = m.rest[i];
+                uint8_t *mine = ks + (key ? Smem::kK : Smem::kQ);
+                float inter = 0.f, ahead = 0.f;
+                float *wide = (key ? a.dk_wide : a.dq_wide) + ((row0 + i) * a.heads + w.h) * (size_t)DK;
+#pragma unroll
+                for (int p = 0; p < kKB; ++p) {            // 32 of this half's columns
+                    const int col = hf * (DK / 2) + 32 * p;
+                    uint32_t c1[32], c3[32], c2[32];
+                    tmem_ld32(tl + kC1 + col, c1);
+                    tmem_ld32(tl + kC3 + col, c3);
+                    if (key) tmem_ld32(tl + kC2 + col, c2);
                     tmem_wait_ld();
+                    float r[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] += __uint_as_float(c1[j]);
+                    for (int j8 = 0; j8 < 4; ++j8) {
+                        float own[8];
+                        load8(reinterpret_cast<const __nv_bfloat16 *>(
+                                  mine + (col / 64) * Smem::kKeyStep + tile_off(i, (col & 63) + 8 * j8)), own);
+#pragma unroll
+                        for (int jj = 0; jj < 8; ++jj) {
+                            const int j = 8 * j8 + jj;
+                            const float z = f1 * __uint_as_float(c1[j]);
+                            inter = fmaf(own[jj], z, inter);
+                            r[j] = z + __uint_as_float(c3[j]);
+                            if (key) {
+                                const float x = f2 * __uint_as_float(c2[j]);
+                                ahead = fmaf(own[jj], x, ahead);
+                                r[j] += x;
+                            }
+                        }
+                    }
+                    if (key) {
+                        tmem_ld32(tl + kC4 + col, c1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] += __uint_as_float(c1[j]);
+                    }
+                    if (p == kKB - 1) {                    // the accumulators are read
+                        tc_fence_before();
+                        warp_arrive(&m.acc_free);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = in ? r[j] : 0.f;
+                    if (shared_keys) {
+                        if (i < room)
+#pragma unroll
+                            for (int j8 = 0; j8 < 4; ++j8) store8(wide + col + 8 * j8, &r[8 * j8]);
+                    } else {                               // where this thread read its own row
+#pragma unroll
+                        for (int j8 = 0; j8 < 4; ++j8)
+                            store8(reinterpret_cast<__nv_bfloat16 *>(
+                                       mine + (col / 64) * Smem::kKeyStep + tile_off(i, (col & 63) + 8 * j8)), &r[8 * j8]);
+                    }
                 }
+                m.inter[key][hf][i] = in ? inter : 0.f;
+                if (key) m.ahead[hf][i] = in ? ahead : 0.f;
+                fence_async_shared();
+            }
+            named_barrier(1, 256);
+            if (ok) {
+                if (tid == 0 && !shared_keys) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = in ? r[j] : 0.f;
-                if (shared_keys) {
-                    if (i < room)
+                    for (int x = 0; x < kKB; ++x) {
+                        tma_store_4d(&tm_dq, ks + Smem::kQ + x * Smem::kKeyStep, 64 * x, w.kh, w.t0, w.b);
+                        tma_store_4d(&tm_dk, ks + Smem::kK + x * Smem::kKeyStep, 64 * x, w.kh, w.t0, w.b);
+                    }
+                    tma_store_commit();
+                }
+                if (tid < kC) {
+                    float t = m.inter[0][0][tid] + m.inter[0][1][tid] + m.inter[1][0][tid] + m.inter[1][1][tid];
+                    t += m.rowsum[0][0][tid] + m.rowsum[0][1][tid] + m.rowsum[1][0][tid] + m.rowsum[1][1][tid];
 #pragma unroll
-                        for (int j8 = 0; j8 < 4; ++j8) store8(wide + col + 8 * j8, &r[8 * j8]);
-                } else {
-#pragma unroll
-                    for (int j8 = 0; j8 < 4; ++j8)
-                        store8(reinterpret_cast<__nv_bfloat16 *>(leave + tile_off(i, col + 8 * j8)), &r[8 * j8]);
+                    for (int v = 0; v < 4; ++v) t -= m.colsum[4 * (tid / 32) + v][tid % 32];
+                    m.total[tid] = t;
+                    m.front[tid] = m.ahead[0][tid] + m.ahead[1][tid];
                 }
             }
-            m.inter[key][hf][i] = in ? inter : 0.f;
-            if (key) m.ahead[hf][i] = in ? ahead : 0.f;
-            fence_async_shared();
-        }
-        named_barrier(1, 256);
-        if (ok) {
-            if (tid == 0 && !shared_keys) {
+            const bool stop = named_barrier_or(1, 256, !ok);
+            if (stop) break;                               // all eight warps
+            if (tid < room) {
+                float s = 0.f;
+                if (tid < cnt) {
 #pragma unroll
-                for (int x = 0; x < kKB; ++x) {
-                    tma_store_4d(&tm_dq, smem + Smem::kStage0 + x * kBox64, 64 * x, kh, t0, b);
-                    tma_store_4d(&tm_dk, smem + Smem::kStage0 + (kKB + x) * kBox64, 64 * x, kh, t0, b);
+                    for (int v = 0; v < 8; ++v) s += m.sd[v];
+                    s *= expf((float)m.G[kC - 1]);
+                    for (int t = cnt - 1; t >= tid; --t) s += m.total[t];
+                    for (int t = 0; t < tid; ++t) s += m.front[t];
                 }
-                tma_store_commit();
+                const size_t r = (row0 + tid) * a.heads + w.h;
+                a.dg[r] = from_f32<__nv_bfloat16>(s);
+                a.dbeta[r] = from_f32<__nv_bfloat16>(tid < cnt ? m.db[tid] / (m.beta[tid] * m.beta[tid]) : 0.f);
             }
-            if (tid < kC) {
-                float t = m.inter[0][0][tid] + m.inter[0][1][tid] + m.inter[1][0][tid] + m.inter[1][1][tid];
-                t += m.rowsum[0][0][tid] + m.rowsum[0][1][tid] + m.rowsum[1][0][tid] + m.rowsum[1][1][tid];
-#pragma unroll
-                for (int w = 0; w < 4; ++w) t -= m.colsum[4 * (tid / 32) + w][tid % 32];
-                m.rowsum[0][0][tid] = t;
-                m.ahead[0][tid] += m.ahead[1][tid];
-            }
-        }
-        named_barrier(1, 256);
-        if (ok && tid < room) {
-            float s = 0.f;
-            if (tid < cnt) {
-#pragma unroll
-                for (int w = 0; w < 8; ++w) s += m.sd[w];
-                s *= expf((float)m.G[kC - 1]);
-                for (int t = cnt - 1; t >= tid; --t) s += m.rowsum[0][0][t];
-                for (int t = 0; t < tid; ++t) s += m.ahead[0][t];
-            }
-            const size_t r = (row0 + tid) * a.heads + h;
-            a.dg[r] = from_f32<__nv_bfloat16>(s);
-            a.dbeta[r] = from_f32<__nv_bfloat16>(tid < cnt ? m.db[tid] / (m.beta[tid] * m.beta[tid]) : 0.f);
+            ++n;
         }
         if (tid == 0) tma_store_wait_read();
     }
     tc_fence_before();
     __syncthreads();
     if (*abort_flag && warp == 8 && lane == 0) {           // as in the walks
-        mbar_drain(&m.keys, 0, err);
+        for (int j = max(0, kit - 2); j < kit; ++j) mbar_drain(&m.keys[j & 1], (j >> 1) & 1, err);
         for (int j = max(0, it - 2); j < it; ++j) mbar_drain(&m.full[j & 1], (j >> 1) & 1, err);
     }
     if (warp == 9) {
@@ -1611,10 +1693,10 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
                              (__nv_bfloat16 *)a.dq, (__nv_bfloat16 *)a.dk_grad,
                              (__nv_bfloat16 *)a.dv_grad, (__nv_bfloat16 *)a.dg,
                              (__nv_bfloat16 *)a.dbeta, dq_wide, dk_wide, a.scale, a.heads,
-                             a.key_heads, a.seqlen, nc, a.dv, device_error_word()};
+                             a.key_heads, a.seqlen, nc, a.dv, (int)(bh * nc), device_error_word()};
         KernelTimer timer("delta_grad_tc", stream);
         count_launch();
-        e = launch_overlapped(delta_grad_tc_kernel<DK>, dim3((unsigned)(bh * nc)),
+        e = launch_overlapped(delta_grad_tc_kernel<DK>, dim3((unsigned)(bh * nc < 148 ? bh * nc : 148)),
                               dim3(kGradTcThreads), Smem::kBytes, stream, tm_q, tm_k, tm_do, tm_dv,
                               tm_dq, tm_dk, g);
         if (e != cudaSuccess) return e;

@@ -20,6 +20,19 @@ __device__ __forceinline__ bool warp_spin_wait(uint64_t *bar, uint32_t parity, v
     return warp_wait(bar, parity, abort, err);
 }
 
+// A named barrier of whole warps that tells all of them whether any warp
+// brought `bad`, so that they leave a loop of barriers together.
+__device__ __forceinline__ bool named_barrier_or(int id, int nthreads, bool bad) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)bad), "r"(id), "r"(nthreads)
+        : "memory");
+    return r != 0;
+}
+
 // Contiguous copy global -> shared; both addresses and the size are
 // multiples of 16 bytes.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,

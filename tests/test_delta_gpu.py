@@ -268,6 +268,25 @@ def test_backward(rn, dtype, algo, B, n, Hk, H, dk, dv):
         assert err(a, w) < tol, name
 
 
+def test_backward_of_many_chunks(rn):
+    """Several chunks for every CTA that walks over them, with uneven lengths."""
+    B, n, Hk, H, dk, dv = 3, 1100, 4, 8, 64, 128
+    x, ref = make(21, B, n, Hk, H, dk, dv, "bf16")
+    lens = [1100, 500, 1037]
+    for r in ref:
+        for b, c in enumerate(lens):
+            r[b, c:] = 0.0
+    lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = rn.retnet_delta_backward(*x, lengths=lengths)
+    again = [rn.retnet_delta_backward(*x, lengths=lengths) for _ in range(3)]
+    done(rn)
+    want = oracle.delta_backward(*ref, dk ** -0.5, lens)
+    for i, (name, a, w) in enumerate(zip(("dq", "dk", "dv", "dg", "dbeta"), got, want)):
+        assert all(torch.equal(a, g[i]) for g in again), name
+        w, a = together(w, a)
+        assert err(a, w) < bound("bf16", True), name
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_backward_lengths_and_gates(rn, dtype):
     B, n, Hk, H, dk, dv = 4, 140, 2, 4, 64, 64
