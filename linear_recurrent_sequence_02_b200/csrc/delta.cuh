@@ -20,8 +20,59 @@ __device__ __forceinline__ int delta_tokens_of(const int *lengths, int b, int se
 // quotient is the limit, and what it writes to the state is nothing beside it.
 __device__ __forceinline__ float nonzero_beta(float b) { return fabsf(b) < 1e-15f ? 1e-15f : b; }
 
-// g where sums of it are formed: e^g is 0 in float32 far above this bound,
-// and differences of sums stay finite when g is -inf.
-__device__ __forceinline__ float log_decay(float g) { return g < -1000.f ? -1000.f : g; }
+// g where sums of it are formed: e^g is 0 in float32 from here on, and
+// differences of sums stay finite when g is -inf.
+__device__ __forceinline__ float log_decay(float g) { return g < -105.f ? -105.f : g; }
+
+// Sums of a chunk's log decays, so that a difference of two keeps float32
+// accuracy behind any decays before it: each is an unevaluated sum of two
+// floats (the second what the first rounded away), and they start anew every
+// 16 tokens.  (In float64 these differences were a third of the gradients'
+// time.)
+struct DecaySums {
+    float2 in[64];                         // from the 16-token block's start, inclusive
+    float total[4];                        // of a block
+    // G_i - G_j for tokens of one block
+    __device__ __forceinline__ float within(int i, int j) const {
+        const float2 a = in[i], b = in[j];
+        return (a.x - b.x) + (a.y - b.y);
+    }
+    __device__ __forceinline__ float since_start(int i) const {            // G_i
+        float s = 0.f;
+        for (int b = 0; b < i / 16; ++b) s += total[b];
+        return s + (in[i].x + in[i].y);
+    }
+    // from token j to the end of block `last` (not before j's own)
+    __device__ __forceinline__ float until(int j, int last) const {
+        const float2 e = in[j | 15], a = in[j];
+        float s = (e.x - a.x) + (e.y - a.y);
+        for (int b = j / 16 + 1; b <= last; ++b) s += total[b];
+        return s;
+    }
+};
+// By one warp; lo, hi: log decays of tokens lane and lane + 32.
+__device__ __forceinline__ void sum_decays(DecaySums &d, int lane, float lo, float hi) {
+    float2 a = make_float2(lo, 0.f), b = make_float2(hi, 0.f);
+    auto add = [](float2 &x, float h, float l) {           // x + (h + l)
+        const float s = x.x + h, v = s - x.x;
+        x.y += l + ((x.x - (s - v)) + (h - v));
+        x.x = s;
+    };
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+        const float ah = __shfl_up_sync(0xffffffffu, a.x, o), al = __shfl_up_sync(0xffffffffu, a.y, o);
+        const float bh = __shfl_up_sync(0xffffffffu, b.x, o), bl = __shfl_up_sync(0xffffffffu, b.y, o);
+        if ((lane & 15) >= o) {
+            add(a, ah, al);
+            add(b, bh, bl);
+        }
+    }
+    d.in[lane] = a;
+    d.in[lane + 32] = b;
+    if ((lane & 15) == 15) {
+        d.total[lane / 16] = a.x + a.y;
+        d.total[2 + lane / 16] = b.x + b.y;
+    }
+}
 
 }  // namespace retnet

@@ -482,7 +482,8 @@ struct DeltaGradSmem {
     float Ks[64][kGradPadK], Qs[64][kGradPadK];
     float X[64][kGradPad], R[64][kGradPad], O[64][kGradPad];
     float S[64][kGradPad], D[64][kGradPad];
-    double G[64];                          // sums of g: their differences are taken
+    DecaySums G;
+    float e[64], rest[64];                 // e^G, e^{G_L - G}
     float beta[64], rowsum[64], colsum[64], inter[64], ahead[64], db[64];
     float part[kGradThreads / 32];
 };
@@ -558,19 +559,15 @@ delta_grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
         m.rowsum[tid] = m.colsum[tid] = m.inter[tid] = m.ahead[tid] = m.db[tid] = 0.f;
     }
     if (warp == 0) {
-        double a = lane < cnt ? log_decay(to_f32(g[(row0 + lane) * heads + h])) : 0.0;
-        double z = lane + 32 < cnt ? log_decay(to_f32(g[(row0 + lane + 32) * heads + h])) : 0.0;
+        const float lo = lane < cnt ? log_decay(to_f32(g[(row0 + lane) * heads + h])) : 0.f;
+        const float hi = lane + 32 < cnt ? log_decay(to_f32(g[(row0 + lane + 32) * heads + h])) : 0.f;
+        sum_decays(m.G, lane, lo, hi);
+        __syncwarp();
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double ua = __shfl_up_sync(0xffffffffu, a, o);
-            const double uz = __shfl_up_sync(0xffffffffu, z, o);
-            if (lane >= o) {
-                a += ua;
-                z += uz;
-            }
+        for (int t = lane; t < 64; t += 32) {
+            m.e[t] = expf(m.G.since_start(t));
+            m.rest[t] = expf(m.G.until(t, 3));
         }
-        m.G[lane] = a;
-        m.G[lane + 32] = z + __shfl_sync(0xffffffffu, a, 31);
     }
     __syncthreads();
 
@@ -633,7 +630,10 @@ delta_grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
 #pragma unroll
         for (int l = 0; l < 4; ++l) {
             const int cj = c0 + 16 * l;
-            const float dec = ri >= cj && ri < cnt ? expf((float)(m.G[ri] - m.G[cj])) : 0.f;
+            float dec = 0.f;
+            if (ri >= cj && ri < cnt)
+                dec = expf(ri / 16 == cj / 16 ? m.G.within(ri, cj)
+                                              : m.G.until(cj, ri / 16 - 1) + (m.G.in[ri].x + m.G.in[ri].y));
             const float va = scale * dec * pa[i][l];
             const float vb = ri > cj ? -m.beta[ri] * dec * pb[i][l] : 0.f;
             m.A[ri][cj] = va;
@@ -661,7 +661,6 @@ delta_grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
 
     // ---- through the states, 64 rows of S and D at a time
     float sd = 0.f;
-    const double GL = m.G[cnt - 1];
     for (int j0 = 0; j0 < dk; j0 += 64) {
         float aq[4][4] = {}, ar[4][4] = {}, ax[4][4] = {};
         load_keys(m.Ks, k + krow + j0);
@@ -686,7 +685,7 @@ delta_grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int ri = r0 + 16 * i;
-            const float e = expf((float)m.G[ri]), rest = ri < cnt ? expf((float)(GL - m.G[ri])) : 0.f;
+            const float e = m.e[ri], rest = m.rest[ri];
             const float bt = m.beta[ri];
             float inter = 0.f, ahead = 0.f;
 #pragma unroll
@@ -758,7 +757,7 @@ delta_grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < kGradThreads / 32; ++w) s += m.part[w];
-        s *= expf((float)GL);
+        s *= m.e[63];
         for (int i = cnt - 1; i >= tid; --i) s += (m.rowsum[i] - m.colsum[i]) + m.inter[i];
         for (int i = 0; i < tid; ++i) s += m.ahead[i];
         dg[(row0 + tid) * heads + h] = from_f32<T>(s);

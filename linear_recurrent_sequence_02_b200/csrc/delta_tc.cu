@@ -137,9 +137,10 @@ template <int DK, bool kSplit>
 struct DeltaPrepSmem {
     uint8_t block[DeltaBlock<DK, kSplit>::kBytes];
     float M[kC][kMPad];                    // M, then T in its place
-    double G[kC];
+    DecaySums G;
     float beta[kC], e[kC], in[kC];         // e^G; e^{G_i - G_r}
     float across[3][kC];                   // [block - 1][j]: e^{G_r - G_j}
+    float diag[kC][20];                    // [i][j - r - 1]: e^{G_i - G_j} in a block, 0 above
 };
 
 struct DeltaPrepArgs {
@@ -232,19 +233,9 @@ delta_prep_kernel(DeltaPrepArgs a) {
         }
         if (warp == 0) {                                   // running sums of g
             const size_t at = row0 * a.heads + h;
-            double lo = lane < cnt ? log_decay(to_f32(a.g[at + (size_t)lane * a.heads])) : 0.0;
-            double hi = lane + 32 < cnt ? log_decay(to_f32(a.g[at + (size_t)(lane + 32) * a.heads])) : 0.0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double ul = __shfl_up_sync(0xffffffffu, lo, o);
-                const double uh = __shfl_up_sync(0xffffffffu, hi, o);
-                if (lane >= o) {
-                    lo += ul;
-                    hi += uh;
-                }
-            }
-            m.G[lane] = lo;
-            m.G[lane + 32] = hi + __shfl_sync(0xffffffffu, lo, 31);
+            const float lo = lane < cnt ? log_decay(to_f32(a.g[at + (size_t)lane * a.heads])) : 0.f;
+            const float hi = lane + 32 < cnt ? log_decay(to_f32(a.g[at + (size_t)(lane + 32) * a.heads])) : 0.f;
+            sum_decays(m.G, lane, lo, hi);
         } else if (warp == 1) {
 #pragma unroll
             for (int i = lane; i < kC; i += 32) {
@@ -265,17 +256,21 @@ delta_prep_kernel(DeltaPrepArgs a) {
     }
     __syncthreads();
     if (tid < 64) {
-        const int r = (tid & ~15) - 1;
-        m.e[tid] = expf((float)m.G[tid]);
-        m.in[tid] = expf((float)(m.G[tid] - (r < 0 ? 0.0 : m.G[r])));
+        m.e[tid] = expf(m.G.since_start(tid));
+        m.in[tid] = expf(m.G.in[tid].x + m.G.in[tid].y);
     } else if (tid < 128) {
         float *hdr = reinterpret_cast<float *>(m.block + Block::kHdr);
-        hdr[tid - 64] = expf((float)(m.G[kC - 1] - m.G[tid - 64]));
-        if (tid == 64) hdr[64] = expf((float)m.G[kC - 1]);
+        hdr[tid - 64] = expf(m.G.until(tid - 64, 3));
+        if (tid == 64) hdr[64] = expf(m.G.since_start(kC - 1));
     } else if (tid < 224) {                                // 16, 32 and 48 columns
         const int t = tid - 128, blk = t < 16 ? 1 : t < 48 ? 2 : 3;
         const int j = t - (blk == 1 ? 0 : blk == 2 ? 16 : 48);
-        m.across[blk - 1][j] = expf((float)(m.G[16 * blk - 1] - m.G[j]));
+        m.across[blk - 1][j] = expf(m.G.until(j, blk - 1));
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int i = tid / 4, j = 4 * (tid % 4) + u;
+        m.diag[i][j] = (i & 15) >= j ? expf(m.G.within(i, (i & ~15) + j)) : 0.f;
     }
     __syncthreads();
 
@@ -305,24 +300,23 @@ delta_prep_kernel(DeltaPrepArgs a) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             const int i = 16 * rb + gr + 8 * hf;
-            const double Gi = m.G[i];
             const float f = (isP ? a.scale : m.beta[i]), far = f * m.in[i];
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
                 const int j = 8 * t + 2 * tq;
-                float w[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float x = acc[t][2 * hf + e];
-                    if (t / 2 < rb) w[e] = x * far * m.across[rb - 1][j + e];
-                    else if (t / 2 == rb)
-                        w[e] = i > j + e || (isP && i == j + e) ? x * f * expf((float)(Gi - m.G[j + e])) : 0.f;
-                    else w[e] = 0.f;
+                const float2 x = make_float2(acc[t][2 * hf], acc[t][2 * hf + 1]);
+                float2 w = both(0.f);
+                if (t / 2 < rb)
+                    w = mul2(mul2(x, both(far)), *reinterpret_cast<const float2 *>(&m.across[rb - 1][j]));
+                else if (t / 2 == rb) {                    // M has no diagonal
+                    w = mul2(mul2(x, both(f)), *reinterpret_cast<const float2 *>(&m.diag[i][j & 15]));
+                    if (!isP && i == j) w.x = 0.f;
+                    if (!isP && i == j + 1) w.y = 0.f;
                 }
                 if (isP)
-                    *reinterpret_cast<uint32_t *>(m.block + Block::kP + tile_off(i, j)) = pack_bf16x2(w[0], w[1]);
+                    *reinterpret_cast<uint32_t *>(m.block + Block::kP + tile_off(i, j)) = pack_bf16x2(w.x, w.y);
                 else
-                    *reinterpret_cast<float2 *>(&m.M[i][j]) = make_float2(w[0], w[1]);
+                    *reinterpret_cast<float2 *>(&m.M[i][j]) = w;
             }
         }
     }
@@ -1121,11 +1115,13 @@ struct DeltaGradTcBars {
     uint64_t full[2], empty[2], keys[2], keys_free[2], pair_full, ab_ready, c_full, acc_free, drain;
     uint32_t tmem_slot;
     int abort_flag;
-    double G[kC];
-    float beta[kC], rest[kC];
+    DecaySums G;
+    float beta[kC], rest[kC], e[kC], since[kC];            // e^{G_L - G}, e^G, e^{G_i - G_r}
+    float across[3][kC];                                   // as in the prep
+    float decay[kC][kC + 1];                               // e^{G_i - G_j}, i >= j
     float rowsum[2][2][kC];                // [queries, keys][column half]
     float colsum[8][32];                   // by warp: its column half
-    float inter[2][2][kC], ahead[2][kC], total[kC], front[kC], db[kC], sd[8];
+    float inter[2][2][kC], ahead[2][kC], db[kC], sd[8];
 };
 template <int DK>
 struct DeltaGradTcSmem {
@@ -1371,23 +1367,18 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 continue;
             }
             if (warp < 2) named_barrier(2, 64);            // both have read the last item's
-            if (warp == 0) {                               // running sums of g
-                double l = log_decay(lo), u = log_decay(hi);
+            if (warp == 0) {
+                sum_decays(m.G, lane, log_decay(lo), log_decay(hi));
+                __syncwarp();
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double ul = __shfl_up_sync(0xffffffffu, l, o);
-                    const double uu = __shfl_up_sync(0xffffffffu, u, o);
-                    if (lane >= o) {
-                        l += ul;
-                        u += uu;
-                    }
+                for (int t = lane; t < kC; t += 32) {
+                    m.rest[t] = expf(m.G.until(t, 3));
+                    m.e[t] = expf(m.G.since_start(t));
+                    m.since[t] = expf(m.G.in[t].x + m.G.in[t].y);
+#pragma unroll
+                    for (int r = 1; r < 4; ++r)
+                        if (t < 16 * r) m.across[r - 1][t] = expf(m.G.until(t, r - 1));
                 }
-                u += __shfl_sync(0xffffffffu, l, 31);
-                const double GL = __shfl_sync(0xffffffffu, u, 31);
-                m.G[lane] = l;
-                m.G[lane + 32] = u;
-                m.rest[lane] = expf((float)(GL - l));
-                m.rest[lane + 32] = expf((float)(GL - u));
             } else if (warp == 1) {
                 m.beta[lane] = lane < cnt ? nonzero_beta(lo) : 1.f;
                 m.beta[lane + 32] = lane + 32 < cnt ? nonzero_beta(hi) : 1.f;
@@ -1397,6 +1388,21 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             const bool in = i < cnt;
             const int kb = n & 1;
             uint8_t *ks = smem + kb * Smem::kKeys;
+            {   // the decays between tokens, 16 x 16 at a time (a thread an element)
+                const int r = tid / 16, q = tid % 16;
+#pragma unroll
+                for (int rb = 0; rb < 4; ++rb) {
+                    const int t = 16 * rb + r;
+                    const float f = m.since[t];
+#pragma unroll
+                    for (int cb = 0; cb < rb; ++cb)
+                        m.decay[t][16 * cb + q] = f * m.across[rb - 1][16 * cb + q];
+                    m.decay[t][16 * rb + q] = r >= q ? expf(m.G.within(t, 16 * rb + q)) : 0.f;
+#pragma unroll
+                    for (int cb = rb + 1; cb < 4; ++cb) m.decay[t][16 * cb + q] = 0.f;
+                }
+            }
+            named_barrier(1, 256);
             float sd = 0.f;                                // this thread's part of <S, D>
             for (int u = 0; ok && u < nv; ++u, ++g) {
                 const int s = g & 1;
@@ -1425,8 +1431,8 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 tmem_ld32(tl + kPd + 32 * hf, pd);
                 tmem_ld32(tl + kPk + 32 * hf, pk);
                 tmem_wait_ld();
-                const double Gi = m.G[i];
-                float e[32], rs = 0.f;
+                const float f = key ? -1.f : a.scale;
+                float e[32], rs = 0.f, mid = 0.f;
                 uint8_t *tile = smem + (key ? Smem::kB : Smem::kA);
 #pragma unroll
                 for (int j8 = 0; j8 < 4; ++j8) {
@@ -1434,17 +1440,17 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
                     for (int jj = 0; jj < 8; ++jj) {
                         const int jl = 8 * j8 + jj, j = 32 * hf + jl;
-                        const float p = __uint_as_float(pd[jl]);
+                        const bool diag = i == j;
                         // a row behind the sequence may be NaN: chosen, not multiplied
-                        const bool on = in && (key ? i > j : i >= j);
-                        const float dec = on ? expf((float)(Gi - m.G[j])) : 0.f;
-                        w8[jj] = on ? (key ? -p : a.scale * p) * dec : 0.f;
-                        e[jl] = on && i != j ? w8[jj] * __uint_as_float(pk[jl]) : 0.f;
+                        const float p = in ? __uint_as_float(pd[jl]) : 0.f;
+                        if (diag) mid = p;
+                        w8[jj] = diag && key ? 0.f : f * p * m.decay[i][j];
+                        e[jl] = diag ? 0.f : w8[jj] * __uint_as_float(pk[jl]);
                         rs += e[jl];
-                        if (key && i == j) m.db[i] = p;
                     }
                     store8(reinterpret_cast<__nv_bfloat16 *>(tile + tile_off(i, 32 * hf + 8 * j8)), w8);
                 }
+                if (key && (warp & 1) == hf) m.db[i] = mid;
                 fence_async_shared();
                 tc_fence_before();
                 warp_arrive(&m.ab_ready);
@@ -1469,7 +1475,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             }
             if (ok) {
                 tc_fence_after();
-                const float ei = expf((float)m.G[i]), f1 = key ? -ei : a.scale * ei, f2 = m.rest[i];
+                const float ei = m.e[i], f1 = key ? -ei : a.scale * ei, f2 = m.rest[i];
                 uint8_t *mine = ks + (key ? Smem::kK : Smem::kQ);
                 float inter = 0.f, ahead = 0.f;
                 float *wide = (key ? a.dk_wide : a.dq_wide) + ((row0 + i) * a.heads + w.h) * (size_t)DK;
@@ -1537,29 +1543,49 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     }
                     tma_store_commit();
                 }
-                if (tid < kC) {
-                    float t = m.inter[0][0][tid] + m.inter[0][1][tid] + m.inter[1][0][tid] + m.inter[1][1][tid];
-                    t += m.rowsum[0][0][tid] + m.rowsum[0][1][tid] + m.rowsum[1][0][tid] + m.rowsum[1][1][tid];
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) t -= m.colsum[4 * (tid / 32) + v][tid % 32];
-                    m.total[tid] = t;
-                    m.front[tid] = m.ahead[0][tid] + m.ahead[1][tid];
-                }
             }
             const bool stop = named_barrier_or(1, 256, !ok);
             if (stop) break;                               // all eight warps
-            if (tid < room) {
-                float s = 0.f;
-                if (tid < cnt) {
+            if (warp == 0) {
+                // dg of tokens lane and lane + 32: what leaves S and the pairs
+                // from a token on, what reaches D from before it, <S, D>
+                float back[2], front[2];
 #pragma unroll
-                    for (int v = 0; v < 8; ++v) s += m.sd[v];
-                    s *= expf((float)m.G[kC - 1]);
-                    for (int t = cnt - 1; t >= tid; --t) s += m.total[t];
-                    for (int t = 0; t < tid; ++t) s += m.front[t];
+                for (int v = 0; v < 2; ++v) {
+                    const int t = lane + 32 * v;
+                    float x = m.inter[0][0][t] + m.inter[0][1][t] + m.inter[1][0][t] + m.inter[1][1][t];
+                    x += m.rowsum[0][0][t] + m.rowsum[0][1][t] + m.rowsum[1][0][t] + m.rowsum[1][1][t];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) x -= m.colsum[4 * v + q][lane];
+                    back[v] = x;
+                    front[v] = m.ahead[0][t] + m.ahead[1][t];
                 }
-                const size_t r = (row0 + tid) * a.heads + w.h;
-                a.dg[r] = from_f32<__nv_bfloat16>(s);
-                a.dbeta[r] = from_f32<__nv_bfloat16>(tid < cnt ? m.db[tid] / (m.beta[tid] * m.beta[tid]) : 0.f);
+                const float own[2] = {front[0], front[1]};
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        const float d = __shfl_down_sync(0xffffffffu, back[v], o);
+                        const float u = __shfl_up_sync(0xffffffffu, front[v], o);
+                        if (lane + o < 32) back[v] += d;
+                        if (lane >= o) front[v] += u;
+                    }
+                back[0] += __shfl_sync(0xffffffffu, back[1], 0);
+                front[1] += __shfl_sync(0xffffffffu, front[0], 31);
+                float s = 0.f;
+#pragma unroll
+                for (int v = 0; v < 8; ++v) s += m.sd[v];
+                s *= m.e[kC - 1];
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const int t = lane + 32 * v;
+                    if (t < room) {
+                        const size_t r = (row0 + t) * a.heads + w.h;
+                        const float dg = s + back[v] + (front[v] - own[v]);
+                        a.dg[r] = from_f32<__nv_bfloat16>(t < cnt ? dg : 0.f);
+                        a.dbeta[r] = from_f32<__nv_bfloat16>(t < cnt ? m.db[t] / (m.beta[t] * m.beta[t]) : 0.f);
+                    }
+                }
             }
             ++n;
         }
