@@ -1109,19 +1109,26 @@ delta_walks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 // Persistent, a CTA an SM: the copies of the next chunk run beside the pairs
 // and the epilogue of this one (a CTA a chunk, 2048 chunks of 128 x 128: 175
 // us, persistent 98 us).
-constexpr int kGradTcThreads = 320;        // warps 0-7 rows, 8 copies, 9 MMAs
+constexpr int kGradTcThreads = 352;        // warps 0-7 rows, 8 copies, 9 MMAs, 10 gates and sums
 
 struct DeltaGradTcBars {
-    uint64_t full[2], empty[2], keys[2], keys_free[2], pair_full, ab_ready, c_full, acc_free, drain;
+    uint64_t full[2], empty[2], keys[2], keys_free[2], gates[2], done[2];
+    uint64_t pair_full, ab_ready, c_full, acc_free, drain;
     uint32_t tmem_slot;
     int abort_flag;
-    DecaySums G;
-    float beta[kC], rest[kC], e[kC], since[kC];            // e^{G_L - G}, e^G, e^{G_i - G_r}
-    float across[3][kC];                                   // as in the prep
+    // By turns of two items, so that warp 10 prepares the one after next and
+    // closes the last one while the row warps work.
+    struct Gates {
+        DecaySums G;
+        float beta[kC], rest[kC], e[kC], since[kC];        // e^{G_L - G}, e^G, e^{G_i - G_r}
+        float across[3][kC];                               // as in the prep
+    } gate[2];
+    struct Sums {
+        float row[2][2][kC];               // of E: [queries, keys][column half]
+        float col[8][32];                  // by warp: its column half
+        float inter[2][2][kC], ahead[2][kC], db[kC], sd[8];
+    } sum[2];
     float decay[kC][kC + 1];                               // e^{G_i - G_j}, i >= j
-    float rowsum[2][2][kC];                // [queries, keys][column half]
-    float colsum[8][32];                   // by warp: its column half
-    float inter[2][2][kC], ahead[2][kC], db[kC], sd[8];
 };
 template <int DK>
 struct DeltaGradTcSmem {
@@ -1178,6 +1185,10 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             mbar_init(&m.empty[s], 9);                     // the MMAs and 8 warps
             mbar_init(&m.keys[s], 1);
             mbar_init(&m.keys_free[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&m.gates[s], 1);
+            mbar_init(&m.done[s], 8);
         }
         mbar_init(&m.pair_full, 1);
         mbar_init(&m.ab_ready, 8);
@@ -1324,106 +1335,186 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             __syncwarp();
             ++n;
         }
+    } else if (warp == 10) {
+        // gates of the items ahead; rows without a sequence; dq and dk out, dg
+        // and dbeta of the items behind
+        int ahead_i = blockIdx.x, ahead_n = 0;
+        auto prepare = [&]() {
+            for (; ahead_i < a.items; ahead_i += gridDim.x) {
+                const Item w = item_of(ahead_i);
+                const int room = min(kC, a.tokens - w.t0);
+                const size_t row0 = (size_t)w.b * a.tokens + w.t0;
+                if (w.cnt <= 0) {                          // no gradients here
+                    for (int r1 = 0; r1 < room; ++r1) {
+                        const size_t r = (row0 + r1) * a.heads + w.h;
+                        for (int j = lane; j < a.dv; j += 32) a.dv_[r * a.dv + j] = from_f32<__nv_bfloat16>(0.f);
+                        for (int j = lane; j < DK; j += 32) {
+                            if (shared_keys) {
+                                a.dq_wide[r * DK + j] = 0.f;
+                                a.dk_wide[r * DK + j] = 0.f;
+                            } else {
+                                a.dq[r * DK + j] = from_f32<__nv_bfloat16>(0.f);
+                                a.dk_[r * DK + j] = from_f32<__nv_bfloat16>(0.f);
+                            }
+                        }
+                        if (lane == 0) {
+                            a.dg[r] = from_f32<__nv_bfloat16>(0.f);
+                            a.dbeta[r] = from_f32<__nv_bfloat16>(0.f);
+                        }
+                    }
+                    continue;
+                }
+                DeltaGradTcBars::Gates &G = m.gate[ahead_n & 1];
+                const size_t at = row0 * a.heads + w.h;
+                float g[2], bt[2];
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const int t = lane + 32 * v;
+                    g[v] = t < w.cnt ? log_decay(to_f32(a.g[at + (size_t)t * a.heads])) : 0.f;
+                    bt[v] = t < w.cnt ? nonzero_beta(to_f32(a.beta[at + (size_t)t * a.heads])) : 1.f;
+                }
+                sum_decays(G.G, lane, g[0], g[1]);
+                __syncwarp();
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const int t = lane + 32 * v;
+                    G.beta[t] = bt[v];
+                    G.rest[t] = expf(G.G.until(t, 3));
+                    G.e[t] = expf(G.G.since_start(t));
+                    G.since[t] = expf(G.G.in[t].x + G.G.in[t].y);
+#pragma unroll
+                    for (int r = 1; r < 4; ++r)
+                        if (t < 16 * r) G.across[r - 1][t] = expf(G.G.until(t, r - 1));
+                }
+                warp_arrive(&m.gates[ahead_n & 1]);
+                ++ahead_n;
+                ahead_i += gridDim.x;
+                return;
+            }
+        };
+        prepare();
+        prepare();
+        int n = 0;
+        for (int i = blockIdx.x; i < a.items; i += gridDim.x) {
+            const Item w = item_of(i);
+            if (w.cnt <= 0) continue;
+            if (!warp_spin_wait(&m.done[n & 1], (n >> 1) & 1, abort_flag, err)) break;
+            const int room = min(kC, a.tokens - w.t0);
+            const size_t row0 = (size_t)w.b * a.tokens + w.t0;
+            uint8_t *ks = smem + (n & 1) * Smem::kKeys;
+            if (!shared_keys && elect_one()) {
+#pragma unroll
+                for (int x = 0; x < kKB; ++x) {
+                    tma_store_4d(&tm_dq, ks + Smem::kQ + x * Smem::kKeyStep, 64 * x, w.kh, w.t0, w.b);
+                    tma_store_4d(&tm_dk, ks + Smem::kK + x * Smem::kKeyStep, 64 * x, w.kh, w.t0, w.b);
+                }
+                tma_store_commit();
+            }
+            __syncwarp();
+            // dg: what leaves S and the pairs from a token on, what reaches D
+            // from before it, <S, D>
+            const DeltaGradTcBars::Sums &S = m.sum[n & 1];
+            const DeltaGradTcBars::Gates &G = m.gate[n & 1];
+            float back[2], front[2];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const int t = lane + 32 * v;
+                float x = S.inter[0][0][t] + S.inter[0][1][t] + S.inter[1][0][t] + S.inter[1][1][t];
+                x += S.row[0][0][t] + S.row[0][1][t] + S.row[1][0][t] + S.row[1][1][t];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x -= S.col[4 * v + q][lane];
+                back[v] = x;
+                front[v] = S.ahead[0][t] + S.ahead[1][t];
+            }
+            const float own[2] = {front[0], front[1]};
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const float d = __shfl_down_sync(0xffffffffu, back[v], o);
+                    const float u = __shfl_up_sync(0xffffffffu, front[v], o);
+                    if (lane + o < 32) back[v] += d;
+                    if (lane >= o) front[v] += u;
+                }
+            back[0] += __shfl_sync(0xffffffffu, back[1], 0);
+            front[1] += __shfl_sync(0xffffffffu, front[0], 31);
+            float s = 0.f;
+#pragma unroll
+            for (int v = 0; v < 8; ++v) s += S.sd[v];
+            s *= G.e[kC - 1];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const int t = lane + 32 * v;
+                if (t < room) {
+                    const size_t r = (row0 + t) * a.heads + w.h;
+                    const float dg = s + back[v] + (front[v] - own[v]);
+                    a.dg[r] = from_f32<__nv_bfloat16>(t < w.cnt ? dg : 0.f);
+                    a.dbeta[r] = from_f32<__nv_bfloat16>(t < w.cnt ? S.db[t] / (G.beta[t] * G.beta[t]) : 0.f);
+                }
+            }
+            __syncwarp();
+            prepare();                                     // this item's turn is free
+            if (elect_one()) {
+                tma_store_wait_read();
+                mbar_arrive(&m.keys_free[n & 1]);
+            }
+            __syncwarp();
+            ++n;
+        }
     } else {
         const bool key = (warp & 2) != 0;                  // rows 64-127
         const int hf = warp / 4, i = 32 * (warp & 1) + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
         int g = 0, n = 0;
-        bool ok = true;
-        // warp 0: decays, warp 1: write strengths, loaded an item ahead
-        float lo = 0.f, hi = 0.f;
-        auto gates = [&](int item) {
-            if (warp > 1 || item >= a.items) return;
-            const Item w = item_of(item);
-            const size_t at = ((size_t)w.b * a.tokens + w.t0) * a.heads + w.h;
-            const __nv_bfloat16 *src = warp == 0 ? a.g : a.beta;
-            lo = lane < w.cnt ? to_f32(src[at + (size_t)lane * a.heads]) : 0.f;
-            hi = lane + 32 < w.cnt ? to_f32(src[at + (size_t)(lane + 32) * a.heads]) : 0.f;
-        };
-        gates(blockIdx.x);
         for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
             const Item w = item_of(item);
+            if (w.cnt <= 0) continue;
             const int cnt = w.cnt, room = min(kC, a.tokens - w.t0);
             const size_t row0 = (size_t)w.b * a.tokens + w.t0;
-            if (cnt <= 0) {                                // no gradients here
-                for (int r8 = warp; r8 < room; r8 += 8) {
-                    const size_t r = (row0 + r8) * a.heads + w.h;
-                    for (int j = lane; j < a.dv; j += 32) a.dv_[r * a.dv + j] = from_f32<__nv_bfloat16>(0.f);
-                    for (int j = lane; j < DK; j += 32) {
-                        if (shared_keys) {
-                            a.dq_wide[r * DK + j] = 0.f;
-                            a.dk_wide[r * DK + j] = 0.f;
-                        } else {
-                            a.dq[r * DK + j] = from_f32<__nv_bfloat16>(0.f);
-                            a.dk_[r * DK + j] = from_f32<__nv_bfloat16>(0.f);
-                        }
-                    }
-                    if (lane == 0) {
-                        a.dg[r] = from_f32<__nv_bfloat16>(0.f);
-                        a.dbeta[r] = from_f32<__nv_bfloat16>(0.f);
-                    }
-                }
-                gates(item + gridDim.x);
-                continue;
-            }
-            if (warp < 2) named_barrier(2, 64);            // both have read the last item's
-            if (warp == 0) {
-                sum_decays(m.G, lane, log_decay(lo), log_decay(hi));
-                __syncwarp();
-#pragma unroll
-                for (int t = lane; t < kC; t += 32) {
-                    m.rest[t] = expf(m.G.until(t, 3));
-                    m.e[t] = expf(m.G.since_start(t));
-                    m.since[t] = expf(m.G.in[t].x + m.G.in[t].y);
-#pragma unroll
-                    for (int r = 1; r < 4; ++r)
-                        if (t < 16 * r) m.across[r - 1][t] = expf(m.G.until(t, r - 1));
-                }
-            } else if (warp == 1) {
-                m.beta[lane] = lane < cnt ? nonzero_beta(lo) : 1.f;
-                m.beta[lane + 32] = lane + 32 < cnt ? nonzero_beta(hi) : 1.f;
-            }
-            gates(item + gridDim.x);
-            named_barrier(1, 256);                         // and the last item's sums are read
             const bool in = i < cnt;
-            const int kb = n & 1;
-            uint8_t *ks = smem + kb * Smem::kKeys;
+            const DeltaGradTcBars::Gates &G = m.gate[n & 1];
+            DeltaGradTcBars::Sums &S = m.sum[n & 1];
+            uint8_t *ks = smem + (n & 1) * Smem::kKeys;
+            bool ok = warp_spin_wait(&m.gates[n & 1], (n >> 1) & 1, abort_flag, err);
             {   // the decays between tokens, 16 x 16 at a time (a thread an element)
                 const int r = tid / 16, q = tid % 16;
 #pragma unroll
                 for (int rb = 0; rb < 4; ++rb) {
                     const int t = 16 * rb + r;
-                    const float f = m.since[t];
+                    const float f = G.since[t];
 #pragma unroll
                     for (int cb = 0; cb < rb; ++cb)
-                        m.decay[t][16 * cb + q] = f * m.across[rb - 1][16 * cb + q];
-                    m.decay[t][16 * rb + q] = r >= q ? expf(m.G.within(t, 16 * rb + q)) : 0.f;
+                        m.decay[t][16 * cb + q] = f * G.across[rb - 1][16 * cb + q];
+                    m.decay[t][16 * rb + q] = r >= q ? expf(G.G.within(t, 16 * rb + q)) : 0.f;
 #pragma unroll
                     for (int cb = rb + 1; cb < 4; ++cb) m.decay[t][16 * cb + q] = 0.f;
                 }
             }
-            named_barrier(1, 256);
-            float sd = 0.f;                                // this thread's part of <S, D>
-            for (int u = 0; ok && u < nv; ++u, ++g) {
+            if (named_barrier_or(1, 256, !ok)) break;      // all eight warps
+            // this thread's part of <S, D>: of the last two stages beside the
+            // MMAs on A and B, of those before them at once, for the pairs
+            // wait for all
+            float2 sd = both(0.f);
+            auto dot_states = [&]() {
                 const int s = g & 1;
-                ok = warp_spin_wait(&m.full[s], (g >> 1) & 1, abort_flag, err);
-                if (!ok) break;
+                ok = ok && warp_spin_wait(&m.full[s], (g >> 1) & 1, abort_flag, err);
+                ++g;
+                if (!ok) return;
                 const uint8_t *st = smem + Smem::kStage0 + s * Smem::kStage;
 #pragma unroll
                 for (int e = 0; e < 2 * kKB; ++e) {
                     const int o = (tid + 256 * e) * 16;    // both tiles have one layout
-                    float sv[8], dv[8];
-                    load8(reinterpret_cast<const __nv_bfloat16 *>(st + Smem::kS + o), sv);
-                    load8(reinterpret_cast<const __nv_bfloat16 *>(st + Smem::kD + o), dv);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sd = fmaf(sv[j], dv[j], sd);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(st + Smem::kS + o);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(st + Smem::kD + o);
+                    sd = fma2(as_pair(x.x << 16, x.x & 0xffff0000u), as_pair(y.x << 16, y.x & 0xffff0000u), sd);
+                    sd = fma2(as_pair(x.y << 16, x.y & 0xffff0000u), as_pair(y.y << 16, y.y & 0xffff0000u), sd);
+                    sd = fma2(as_pair(x.z << 16, x.z & 0xffff0000u), as_pair(y.z << 16, y.z & 0xffff0000u), sd);
+                    sd = fma2(as_pair(x.w << 16, x.w & 0xffff0000u), as_pair(y.w << 16, y.w & 0xffff0000u), sd);
                 }
                 warp_arrive(&m.empty[s]);
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
-            if (lane == 0) m.sd[warp] = sd;
-            ok = ok && warp_spin_wait(&m.keys[kb], (n >> 1) & 1, abort_flag, err) &&
+            };
+            for (int u = 0; u < nv - 2; ++u) dot_states();
+            ok = ok && warp_spin_wait(&m.keys[n & 1], (n >> 1) & 1, abort_flag, err) &&
                  warp_spin_wait(&m.pair_full, n & 1, abort_flag, err);
             if (ok) {                                      // A, B, and the sums of E
                 tc_fence_after();
@@ -1450,11 +1541,11 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     }
                     store8(reinterpret_cast<__nv_bfloat16 *>(tile + tile_off(i, 32 * hf + 8 * j8)), w8);
                 }
-                if (key && (warp & 1) == hf) m.db[i] = mid;
                 fence_async_shared();
                 tc_fence_before();
                 warp_arrive(&m.ab_ready);
-                m.rowsum[key][hf][i] = rs;
+                if (key && (warp & 1) == hf) S.db[i] = mid;
+                S.row[key][hf][i] = rs;
                 // column sums over the warp's rows: halves swapped and added
                 // until a lane holds one column
 #pragma unroll
@@ -1465,19 +1556,19 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         const float keep = lane & o ? e[j + o] : e[j];
                         e[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
                     }
-                m.colsum[warp][lane] = e[0];
-                // the last item's dq and dk have left their keys
-                if (tid == 0 && n > 0) {
-                    tma_store_wait_read();
-                    mbar_arrive(&m.keys_free[kb ^ 1]);
-                }
-                ok = warp_spin_wait(&m.c_full, n & 1, abort_flag, err);
+                S.col[warp][lane] = e[0];
             }
+            for (int u = max(0, nv - 2); u < nv; ++u) dot_states();
+            float sd1 = sd.x + sd.y;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sd1 += __shfl_xor_sync(0xffffffffu, sd1, o);
+            if (lane == 0) S.sd[warp] = sd1;
+            ok = ok && warp_spin_wait(&m.c_full, n & 1, abort_flag, err);
             if (ok) {
                 tc_fence_after();
-                const float ei = m.e[i], f1 = key ? -ei : a.scale * ei, f2 = m.rest[i];
+                const float f1 = key ? -G.e[i] : a.scale * G.e[i], f2 = G.rest[i];
                 uint8_t *mine = ks + (key ? Smem::kK : Smem::kQ);
-                float inter = 0.f, ahead = 0.f;
+                float2 inter = both(0.f), ahead = both(0.f);
                 float *wide = (key ? a.dk_wide : a.dq_wide) + ((row0 + i) * a.heads + w.h) * (size_t)DK;
 #pragma unroll
                 for (int p = 0; p < kKB; ++p) {            // 32 of this half's columns
@@ -1487,22 +1578,23 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     tmem_ld32(tl + kC3 + col, c3);
                     if (key) tmem_ld32(tl + kC2 + col, c2);
                     tmem_wait_ld();
-                    float r[32];
+                    float2 r[16];
 #pragma unroll
                     for (int j8 = 0; j8 < 4; ++j8) {
-                        float own[8];
-                        load8(reinterpret_cast<const __nv_bfloat16 *>(
-                                  mine + (col / 64) * Smem::kKeyStep + tile_off(i, (col & 63) + 8 * j8)), own);
+                        const uint4 ov = *reinterpret_cast<const uint4 *>(
+                            mine + (col / 64) * Smem::kKeyStep + tile_off(i, (col & 63) + 8 * j8));
+                        const uint32_t own[4] = {ov.x, ov.y, ov.z, ov.w};
 #pragma unroll
-                        for (int jj = 0; jj < 8; ++jj) {
-                            const int j = 8 * j8 + jj;
-                            const float z = f1 * __uint_as_float(c1[j]);
-                            inter = fmaf(own[jj], z, inter);
-                            r[j] = z + __uint_as_float(c3[j]);
+                        for (int jj = 0; jj < 4; ++jj) {
+                            const int j = 4 * j8 + jj;
+                            const float2 o2 = as_pair(own[jj] << 16, own[jj] & 0xffff0000u);
+                            const float2 z = mul2(both(f1), as_pair(c1[2 * j], c1[2 * j + 1]));
+                            inter = fma2(o2, z, inter);
+                            r[j] = add2(z, as_pair(c3[2 * j], c3[2 * j + 1]));
                             if (key) {
-                                const float x = f2 * __uint_as_float(c2[j]);
-                                ahead = fmaf(own[jj], x, ahead);
-                                r[j] += x;
+                                const float2 x = mul2(both(f2), as_pair(c2[2 * j], c2[2 * j + 1]));
+                                ahead = fma2(o2, x, ahead);
+                                r[j] = add2(r[j], x);
                             }
                         }
                     }
@@ -1510,86 +1602,37 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         tmem_ld32(tl + kC4 + col, c1);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) r[j] += __uint_as_float(c1[j]);
+                        for (int j = 0; j < 16; ++j) r[j] = add2(r[j], as_pair(c1[2 * j], c1[2 * j + 1]));
                     }
                     if (p == kKB - 1) {                    // the accumulators are read
                         tc_fence_before();
                         warp_arrive(&m.acc_free);
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = in ? r[j] : 0.f;
-                    if (shared_keys) {
-                        if (i < room)
+                    for (int j = 0; j < 16; ++j) r[j] = in ? r[j] : both(0.f);
 #pragma unroll
-                            for (int j8 = 0; j8 < 4; ++j8) store8(wide + col + 8 * j8, &r[8 * j8]);
-                    } else {                               // where this thread read its own row
-#pragma unroll
-                        for (int j8 = 0; j8 < 4; ++j8)
-                            store8(reinterpret_cast<__nv_bfloat16 *>(
-                                       mine + (col / 64) * Smem::kKeyStep + tile_off(i, (col & 63) + 8 * j8)), &r[8 * j8]);
+                    for (int j8 = 0; j8 < 4; ++j8) {
+                        const float2 *v = &r[4 * j8];
+                        if (shared_keys) {
+                            if (i < room) {
+                                reinterpret_cast<float4 *>(wide + col + 8 * j8)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+                                reinterpret_cast<float4 *>(wide + col + 8 * j8)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+                            }
+                        } else {                           // where this thread read its own row
+                            *reinterpret_cast<uint4 *>(
+                                mine + (col / 64) * Smem::kKeyStep + tile_off(i, (col & 63) + 8 * j8)) =
+                                make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                           pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+                        }
                     }
                 }
-                m.inter[key][hf][i] = in ? inter : 0.f;
-                if (key) m.ahead[hf][i] = in ? ahead : 0.f;
+                S.inter[key][hf][i] = in ? inter.x + inter.y : 0.f;
+                if (key) S.ahead[hf][i] = in ? ahead.x + ahead.y : 0.f;
                 fence_async_shared();
+                warp_arrive(&m.done[n & 1]);
             }
-            named_barrier(1, 256);
-            if (ok) {
-                if (tid == 0 && !shared_keys) {
-#pragma unroll
-                    for (int x = 0; x < kKB; ++x) {
-                        tma_store_4d(&tm_dq, ks + Smem::kQ + x * Smem::kKeyStep, 64 * x, w.kh, w.t0, w.b);
-                        tma_store_4d(&tm_dk, ks + Smem::kK + x * Smem::kKeyStep, 64 * x, w.kh, w.t0, w.b);
-                    }
-                    tma_store_commit();
-                }
-            }
-            const bool stop = named_barrier_or(1, 256, !ok);
-            if (stop) break;                               // all eight warps
-            if (warp == 0) {
-                // dg of tokens lane and lane + 32: what leaves S and the pairs
-                // from a token on, what reaches D from before it, <S, D>
-                float back[2], front[2];
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const int t = lane + 32 * v;
-                    float x = m.inter[0][0][t] + m.inter[0][1][t] + m.inter[1][0][t] + m.inter[1][1][t];
-                    x += m.rowsum[0][0][t] + m.rowsum[0][1][t] + m.rowsum[1][0][t] + m.rowsum[1][1][t];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) x -= m.colsum[4 * v + q][lane];
-                    back[v] = x;
-                    front[v] = m.ahead[0][t] + m.ahead[1][t];
-                }
-                const float own[2] = {front[0], front[1]};
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const float d = __shfl_down_sync(0xffffffffu, back[v], o);
-                        const float u = __shfl_up_sync(0xffffffffu, front[v], o);
-                        if (lane + o < 32) back[v] += d;
-                        if (lane >= o) front[v] += u;
-                    }
-                back[0] += __shfl_sync(0xffffffffu, back[1], 0);
-                front[1] += __shfl_sync(0xffffffffu, front[0], 31);
-                float s = 0.f;
-#pragma unroll
-                for (int v = 0; v < 8; ++v) s += m.sd[v];
-                s *= m.e[kC - 1];
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const int t = lane + 32 * v;
-                    if (t < room) {
-                        const size_t r = (row0 + t) * a.heads + w.h;
-                        const float dg = s + back[v] + (front[v] - own[v]);
-                        a.dg[r] = from_f32<__nv_bfloat16>(t < cnt ? dg : 0.f);
-                        a.dbeta[r] = from_f32<__nv_bfloat16>(t < cnt ? m.db[t] / (m.beta[t] * m.beta[t]) : 0.f);
-                    }
-                }
-            }
-            ++n;
+            ++n;                                           // a failed wait shows at the next barrier
         }
-        if (tid == 0) tma_store_wait_read();
     }
     tc_fence_before();
     __syncthreads();
