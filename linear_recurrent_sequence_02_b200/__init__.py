@@ -804,9 +804,9 @@ def retnet_residual_norm_backward(x: torch.Tensor, y: torch.Tensor, dn: torch.Te
         dgate = torch.empty_like(x) if dgate is None else _dev(dgate, "dgate", x.dtype, x.shape)
     dpost = None if post_weight is None else torch.empty_like(post_weight)
     dpre = None if pre_weight is None else torch.empty_like(pre_weight)
-    if workspace is None:
-        workspace = retnet_workspace(retnet_residual_norm_backward_workspace_size(rows, hidden),
-                                     x.device)
+    if workspace is None:              # the allocator's 512-byte alignment is enough here
+        workspace = torch.empty(retnet_residual_norm_backward_workspace_size(rows, hidden),
+                                dtype=torch.uint8, device=x.device)
     else:
         _dev(workspace, "workspace", torch.uint8)
     _one_device(x, dn, dh, dx, dy, dgate, workspace)

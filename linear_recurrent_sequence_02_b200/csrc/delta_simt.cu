@@ -20,6 +20,7 @@
 //     rows, so that the chain is nine shuffles and no barrier (1000 tokens of
 //     128 x 64: 650 us in slabs of 32 columns, 190 us so).
 #include "delta.cuh"
+#include "pairs.cuh"
 
 namespace retnet {
 
@@ -323,140 +324,201 @@ delta_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
 // save: x (kSweepSave) or r (kSweepReverse), float32 [B, n, H, dv];
 // marks: the state before (D behind) every chunk of kDeltaChunk tokens,
 // float32 [B, H, chunks, dk, dv].
+// N neighbouring values of a row.
+template <int N, typename T>
+__device__ __forceinline__ void load_row(T (&x)[N], const T *p) {
+    constexpr int kBytes = N * (int)sizeof(T);
+    if constexpr (kBytes == 4) {
+        *reinterpret_cast<uint32_t *>(x) = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (kBytes == 8) {
+        *reinterpret_cast<uint2 *>(x) = *reinterpret_cast<const uint2 *>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i)
+            reinterpret_cast<uint4 *>(x)[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+}
 constexpr int kWalkWarps = 4, kWalkCols = 4;         // columns per warp
 constexpr int kWalkAhead = 4;                        // tokens loaded ahead
 
 template <typename T, int DK, DeltaSweep kSweep>
-__global__ void __launch_bounds__(32 * kWalkWarps)
-delta_walk_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-                  const T *__restrict__ g, const T *__restrict__ beta,
-                  const int *__restrict__ lengths, const float *state_in, float *state_out,
-                  T *__restrict__ out, float *__restrict__ save, float *__restrict__ marks,
-                  float scale, int heads, int key_heads, int tokens, int dv) {
-    constexpr int RPL = DK / 32;                     // rows lane, lane + 32, ...
+__device__ __forceinline__ void delta_walk(const T *__restrict__ q, const T *__restrict__ k,
+                                           const T *__restrict__ v, const T *__restrict__ g,
+                                           const T *__restrict__ beta,
+                                           const int *__restrict__ lengths, const float *state_in,
+                                           float *state_out, T *__restrict__ out,
+                                           float *__restrict__ save, float *__restrict__ marks,
+                                           float scale, int heads, int key_heads, int tokens,
+                                           int dv, int cta) {
+    constexpr int RPL = DK / 32;                     // rows RPL lane, RPL lane + 1, ...
     constexpr bool kFwd = kSweep == kSweepForward, kRev = kSweep == kSweepReverse;
     const int slabs = dv / (kWalkWarps * kWalkCols);
-    const int bh = blockIdx.x / slabs;
+    const int bh = cta / slabs;
     const int b = bh / heads, h = bh % heads, kh = h / (heads / key_heads);
     const int lane = threadIdx.x % 32;
-    const int col = (blockIdx.x % slabs) * (kWalkWarps * kWalkCols) + (threadIdx.x / 32) * kWalkCols;
+    const int col = (cta % slabs) * (kWalkWarps * kWalkCols) + (threadIdx.x / 32) * kWalkCols;
 
     grid_dependency_wait();
     const int n = delta_tokens_of(lengths, b, tokens);
     const int nc = (tokens + kDeltaChunk - 1) / kDeltaChunk;
-    const size_t row0 = (size_t)b * tokens, sbase = (size_t)bh * DK * dv + col;
-    float4 s[RPL];
+    const size_t sbase = ((size_t)bh * DK + RPL * lane) * dv + col;
+    float2 s[RPL][2];
 #pragma unroll
-    for (int i = 0; i < RPL; ++i)
-        s[i] = state_in ? load_f4(state_in + sbase + (size_t)(lane + 32 * i) * dv)
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < RPL; ++i) {
+        const float4 x = state_in ? load_f4(state_in + sbase + (size_t)i * dv) : make_float4(0.f, 0.f, 0.f, 0.f);
+        s[i][0] = make_float2(x.x, x.y);
+        s[i][1] = make_float2(x.z, x.w);
+    }
+    auto store_state = [&](float *dst) {
+#pragma unroll
+        for (int i = 0; i < RPL; ++i)
+            store_f4(dst + (size_t)i * dv, make_float4(s[i][0].x, s[i][0].y, s[i][1].x, s[i][1].y));
+    };
 
+    // the tokens ahead, as they lie in memory; pointers step along the walk
     struct Token {
-        float k[RPL], q[RPL], g, b, qk;
-        float4 v;
+        alignas(16) T k[RPL];
+        alignas(16) T q[RPL];
+        alignas(16) T v[4];
+        T g, b;
     } ahead[kWalkAhead];
-    auto load = [&](Token &w, int step) {            // the step-th token of the walk
-        if (step >= n) return;
-        const size_t t = row0 + (kRev ? n - 1 - step : step);
-        const size_t o = (t * key_heads + kh) * (size_t)DK + lane;
-#pragma unroll
-        for (int i = 0; i < RPL; ++i) {
-            w.k[i] = to_f32(k[o + 32 * i]);
-            w.q[i] = kSweep == kSweepSave ? 0.f : to_f32(q[o + 32 * i]);
+    const long long dir = kRev ? -1 : 1;
+    const size_t start = (size_t)b * tokens + (kRev ? max(n - 1, 0) : 0);
+    const T *kp = k + (start * key_heads + kh) * DK + RPL * lane;
+    const T *qp = q + (start * key_heads + kh) * DK + RPL * lane;
+    const T *vp = v + (start * heads + h) * dv + col;
+    const T *gp = g + start * heads + h, *bp = beta + start * heads + h;
+    const long long kstep = dir * key_heads * DK, vstep = dir * heads * dv, gstep = dir * heads;
+    auto load = [&](Token &w, bool more) {
+        if (more) {
+            load_row<RPL>(w.k, kp);
+            if (kSweep != kSweepSave) load_row<RPL>(w.q, qp);
+            load_row<4>(w.v, vp);
+            w.g = *gp;
+            w.b = *bp;
+            kp += kstep;
+            qp += kstep;
+            vp += vstep;
+            gp += gstep;
+            bp += gstep;
         }
-        w.v = load_f4(v + (t * heads + h) * (size_t)dv + col);
-        w.g = to_f32(g[t * heads + h]);
-        w.b = to_f32(beta[t * heads + h]);
-    };
-    auto dot = [&](Token &w) {                       // q.k, off the chain
-        if (kSweep == kSweepSave) return;
-        float d = 0.f;
-#pragma unroll
-        for (int i = 0; i < RPL; ++i) d = fmaf(w.q[i], w.k[i], d);
-#pragma unroll
-        for (int m = 16; m; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
-        w.qk = d;
     };
 #pragma unroll
-    for (int u = 0; u < kWalkAhead; ++u) load(ahead[u], u);
+    for (int u = 0; u < kWalkAhead; ++u) load(ahead[u], u < n);
+    size_t vo = (start * heads + h) * dv + col;
     for (int s0 = 0; s0 < n; s0 += kWalkAhead) {
 #pragma unroll
         for (int u = 0; u < kWalkAhead; ++u) {
             const int step = s0 + u;
             if (step >= n) break;
-            Token w = ahead[u];
-            load(ahead[u], step + kWalkAhead);
-            dot(w);
-            const int t = kRev ? n - 1 - step : step;
-            if (!kFwd && (kRev ? step == 0 || t % kDeltaChunk == kDeltaChunk - 1 : t % kDeltaChunk == 0)) {
-                float *m = marks + ((size_t)bh * nc + t / kDeltaChunk) * DK * dv + col;
-#pragma unroll
-                for (int i = 0; i < RPL; ++i) store_f4(m + (size_t)(lane + 32 * i) * dv, s[i]);
-            }
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
+            float wk[RPL], wq[RPL];
 #pragma unroll
             for (int i = 0; i < RPL; ++i) {
-                fma4(y, w.k[i], s[i]);
-                if (kFwd) fma4(z, w.q[i], s[i]);
+                wk[i] = to_f32(ahead[u].k[i]);
+                if (kSweep != kSweepSave) wq[i] = to_f32(ahead[u].q[i]);
+            }
+            const float2 v0 = make_float2(to_f32(ahead[u].v[0]), to_f32(ahead[u].v[1]));
+            const float2 v1 = make_float2(to_f32(ahead[u].v[2]), to_f32(ahead[u].v[3]));
+            const float a = expf(to_f32(ahead[u].g)), bt0 = to_f32(ahead[u].b);
+            const float bt = kSweep == kSweepSave ? nonzero_beta(bt0) : bt0;
+            load(ahead[u], step + kWalkAhead < n);
+            if (!kFwd) {
+                const int t = kRev ? n - 1 - step : step;
+                if (kRev ? step == 0 || t % kDeltaChunk == kDeltaChunk - 1 : t % kDeltaChunk == 0)
+                    store_state(marks + (((size_t)bh * nc + t / kDeltaChunk) * DK + RPL * lane) * dv + col);
+            }
+            float2 y0 = both(0.f), y1 = y0, z0 = y0, z1 = y0;
+            float d = 0.f;                           // q.k
+#pragma unroll
+            for (int i = 0; i < RPL; ++i) {
+                y0 = fma2(both(wk[i]), s[i][0], y0);
+                y1 = fma2(both(wk[i]), s[i][1], y1);
+                if (kFwd) {
+                    z0 = fma2(both(wq[i]), s[i][0], z0);
+                    z1 = fma2(both(wq[i]), s[i][1], z1);
+                }
+                if (kSweep != kSweepSave) d = fmaf(wq[i], wk[i], d);
             }
             // sums over the lanes: a lane gives away the half of the values
-            // that it does not keep, so that it ends with one
-            float e0, e1;
+            // that it does not keep, so that it ends with one; q.k goes along
+            auto pass = [](float x, int m) { return __shfl_xor_sync(0xffffffffu, x, m); };
             if (kFwd) {                              // lanes 0-15 y, 16-31 z
                 const bool up = lane & 16;
-                y.x = (up ? z.x : y.x) + __shfl_xor_sync(0xffffffffu, up ? y.x : z.x, 16);
-                y.y = (up ? z.y : y.y) + __shfl_xor_sync(0xffffffffu, up ? y.y : z.y, 16);
-                y.z = (up ? z.z : y.z) + __shfl_xor_sync(0xffffffffu, up ? y.z : z.z, 16);
-                y.w = (up ? z.w : y.w) + __shfl_xor_sync(0xffffffffu, up ? y.w : z.w, 16);
+                const float2 k0 = up ? z0 : y0, k1 = up ? z1 : y1, g0 = up ? y0 : z0, g1 = up ? y1 : z1;
+                y0 = add2(k0, make_float2(pass(g0.x, 16), pass(g0.y, 16)));
+                y1 = add2(k1, make_float2(pass(g1.x, 16), pass(g1.y, 16)));
             }
+            if (kSweep != kSweepSave) d += pass(d, 16);
             const bool far = lane & 8, odd = lane & 4;
-            e0 = (far ? y.z : y.x) + __shfl_xor_sync(0xffffffffu, far ? y.x : y.z, 8);
-            e1 = (far ? y.w : y.y) + __shfl_xor_sync(0xffffffffu, far ? y.y : y.w, 8);
-            e0 = (odd ? e1 : e0) + __shfl_xor_sync(0xffffffffu, odd ? e0 : e1, 4);
-            if (!kFwd) e0 += __shfl_xor_sync(0xffffffffu, e0, 16);
-            e0 += __shfl_xor_sync(0xffffffffu, e0, 2);
-            e0 += __shfl_xor_sync(0xffffffffu, e0, 1);
-            y.x = __shfl_sync(0xffffffffu, e0, 0);
-            y.y = __shfl_sync(0xffffffffu, e0, 4);
-            y.z = __shfl_sync(0xffffffffu, e0, 8);
-            y.w = __shfl_sync(0xffffffffu, e0, 12);
-            const float a = expf(w.g), bt = kSweep == kSweepSave ? nonzero_beta(w.b) : w.b;
-            float4 x;
+            const float2 k2 = far ? y1 : y0, g2 = far ? y0 : y1;
+            const float2 h2 = add2(k2, make_float2(pass(g2.x, 8), pass(g2.y, 8)));
+            if (kSweep != kSweepSave) d += pass(d, 8);
+            float e = (odd ? h2.y : h2.x) + pass(odd ? h2.x : h2.y, 4);
+            if (kSweep != kSweepSave) d += pass(d, 4);
+            if (!kFwd) e += pass(e, 16);
+            e += pass(e, 2);
+            if (kSweep != kSweepSave) d += pass(d, 2);
+            e += pass(e, 1);
+            if (kSweep != kSweepSave) d += pass(d, 1);
+            y0 = make_float2(__shfl_sync(0xffffffffu, e, 0), __shfl_sync(0xffffffffu, e, 4));
+            y1 = make_float2(__shfl_sync(0xffffffffu, e, 8), __shfl_sync(0xffffffffu, e, 12));
+            float2 x0, x1;
             if (kRev) {
-                x = y;
-                fma4(x, scale * w.qk, w.v);                        // r
-                const float4 xb = scale4(-bt, x);
+                x0 = fma2(both(scale * d), v0, y0);                // r
+                x1 = fma2(both(scale * d), v1, y1);
+                const float2 b0 = mul2(both(-bt), x0), b1 = mul2(both(-bt), x1);
+                const float2 o0 = mul2(both(scale), v0), o1 = mul2(both(scale), v1);
 #pragma unroll
                 for (int i = 0; i < RPL; ++i) {
-                    fma4(s[i], scale * w.q[i], w.v);
-                    fma4(s[i], w.k[i], xb);
-                    s[i] = scale4(a, s[i]);
+                    s[i][0] = mul2(both(a), fma2(both(wk[i]), b0, fma2(both(wq[i]), o0, s[i][0])));
+                    s[i][1] = mul2(both(a), fma2(both(wk[i]), b1, fma2(both(wq[i]), o1, s[i][1])));
                 }
             } else {
-                x = w.v;
-                fma4(x, -a, y);
-                x = scale4(bt, x);
+                x0 = mul2(both(bt), fma2(both(-a), y0, v0));
+                x1 = mul2(both(bt), fma2(both(-a), y1, v1));
 #pragma unroll
                 for (int i = 0; i < RPL; ++i) {
-                    s[i] = scale4(a, s[i]);
-                    fma4(s[i], w.k[i], x);
+                    s[i][0] = fma2(both(wk[i]), x0, mul2(both(a), s[i][0]));
+                    s[i][1] = fma2(both(wk[i]), x1, mul2(both(a), s[i][1]));
                 }
             }
-            const size_t vo = ((row0 + t) * heads + h) * (size_t)dv + col;
             if (kFwd) {
                 // lanes 16, 20, 24, 28 hold z of columns 0 .. 3
-                const float xe = far ? (odd ? x.w : x.z) : (odd ? x.y : x.x);
-                if ((lane & 19) == 16)
-                    out[vo + (lane - 16) / 4] = from_f32<T>(scale * fmaf(w.qk, xe, a * e0));
+                const float xe = far ? (odd ? x1.y : x1.x) : (odd ? x0.y : x0.x);
+                if ((lane & 19) == 16) out[vo + (lane - 16) / 4] = from_f32<T>(scale * fmaf(d, xe, a * e));
             } else if (lane == 0) {
-                store_f4(save + vo, x);
+                store_f4(save + vo, make_float4(x0.x, x0.y, x1.x, x1.y));
             }
+            vo += vstep;
         }
     }
-    if (kFwd && state_out && (n > 0 || state_out != state_in)) {
-#pragma unroll
-        for (int i = 0; i < RPL; ++i) store_f4(state_out + sbase + (size_t)(lane + 32 * i) * dv, s[i]);
-    }
+    if (kFwd && state_out && (n > 0 || state_out != state_in)) store_state(state_out + sbase);
+}
+
+template <typename T, int DK>
+__global__ void __launch_bounds__(32 * kWalkWarps)
+delta_walk_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                  const T *__restrict__ g, const T *__restrict__ beta,
+                  const int *__restrict__ lengths, const float *state_in, float *state_out,
+                  T *__restrict__ out, float scale, int heads, int key_heads, int tokens, int dv) {
+    delta_walk<T, DK, kSweepForward>(q, k, v, g, beta, lengths, state_in, state_out, out, nullptr,
+                                     nullptr, scale, heads, key_heads, tokens, dv, blockIdx.x);
+}
+// The backward's two sweeps: neither needs the other, so they share a launch.
+template <typename T, int DK>
+__global__ void __launch_bounds__(32 * kWalkWarps)
+delta_sweeps_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                    const T *__restrict__ d_out, const T *__restrict__ g, const T *__restrict__ beta,
+                    const int *__restrict__ lengths, float *xs, float *ss, float *rs, float *ds,
+                    float scale, int heads, int key_heads, int tokens, int dv) {
+    const int half = gridDim.x / 2;
+    if ((int)blockIdx.x < half)
+        delta_walk<T, DK, kSweepSave>(q, k, v, g, beta, lengths, nullptr, nullptr, nullptr, xs, ss,
+                                      scale, heads, key_heads, tokens, dv, blockIdx.x);
+    else
+        delta_walk<T, DK, kSweepReverse>(q, k, d_out, g, beta, lengths, nullptr, nullptr, nullptr,
+                                         rs, ds, scale, heads, key_heads, tokens, dv,
+                                         blockIdx.x - half);
 }
 
 // ------------------------------------------------------------------ gradients
@@ -783,14 +845,24 @@ delta_share_kernel(const float *__restrict__ dq_wide, const float *__restrict__ 
 }
 
 // ------------------------------------------------------------------ launches
-template <typename T, int DK, DeltaSweep kSweep>
-static cudaError_t launch_walk(const DeltaArgs &a, const void *v, float *save, float *marks,
-                               cudaStream_t stream) {
-    const size_t grid = (size_t)a.batch * a.heads * (a.dv / (kWalkWarps * kWalkCols));
-    return launch_overlapped(delta_walk_kernel<T, DK, kSweep>, dim3((unsigned)grid),
+static size_t walk_ctas(const DeltaArgs &a) {
+    return (size_t)a.batch * a.heads * (a.dv / (kWalkWarps * kWalkCols));
+}
+template <typename T, int DK>
+static cudaError_t launch_walk(const DeltaArgs &a, cudaStream_t stream) {
+    return launch_overlapped(delta_walk_kernel<T, DK>, dim3((unsigned)walk_ctas(a)),
                              dim3(32 * kWalkWarps), 0, stream, (const T *)a.q, (const T *)a.k,
-                             (const T *)v, (const T *)a.g, (const T *)a.beta, a.lengths,
-                             a.state_in, a.state_out, (T *)a.out, save, marks, a.scale, a.heads,
+                             (const T *)a.v, (const T *)a.g, (const T *)a.beta, a.lengths,
+                             a.state_in, a.state_out, (T *)a.out, a.scale, a.heads, a.key_heads,
+                             a.seqlen, a.dv);
+}
+template <typename T, int DK>
+static cudaError_t launch_sweeps(const DeltaArgs &a, float *xs, float *ss, float *rs, float *ds,
+                                 cudaStream_t stream) {
+    return launch_overlapped(delta_sweeps_kernel<T, DK>, dim3((unsigned)(2 * walk_ctas(a))),
+                             dim3(32 * kWalkWarps), 0, stream, (const T *)a.q, (const T *)a.k,
+                             (const T *)a.v, (const T *)a.d_out, (const T *)a.g,
+                             (const T *)a.beta, a.lengths, xs, ss, rs, ds, a.scale, a.heads,
                              a.key_heads, a.seqlen, a.dv);
 }
 template <typename T, int DK>
@@ -816,32 +888,33 @@ static cudaError_t launch_tokens(const DeltaArgs &a, cudaStream_t stream) {
 
 #define RETNET_DELTA_CASES(CALL, ...)                                            \
     if (a.dtype == RETNET_BF16) switch (a.dk) {                                  \
-            case 64: return CALL<__nv_bfloat16, 64 __VA_ARGS__;                  \
-            case 128: return CALL<__nv_bfloat16, 128 __VA_ARGS__;                \
-            default: return CALL<__nv_bfloat16, 256 __VA_ARGS__;                 \
+            case 64: return CALL<__nv_bfloat16, 64>(__VA_ARGS__);                \
+            case 128: return CALL<__nv_bfloat16, 128>(__VA_ARGS__);              \
+            default: return CALL<__nv_bfloat16, 256>(__VA_ARGS__);               \
         }                                                                        \
     switch (a.dk) {                                                              \
-        case 64: return CALL<float, 64 __VA_ARGS__;                              \
-        case 128: return CALL<float, 128 __VA_ARGS__;                            \
-        default: return CALL<float, 256 __VA_ARGS__;                             \
+        case 64: return CALL<float, 64>(__VA_ARGS__);                            \
+        case 128: return CALL<float, 128>(__VA_ARGS__);                          \
+        default: return CALL<float, 256>(__VA_ARGS__);                           \
     }
-
-template <DeltaSweep kSweep>
-static cudaError_t launch_sweep(const char *name, const DeltaArgs &a, const void *v, float *save,
-                                float *marks, cudaStream_t stream) {
-    KernelTimer timer(name, stream);
-    count_launch();
-    RETNET_DELTA_CASES(launch_walk, , kSweep>(a, v, save, marks, stream))
-}
 
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, cudaStream_t stream) {
     KernelTimer timer(a.seqlen == 1 ? "delta_step" : "delta_tokens", stream);
     count_launch();
-    RETNET_DELTA_CASES(launch_tokens, >(a, stream))
+    RETNET_DELTA_CASES(launch_tokens, a, stream)
 }
 
 cudaError_t launch_delta_walk(const DeltaArgs &a, cudaStream_t stream) {
-    return launch_sweep<kSweepForward>("delta_walk", a, a.v, nullptr, nullptr, stream);
+    KernelTimer timer("delta_walk", stream);
+    count_launch();
+    RETNET_DELTA_CASES(launch_walk, a, stream)
+}
+
+static cudaError_t sweep(const DeltaArgs &a, float *xs, float *ss, float *rs, float *ds,
+                         cudaStream_t stream) {
+    KernelTimer timer("delta_sweeps", stream);
+    count_launch();
+    RETNET_DELTA_CASES(launch_sweeps, a, xs, ss, rs, ds, stream)
 }
 
 static size_t up1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
@@ -913,11 +986,8 @@ cudaError_t launch_delta_share(const DeltaArgs &a, const float *dq_wide, const f
 cudaError_t launch_delta_backward_simt(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
     const DeltaGradLayout l = grad_layout(a.batch, a.heads, a.key_heads, a.seqlen, a.dk, a.dv);
     char *ws = (char *)workspace;
-    cudaError_t e = launch_sweep<kSweepSave>("delta_forward_sweep", a, a.v, (float *)(ws + l.x),
-                                             (float *)(ws + l.s), stream);
-    if (e != cudaSuccess) return e;
-    e = launch_sweep<kSweepReverse>("delta_reverse_sweep", a, a.d_out, (float *)(ws + l.r),
-                                    (float *)(ws + l.d), stream);
+    cudaError_t e = sweep(a, (float *)(ws + l.x), (float *)(ws + l.s), (float *)(ws + l.r),
+                          (float *)(ws + l.d), stream);
     if (e != cudaSuccess) return e;
     return a.dtype == RETNET_BF16 ? launch_grad<__nv_bfloat16>(a, l, ws, stream)
                                   : launch_grad<float>(a, l, ws, stream);

@@ -1108,7 +1108,7 @@ delta_walks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 // (*: whatever precedes the operand in shared memory; those rows are not read.)
 // Persistent, a CTA an SM: the copies of the next chunk run beside the pairs
 // and the epilogue of this one (a CTA a chunk, 2048 chunks of 128 x 128: 175
-// us, persistent 98 us).
+// us, persistent 100 us).
 constexpr int kGradTcThreads = 352;        // warps 0-7 rows, 8 copies, 9 MMAs, 10 gates and sums
 
 struct DeltaGradTcBars {
