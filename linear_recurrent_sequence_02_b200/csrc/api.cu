@@ -599,7 +599,7 @@ retnet_status retnet_delta_workspace_size(const retnet_delta_shape *shape, retne
     if (st != RETNET_OK) return st;
     const bool tensor = delta_tensor(shape, algo);
     if (algo == RETNET_ALGO_TENSOR && !tensor) return RETNET_ERR_UNSUPPORTED;
-    *bytes = tensor ? delta_tc_workspace(shape->batch, shape->heads, shape->seqlen, shape->dk) : 0;
+    *bytes = tensor ? delta_tc_workspace(shape->batch, shape->heads, shape->seqlen, shape->dk, shape->dv) : 0;
     return RETNET_OK;
 }
 

@@ -493,12 +493,31 @@ struct DeltaScanArgs {
     __nv_bfloat16 *x_save, *s_save;        // kSave: X^T, S^T of every chunk (keep_row)
     int heads, key_heads, tokens, nc, dv;
     unsigned *err;
+    // walks in segments (delta_segments_kernel)
+    int segments, segment;                 // how many, and chunks of each
+    float *starts, *units;
 };
+// What one CTA walks: chunks [first, last) of (sequence, head) bh with the
+// columns v0 .. of the state, from `from` (may be null: zero) to `to` (may be
+// null), both [dk, width].  unit: the state starts as the identity and no
+// values are written, so that it ends as the segment's transition.
+struct DeltaWalk {
+    int bh, v0, first, last, width;
+    const float *from;
+    float *to;
+    bool out, unit;
+};
+__device__ __forceinline__ DeltaWalk whole_walk(const DeltaScanArgs &a, int dk, int cta, bool out) {
+    const int slabs = (a.dv + 127) / 128, bh = cta / slabs;
+    const size_t at = (size_t)bh * dk * a.dv;
+    return {bh, (cta % slabs) * 128, 0, a.nc, a.dv, a.state_in ? a.state_in + at : nullptr,
+            a.state_out ? a.state_out + at : nullptr, out, false};
+}
 
 template <int DK, bool kSplit, bool kOut, bool kSave>
 __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                              const CUtensorMap &tm_o, const DeltaScanArgs &a,
-                                             int cta) {
+                                             const DeltaWalk &w) {
     using Smem = DeltaScanSmem<DK, kSplit>;
     using Block = DeltaBlock<DK, kSplit>;
     using Tm = DeltaScanTmem<DK, kSplit>;
@@ -509,9 +528,9 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
 
     // warp-uniform as the compiler sees it
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    const int slabs = (a.dv + 127) / 128;
-    const int bh = cta / slabs, v0 = (cta % slabs) * 128;
+    const int bh = w.bh, v0 = w.v0;
     const int b = bh / a.heads, h = bh % a.heads;
+    const bool out = kOut && w.out;
     unsigned *err = a.err;
     int *abort_flag = &bar.abort_flag;
 
@@ -544,27 +563,29 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
     // constant it keeps the MMAs' operands out of general registers.
     constexpr uint32_t tmem = 0;
     grid_dependency_wait();
-    const int n = delta_tokens_of(a.lengths, b, a.tokens);
-    const int nc = (n + kC - 1) / kC;
+    const int n = delta_tokens_of(a.lengths, b, a.tokens) - w.first * kC;   // from the first chunk on
+    const int nc = max(0, min(w.last - w.first, (n + kC - 1) / kC));
 
     int it = 0;                                            // chunks whose copies were issued
     if (warp == 0) {
         const int kh = h / (a.heads / a.key_heads);
-        const uint8_t *blocks = a.blocks + (size_t)bh * a.nc * Block::kBytes;
+        const uint8_t *blocks = a.blocks + ((size_t)bh * a.nc + w.first) * Block::kBytes;
         for (; it < nc; ++it) {
             const int s = it & 1;
             if (it >= 2 && !warp_spin_wait(&bar.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
             uint8_t *st = smem + s * Smem::kStage;
             if (elect_one()) {
-                constexpr uint32_t kBlock = kOut ? Block::kBytes : Block::kQ;
-                mbar_expect_tx(&bar.full[s], kBlock + Smem::kStage - Smem::kK);
-                bulk_load(st, blocks + (size_t)it * Block::kBytes, kBlock, &bar.full[s]);
+                const uint32_t block = out ? Block::kBytes : Block::kQ;
+                const int t0 = (w.first + it) * kC;
+                mbar_expect_tx(&bar.full[s], block + (w.unit ? Smem::kV : Smem::kStage) - Smem::kK);
+                bulk_load(st, blocks + (size_t)it * Block::kBytes, block, &bar.full[s]);
+                if (!w.unit)
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    tma_load_4d(st + Smem::kV + x * kBox64, &tm_v, &bar.full[s], v0 + 64 * x, h, it * kC, b);
+                    for (int x = 0; x < 2; ++x)
+                        tma_load_4d(st + Smem::kV + x * kBox64, &tm_v, &bar.full[s], v0 + 64 * x, h, t0, b);
 #pragma unroll
                 for (int x = 0; x < DK / 64; ++x)
-                    tma_load_4d(st + Smem::kK + x * kBox64, &tm_k, &bar.full[s], 64 * x, kh, it * kC, b);
+                    tma_load_4d(st + Smem::kK + x * kBox64, &tm_k, &bar.full[s], 64 * x, kh, t0, b);
             }
             __syncwarp();
         }
@@ -581,7 +602,7 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
             if (!warp_spin_wait(&bar.full[s], (c >> 1) & 1, abort_flag, err)) break;
             if (n - c * kC < kC) clear_rows(st + Smem::kK, DK / 64 + 2, n - c * kC, lane);
             tc_fence_after();
-            if (elect_one()) {
+            if (!w.unit && elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
                     const uint64_t ad = mnmaj + ((Smem::kV + ks * 2048) >> 4);
@@ -602,10 +623,10 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                     for (int k4 = 0; k4 < 4; ++k4) {
                         const int ks = 4 * p + k4;
                         const uint32_t o = p * kBox64 + k4 * 32;
-                        const uint64_t w = kmaj + ((Block::kW + o) >> 4);
-                        mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kShi + 8 * ks, w, id_x, 1);
+                        const uint64_t wd = kmaj + ((Block::kW + o) >> 4);
+                        mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kShi + 8 * ks, wd, id_x, ks > 0 || !w.unit);
                         if (kSplit) {
-                            mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kSlo + 8 * ks, w, id_x, 1);
+                            mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kSlo + 8 * ks, wd, id_x, 1);
                             mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kShi + 8 * ks,
                                         kmaj + ((Block::kWlo + o) >> 4), id_x, 1);
                         }
@@ -615,7 +636,7 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                 __syncwarp();
             }
             if (!ok) break;
-            if (kOut) {
+            if (out) {
                 if (c > 0 && !warp_spin_wait(&bar.o_free, (c - 1) & 1, abort_flag, err)) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -641,7 +662,7 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                     }
                     mma_commit(&bar.z_full[p]);
                 }
-                if (kOut) {
+                if (out) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         mma_bf16_ts(tmem + Tm::kO, tmem + Tm::kXb + 8 * ks,
@@ -655,16 +676,18 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
     } else if (warp < 10) {
         const int wg = (warp - 2) / 4;                     // k columns 64 p + 32 wg ..
         const int v = v0 + 32 * (warp % 4) + lane;
-        const bool live = v < a.dv;
+        const bool live = v < w.width;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
-        const size_t sbase = ((size_t)bh * DK + 32 * wg) * a.dv + v;
+        const size_t sbase = (size_t)(32 * wg) * w.width + v;
         float2 S[kPieces][16];
 #pragma unroll
         for (int p = 0; p < kPieces; ++p)
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const float *src = a.state_in + sbase + (size_t)(64 * p + 2 * j) * a.dv;
-                S[p][j] = a.state_in && live ? make_float2(src[0], src[a.dv]) : both(0.f);
+                const int k = 64 * p + 32 * wg + 2 * j;
+                const float *src = w.from + sbase + (size_t)(64 * p + 2 * j) * w.width;
+                S[p][j] = w.unit ? make_float2(k == v ? 1.f : 0.f, k + 1 == v ? 1.f : 0.f)
+                          : w.from && live ? make_float2(src[0], src[w.width]) : both(0.f);
             }
         // the operand copies of a piece of S; c: the chunk that starts with it
         auto put_state = [&](int p, int c) {
@@ -728,16 +751,16 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
             }
             if (!ok) break;
         }
-        if (a.state_out && live)
+        if (w.to && live)
 #pragma unroll
             for (int p = 0; p < kPieces; ++p)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    float *dst = a.state_out + sbase + (size_t)(64 * p + 2 * j) * a.dv;
+                    float *dst = w.to + sbase + (size_t)(64 * p + 2 * j) * w.width;
                     dst[0] = S[p][j].x;
-                    dst[a.dv] = S[p][j].y;
+                    dst[w.width] = S[p][j].y;
                 }
-    } else if (kOut) {
+    } else if (out) {
         // O through shared memory, token rows of 64 channels (the swizzle of
         // the copy out), so that global memory sees whole lines
         const int col = 32 * (warp % 4) + lane, tid = threadIdx.x - 320;
@@ -763,7 +786,7 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                 if (tid == 0) {
                     for (int x = 0; x < 2; ++x)
                         if (v0 + 64 * x < a.dv)
-                            tma_store_4d(&tm_o, smem + Smem::kOut + x * kBox64, v0 + 64 * x, h, c * kC, b);
+                            tma_store_4d(&tm_o, smem + Smem::kOut + x * kBox64, v0 + 64 * x, h, (w.first + c) * kC, b);
                     tma_store_commit();
                 }
             } else {                                       // rows behind the sequence stay
@@ -771,7 +794,7 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                     const int r = i / 16, ch = i % 16;
                     if (v0 + ch * 8 < a.dv)
                         *reinterpret_cast<uint4 *>(
-                            a.out + (((size_t)b * a.tokens + c * kC + r) * a.heads + h) * a.dv + v0 + ch * 8) =
+                            a.out + (((size_t)b * a.tokens + (w.first + c) * kC + r) * a.heads + h) * a.dv + v0 + ch * 8) =
                             *reinterpret_cast<const uint4 *>(smem + Smem::kOut + (ch / 8) * kBox64 + r * 128 +
                                                              (((ch & 7) ^ (r & 7)) << 4));
                 }
@@ -800,7 +823,98 @@ template <int DK, bool kSplit>
 __global__ void __launch_bounds__(kScanThreads, 1)
 delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_o, DeltaScanArgs a) {
-    forward_walk<DK, kSplit, true, false>(tm_k, tm_v, tm_o, a, blockIdx.x);
+    forward_walk<DK, kSplit, true, false>(tm_k, tm_v, tm_o, a, whole_walk(a, DK, blockIdx.x, true));
+}
+
+// ---- in segments
+// With few (sequence, head)s and many chunks most SMs would have no walk.  A
+// segment of chunks maps the state before it to the state behind it by
+// S -> M S + N, so: first all segments' M (a walk from the identity without
+// values) and N (a walk from zero without output) at once, and the first
+// segment as it is; then the states between segments, S_{j+1} = M_j S_j + N_j,
+// in float32; then all other segments' outputs at once.  Each chunk is walked
+// up to three times, but on all SMs: 8192 tokens and 16 heads of 128 in 6
+// segments, walk 283 us whole, 120 us so.
+// starts [segments - 1][BH][dk, dv]: N_j and then the state before segment
+// j + 1; units [segments - 2][BH][dk, dk]: M of segments 1 ...
+template <int DK>
+__global__ void __launch_bounds__(kScanThreads, 1)
+delta_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap tm_o, DeltaScanArgs a, int bhs, int last) {
+    const int slabs = (a.dv + 127) / 128, walks = bhs * slabs;
+    const size_t ssize = (size_t)DK * a.dv;
+    int cta = blockIdx.x;
+    DeltaWalk w;
+    if (last) {                                            // outputs of segments 1 ...
+        const int seg = 1 + cta / walks;
+        w = whole_walk(a, DK, cta % walks, true);
+        w.from = a.starts + ((size_t)(seg - 1) * bhs + w.bh) * ssize;
+        if (seg < a.segments - 1) w.to = nullptr;
+        w.first = seg * a.segment;
+    } else if (cta < walks) {                              // segment 0
+        w = whole_walk(a, DK, cta, true);
+        w.to = a.starts + (size_t)w.bh * ssize;
+    } else if (cta < walks * (a.segments - 1)) {           // N of segments 1 ...
+        const int seg = cta / walks;
+        w = whole_walk(a, DK, cta % walks, false);
+        w.from = nullptr;
+        w.to = a.starts + ((size_t)seg * bhs + w.bh) * ssize;
+        w.first = seg * a.segment;
+    } else {                                               // M of segments 1 ...
+        cta -= walks * (a.segments - 1);
+        const int seg = 1 + cta / bhs;
+        w.bh = cta % bhs;
+        w.v0 = 0;
+        w.width = DK;
+        w.from = nullptr;
+        w.to = a.units + ((size_t)(seg - 1) * bhs + w.bh) * DK * DK;
+        w.out = false;
+        w.unit = true;
+        w.first = seg * a.segment;
+    }
+    w.last = w.first + a.segment;
+    forward_walk<DK, true, true, false>(tm_k, tm_v, tm_o, a, w);
+}
+
+// starts[j] <- starts[j] + M_j starts[j - 1], j = 1 ..: a CTA takes 16 columns
+// of a (sequence, head)'s states, two threads a row.
+constexpr int kJoinCols = 16;
+template <int DK>
+__global__ void __launch_bounds__(2 * DK)
+delta_join_kernel(float *starts, const float *units, int bhs, int dv, int joins) {
+    extern __shared__ __align__(16) float join_smem[];
+    float *M = join_smem, *S = join_smem + DK * (DK + 1);          // [DK][DK + 1], [DK][16]
+    const int bh = blockIdx.x / (dv / kJoinCols), col = (blockIdx.x % (dv / kJoinCols)) * kJoinCols;
+    const int r = threadIdx.x / 2, c = (threadIdx.x % 2) * 8;
+    const size_t at = (size_t)r * dv + col + c;
+    grid_dependency_wait();
+    float s[8];
+    load8(starts + (size_t)bh * DK * dv + at, s);
+    for (int j = 1; j <= joins; ++j) {
+        store8(&S[r * kJoinCols + c], s);
+        const float *m = units + ((size_t)(j - 1) * bhs + bh) * DK * DK;
+#pragma unroll 8
+        for (int i = threadIdx.x * 4; i < DK * DK; i += 2 * DK * 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(m + i);
+            float *d = &M[(i / DK) * (DK + 1) + i % DK];
+            d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
+        }
+        float *dst = starts + ((size_t)j * bhs + bh) * DK * dv + at;
+        load8(dst, s);
+        __syncthreads();
+#pragma unroll 8
+        for (int k = 0; k < DK; ++k) {
+            const float x = M[r * (DK + 1) + k];
+            const float4 a = *reinterpret_cast<const float4 *>(&S[k * kJoinCols + c]);
+            const float4 b = *reinterpret_cast<const float4 *>(&S[k * kJoinCols + c + 4]);
+            s[0] = fmaf(x, a.x, s[0]); s[1] = fmaf(x, a.y, s[1]);
+            s[2] = fmaf(x, a.z, s[2]); s[3] = fmaf(x, a.w, s[3]);
+            s[4] = fmaf(x, b.x, s[4]); s[5] = fmaf(x, b.y, s[5]);
+            s[6] = fmaf(x, b.z, s[6]); s[7] = fmaf(x, b.w, s[7]);
+        }
+        store8(dst, s);
+        __syncthreads();
+    }
 }
 
 // ------------------------------------------------------------------ reverse scan
@@ -1087,7 +1201,8 @@ delta_walks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                    const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dv,
                    DeltaScanArgs f, DeltaReverseArgs r) {
     const int half = gridDim.x / 2;
-    if ((int)blockIdx.x < half) forward_walk<DK, false, false, true>(tm_k, tm_v, tm_v, f, blockIdx.x);
+    if ((int)blockIdx.x < half)
+        forward_walk<DK, false, false, true>(tm_k, tm_v, tm_v, f, whole_walk(f, DK, blockIdx.x, false));
     else reverse_walk<DK>(tm_k, tm_do, tm_dv, r, blockIdx.x - half);
 }
 
@@ -1677,6 +1792,48 @@ cudaError_t launch_prep(const DeltaArgs &a, int nc, uint8_t *blocks, bool backwa
                              sizeof(DeltaPrepSmem<DK, kSplit>), stream, p);
 }
 
+// Segments of the walk over nc chunks: the count with the least chunks walked
+// behind one another (waves of 148 CTAs, first pass and second), if that is a
+// gain over the whole walk.  Against the two extra launches and the states
+// between count as 8 chunks, and 2 a segment.  16 heads, 128 chunks: 6
+// segments; from 75 walks on, or below 24 chunks, 1.
+int delta_segments(int batch, int heads, int nc, int dv) {
+    const long long units = (long long)batch * heads, walks = units * ((dv + 127) / 128);
+    auto waves = [](long long ctas) { return (ctas + 147) / 148; };
+    long long best = waves(walks) * nc * 4 / 5;
+    int count = 1;
+    for (int s = 3; s <= 16 && 4 * s <= nc; ++s) {
+        const long long cost = (waves(walks + (s - 2) * (walks + units)) + waves(walks * (s - 1))) * ((nc + s - 1) / s) + 8 + 2 * s;
+        if (cost < best) {
+            best = cost;
+            count = s;
+        }
+    }
+    return count;
+}
+
+struct DeltaTcLayout {
+    int nc, segments, segment;
+    size_t starts, units, total;
+};
+DeltaTcLayout tc_layout(int batch, int heads, int seqlen, int dk, int dv) {
+    DeltaTcLayout l;
+    l.nc = (seqlen + kC - 1) / kC;
+    l.segments = delta_segments(batch, heads, l.nc, dv);
+    l.segment = (l.nc + l.segments - 1) / l.segments;
+    const size_t bh = (size_t)batch * heads;
+    l.starts = bh * l.nc * (dk == 64 ? DeltaBlock<64, true>::kBytes : DeltaBlock<128, true>::kBytes);
+    l.units = l.starts + (l.segments > 1 ? (size_t)(l.segments - 1) * bh * dk * dv * 4 : 0);
+    l.total = l.units + (l.segments > 1 ? (size_t)(l.segments - 2) * bh * dk * dk * 4 : 0);
+    return l;
+}
+
+bool scan_maps(const DeltaArgs &a, CUtensorMap *k, CUtensorMap *v, CUtensorMap *o) {
+    return token_map(k, a.k, a.batch, a.seqlen, a.key_heads, a.dk) &&
+           token_map(v, a.v, a.batch, a.seqlen, a.heads, a.dv) &&
+           token_map(o, a.out, a.batch, a.seqlen, a.heads, a.dv);
+}
+
 template <int DK, bool kSplit>
 cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, cudaStream_t stream) {
     using Smem = DeltaScanSmem<DK, kSplit>;
@@ -1685,18 +1842,52 @@ cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, cudaS
                                          (int)Smem::kBytes);
     if (e != cudaSuccess) return e;
     CUtensorMap tm_k, tm_v, tm_o;
-    if (!token_map(&tm_k, a.k, a.batch, a.seqlen, a.key_heads, a.dk) ||
-        !token_map(&tm_v, a.v, a.batch, a.seqlen, a.heads, a.dv) ||
-        !token_map(&tm_o, a.out, a.batch, a.seqlen, a.heads, a.dv))
-        return cudaErrorInvalidValue;
+    if (!scan_maps(a, &tm_k, &tm_v, &tm_o)) return cudaErrorInvalidValue;
     DeltaScanArgs s = {blocks, a.lengths, a.state_in, a.state_out, (__nv_bfloat16 *)a.out, nullptr,
-                       nullptr, a.heads, a.key_heads, a.seqlen, nc, a.dv, device_error_word()};
+                       nullptr, a.heads, a.key_heads, a.seqlen, nc, a.dv, device_error_word(),
+                       1, nc, nullptr, nullptr};
     const int slabs = (a.dv + 127) / 128;
     KernelTimer timer("delta_scan", stream);
     count_launch();
     return launch_overlapped(delta_scan_kernel<DK, kSplit>,
                              dim3((unsigned)(a.batch * a.heads * slabs)), dim3(kScanThreads),
                              Smem::kBytes, stream, tm_k, tm_v, tm_o, s);
+}
+
+template <int DK>
+cudaError_t launch_segments(const DeltaArgs &a, const DeltaTcLayout &l, uint8_t *ws, cudaStream_t stream) {
+    using Smem = DeltaScanSmem<DK, true>;
+    constexpr int kJoinBytes = (DK * (DK + 1) + DK * kJoinCols) * 4;
+    cudaError_t e = cudaFuncSetAttribute(delta_segments_kernel<DK>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Smem::kBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(delta_join_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinBytes);
+    if (e != cudaSuccess) return e;
+    CUtensorMap tm_k, tm_v, tm_o;
+    if (!scan_maps(a, &tm_k, &tm_v, &tm_o)) return cudaErrorInvalidValue;
+    float *starts = (float *)(ws + l.starts), *units = (float *)(ws + l.units);
+    DeltaScanArgs s = {ws, a.lengths, a.state_in, a.state_out, (__nv_bfloat16 *)a.out, nullptr,
+                       nullptr, a.heads, a.key_heads, a.seqlen, l.nc, a.dv, device_error_word(),
+                       l.segments, l.segment, starts, units};
+    const int bhs = a.batch * a.heads, walks = bhs * ((a.dv + 127) / 128);
+    auto pass = [&](int ctas, int last) {
+        KernelTimer timer("delta_segments", stream);
+        count_launch();
+        return launch_overlapped(delta_segments_kernel<DK>, dim3((unsigned)ctas), dim3(kScanThreads),
+                                 Smem::kBytes, stream, tm_k, tm_v, tm_o, s, bhs, last);
+    };
+    e = pass(walks * (l.segments - 1) + bhs * (l.segments - 2), 0);
+    if (e != cudaSuccess) return e;
+    {
+        KernelTimer timer("delta_join", stream);
+        count_launch();
+        e = launch_overlapped(delta_join_kernel<DK>, dim3((unsigned)(bhs * (a.dv / kJoinCols))),
+                              dim3(2 * DK), kJoinBytes, stream, starts, (const float *)units, bhs,
+                              a.dv, l.segments - 2);
+        if (e != cudaSuccess) return e;
+    }
+    return pass(walks * (l.segments - 1), 1);
 }
 
 size_t up1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
@@ -1744,7 +1935,7 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
                                  (int)Smem::kBytes);
         if (e != cudaSuccess) return e;
         DeltaScanArgs f = {ws + l.blocks, a.lengths, nullptr, nullptr, nullptr, xs, ss, a.heads,
-                           a.key_heads, a.seqlen, nc, a.dv, device_error_word()};
+                           a.key_heads, a.seqlen, nc, a.dv, device_error_word(), 1, nc, nullptr, nullptr};
         DeltaReverseArgs r = {ws + l.blocks, a.lengths, ds, a.heads, a.key_heads, a.seqlen, nc, a.dv,
                               device_error_word()};
         KernelTimer timer("delta_walks", stream);
@@ -1773,12 +1964,20 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
     return launch_delta_share(a, dq_wide, dk_wide, stream);
 }
 
-template <int DK, bool kSplit>
+// The walk in segments carries every state between them in float32, and the
+// products of a segment's transition with it, so it takes operands in two
+// parts whether or not the final state is asked for.
+template <int DK>
 cudaError_t launch_forward(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
-    const int nc = (a.seqlen + kC - 1) / kC;
-    cudaError_t e = launch_prep<DK, kSplit>(a, nc, (uint8_t *)workspace, false, stream);
+    const DeltaTcLayout l = tc_layout(a.batch, a.heads, a.seqlen, DK, a.dv);
+    uint8_t *ws = (uint8_t *)workspace;
+    const bool split = a.state_out || l.segments > 1;
+    cudaError_t e = split ? launch_prep<DK, true>(a, l.nc, ws, false, stream)
+                          : launch_prep<DK, false>(a, l.nc, ws, false, stream);
     if (e != cudaSuccess) return e;
-    return launch_scan<DK, kSplit>(a, nc, (const uint8_t *)workspace, stream);
+    if (l.segments > 1) return launch_segments<DK>(a, l, ws, stream);
+    return split ? launch_scan<DK, true>(a, l.nc, ws, stream)
+                 : launch_scan<DK, false>(a, l.nc, ws, stream);
 }
 
 }  // namespace
@@ -1796,17 +1995,13 @@ bool delta_tc_shape_ok(int dk, int dv, retnet_dtype dtype) {
     return dtype == RETNET_BF16 && (dk == 64 || dk == 128) && dv >= 64;
 }
 
-size_t delta_tc_workspace(int batch, int heads, int seqlen, int dk) {
-    const size_t chunks = (size_t)batch * heads * ((seqlen + kC - 1) / kC);
-    return chunks * (dk == 64 ? DeltaBlock<64, true>::kBytes : DeltaBlock<128, true>::kBytes);
+size_t delta_tc_workspace(int batch, int heads, int seqlen, int dk, int dv) {
+    return tc_layout(batch, heads, seqlen, dk, dv).total;
 }
 
 cudaError_t launch_delta_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
-    if (a.dk == 64)
-        return a.state_out ? launch_forward<64, true>(a, workspace, stream)
-                           : launch_forward<64, false>(a, workspace, stream);
-    return a.state_out ? launch_forward<128, true>(a, workspace, stream)
-                       : launch_forward<128, false>(a, workspace, stream);
+    return a.dk == 64 ? launch_forward<64>(a, workspace, stream)
+                      : launch_forward<128>(a, workspace, stream);
 }
 
 }  // namespace retnet

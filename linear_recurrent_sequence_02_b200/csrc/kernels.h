@@ -157,7 +157,7 @@ size_t delta_backward_simt_workspace(int batch, int heads, int key_heads, int se
 cudaError_t launch_delta_backward_simt(const DeltaArgs &a, void *workspace, cudaStream_t stream);
 // delta_tc.cu: bf16, dk 64 or 128.
 bool delta_tc_shape_ok(int dk, int dv, retnet_dtype dtype);
-size_t delta_tc_workspace(int batch, int heads, int seqlen, int dk);
+size_t delta_tc_workspace(int batch, int heads, int seqlen, int dk, int dv);
 cudaError_t launch_delta_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream);
 size_t delta_backward_tc_workspace(int batch, int heads, int key_heads, int seqlen, int dk, int dv);
 cudaError_t launch_delta_backward_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream);

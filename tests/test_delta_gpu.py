@@ -195,6 +195,32 @@ def test_chunkwise_lengths(rn, dtype, dk, dv):
     assert err(S, St, 1) < 3e-5
 
 
+@pytest.mark.parametrize("dk,dv,H", [(128, 128, 2), (64, 256, 1), (128, 64, 3)])
+def test_chunkwise_long_with_few_heads(rn, dk, dv, H):
+    """Long enough for a walk in segments (4000 tokens, few heads), uneven
+    lengths that end in different segments, the state updated in place."""
+    B, n = 3, 4000
+    (q, k, v, g, beta, _), ref = make(22, B, n, 1, H, dk, dv, "bf16", decay=0.02)
+    lens = [4000, 0, 1500]
+    for x, r in zip((q, k, v, g, beta), ref):
+        for b, c in enumerate(lens):
+            x[b, c:] = float("nan")
+            r[b, c:] = 0.0
+    lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    S, S0 = states(23, B, H, dk, dv)
+    out, plain = torch.full_like(v, 5.0), torch.full_like(v, 5.0)
+    rn.retnet_delta_chunkwise(q, k, v, g, beta, lengths=lengths, state_in=S, out=plain)
+    rn.retnet_delta_chunkwise(q, k, v, g, beta, lengths=lengths, state_in=S, state_out=S, out=out)
+    done(rn)
+    o, St = oracle.delta_recurrent(*ref[:5], dk ** -0.5, S0, lens)
+    for b, c in enumerate(lens):
+        assert (out[b, c:] == 5).all() and (plain[b, c:] == 5).all()
+        out[b, c:] = plain[b, c:] = 0
+    assert err(out, o) < bound("bf16", True) and err(plain, o) < bound("bf16", True)
+    # a state passes through the segments before it in two more parts each way
+    assert err(S, St, 1) < 3e-5
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_chunkwise_gates_at_their_ends(rn, dtype):
     """g: -inf (the state is emptied), 0, and far below what float32 resolves;
