@@ -162,6 +162,49 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], const void *
                  : "r"(smem_u32(p)));
 }
 
+// Rows 16 RB .. and 16-column tiles T0 .. T0 + NT - 1 of M or P.
+template <int DK, bool kSplit, int RB, int T0, int NT>
+__device__ __forceinline__ void pair_tiles(DeltaPrepSmem<DK, kSplit> &m, bool isP, float scale, int lane) {
+    using Block = DeltaBlock<DK, kSplit>;
+    const uint8_t *Kt = m.block + Block::kW, *At = isP ? m.block + Block::kQ : Kt;
+    const int gr = lane / 4, tq = lane % 4;
+    float acc[2 * NT][4] = {};
+#pragma unroll
+    for (int k0 = 0; k0 < DK; k0 += 16) {
+        uint32_t av[4];
+        ldmatrix_x4(av, At + tile_off(16 * RB + (lane & 15), k0 + 8 * (lane >> 4)));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            uint32_t bv[4];
+            ldmatrix_x4(bv, Kt + tile_off(16 * (T0 + t) + (lane & 7) + ((lane >> 4) << 3),
+                                          k0 + 8 * ((lane >> 3) & 1)));
+            mma16816(acc[2 * t], av, bv[0], bv[1]);
+            mma16816(acc[2 * t + 1], av, bv[2], bv[3]);
+        }
+    }
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+        const int i = 16 * RB + gr + 8 * hf;
+        const float f = isP ? scale : m.beta[i], far = f * m.in[i];
+#pragma unroll
+        for (int t = 0; t < 2 * NT; ++t) {
+            const int j = 16 * T0 + 8 * t + 2 * tq;
+            float2 w = make_float2(acc[t][2 * hf], acc[t][2 * hf + 1]);
+            if (T0 + t / 2 < RB) {
+                w = mul2(mul2(w, both(far)), *reinterpret_cast<const float2 *>(&m.across[RB > 0 ? RB - 1 : 0][j]));
+            } else {                                       // M has no diagonal
+                w = mul2(mul2(w, both(f)), *reinterpret_cast<const float2 *>(&m.diag[i][j & 15]));
+                if (!isP && i == j) w.x = 0.f;
+                if (!isP && i == j + 1) w.y = 0.f;
+            }
+            if (isP)
+                *reinterpret_cast<uint32_t *>(m.block + Block::kP + tile_off(i, j)) = pack_bf16x2(w.x, w.y);
+            else
+                *reinterpret_cast<float2 *>(&m.M[i][j]) = w;
+        }
+    }
+}
+
 // An 8-column tile of sign A B for 16 rows of A (both kMPad wide, K columns
 // deep) by one warp, in three tf32 products (x = hi + lo, lo lo left out:
 // 2^-22), to C.
@@ -200,7 +243,7 @@ __device__ __forceinline__ void square_tile(const float *A, const float *B, floa
 }
 
 template <int DK, bool kSplit>
-__global__ void __launch_bounds__(kPrepThreads, kSplit ? 2 : 3)
+__global__ void __launch_bounds__(kPrepThreads, DK == 128 && kSplit ? 2 : 3)
 delta_prep_kernel(DeltaPrepArgs a) {
     using Block = DeltaBlock<DK, kSplit>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -267,6 +310,13 @@ delta_prep_kernel(DeltaPrepArgs a) {
         const int j = t - (blk == 1 ? 0 : blk == 2 ? 16 : 48);
         m.across[blk - 1][j] = expf(m.G.until(j, blk - 1));
     }
+    {   // above the diagonal: P, and M where its triangles' inverses are multiplied
+        const int r = tid / 4;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            *reinterpret_cast<uint4 *>(m.block + Block::kP + tid * 32 + 16 * u) = make_uint4(0, 0, 0, 0);
+        if ((r & 16) == 0) *reinterpret_cast<float4 *>(&m.M[r][(r & 32) + 16 + 4 * (tid % 4)]) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int i = tid / 4, j = 4 * (tid % 4) + u;
@@ -274,51 +324,15 @@ delta_prep_kernel(DeltaPrepArgs a) {
     }
     __syncthreads();
 
-    {   // warps 0-3: M from K K^T, warps 4-7: P from Q K^T; 16 rows each, up to the diagonal
-        const int rb = warp & 3;
-        const bool isP = warp >= 4;
-        const uint8_t *At = isP ? Qt : Kt;
-        float acc[8][4];
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
-#pragma unroll
-        for (int k0 = 0; k0 < DK; k0 += 16) {
-            uint32_t av[4];
-            ldmatrix_x4(av, At + tile_off(16 * rb + (lane & 15), k0 + 8 * (lane >> 4)));
-#pragma unroll
-            for (int t2 = 0; t2 < 4; ++t2)
-                if (t2 <= rb) {
-                    uint32_t bv[4];
-                    ldmatrix_x4(bv, Kt + tile_off(16 * t2 + (lane & 7) + ((lane >> 4) << 3),
-                                                  k0 + 8 * ((lane >> 3) & 1)));
-                    mma16816(acc[2 * t2], av, bv[0], bv[1]);
-                    mma16816(acc[2 * t2 + 1], av, bv[2], bv[3]);
-                }
-        }
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const int i = 16 * rb + gr + 8 * hf;
-            const float f = (isP ? a.scale : m.beta[i]), far = f * m.in[i];
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const int j = 8 * t + 2 * tq;
-                const float2 x = make_float2(acc[t][2 * hf], acc[t][2 * hf + 1]);
-                float2 w = both(0.f);
-                if (t / 2 < rb)
-                    w = mul2(mul2(x, both(far)), *reinterpret_cast<const float2 *>(&m.across[rb - 1][j]));
-                else if (t / 2 == rb) {                    // M has no diagonal
-                    w = mul2(mul2(x, both(f)), *reinterpret_cast<const float2 *>(&m.diag[i][j & 15]));
-                    if (!isP && i == j) w.x = 0.f;
-                    if (!isP && i == j + 1) w.y = 0.f;
-                }
-                if (isP)
-                    *reinterpret_cast<uint32_t *>(m.block + Block::kP + tile_off(i, j)) = pack_bf16x2(w.x, w.y);
-                else
-                    *reinterpret_cast<float2 *>(&m.M[i][j]) = w;
-            }
-        }
+    // warps 0-3: M from K K^T, warps 4-7: P from Q K^T, two or three of the ten
+    // 16 x 16 tiles up to the diagonal each
+    switch (warp & 3) {
+        case 0: pair_tiles<DK, kSplit, 3, 0, 2>(m, warp >= 4, a.scale, lane); break;
+        case 1: pair_tiles<DK, kSplit, 3, 2, 2>(m, warp >= 4, a.scale, lane); break;
+        case 2: pair_tiles<DK, kSplit, 2, 0, 3>(m, warp >= 4, a.scale, lane); break;
+        default:
+            pair_tiles<DK, kSplit, 1, 0, 2>(m, warp >= 4, a.scale, lane);
+            pair_tiles<DK, kSplit, 0, 0, 1>(m, warp >= 4, a.scale, lane);
     }
     __syncthreads();
     if (warp < 4) {
@@ -834,7 +848,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 // segment as it is; then the states between segments, S_{j+1} = M_j S_j + N_j,
 // in float32; then all other segments' outputs at once.  Each chunk is walked
 // up to three times, but on all SMs: 8192 tokens and 16 heads of 128 in 6
-// segments, walk 283 us whole, 120 us so.
+// segments, walk 283 us whole, 145 us so with the join.
 // starts [segments - 1][BH][dk, dv]: N_j and then the state before segment
 // j + 1; units [segments - 2][BH][dk, dk]: M of segments 1 ...
 template <int DK>
@@ -877,44 +891,66 @@ delta_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
 }
 
 // starts[j] <- starts[j] + M_j starts[j - 1], j = 1 ..: a CTA takes 16 columns
-// of a (sequence, head)'s states, two threads a row.
+// of a (sequence, head)'s states, a thread 8 rows of one; the next M is copied
+// while this one is used (4 joins for 16 heads of 128: 28 us without, 20 with).
 constexpr int kJoinCols = 16;
 template <int DK>
 __global__ void __launch_bounds__(2 * DK)
 delta_join_kernel(float *starts, const float *units, int bhs, int dv, int joins) {
     extern __shared__ __align__(16) float join_smem[];
-    float *M = join_smem, *S = join_smem + DK * (DK + 1);          // [DK][DK + 1], [DK][16]
+    float *S = join_smem + 2 * DK * DK;                    // M twice [row][k], S [k][16]
     const int bh = blockIdx.x / (dv / kJoinCols), col = (blockIdx.x % (dv / kJoinCols)) * kJoinCols;
-    const int r = threadIdx.x / 2, c = (threadIdx.x % 2) * 8;
+    const int c = threadIdx.x % kJoinCols, r = (threadIdx.x / kJoinCols) * 8;
     const size_t at = (size_t)r * dv + col + c;
     grid_dependency_wait();
-    float s[8];
-    load8(starts + (size_t)bh * DK * dv + at, s);
+    auto fetch = [&](int j) {
+        if (j <= joins) {
+            const float *m = units + ((size_t)(j - 1) * bhs + bh) * DK * DK;
+            float *dst = join_smem + (j & 1) * DK * DK;
+#pragma unroll 8
+            for (int i = threadIdx.x * 4; i < DK * DK; i += 2 * DK * 4)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst + i)), "l"(m + i) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(1);
+    float s[8], next[8] = {};
+    auto get = [&](int j, float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = starts[((size_t)j * bhs + bh) * DK * dv + at + (size_t)i * dv];
+    };
+    get(0, s);
+    if (joins > 0) get(1, next);
     for (int j = 1; j <= joins; ++j) {
-        store8(&S[r * kJoinCols + c], s);
-        const float *m = units + ((size_t)(j - 1) * bhs + bh) * DK * DK;
-#pragma unroll 8
-        for (int i = threadIdx.x * 4; i < DK * DK; i += 2 * DK * 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(m + i);
-            float *d = &M[(i / DK) * (DK + 1) + i % DK];
-            d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
+        fetch(j + 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            S[(r + i) * kJoinCols + c] = s[i];
+            s[i] = next[i];
         }
-        float *dst = starts + ((size_t)j * bhs + bh) * DK * dv + at;
-        load8(dst, s);
+        if (j < joins) get(j + 1, next);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
-#pragma unroll 8
-        for (int k = 0; k < DK; ++k) {
-            const float x = M[r * (DK + 1) + k];
-            const float4 a = *reinterpret_cast<const float4 *>(&S[k * kJoinCols + c]);
-            const float4 b = *reinterpret_cast<const float4 *>(&S[k * kJoinCols + c + 4]);
-            s[0] = fmaf(x, a.x, s[0]); s[1] = fmaf(x, a.y, s[1]);
-            s[2] = fmaf(x, a.z, s[2]); s[3] = fmaf(x, a.w, s[3]);
-            s[4] = fmaf(x, b.x, s[4]); s[5] = fmaf(x, b.y, s[5]);
-            s[6] = fmaf(x, b.z, s[6]); s[7] = fmaf(x, b.w, s[7]);
+        const float *M = join_smem + (j & 1) * DK * DK + r * DK;
+#pragma unroll 4
+        for (int k = 0; k < DK; k += 4) {
+            float x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = S[(k + u) * kJoinCols + c];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 m = *reinterpret_cast<const float4 *>(M + i * DK + k);
+                s[i] = fmaf(m.x, x[0], s[i]);
+                s[i] = fmaf(m.y, x[1], s[i]);
+                s[i] = fmaf(m.z, x[2], s[i]);
+                s[i] = fmaf(m.w, x[3], s[i]);
+            }
         }
-        store8(dst, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) starts[((size_t)j * bhs + bh) * DK * dv + at + (size_t)i * dv] = s[i];
         __syncthreads();
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ reverse scan
@@ -1857,7 +1893,7 @@ cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, cudaS
 template <int DK>
 cudaError_t launch_segments(const DeltaArgs &a, const DeltaTcLayout &l, uint8_t *ws, cudaStream_t stream) {
     using Smem = DeltaScanSmem<DK, true>;
-    constexpr int kJoinBytes = (DK * (DK + 1) + DK * kJoinCols) * 4;
+    constexpr int kJoinBytes = (2 * DK * DK + DK * kJoinCols) * 4;
     cudaError_t e = cudaFuncSetAttribute(delta_segments_kernel<DK>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Smem::kBytes);
