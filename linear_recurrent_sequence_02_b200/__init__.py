@@ -214,6 +214,9 @@ def _dtype_code(t: torch.Tensor) -> int:
 def _dev(t: Optional[torch.Tensor], name: str, dtype=None, shape=None):
     if t is None:
         return None
+    if (type(t) is torch.Tensor and t.is_cuda and t.is_contiguous() and
+            (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:

@@ -18,7 +18,9 @@
 //     the float32 backward), bound by the latency of the chain product ->
 //     reduction -> update from token to token: a warp owns 4 columns and all
 //     rows, so that the chain is nine shuffles and no barrier (1000 tokens of
-//     128 x 64: 650 us in slabs of 32 columns, 190 us so).
+//     128 x 64: 650 us in slabs of 32 columns, 265 us so; four tokens a turn
+//     by the triangle between them gained a tenth forward and lost it back:
+//     one warp a scheduler is then bound by its instructions).
 #include "delta.cuh"
 #include "pairs.cuh"
 

@@ -363,7 +363,7 @@ residual_norm_backward_kernel(NormArgs a) {
 }
 
 // out[c] = sum of `parts` partial rows, in a fixed order.
-constexpr int kSumCols = 32, kSumLanes = 16;
+constexpr int kSumCols = 32, kSumLanes = 32;
 __global__ void __launch_bounds__(kSumCols *kSumLanes)
 norm_weight_sum_kernel(const float *part_post, const float *part_pre, float *dpost, float *dpre,
                        int parts, int hidden) {
@@ -375,7 +375,7 @@ norm_weight_sum_kernel(const float *part_post, const float *part_pre, float *dpo
     if (!out) return;
     float s = 0.f;
     if (c < hidden)
-#pragma unroll 4
+#pragma unroll 8
         for (int p = r; p < parts; p += kSumLanes) s += part[(size_t)p * hidden + c];
     red[r][threadIdx.x % kSumCols] = s;
     __syncthreads();
