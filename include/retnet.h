@@ -390,8 +390,9 @@ typedef struct retnet_delta_shape {
 
 /* Recurrent form: one decode step (seqlen = 1) or a run of tokens, with the
  * state read and written once per call and updated in place.  A sequence of
- * length 0 keeps its state.  Work grows with seqlen on CUDA cores; for long
- * runs use retnet_delta_chunkwise.  out must not overlap the inputs.
+ * length 0 keeps its state.  Float32 arithmetic; a run of tokens gives what
+ * its single steps give up to the order of float32 sums.  Work grows with
+ * seqlen on CUDA cores; for long runs use retnet_delta_chunkwise.  out must not overlap the inputs.
  * Errors: INVALID_ARG, UNSUPPORTED (dk/dv), CUDA. */
 RETNET_API retnet_status retnet_delta_recurrent(const void *q, const void *k, const void *v,
                                                 const void *g, const void *beta, float scale,
@@ -402,7 +403,10 @@ RETNET_API retnet_status retnet_delta_recurrent(const void *q, const void *k, co
 /* Prefill: all tokens of a batch, with an optional state before the first
  * (NULL: zero) and after the last token (NULL: not wanted; may equal
  * state_in).  RETNET_ALGO_SIMT runs the recurrent form; the tensor-core path
- * works in chunks of 64 tokens, for bf16 with dk 64 or 128.  out must not
+ * works in chunks of 64 tokens, for bf16 with dk 64 or 128; AUTO takes it
+ * there for all but a few tokens.  On the tensor-core path operands are
+ * rounded to bf16 on the way to `out`, and a final state keeps float32
+ * accuracy.  out must not
  * overlap the inputs, the states or the workspace.
  *   workspace  retnet_delta_workspace_size() bytes, 1024-byte aligned.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */

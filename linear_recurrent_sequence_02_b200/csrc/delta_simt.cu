@@ -7,20 +7,19 @@
 //   reverse   D is the gradient of the state behind a token:
 //             r = k D + scale (k.q) do;  D <- a (D + scale q^T do - b k^T r).
 //             r is the gradient of x; dv = b r.
-// Three kernels hold S in registers in float32:
+// Two kernels hold S in registers in float32:
 //   delta_step_kernel    one token (decode): an HBM stream of 8 dk dv bytes a
-//     head.  CTA (sequence, head, 32 columns) as in the retention step: 8
-//     float4 column groups by 32 row lanes, a column's row lanes reduced by
-//     shuffles and then over the eight warps in shared memory.
-//   delta_tokens_kernel  a few tokens, with the same arithmetic in the same
-//     order, so that a run equals its single steps bit for bit.
-//   delta_walk_kernel    long runs (the float32 prefill and the two sweeps of
-//     the float32 backward), bound by the latency of the chain product ->
-//     reduction -> update from token to token: a warp owns 4 columns and all
-//     rows, so that the chain is nine shuffles and no barrier (1000 tokens of
-//     128 x 64: 650 us in slabs of 32 columns, 265 us so; four tokens a turn
-//     by the triangle between them gained a tenth forward and lost it back:
-//     one warp a scheduler is then bound by its instructions).
+//     head.  A CTA takes 32 columns as the retention step does: 8 float4
+//     column groups by 32 row lanes, a column's row lanes reduced by shuffles
+//     and then over the eight warps in shared memory.
+//   delta_walk_kernel    more tokens (multi-token decode, the float32 prefill,
+//     short bf16 ones, and the two sweeps of the float32 backward), bound by
+//     the latency of the chain product -> reduction -> update from token to
+//     token: a warp owns 4 columns and all rows, so that the chain is nine
+//     shuffles and no barrier (1000 tokens of 128 x 64: 650 us in slabs of 32
+//     columns, 265 us so; four tokens a turn by the triangle between them
+//     gained a tenth forward and lost it back: one warp a scheduler is then
+//     bound by its instructions).
 #include "delta.cuh"
 #include "pairs.cuh"
 
@@ -30,7 +29,6 @@ constexpr int kDeltaThreads = 256;
 constexpr int kDeltaCols = 32;                 // state columns per CTA
 constexpr int kDeltaGroups = kDeltaCols / 4;   // float4 column groups
 constexpr int kDeltaLanes = kDeltaThreads / kDeltaGroups;   // 32 row lanes
-constexpr int kDeltaStage = 8;                 // tokens staged in shared memory at a time
 
 enum DeltaSweep { kSweepForward, kSweepSave, kSweepReverse };
 
@@ -75,8 +73,7 @@ __device__ __forceinline__ void reduce_row_lanes(float4 &a) {
     }
 }
 
-// ---- the arithmetic of a token that the step and the run of tokens share
-// (explicit fused operations: nothing is contracted differently in the two)
+// ---- one token in slabs of 32 columns
 
 // q.k by one warp.
 template <int DK, typename R>
@@ -87,25 +84,6 @@ __device__ __forceinline__ float token_dot(const R *q, const R *k, int lane) {
 #pragma unroll
     for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
     return dot;
-}
-// q and k rows (of row krow of their tensors), q.k, the decay and the write
-// strength (of element row), by one warp.
-template <typename T, int DK>
-__device__ __forceinline__ void stage_token(const T *q, const T *k, const T *g, const T *beta,
-                                            size_t krow, size_t row, int lane, float *qs, float *ks,
-                                            float &qk, float &al, float &be) {
-#pragma unroll
-    for (int j = 0; j < DK / 32; ++j) {
-        ks[lane + 32 * j] = to_f32(k[krow * DK + lane + 32 * j]);
-        qs[lane + 32 * j] = to_f32(q[krow * DK + lane + 32 * j]);
-    }
-    __syncwarp();
-    const float dot = token_dot<DK>(qs, ks, lane);
-    if (lane == 0) {
-        qk = dot;
-        al = expf(to_f32(g[row]));
-        be = to_f32(beta[row]);
-    }
 }
 // This warp's part of y = k S and z = q S.
 template <int RPL, typename R>
@@ -150,66 +128,6 @@ __device__ __forceinline__ float4 token_output(const float4 (*red)[kDeltaGroups]
     float4 o = scale4(a, z);
     fma4(o, qk, x);
     return scale4(scale, o);
-}
-
-// v [batch, tokens, heads, dv]; the state is updated in place.
-template <typename T, int DK>
-__global__ void __launch_bounds__(kDeltaThreads)
-delta_tokens_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-                    const T *__restrict__ g, const T *__restrict__ beta,
-                    const int *__restrict__ lengths, float *state, T *__restrict__ out,
-                    float scale, int heads, int key_heads, int tokens, int dv) {
-    constexpr int RPL = DK / kDeltaLanes;            // rows per thread: 2, 4 or 8
-    const int slabs = dv / kDeltaCols;
-    const int bh = blockIdx.x / slabs;
-    const int b = bh / heads, h = bh % heads;
-    const int cg = threadIdx.x % kDeltaGroups, rl = threadIdx.x / kDeltaGroups;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int col = (blockIdx.x % slabs) * kDeltaCols + cg * 4;
-
-    __shared__ float qs[kDeltaStage][DK], ks[kDeltaStage][DK];
-    __shared__ float qk[kDeltaStage], al[kDeltaStage], be[kDeltaStage];
-    __shared__ float4 red[2][2][kDeltaThreads / 32][kDeltaGroups];
-
-    grid_dependency_wait();
-    const int n = delta_tokens_of(lengths, b, tokens);
-    if (n == 0) return;                              // the whole CTA
-    float *S = state + (size_t)bh * DK * dv + col;
-    float4 s[RPL];
-#pragma unroll
-    for (int i = 0; i < RPL; ++i) s[i] = load_f4(S + (size_t)(rl + i * kDeltaLanes) * dv);
-
-    const size_t row0 = (size_t)b * tokens;
-    const int kh = h / (heads / key_heads);
-    int flip = 0;
-    for (int g0 = 0; g0 < n; g0 += kDeltaStage) {
-        const int cnt = min(kDeltaStage, n - g0);
-        float4 vv[kDeltaStage];
-#pragma unroll
-        for (int u = 0; u < kDeltaStage; ++u)
-            if (u < cnt) vv[u] = load_f4(v + ((row0 + g0 + u) * heads + h) * (size_t)dv + col);
-        if (warp < cnt)                              // warp u stages token u
-            stage_token<T, DK>(q, k, g, beta, (row0 + g0 + warp) * key_heads + kh,
-                               (row0 + g0 + warp) * heads + h, lane, qs[warp], ks[warp], qk[warp],
-                               al[warp], be[warp]);
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kDeltaStage; ++u) {
-            if (u < cnt) {
-                token_products<RPL>(s, qs[u], ks[u], rl, lane, red[flip][0][warp], red[flip][1][warp]);
-                __syncthreads();
-                const float a = al[u];
-                const float4 x = token_update<RPL>(s, ks[u], rl, red[flip][0], cg, vv[u], a, be[u]);
-                if (warp == u && lane < kDeltaGroups)
-                    store_f4(out + ((row0 + g0 + u) * heads + h) * (size_t)dv + col,
-                             token_output(red[flip][1], cg, x, a, qk[u], scale));
-                flip ^= 1;
-            }
-        }
-        __syncthreads();                             // the stage is rewritten
-    }
-#pragma unroll
-    for (int i = 0; i < RPL; ++i) store_f4(S + (size_t)(rl + i * kDeltaLanes) * dv, s[i]);
 }
 
 // One token; q, k [batch, key_heads, DK], v, out [batch, heads, dv].
@@ -868,24 +786,16 @@ static cudaError_t launch_sweeps(const DeltaArgs &a, float *xs, float *ss, float
                              a.key_heads, a.seqlen, a.dv);
 }
 template <typename T, int DK>
-static cudaError_t launch_tokens(const DeltaArgs &a, cudaStream_t stream) {
-    const dim3 grid((unsigned)((size_t)a.batch * a.heads * (a.dv / kDeltaCols)));
-    if (a.seqlen == 1) {
-        constexpr int kBytes = (int)sizeof(DeltaStepSmem<T, DK>);
-        cudaError_t e = cudaFuncSetAttribute(delta_step_kernel<T, DK>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-        if (e != cudaSuccess) return e;
-        const unsigned resident = 148 * 3;
-        return launch_overlapped(delta_step_kernel<T, DK>, dim3(grid.x < resident ? grid.x : resident),
-                                 dim3(kDeltaThreads), kBytes, stream, (const T *)a.q,
-                                 (const T *)a.k, (const T *)a.v, (const T *)a.g, (const T *)a.beta,
-                                 a.lengths, a.state_out, (T *)a.out, a.scale, a.heads,
-                                 a.key_heads, a.dv, (int)grid.x);
-    }
-    return launch_overlapped(delta_tokens_kernel<T, DK>, grid, dim3(kDeltaThreads), 0, stream,
-                             (const T *)a.q, (const T *)a.k, (const T *)a.v, (const T *)a.g,
-                             (const T *)a.beta, a.lengths, a.state_out, (T *)a.out, a.scale,
-                             a.heads, a.key_heads, a.seqlen, a.dv);
+static cudaError_t launch_step(const DeltaArgs &a, cudaStream_t stream) {
+    constexpr int kBytes = (int)sizeof(DeltaStepSmem<T, DK>);
+    cudaError_t e = cudaFuncSetAttribute(delta_step_kernel<T, DK>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e != cudaSuccess) return e;
+    const int items = a.batch * a.heads * (a.dv / kDeltaCols), resident = 148 * 3;
+    return launch_overlapped(delta_step_kernel<T, DK>, dim3((unsigned)(items < resident ? items : resident)),
+                             dim3(kDeltaThreads), kBytes, stream, (const T *)a.q, (const T *)a.k,
+                             (const T *)a.v, (const T *)a.g, (const T *)a.beta, a.lengths,
+                             a.state_out, (T *)a.out, a.scale, a.heads, a.key_heads, a.dv, items);
 }
 
 #define RETNET_DELTA_CASES(CALL, ...)                                            \
@@ -900,10 +810,10 @@ static cudaError_t launch_tokens(const DeltaArgs &a, cudaStream_t stream) {
         default: return CALL<float, 256>(__VA_ARGS__);                           \
     }
 
-cudaError_t launch_delta_recurrent(const DeltaArgs &a, cudaStream_t stream) {
-    KernelTimer timer(a.seqlen == 1 ? "delta_step" : "delta_tokens", stream);
+cudaError_t launch_delta_step(const DeltaArgs &a, cudaStream_t stream) {
+    KernelTimer timer("delta_step", stream);
     count_launch();
-    RETNET_DELTA_CASES(launch_tokens, a, stream)
+    RETNET_DELTA_CASES(launch_step, a, stream)
 }
 
 cudaError_t launch_delta_walk(const DeltaArgs &a, cudaStream_t stream) {

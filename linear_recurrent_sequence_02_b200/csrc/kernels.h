@@ -148,9 +148,9 @@ struct DeltaArgs {
     int batch, heads, key_heads, seqlen, dk, dv;
     retnet_dtype dtype;
 };
-// Token by token, any supported shape: the recurrent form, state_in and
-// state_out the same and seqlen > 0; and the prefill.
-cudaError_t launch_delta_recurrent(const DeltaArgs &a, cudaStream_t stream);
+// Token by token, any supported shape: a single token with the state updated
+// in place (state_in and state_out the same), and runs of tokens.
+cudaError_t launch_delta_step(const DeltaArgs &a, cudaStream_t stream);
 cudaError_t launch_delta_walk(const DeltaArgs &a, cudaStream_t stream);
 size_t delta_backward_simt_workspace(int batch, int heads, int key_heads, int seqlen, int dk,
                                      int dv);

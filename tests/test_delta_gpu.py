@@ -45,8 +45,8 @@ def bound(dtype, tensor=False):
     return 2e-5 if dtype == "f32" else 1.5e-2 if tensor else 2.0 ** -8 + 2e-5
 
 
-def tensor_path(dtype, dk, algo="auto"):
-    return dtype == "bf16" and dk in (64, 128) and algo != "simt"
+def tensor_path(dtype, dk, algo="auto", n=64):
+    return dtype == "bf16" and dk in (64, 128) and algo != "simt" and (n > 16 or algo == "tensor")
 
 
 def err(got, want, head_axis=2):
@@ -114,8 +114,11 @@ def test_recurrent(rn, dtype, Hk, H, dk, dv, n):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_recurrent_run_equals_single_steps(rn, dtype):
-    B, n, H, d = 2, 11, 3, 128
+@pytest.mark.parametrize("d", [128, 256])
+def test_recurrent_run_is_its_single_steps(rn, dtype, d):
+    """Both in float32 arithmetic, sums in another order: the bound of float32
+    math, and for bf16 outputs two roundings of nearly the same value."""
+    B, n, H = 2, 11, 3
     (q, k, v, g, beta, _), _ = make(5, B, n, H, H, d, d, dtype)
     S, _ = states(8, B, H, d, d)
     S1, S2 = S.clone(), S.clone()
@@ -123,8 +126,8 @@ def test_recurrent_run_equals_single_steps(rn, dtype):
     one = [rn.retnet_delta_recurrent(*(x[:, t:t + 1].contiguous() for x in (q, k, v, g, beta)), S2)
            for t in range(n)]
     done(rn)
-    assert torch.equal(out, torch.cat(one, 1))
-    assert torch.equal(S1, S2)
+    assert err(out, torch.cat(one, 1).double().cpu().numpy()) < bound(dtype)
+    assert err(S1, S2.double().cpu().numpy(), 1) < 2e-5
 
 
 @pytest.mark.parametrize("n", [1, 5])
@@ -153,16 +156,21 @@ SHAPES = [  # B, n, Hk, H, dk, dv
 ]
 
 
-@pytest.mark.parametrize("dtype,algo", [("f32", "auto"), ("bf16", "auto"), ("bf16", "simt")])
+@pytest.mark.parametrize("dtype,algo", [("f32", "auto"), ("bf16", "auto"), ("bf16", "simt"),
+                                        ("bf16", "tensor")])
 @pytest.mark.parametrize("B,n,Hk,H,dk,dv", SHAPES)
 def test_chunkwise(rn, dtype, algo, B, n, Hk, H, dk, dv):
     (q, k, v, g, beta, _), ref = make(n, B, n, Hk, H, dk, dv, dtype)
+    if algo == "tensor" and dk == 256:              # there is none
+        with pytest.raises(rn.RetnetError):
+            rn.retnet_delta_chunkwise(q, k, v, g, beta, algo=algo)
+        return
     S, S0 = states(10, B, H, dk, dv)
     end = torch.empty_like(S)
     out = rn.retnet_delta_chunkwise(q, k, v, g, beta, state_in=S, state_out=end, algo=algo)
     plain = rn.retnet_delta_chunkwise(q, k, v, g, beta, algo=algo)
     done(rn)
-    tc = tensor_path(dtype, dk, algo)
+    tc = tensor_path(dtype, dk, algo, n)
     o, St = oracle.delta_recurrent(*ref[:5], dk ** -0.5, S0)
     assert err(out, o) < bound(dtype, tc)
     assert err(end, St, 1) < (3e-5 if tc else 2e-5)
