@@ -10,8 +10,8 @@
 //   dy  = r_y (u - y^ mean(u y^)),       u = dz post.
 // Every row is read once and written once: an HBM stream of 5 tensors
 // forward (x, y, g; h, n) and 8 backward (x, y, g, dh, dn; dx, dy, dg).  A
-// row stays in the registers of the threads that own it (a vector of 8
-// channels each, two above 8192), so the two (three) sums over the row cost
+// row stays in the registers of the threads that own it (vectors of 8
+// channels, up to 4 each forward and 2 backward), so the two (three) sums over the row cost
 // shuffles and one barrier each and nothing is read twice; h is formed from
 // x, y and g again in the backward, which reads no more than a stored h would.
 #include "kernels.h"
@@ -198,7 +198,7 @@ residual_norm_kernel(NormArgs a) {
 // partial row a CTA instead of an atomic a channel and row, and their order
 // does not change from run to run.  With kAhead every thread copies its
 // vectors of the next row to shared memory while it works on this one (8192 x
-// 4096 bf16: 157 us without, 116 with), and reads them again in each pass
+// 4096 bf16: 157 us without, 131 with), and reads them again in each pass
 // instead of holding them; without (rows too long for two in shared memory)
 // they come from global memory as they are needed.
 template <typename T, int TPR, int kVecs, bool kAhead>
