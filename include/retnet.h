@@ -377,7 +377,8 @@ RETNET_API retnet_status retnet_msr_layer(const void *x, const void *w_qkvg, con
  *           gradients are zero.
  *   state   device float32 [batch, heads, dk, dv], as for retention.
  * Sizes: batch, seqlen >= 0; 1 <= key_heads <= heads <= 256 with heads a
- * multiple of key_heads; dk, dv in {64, 128, 256}; scale finite. */
+ * multiple of key_heads; dk, dv in {64, 128, 256}; at most 2^23 chunks of 64
+ * tokens over all sequences and heads (UNSUPPORTED beyond); scale finite. */
 typedef struct retnet_delta_shape {
     int batch;
     int heads;       /* value heads */
@@ -392,7 +393,8 @@ typedef struct retnet_delta_shape {
  * state read and written once per call and updated in place.  A sequence of
  * length 0 keeps its state.  Float32 arithmetic; a run of tokens gives what
  * its single steps give up to the order of float32 sums.  Work grows with
- * seqlen on CUDA cores; for long runs use retnet_delta_chunkwise.  out must not overlap the inputs.
+ * seqlen on CUDA cores; for long runs use retnet_delta_chunkwise.  out must
+ * not overlap the inputs.
  * Errors: INVALID_ARG, UNSUPPORTED (dk/dv), CUDA. */
 RETNET_API retnet_status retnet_delta_recurrent(const void *q, const void *k, const void *v,
                                                 const void *g, const void *beta, float scale,
@@ -406,8 +408,7 @@ RETNET_API retnet_status retnet_delta_recurrent(const void *q, const void *k, co
  * works in chunks of 64 tokens, for bf16 with dk 64 or 128; AUTO takes it
  * there for all but a few tokens.  On the tensor-core path operands are
  * rounded to bf16 on the way to `out`, and a final state keeps float32
- * accuracy.  out must not
- * overlap the inputs, the states or the workspace.
+ * accuracy.  out must not overlap the inputs, the states or the workspace.
  *   workspace  retnet_delta_workspace_size() bytes, 1024-byte aligned.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 RETNET_API retnet_status retnet_delta_workspace_size(const retnet_delta_shape *shape,

@@ -172,7 +172,7 @@ static retnet_status check_delta_shape(const retnet_delta_shape *s) {
         return RETNET_ERR_INVALID_ARG;
     if (!head_dim_ok(s->dk) || !head_dim_ok(s->dv)) return RETNET_ERR_UNSUPPORTED;
     // a CTA per (sequence, head) and slab of columns or chunk of tokens
-    const long long bh = (long long)s->batch * s->heads;
+    const long long bh = (long long)(s->batch > 0 ? s->batch : 1) * s->heads;
     const long long chunks = (s->seqlen + (long long)kDeltaChunk - 1) / kDeltaChunk;
     // (and a row of the saved operands per value channel of each)
     if (bh > 0x7fffffffll / 256 / (chunks > 0 ? chunks : 1)) return RETNET_ERR_UNSUPPORTED;

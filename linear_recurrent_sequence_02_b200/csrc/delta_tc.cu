@@ -848,7 +848,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 // segment as it is; then the states between segments, S_{j+1} = M_j S_j + N_j,
 // in float32; then all other segments' outputs at once.  Each chunk is walked
 // up to three times, but on all SMs: 8192 tokens and 16 heads of 128 in 6
-// segments, walk 283 us whole, 145 us so with the join.
+// segments, walk 274 us whole, 125 us so, and 20 us the join.
 // starts [segments - 1][BH][dk, dv]: N_j and then the state before segment
 // j + 1; units [segments - 2][BH][dk, dk]: M of segments 1 ...
 template <int DK>
@@ -1828,18 +1828,23 @@ cudaError_t launch_prep(const DeltaArgs &a, int nc, uint8_t *blocks, bool backwa
                              sizeof(DeltaPrepSmem<DK, kSplit>), stream, p);
 }
 
-// Segments of the walk over nc chunks: the count with the least chunks walked
-// behind one another (waves of 148 CTAs, first pass and second), if that is a
-// gain over the whole walk.  Against the two extra launches and the states
-// between count as 8 chunks, and 2 a segment.  16 heads, 128 chunks: 6
-// segments; from 75 walks on, or below 24 chunks, 1.
-int delta_segments(int batch, int heads, int nc, int dv) {
+// Segments of the walk over nc chunks: the count with the least time, counted
+// in chunks walked behind one another (a wave of 148 CTAs each, first pass
+// and second).  The two further launches cost 4 of them and a join of states
+// 1.5 (1 for dk 64); without a final state the whole walk has its operands in
+// one part and takes 5/8 of the time (3/4 for dk 64).  Measured with a final state, 128 x 128:
+// 16 heads, 128 chunks: 360 us whole, 212 in 6 segments; 32 chunks: 96 and 79;
+// 48 heads, 32 chunks: 143 and 147 (whole); 64 heads, 128 chunks: 611 and 640
+// (whole).  Without: 16 heads, 128 chunks: 239 and 212; 32 heads: 303 and 377
+// (whole).
+int delta_segments(int batch, int heads, int nc, int dk, int dv, bool final_state) {
     const long long units = (long long)batch * heads, walks = units * ((dv + 127) / 128);
     auto waves = [](long long ctas) { return (ctas + 147) / 148; };
-    long long best = waves(walks) * nc * 4 / 5;
+    float best = (float)(waves(walks) * nc) * (final_state ? 0.95f : dk == 64 ? 0.72f : 0.6f);
     int count = 1;
     for (int s = 3; s <= 16 && 4 * s <= nc; ++s) {
-        const long long cost = (waves(walks + (s - 2) * (walks + units)) + waves(walks * (s - 1))) * ((nc + s - 1) / s) + 8 + 2 * s;
+        const long long both = waves(walks + (s - 2) * (walks + units)) + waves(walks * (s - 1));
+        const float cost = (float)(both * ((nc + s - 1) / s)) + 4.f + (dk == 64 ? 1.f : 1.5f) * s;
         if (cost < best) {
             best = cost;
             count = s;
@@ -1852,10 +1857,10 @@ struct DeltaTcLayout {
     int nc, segments, segment;
     size_t starts, units, total;
 };
-DeltaTcLayout tc_layout(int batch, int heads, int seqlen, int dk, int dv) {
+DeltaTcLayout tc_layout(int batch, int heads, int seqlen, int dk, int dv, bool final_state) {
     DeltaTcLayout l;
     l.nc = (seqlen + kC - 1) / kC;
-    l.segments = delta_segments(batch, heads, l.nc, dv);
+    l.segments = delta_segments(batch, heads, l.nc, dk, dv, final_state);
     l.segment = (l.nc + l.segments - 1) / l.segments;
     const size_t bh = (size_t)batch * heads;
     l.starts = bh * l.nc * (dk == 64 ? DeltaBlock<64, true>::kBytes : DeltaBlock<128, true>::kBytes);
@@ -2005,7 +2010,7 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
 // parts whether or not the final state is asked for.
 template <int DK>
 cudaError_t launch_forward(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
-    const DeltaTcLayout l = tc_layout(a.batch, a.heads, a.seqlen, DK, a.dv);
+    const DeltaTcLayout l = tc_layout(a.batch, a.heads, a.seqlen, DK, a.dv, a.state_out != nullptr);
     uint8_t *ws = (uint8_t *)workspace;
     const bool split = a.state_out || l.segments > 1;
     cudaError_t e = split ? launch_prep<DK, true>(a, l.nc, ws, false, stream)
@@ -2032,7 +2037,9 @@ bool delta_tc_shape_ok(int dk, int dv, retnet_dtype dtype) {
 }
 
 size_t delta_tc_workspace(int batch, int heads, int seqlen, int dk, int dv) {
-    return tc_layout(batch, heads, seqlen, dk, dv).total;
+    const size_t with = tc_layout(batch, heads, seqlen, dk, dv, true).total;
+    const size_t without = tc_layout(batch, heads, seqlen, dk, dv, false).total;
+    return with > without ? with : without;
 }
 
 cudaError_t launch_delta_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream) {

@@ -27,6 +27,7 @@ BAD_SHAPES = [
     (dict(H=3), INVALID), (dict(Hk=8), INVALID), (dict(H=257, Hk=257), INVALID),
     (dict(dk=0), INVALID), (dict(dt=2), INVALID), (dict(dk=96), UNSUPPORTED),
     (dict(dv=512), UNSUPPORTED), (dict(B=1 << 30, H=256, Hk=256), UNSUPPORTED),
+    (dict(B=0, n=2 ** 31 - 1), UNSUPPORTED),
 ]
 
 

@@ -453,3 +453,69 @@ def test_training_step_through_autograd(rn):
         # (a few at most: the loss is a short polynomial in each input), and
         # float32 outputs: 1e-7 * |loss terms| / step
         assert abs(diff - want) < 5e-3 * want, i
+
+
+def test_two_streams_at_once(rn):
+    """A prefill and a backward that run beside each other, several times,
+    give what each gives alone."""
+    B, n, H, d = 2, 700, 8, 128
+    x, _ = make(21, B, n, H, H, d, d, "bf16")
+    y, _ = make(22, B, n, H, H, d, d, "bf16")
+    S, want_S = torch.empty(B, H, d, d, device="cuda"), torch.empty(B, H, d, d, device="cuda")
+    want = rn.retnet_delta_chunkwise(*x[:5], state_out=want_S)
+    want_grads = rn.retnet_delta_backward(*y)
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(4):
+        with torch.cuda.stream(streams[0]):
+            out = rn.retnet_delta_chunkwise(*x[:5], state_out=S)
+        with torch.cuda.stream(streams[1]):
+            grads = rn.retnet_delta_backward(*y)
+    done(rn)
+    assert torch.equal(out, want) and torch.equal(S, want_S)
+    for a, b in zip(grads, want_grads):
+        assert torch.equal(a, b)
+
+
+def noise(seed, *shape):
+    """bf16 of little precision, made without a float32 copy."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.empty(*shape, device="cuda", dtype=torch.bfloat16).uniform_(-0.5, 0.5, generator=gen)
+
+
+def test_states_and_workspaces_beyond_32_bits(rn):
+    """More than 2^31 state elements and workspaces above 2^32 bytes: the last
+    sequences as they come out alone."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    B, H, d = 2050, 16, 256
+    x = [noise(30 + i, B, 1, H, d) * 0.1 for i in range(3)]
+    x += [noise(33, B, 1, H) - 0.5, noise(34, B, 1, H) + 0.5]
+    S = torch.empty(B, H, d, d, device="cuda").uniform_(-0.5, 0.5)
+    assert S.numel() > 2 ** 31
+    mine = S[-1:].clone()
+    out = rn.retnet_delta_recurrent(*x, S)
+    alone = rn.retnet_delta_recurrent(*(t[-1:].contiguous() for t in x), mine)
+    done(rn)
+    assert torch.equal(out[-1:], alone) and torch.equal(S[-1:], mine)
+    del S
+
+    B, n, d = 128, 2048, 128
+    x = [noise(40 + i, B, n, H, d) * 0.1 for i in range(2)] + [noise(42, B, n, H, d)]
+    x += [noise(43, B, n, H) - 0.5, noise(44, B, n, H) + 0.5]
+    size = rn.retnet_delta_workspace_size(B, H, H, n, d, d, torch.bfloat16)
+    assert size > 2 ** 32
+    S = torch.empty(B, H, d, d, device="cuda")
+    out = rn.retnet_delta_chunkwise(*x, state_out=S)
+    few = [t[-16:].contiguous() for t in x]        # as many as walk whole
+    mine = torch.empty(16, H, d, d, device="cuda")
+    alone = rn.retnet_delta_chunkwise(*few, state_out=mine)
+    done(rn)
+    assert torch.equal(out[-16:], alone) and torch.equal(S[-16:], mine)
+    del out, S
+    do = noise(45, B, n, H, d)
+    grads = rn.retnet_delta_backward(*x, do)
+    alone = rn.retnet_delta_backward(*few, do[-16:].contiguous())
+    done(rn)
+    for a, b in zip(grads, alone):
+        assert torch.isfinite(b).all() and torch.equal(a[-16:], b)

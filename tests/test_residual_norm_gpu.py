@@ -128,3 +128,24 @@ def test_captured_graph(rn):
     for a, b in zip((*out, *grads), (*rn.retnet_residual_norm(x, y, **kw),
                                      *rn.retnet_residual_norm_backward(x, y, dn, dh, **kw))):
         assert torch.equal(a, b)
+
+
+def test_offsets_beyond_32_bits(rn):
+    """More than 2^31 elements a tensor: the last rows as they come out alone."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    rows, hidden = (1 << 31) // 8192 + 3, 8192
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x, y, dn = (torch.empty(rows, hidden, device="cuda", dtype=torch.bfloat16).uniform_(
+        -1, 1, generator=gen) for _ in range(3))
+    assert x.numel() > 2 ** 31
+    last = [t[-3:].clone() for t in (x, y, dn)]
+    grads = rn.retnet_residual_norm_backward(x, y, dn, dy=dn)
+    for a, b in zip(grads[:2], rn.retnet_residual_norm_backward(*last)[:2]):
+        assert torch.equal(a[-3:], b)
+    del grads, dn
+    out = rn.retnet_residual_norm(x, y, h=x, n=y)
+    for a, b in zip(out, rn.retnet_residual_norm(*last[:2])):
+        assert torch.equal(a[-3:], b)
+    torch.cuda.synchronize()
+    rn.retnet_check_device_errors()
