@@ -404,11 +404,13 @@ RETNET_API retnet_status retnet_delta_recurrent(const void *q, const void *k, co
 
 /* Prefill: all tokens of a batch, with an optional state before the first
  * (NULL: zero) and after the last token (NULL: not wanted; may equal
- * state_in).  RETNET_ALGO_SIMT runs the recurrent form; the tensor-core path
- * works in chunks of 64 tokens, for bf16 with dk 64 or 128; AUTO takes it
- * there for all but a few tokens.  On the tensor-core path operands are
- * rounded to bf16 on the way to `out`, and a final state keeps float32
- * accuracy.  out must not overlap the inputs, the states or the workspace.
+ * state_in).  RETNET_ALGO_SIMT runs the recurrent form (AUTO does so for
+ * float32 too, in segments of a long sequence beside one another); the
+ * tensor-core path works in chunks of 64 tokens, for bf16 with dk 64 or 128;
+ * AUTO takes it there for all but a few tokens.  On the tensor-core path
+ * operands are rounded to bf16 on the way to `out`, and a final state keeps
+ * float32 accuracy.  out must not overlap the inputs, the states or the
+ * workspace.
  *   workspace  retnet_delta_workspace_size() bytes, 1024-byte aligned.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 RETNET_API retnet_status retnet_delta_workspace_size(const retnet_delta_shape *shape,

@@ -195,6 +195,13 @@ static bool delta_prefill_tensor(const retnet_delta_shape *s, retnet_algo algo) 
                      (long long)s->batch * s->heads * s->dv * s->seqlen <= (1 << 19);
     return delta_tensor(s, algo) && !(algo == RETNET_ALGO_AUTO && few);
 }
+// A float32 prefill walks in segments, which need a workspace.
+static size_t delta_prefill_workspace(const retnet_delta_shape *s, retnet_algo algo) {
+    if (delta_prefill_tensor(s, algo))
+        return delta_tc_workspace(s->batch, s->heads, s->seqlen, s->dk, s->dv);
+    return algo == RETNET_ALGO_AUTO && s->dtype == RETNET_F32
+               ? delta_walk_workspace(s->batch, s->heads, s->seqlen, s->dk, s->dv) : 0;
+}
 static DeltaArgs delta_args(const void *q, const void *k, const void *v, const void *g,
                             const void *beta, float scale, const int *lengths,
                             const retnet_delta_shape *s) {
@@ -610,9 +617,8 @@ retnet_status retnet_delta_workspace_size(const retnet_delta_shape *shape, retne
     if (!bytes || !algo_ok(algo)) return RETNET_ERR_INVALID_ARG;
     retnet_status st = check_delta_shape(shape);
     if (st != RETNET_OK) return st;
-    const bool tensor = delta_prefill_tensor(shape, algo);
-    if (algo == RETNET_ALGO_TENSOR && !tensor) return RETNET_ERR_UNSUPPORTED;
-    *bytes = tensor ? delta_tc_workspace(shape->batch, shape->heads, shape->seqlen, shape->dk, shape->dv) : 0;
+    if (algo == RETNET_ALGO_TENSOR && !delta_prefill_tensor(shape, algo)) return RETNET_ERR_UNSUPPORTED;
+    *bytes = delta_prefill_workspace(shape, algo);
     return RETNET_OK;
 }
 
@@ -636,6 +642,8 @@ retnet_status retnet_delta_chunkwise(const void *q, const void *k, const void *v
     a.state_in = state_in; a.state_out = state_out; a.out = out;
     if (tokens > 0 && delta_prefill_tensor(shape, algo))
         RETNET_CUDA_TRY(launch_delta_tc(a, workspace, (cudaStream_t)stream));
+    else if (tokens > 0 && need > 0)
+        RETNET_CUDA_TRY(launch_delta_walk_segments(a, workspace, (cudaStream_t)stream));
     else
         RETNET_CUDA_TRY(launch_delta_walk(a, (cudaStream_t)stream));
     return RETNET_OK;

@@ -30,7 +30,9 @@ constexpr int kDeltaCols = 32;                 // state columns per CTA
 constexpr int kDeltaGroups = kDeltaCols / 4;   // float4 column groups
 constexpr int kDeltaLanes = kDeltaThreads / kDeltaGroups;   // 32 row lanes
 
-enum DeltaSweep { kSweepForward, kSweepSave, kSweepReverse };
+// What a walk is for: outputs; x and the states, kept for the gradients; r and
+// D, kept, from the last token on; and the state alone, either way.
+enum DeltaSweep { kSweepForward, kSweepSave, kSweepReverse, kSweepCarry, kSweepCarryBack };
 
 template <typename T>
 __device__ __forceinline__ float4 load_f4(const T *p);
@@ -239,11 +241,6 @@ delta_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// v: the values (forward) or the output's gradient (reverse).  state_in and
-// state_out may be missing and may be the same.
-// save: x (kSweepSave) or r (kSweepReverse), float32 [B, n, H, dv];
-// marks: the state before (D behind) every chunk of kDeltaChunk tokens,
-// float32 [B, H, chunks, dk, dv].
 // N neighbouring values of a row.
 template <int N, typename T>
 __device__ __forceinline__ void load_row(T (&x)[N], const T *p) {
@@ -259,40 +256,61 @@ __device__ __forceinline__ void load_row(T (&x)[N], const T *p) {
     }
 }
 constexpr int kWalkWarps = 4, kWalkCols = 4;         // columns per warp
+constexpr int kWalkSlab = kWalkWarps * kWalkCols;    // and per CTA
 constexpr int kWalkAhead = 4;                        // tokens loaded ahead
 
+// Tokens [first, last) of a (sequence, head), from the state `from` (null:
+// zero) to `to` (null: not wanted, may be the same), both [dk, width].  unit
+// (kSweepCarry): the state starts as the identity and no values are written,
+// so that it ends as the transition of these tokens.
+struct DeltaSpan {
+    int bh, col, first, last, width;
+    const float *from;
+    float *to;
+    bool unit;
+};
+// v: the values (forward) or the output's gradient (reverse).
+// save: x (kSweepSave) or r (kSweepReverse), float32 [B, n, H, dv];
+// marks: the state before (D behind) every chunk of kDeltaChunk tokens,
+// float32 [B, H, chunks, dk, dv].
 template <typename T, int DK, DeltaSweep kSweep>
 __device__ __forceinline__ void delta_walk(const T *__restrict__ q, const T *__restrict__ k,
                                            const T *__restrict__ v, const T *__restrict__ g,
                                            const T *__restrict__ beta,
-                                           const int *__restrict__ lengths, const float *state_in,
-                                           float *state_out, T *__restrict__ out,
+                                           const int *__restrict__ lengths, T *__restrict__ out,
                                            float *__restrict__ save, float *__restrict__ marks,
                                            float scale, int heads, int key_heads, int tokens,
-                                           int dv, int cta) {
+                                           int dv, const DeltaSpan &w) {
     constexpr int RPL = DK / 32;                     // rows RPL lane, RPL lane + 1, ...
-    constexpr bool kFwd = kSweep == kSweepForward, kRev = kSweep == kSweepReverse;
-    const int slabs = dv / (kWalkWarps * kWalkCols);
-    const int bh = cta / slabs;
-    const int b = bh / heads, h = bh % heads, kh = h / (heads / key_heads);
+    constexpr bool kFwd = kSweep == kSweepForward;
+    constexpr bool kRev = kSweep == kSweepReverse || kSweep == kSweepCarryBack;
+    constexpr bool kKeep = kSweep == kSweepSave || kSweep == kSweepReverse;
+    constexpr bool kUsesQ = kFwd || kRev;
+    const int bh = w.bh, b = bh / heads, h = bh % heads, kh = h / (heads / key_heads);
     const int lane = threadIdx.x % 32;
-    const int col = (cta % slabs) * (kWalkWarps * kWalkCols) + (threadIdx.x / 32) * kWalkCols;
+    const int col = w.col + (threadIdx.x / 32) * kWalkCols;
+    const bool unit = kSweep == kSweepCarry && w.unit;
 
     grid_dependency_wait();
-    const int n = delta_tokens_of(lengths, b, tokens);
+    const int end = min(w.last, delta_tokens_of(lengths, b, tokens)), begin = min(w.first, end);
+    const int n = end - begin;
     const int nc = (tokens + kDeltaChunk - 1) / kDeltaChunk;
-    const size_t sbase = ((size_t)bh * DK + RPL * lane) * dv + col;
+    const size_t sbase = (size_t)(RPL * lane) * w.width + col;
     float2 s[RPL][2];
 #pragma unroll
     for (int i = 0; i < RPL; ++i) {
-        const float4 x = state_in ? load_f4(state_in + sbase + (size_t)i * dv) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 x = w.from ? load_f4(w.from + sbase + (size_t)i * w.width) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (unit) {
+            const int one = RPL * lane + i - col;
+            x = make_float4(one == 0, one == 1, one == 2, one == 3);
+        }
         s[i][0] = make_float2(x.x, x.y);
         s[i][1] = make_float2(x.z, x.w);
     }
-    auto store_state = [&](float *dst) {
+    auto store_state = [&](float *dst, int stride) {
 #pragma unroll
         for (int i = 0; i < RPL; ++i)
-            store_f4(dst + (size_t)i * dv, make_float4(s[i][0].x, s[i][0].y, s[i][1].x, s[i][1].y));
+            store_f4(dst + (size_t)i * stride, make_float4(s[i][0].x, s[i][0].y, s[i][1].x, s[i][1].y));
     };
 
     // the tokens ahead, as they lie in memory; pointers step along the walk
@@ -303,19 +321,19 @@ __device__ __forceinline__ void delta_walk(const T *__restrict__ q, const T *__r
         T g, b;
     } ahead[kWalkAhead];
     const long long dir = kRev ? -1 : 1;
-    const size_t start = (size_t)b * tokens + (kRev ? max(n - 1, 0) : 0);
+    const size_t start = (size_t)b * tokens + (kRev ? max(end - 1, 0) : begin);
     const T *kp = k + (start * key_heads + kh) * DK + RPL * lane;
     const T *qp = q + (start * key_heads + kh) * DK + RPL * lane;
     const T *vp = v + (start * heads + h) * dv + col;
     const T *gp = g + start * heads + h, *bp = beta + start * heads + h;
     const long long kstep = dir * key_heads * DK, vstep = dir * heads * dv, gstep = dir * heads;
-    auto load = [&](Token &w, bool more) {
+    auto load = [&](Token &t, bool more) {
         if (more) {
-            load_row<RPL>(w.k, kp);
-            if (kSweep != kSweepSave) load_row<RPL>(w.q, qp);
-            load_row<4>(w.v, vp);
-            w.g = *gp;
-            w.b = *bp;
+            load_row<RPL>(t.k, kp);
+            if (kUsesQ) load_row<RPL>(t.q, qp);
+            if (!unit) load_row<4>(t.v, vp);
+            t.g = *gp;
+            t.b = *bp;
             kp += kstep;
             qp += kstep;
             vp += vstep;
@@ -335,17 +353,17 @@ __device__ __forceinline__ void delta_walk(const T *__restrict__ q, const T *__r
 #pragma unroll
             for (int i = 0; i < RPL; ++i) {
                 wk[i] = to_f32(ahead[u].k[i]);
-                if (kSweep != kSweepSave) wq[i] = to_f32(ahead[u].q[i]);
+                if (kUsesQ) wq[i] = to_f32(ahead[u].q[i]);
             }
-            const float2 v0 = make_float2(to_f32(ahead[u].v[0]), to_f32(ahead[u].v[1]));
-            const float2 v1 = make_float2(to_f32(ahead[u].v[2]), to_f32(ahead[u].v[3]));
+            const float2 v0 = unit ? both(0.f) : make_float2(to_f32(ahead[u].v[0]), to_f32(ahead[u].v[1]));
+            const float2 v1 = unit ? both(0.f) : make_float2(to_f32(ahead[u].v[2]), to_f32(ahead[u].v[3]));
             const float a = expf(to_f32(ahead[u].g)), bt0 = to_f32(ahead[u].b);
             const float bt = kSweep == kSweepSave ? nonzero_beta(bt0) : bt0;
             load(ahead[u], step + kWalkAhead < n);
-            if (!kFwd) {
-                const int t = kRev ? n - 1 - step : step;
+            if (kKeep) {
+                const int t = kRev ? end - 1 - step : begin + step;
                 if (kRev ? step == 0 || t % kDeltaChunk == kDeltaChunk - 1 : t % kDeltaChunk == 0)
-                    store_state(marks + (((size_t)bh * nc + t / kDeltaChunk) * DK + RPL * lane) * dv + col);
+                    store_state(marks + (((size_t)bh * nc + t / kDeltaChunk) * DK + RPL * lane) * dv + col, dv);
             }
             float2 y0 = both(0.f), y1 = y0, z0 = y0, z1 = y0;
             float d = 0.f;                           // q.k
@@ -357,7 +375,7 @@ __device__ __forceinline__ void delta_walk(const T *__restrict__ q, const T *__r
                     z0 = fma2(both(wq[i]), s[i][0], z0);
                     z1 = fma2(both(wq[i]), s[i][1], z1);
                 }
-                if (kSweep != kSweepSave) d = fmaf(wq[i], wk[i], d);
+                if (kUsesQ) d = fmaf(wq[i], wk[i], d);
             }
             // sums over the lanes: a lane gives away the half of the values
             // that it does not keep, so that it ends with one; q.k goes along
@@ -368,18 +386,18 @@ __device__ __forceinline__ void delta_walk(const T *__restrict__ q, const T *__r
                 y0 = add2(k0, make_float2(pass(g0.x, 16), pass(g0.y, 16)));
                 y1 = add2(k1, make_float2(pass(g1.x, 16), pass(g1.y, 16)));
             }
-            if (kSweep != kSweepSave) d += pass(d, 16);
+            if (kUsesQ) d += pass(d, 16);
             const bool far = lane & 8, odd = lane & 4;
             const float2 k2 = far ? y1 : y0, g2 = far ? y0 : y1;
             const float2 h2 = add2(k2, make_float2(pass(g2.x, 8), pass(g2.y, 8)));
-            if (kSweep != kSweepSave) d += pass(d, 8);
+            if (kUsesQ) d += pass(d, 8);
             float e = (odd ? h2.y : h2.x) + pass(odd ? h2.x : h2.y, 4);
-            if (kSweep != kSweepSave) d += pass(d, 4);
+            if (kUsesQ) d += pass(d, 4);
             if (!kFwd) e += pass(e, 16);
             e += pass(e, 2);
-            if (kSweep != kSweepSave) d += pass(d, 2);
+            if (kUsesQ) d += pass(d, 2);
             e += pass(e, 1);
-            if (kSweep != kSweepSave) d += pass(d, 1);
+            if (kUsesQ) d += pass(d, 1);
             y0 = make_float2(__shfl_sync(0xffffffffu, e, 0), __shfl_sync(0xffffffffu, e, 4));
             y1 = make_float2(__shfl_sync(0xffffffffu, e, 8), __shfl_sync(0xffffffffu, e, 12));
             float2 x0, x1;
@@ -406,13 +424,22 @@ __device__ __forceinline__ void delta_walk(const T *__restrict__ q, const T *__r
                 // lanes 16, 20, 24, 28 hold z of columns 0 .. 3
                 const float xe = far ? (odd ? x1.y : x1.x) : (odd ? x0.y : x0.x);
                 if ((lane & 19) == 16) out[vo + (lane - 16) / 4] = from_f32<T>(scale * fmaf(d, xe, a * e));
-            } else if (lane == 0) {
+            } else if (kKeep && lane == 0) {
                 store_f4(save + vo, make_float4(x0.x, x0.y, x1.x, x1.y));
             }
             vo += vstep;
         }
     }
-    if (kFwd && state_out && (n > 0 || state_out != state_in)) store_state(state_out + sbase);
+    if (w.to && (n > 0 || w.to != w.from)) store_state(w.to + sbase, w.width);
+}
+
+// All tokens, for the CTA's columns.
+__device__ __forceinline__ DeltaSpan whole_span(int cta, int tokens, int dk, int dv, const float *from,
+                                                float *to) {
+    const int slabs = dv / kWalkSlab, bh = cta / slabs;
+    const size_t at = (size_t)bh * dk * dv;
+    return {bh, (cta % slabs) * kWalkSlab, 0, tokens, dv, from ? from + at : nullptr,
+            to ? to + at : nullptr, false};
 }
 
 template <typename T, int DK>
@@ -421,8 +448,9 @@ delta_walk_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
                   const T *__restrict__ g, const T *__restrict__ beta,
                   const int *__restrict__ lengths, const float *state_in, float *state_out,
                   T *__restrict__ out, float scale, int heads, int key_heads, int tokens, int dv) {
-    delta_walk<T, DK, kSweepForward>(q, k, v, g, beta, lengths, state_in, state_out, out, nullptr,
-                                     nullptr, scale, heads, key_heads, tokens, dv, blockIdx.x);
+    delta_walk<T, DK, kSweepForward>(q, k, v, g, beta, lengths, out, nullptr, nullptr, scale, heads,
+                                     key_heads, tokens, dv,
+                                     whole_span(blockIdx.x, tokens, DK, dv, state_in, state_out));
 }
 // The backward's two sweeps: neither needs the other, so they share a launch.
 template <typename T, int DK>
@@ -431,14 +459,125 @@ delta_sweeps_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *_
                     const T *__restrict__ d_out, const T *__restrict__ g, const T *__restrict__ beta,
                     const int *__restrict__ lengths, float *xs, float *ss, float *rs, float *ds,
                     float scale, int heads, int key_heads, int tokens, int dv) {
-    const int half = gridDim.x / 2;
+    const int half = gridDim.x / 2, cta = (int)blockIdx.x < half ? blockIdx.x : blockIdx.x - half;
+    const DeltaSpan w = whole_span(cta, tokens, DK, dv, nullptr, nullptr);
     if ((int)blockIdx.x < half)
-        delta_walk<T, DK, kSweepSave>(q, k, v, g, beta, lengths, nullptr, nullptr, nullptr, xs, ss,
-                                      scale, heads, key_heads, tokens, dv, blockIdx.x);
+        delta_walk<T, DK, kSweepSave>(q, k, v, g, beta, lengths, nullptr, xs, ss, scale, heads,
+                                      key_heads, tokens, dv, w);
     else
-        delta_walk<T, DK, kSweepReverse>(q, k, d_out, g, beta, lengths, nullptr, nullptr, nullptr,
-                                         rs, ds, scale, heads, key_heads, tokens, dv,
-                                         blockIdx.x - half);
+        delta_walk<T, DK, kSweepReverse>(q, k, d_out, g, beta, lengths, nullptr, rs, ds, scale,
+                                         heads, key_heads, tokens, dv, w);
+}
+
+// ---- in segments, as the tensor-core walk goes with few heads (see
+// delta_segments_kernel): segment 0 as it is and what the later ones do to a
+// state, S -> M S + N, all at once; the states between, by launch_delta_join;
+// then the later segments' outputs all at once.
+// starts [segments - 1][BH][dk, dv], units [segments - 2][BH][dk, dk].
+struct DeltaSegments {
+    int count, tokens;                     // of a segment
+    float *starts, *units, *back;          // back: starts of the reverse sweep
+};
+template <int DK>
+__global__ void __launch_bounds__(32 * kWalkWarps)
+delta_walk_segments_kernel(const float *__restrict__ q, const float *__restrict__ k,
+                           const float *__restrict__ v, const float *__restrict__ g,
+                           const float *__restrict__ beta, const int *__restrict__ lengths,
+                           const float *state_in, float *state_out, float *__restrict__ out,
+                           float scale, int heads, int key_heads, int tokens, int dv,
+                           DeltaSegments x, int bhs, int last) {
+    const int walks = bhs * (dv / kWalkSlab);
+    const size_t ssize = (size_t)DK * dv;
+    int cta = blockIdx.x;
+    if (last || cta < walks) {                               // outputs
+        const int seg = last ? 1 + cta / walks : 0;
+        DeltaSpan w = whole_span(cta % walks, tokens, DK, dv, state_in, state_out);
+        if (last) w.from = x.starts + ((size_t)(seg - 1) * bhs + w.bh) * ssize;
+        else w.to = x.starts + (size_t)w.bh * ssize;
+        if (last && seg < x.count - 1) w.to = nullptr;
+        w.first = seg * x.tokens;
+        w.last = w.first + x.tokens;
+        delta_walk<float, DK, kSweepForward>(q, k, v, g, beta, lengths, out, nullptr, nullptr, scale,
+                                         heads, key_heads, tokens, dv, w);
+    } else {
+        DeltaSpan w;
+        int seg;
+        if (cta < walks * (x.count - 1)) {                   // N
+            seg = cta / walks;
+            w = whole_span(cta % walks, tokens, DK, dv, nullptr, nullptr);
+            w.to = x.starts + ((size_t)seg * bhs + w.bh) * ssize;
+        } else {                                             // M
+            constexpr int kSlabs = DK / kWalkSlab;
+            cta -= walks * (x.count - 1);
+            seg = 1 + cta / (bhs * kSlabs);
+            w = whole_span(cta % (bhs * kSlabs), tokens, DK, DK, nullptr, nullptr);
+            w.to = x.units + ((size_t)(seg - 1) * bhs + w.bh) * DK * DK;
+            w.unit = true;
+        }
+        w.first = seg * x.tokens;
+        w.last = w.first + x.tokens;
+        delta_walk<float, DK, kSweepCarry>(q, k, v, g, beta, lengths, nullptr, nullptr, nullptr, scale,
+                                       heads, key_heads, tokens, dv, w);
+    }
+}
+
+// The backward's two sweeps in segments.  Back through segment j the gradient
+// of the state goes by D -> M_j^T D + N'_j, so the units serve both.
+// back [segments - 1]: D behind segment segments - 2 first.
+template <typename T, int DK>
+__global__ void __launch_bounds__(32 * kWalkWarps)
+delta_sweeps_segments_kernel(const T *__restrict__ q, const T *__restrict__ k,
+                             const T *__restrict__ v, const T *__restrict__ d_out,
+                             const T *__restrict__ g, const T *__restrict__ beta,
+                             const int *__restrict__ lengths, float *xs, float *ss, float *rs,
+                             float *ds, float scale, int heads, int key_heads, int tokens, int dv,
+                             DeltaSegments x, int bhs, int last) {
+    const int walks = bhs * (dv / kWalkSlab), ends = last ? walks * (x.count - 1) : walks;
+    const size_t ssize = (size_t)DK * dv;
+    int cta = blockIdx.x;
+    auto span = [&](int seg, const float *from, float *to) {
+        DeltaSpan w = whole_span(cta % walks, tokens, DK, dv, from, to);
+        w.first = seg * x.tokens;
+        w.last = w.first + x.tokens;
+        return w;
+    };
+    auto state = [&](float *base, int i) { return base + (size_t)i * bhs * ssize; };
+    if (cta < ends) {                                        // kept, forward
+        const int seg = last ? 1 + cta / walks : 0;
+        delta_walk<T, DK, kSweepSave>(q, k, v, g, beta, lengths, nullptr, xs, ss, scale, heads,
+                                      key_heads, tokens, dv,
+                                      last ? span(seg, state(x.starts, seg - 1), nullptr)
+                                           : span(0, nullptr, x.starts));
+    } else if ((cta -= ends) < ends) {                       // kept, back
+        const int seg = last ? x.count - 2 - cta / walks : x.count - 1;
+        delta_walk<T, DK, kSweepReverse>(q, k, d_out, g, beta, lengths, nullptr, rs, ds, scale,
+                                         heads, key_heads, tokens, dv,
+                                         last ? span(seg, state(x.back, x.count - 2 - seg), nullptr)
+                                              : span(seg, nullptr, x.back));
+    } else if ((cta -= ends) < walks * (x.count - 2)) {      // N'
+        const int seg = 1 + cta / walks;
+        delta_walk<T, DK, kSweepCarryBack>(q, k, d_out, g, beta, lengths, nullptr, nullptr, nullptr,
+                                           scale, heads, key_heads, tokens, dv,
+                                           span(seg, nullptr, state(x.back, x.count - 1 - seg)));
+    } else {
+        cta -= walks * (x.count - 2);
+        DeltaSpan w;
+        if (cta < walks * (x.count - 2)) {                   // N
+            const int seg = 1 + cta / walks;
+            w = span(seg, nullptr, state(x.starts, seg));
+        } else {                                             // M
+            constexpr int kSlabs = DK / kWalkSlab;
+            cta -= walks * (x.count - 2);
+            const int seg = 1 + cta / (bhs * kSlabs);
+            w = whole_span(cta % (bhs * kSlabs), tokens, DK, DK, nullptr, nullptr);
+            w.first = seg * x.tokens;
+            w.last = w.first + x.tokens;
+            w.to = x.units + ((size_t)(seg - 1) * bhs + w.bh) * DK * DK;
+            w.unit = true;
+        }
+        delta_walk<T, DK, kSweepCarry>(q, k, v, g, beta, lengths, nullptr, nullptr, nullptr, scale,
+                                       heads, key_heads, tokens, dv, w);
+    }
 }
 
 // ------------------------------------------------------------------ gradients
@@ -766,7 +905,7 @@ delta_share_kernel(const float *__restrict__ dq_wide, const float *__restrict__ 
 
 // ------------------------------------------------------------------ launches
 static size_t walk_ctas(const DeltaArgs &a) {
-    return (size_t)a.batch * a.heads * (a.dv / (kWalkWarps * kWalkCols));
+    return (size_t)a.batch * a.heads * (a.dv / kWalkSlab);
 }
 template <typename T, int DK>
 static cudaError_t launch_walk(const DeltaArgs &a, cudaStream_t stream) {
@@ -776,14 +915,35 @@ static cudaError_t launch_walk(const DeltaArgs &a, cudaStream_t stream) {
                              a.state_in, a.state_out, (T *)a.out, a.scale, a.heads, a.key_heads,
                              a.seqlen, a.dv);
 }
+template <int DK>
+static cudaError_t launch_walk_segments(const DeltaArgs &a, const DeltaSegments &x, int ctas,
+                                        int last, cudaStream_t stream) {
+    return launch_overlapped(delta_walk_segments_kernel<DK>, dim3((unsigned)ctas),
+                             dim3(32 * kWalkWarps), 0, stream, (const float *)a.q, (const float *)a.k,
+                             (const float *)a.v, (const float *)a.g, (const float *)a.beta, a.lengths,
+                             a.state_in, a.state_out, (float *)a.out, a.scale, a.heads, a.key_heads,
+                             a.seqlen, a.dv, x, a.batch * a.heads, last);
+}
+struct DeltaSweepOut {
+    float *xs, *ss, *rs, *ds;
+};
 template <typename T, int DK>
-static cudaError_t launch_sweeps(const DeltaArgs &a, float *xs, float *ss, float *rs, float *ds,
-                                 cudaStream_t stream) {
+static cudaError_t launch_sweeps(const DeltaArgs &a, const DeltaSweepOut &o, cudaStream_t stream) {
     return launch_overlapped(delta_sweeps_kernel<T, DK>, dim3((unsigned)(2 * walk_ctas(a))),
                              dim3(32 * kWalkWarps), 0, stream, (const T *)a.q, (const T *)a.k,
                              (const T *)a.v, (const T *)a.d_out, (const T *)a.g,
-                             (const T *)a.beta, a.lengths, xs, ss, rs, ds, a.scale, a.heads,
-                             a.key_heads, a.seqlen, a.dv);
+                             (const T *)a.beta, a.lengths, o.xs, o.ss, o.rs, o.ds, a.scale,
+                             a.heads, a.key_heads, a.seqlen, a.dv);
+}
+template <typename T, int DK>
+static cudaError_t launch_sweeps_segments(const DeltaArgs &a, const DeltaSweepOut &o,
+                                          const DeltaSegments &x, int ctas, int last,
+                                          cudaStream_t stream) {
+    return launch_overlapped(delta_sweeps_segments_kernel<T, DK>, dim3((unsigned)ctas),
+                             dim3(32 * kWalkWarps), 0, stream, (const T *)a.q, (const T *)a.k,
+                             (const T *)a.v, (const T *)a.d_out, (const T *)a.g,
+                             (const T *)a.beta, a.lengths, o.xs, o.ss, o.rs, o.ds, a.scale,
+                             a.heads, a.key_heads, a.seqlen, a.dv, x, a.batch * a.heads, last);
 }
 template <typename T, int DK>
 static cudaError_t launch_step(const DeltaArgs &a, cudaStream_t stream) {
@@ -822,21 +982,100 @@ cudaError_t launch_delta_walk(const DeltaArgs &a, cudaStream_t stream) {
     RETNET_DELTA_CASES(launch_walk, a, stream)
 }
 
-static cudaError_t sweep(const DeltaArgs &a, float *xs, float *ss, float *rs, float *ds,
-                         cudaStream_t stream) {
+static cudaError_t sweep(const DeltaArgs &a, const DeltaSweepOut &o, cudaStream_t stream) {
     KernelTimer timer("delta_sweeps", stream);
     count_launch();
-    RETNET_DELTA_CASES(launch_sweeps, a, xs, ss, rs, ds, stream)
+    RETNET_DELTA_CASES(launch_sweeps, a, o, stream)
+}
+
+// ---- segments of the walks
+// How many segments, and tokens of each (a multiple of `unit`).  Time in
+// tokens behind one another (0.27 us while an SM has no more than four CTAs):
+// both passes, 30 for the further launches, 5 a join of states.  The join
+// holds two transitions in shared memory, so dk 256 walks whole.
+static DeltaSegments walk_segments(int batch, int heads, int seqlen, int dk, int dv, int unit,
+                                   bool backward) {
+    const double walks = (double)batch * heads * (dv / kWalkSlab), units = (double)batch * heads * (dk / kWalkSlab);
+    const int both = backward ? 2 : 1;                       // ways
+    auto load = [](double ctas) { return ctas > 592 ? ctas / 592 : 1; };
+    DeltaSegments x = {1, seqlen, nullptr, nullptr, nullptr};
+    if (dk > 128) return x;
+    double best = 0.95 * seqlen * load(both * walks);
+    for (int s = 3; s <= 64; ++s) {
+        const long long part = ((long long)seqlen + s - 1) / s, tokens = (part + unit - 1) / unit * unit;
+        if (tokens * (s - 1) >= seqlen) continue;            // the last would be empty
+        const double cost = 30 + 5 * s +
+            (double)tokens * (load(both * walks * (s - 1) + units * (s - 2)) + load(both * walks * (s - 1)));
+        if (cost < best) {
+            best = cost;
+            x.count = s;
+            x.tokens = (int)tokens;
+        }
+    }
+    return x;
+}
+static size_t starts_bytes(const DeltaSegments &x, int batch, int heads, int dk, int dv) {
+    return x.count > 1 ? (size_t)(x.count - 1) * batch * heads * dk * dv * 4 : 0;
+}
+static size_t units_bytes(const DeltaSegments &x, int batch, int heads, int dk) {
+    return x.count > 1 ? (size_t)(x.count - 2) * batch * heads * dk * dk * 4 : 0;
+}
+
+size_t delta_walk_workspace(int batch, int heads, int seqlen, int dk, int dv) {
+    const DeltaSegments x = walk_segments(batch, heads, seqlen, dk, dv, 1, false);
+    return starts_bytes(x, batch, heads, dk, dv) + units_bytes(x, batch, heads, dk);
+}
+
+static cudaError_t walk_pass(const DeltaArgs &a, const DeltaSegments &x, int last, cudaStream_t stream) {
+    const int bhs = a.batch * a.heads, walks = (int)walk_ctas(a);
+    const int ctas = walks * (x.count - 1) + (last ? 0 : bhs * (a.dk / kWalkSlab) * (x.count - 2));
+    KernelTimer timer("delta_walk_segments", stream);
+    count_launch();
+    return a.dk == 64 ? launch_walk_segments<64>(a, x, ctas, last, stream)
+                      : launch_walk_segments<128>(a, x, ctas, last, stream);
+}
+
+cudaError_t launch_delta_walk_segments(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
+    DeltaSegments x = walk_segments(a.batch, a.heads, a.seqlen, a.dk, a.dv, 1, false);
+    if (x.count == 1) return launch_delta_walk(a, stream);
+    x.starts = (float *)workspace;
+    x.units = (float *)((char *)workspace + starts_bytes(x, a.batch, a.heads, a.dk, a.dv));
+    cudaError_t e = walk_pass(a, x, 0, stream);
+    if (e != cudaSuccess) return e;
+    e = launch_delta_join(x.starts, nullptr, x.units, a.batch * a.heads, a.dk, a.dv, x.count - 2, stream);
+    return e != cudaSuccess ? e : walk_pass(a, x, 1, stream);
+}
+
+static cudaError_t sweep_pass(const DeltaArgs &a, const DeltaSweepOut &o, const DeltaSegments &x,
+                              int last, cudaStream_t stream) {
+    const int bhs = a.batch * a.heads, walks = (int)walk_ctas(a);
+    const int ctas = 2 * walks * (x.count - 1) + (last ? 0 : bhs * (a.dk / kWalkSlab) * (x.count - 2));
+    KernelTimer timer("delta_sweeps_segments", stream);
+    count_launch();
+    if (a.dtype == RETNET_BF16)
+        return a.dk == 64 ? launch_sweeps_segments<__nv_bfloat16, 64>(a, o, x, ctas, last, stream)
+                          : launch_sweeps_segments<__nv_bfloat16, 128>(a, o, x, ctas, last, stream);
+    return a.dk == 64 ? launch_sweeps_segments<float, 64>(a, o, x, ctas, last, stream)
+                      : launch_sweeps_segments<float, 128>(a, o, x, ctas, last, stream);
+}
+
+static cudaError_t sweep_segments(const DeltaArgs &a, const DeltaSweepOut &o, const DeltaSegments &x,
+                                  cudaStream_t stream) {
+    cudaError_t e = sweep_pass(a, o, x, 0, stream);
+    if (e != cudaSuccess) return e;
+    e = launch_delta_join(x.starts, x.back, x.units, a.batch * a.heads, a.dk, a.dv, x.count - 2, stream);
+    return e != cudaSuccess ? e : sweep_pass(a, o, x, 1, stream);
 }
 
 static size_t up1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
 
 struct DeltaGradLayout {
-    size_t x, r, s, d, dq, dk, total;
+    size_t x, r, s, d, dq, dk, starts, back, units, total;
+    DeltaSegments segments;
 };
 static DeltaGradLayout grad_layout(int batch, int heads, int key_heads, int seqlen, int dk, int dv) {
     const size_t rows = (size_t)batch * seqlen * heads;
-    const size_t nc = (seqlen + kDeltaChunk - 1) / kDeltaChunk;
+    const size_t nc = ((size_t)seqlen + kDeltaChunk - 1) / kDeltaChunk;
     const size_t rv = up1k(rows * dv * 4), rk = heads != key_heads ? up1k(rows * dk * 4) : 0;
     const size_t st = up1k((size_t)batch * heads * nc * dk * dv * 4);
     DeltaGradLayout l;
@@ -846,7 +1085,11 @@ static DeltaGradLayout grad_layout(int batch, int heads, int key_heads, int seql
     l.d = l.s + st;
     l.dq = l.d + st;
     l.dk = l.dq + rk;
-    l.total = l.dk + rk;
+    l.segments = walk_segments(batch, heads, seqlen, dk, dv, kDeltaChunk, true);
+    l.starts = l.dk + rk;
+    l.back = l.starts + starts_bytes(l.segments, batch, heads, dk, dv);
+    l.units = l.back + starts_bytes(l.segments, batch, heads, dk, dv);
+    l.total = l.units + units_bytes(l.segments, batch, heads, dk);
     return l;
 }
 
@@ -898,8 +1141,12 @@ cudaError_t launch_delta_share(const DeltaArgs &a, const float *dq_wide, const f
 cudaError_t launch_delta_backward_simt(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
     const DeltaGradLayout l = grad_layout(a.batch, a.heads, a.key_heads, a.seqlen, a.dk, a.dv);
     char *ws = (char *)workspace;
-    cudaError_t e = sweep(a, (float *)(ws + l.x), (float *)(ws + l.s), (float *)(ws + l.r),
-                          (float *)(ws + l.d), stream);
+    const DeltaSweepOut o = {(float *)(ws + l.x), (float *)(ws + l.s), (float *)(ws + l.r), (float *)(ws + l.d)};
+    DeltaSegments x = l.segments;
+    x.starts = (float *)(ws + l.starts);
+    x.back = (float *)(ws + l.back);
+    x.units = (float *)(ws + l.units);
+    cudaError_t e = x.count > 1 ? sweep_segments(a, o, x, stream) : sweep(a, o, stream);
     if (e != cudaSuccess) return e;
     return a.dtype == RETNET_BF16 ? launch_grad<__nv_bfloat16>(a, l, ws, stream)
                                   : launch_grad<float>(a, l, ws, stream);

@@ -890,67 +890,132 @@ delta_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     forward_walk<DK, true, true, false>(tm_k, tm_v, tm_o, a, w);
 }
 
-// starts[j] <- starts[j] + M_j starts[j - 1], j = 1 ..: a CTA takes 16 columns
-// of a (sequence, head)'s states, a thread 8 rows of one; the next M is copied
-// while this one is used (4 joins for 16 heads of 128: 28 us without, 20 with).
-constexpr int kJoinCols = 16;
+// starts[j] <- starts[j] + M starts[j - 1], j = 1 .. joins, with M of units
+// [j - 1] (kBack: the transpose of units[joins - j]): a CTA takes 16 columns of
+// a (sequence, head)'s states, a warp 16 rows, in three tf32 products as
+// square_tile; the next M is copied while this one is used.  4 joins for 16
+// heads of 128: @@ us (20 with float32 instructions, bound by their operands
+// from shared memory).
+constexpr int kJoinCols = 16, kJoinPad = 24;
 template <int DK>
-__global__ void __launch_bounds__(2 * DK)
-delta_join_kernel(float *starts, const float *units, int bhs, int dv, int joins) {
-    extern __shared__ __align__(16) float join_smem[];
-    float *S = join_smem + 2 * DK * DK;                    // M twice [row][k], S [k][16]
+struct DeltaJoinSmem {
+    static constexpr int pad(bool back) { return DK + (back ? 8 : 4); }   // rows of M: operands in 32 banks
+    float M[2][DK * pad(true)];
+    uint32_t hi[2][DK * kJoinPad], lo[2][DK * kJoinPad];   // the state, [k][column]
+};
+template <int DK, bool kBack>
+__device__ __forceinline__ void join_states(float *starts, const float *units, int bhs, int dv, int joins) {
+    using Smem = DeltaJoinSmem<DK>;
+    constexpr int kPad = Smem::pad(kBack);
+    extern __shared__ __align__(16) uint8_t join_smem[];
+    Smem &m = *reinterpret_cast<Smem *>(join_smem);
     const int bh = blockIdx.x / (dv / kJoinCols), col = (blockIdx.x % (dv / kJoinCols)) * kJoinCols;
-    const int c = threadIdx.x % kJoinCols, r = (threadIdx.x / kJoinCols) * 8;
-    const size_t at = (size_t)r * dv + col + c;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, gr = lane / 4, tq = lane % 4;
+    // this thread's accumulators: rows r, r + 8, columns 2 tq, + 1 of two tiles
+    const int r = 16 * warp + gr;
+    const size_t at = (size_t)bh * DK * dv + (size_t)r * dv + col + 2 * tq, step = (size_t)bhs * DK * dv;
     grid_dependency_wait();
     auto fetch = [&](int j) {
         if (j <= joins) {
-            const float *m = units + ((size_t)(j - 1) * bhs + bh) * DK * DK;
-            float *dst = join_smem + (j & 1) * DK * DK;
+            const float *src = units + ((size_t)(kBack ? joins - j : j - 1) * bhs + bh) * DK * DK;
 #pragma unroll 8
             for (int i = threadIdx.x * 4; i < DK * DK; i += 2 * DK * 4)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst + i)), "l"(m + i) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 smem_u32(&m.M[j & 1][(i / DK) * kPad + i % DK])), "l"(src + i) : "memory");
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(1);
-    float s[8], next[8] = {};
-    auto get = [&](int j, float (&x)[8]) {
+    auto get = [&](int j, float (&x)[2][4]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = starts[((size_t)j * bhs + bh) * DK * dv + at + (size_t)i * dv];
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+                *reinterpret_cast<float2 *>(&x[t][2 * hf]) =
+                    *reinterpret_cast<const float2 *>(starts + j * step + at + (size_t)(8 * hf) * dv + 8 * t);
     };
+    auto part = [](float x, uint32_t &hi, uint32_t &lo) {
+        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+    };
+    auto mma = [](float (&c)[4], const uint32_t (&x)[4], const uint32_t (&y)[2]) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(y[0]), "r"(y[1]));
+    };
+    fetch(1);
+    float s[2][4], next[2][4];
     get(0, s);
-    if (joins > 0) get(1, next);
     for (int j = 1; j <= joins; ++j) {
+        get(j, next);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int o = (r + 8 * (e >> 1)) * kJoinPad + 8 * t + 2 * tq + (e & 1);
+                part(s[t][e], m.hi[j & 1][o], m.lo[j & 1][o]);
+            }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();                                   // and all are done with the last M
         fetch(j + 1);
+        const float *M = m.M[j & 1];
+        float small[2][4] = {};                            // products of the low parts
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            S[(r + i) * kJoinCols + c] = s[i];
-            s[i] = next[i];
-        }
-        if (j < joins) get(j + 1, next);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncthreads();
-        const float *M = join_smem + (j & 1) * DK * DK + r * DK;
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] = next[t][e];
 #pragma unroll 4
-        for (int k = 0; k < DK; k += 4) {
-            float x[4];
+        for (int k = 0; k < DK; k += 8) {
+            uint32_t ah[4], al[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) x[u] = S[(k + u) * kJoinCols + c];
+            for (int e = 0; e < 4; ++e) {
+                const int row = r + 8 * (e & 1), c = k + tq + 4 * (e >> 1);
+                part(kBack ? M[c * kPad + row] : M[row * kPad + c], ah[e], al[e]);
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 m = *reinterpret_cast<const float4 *>(M + i * DK + k);
-                s[i] = fmaf(m.x, x[0], s[i]);
-                s[i] = fmaf(m.y, x[1], s[i]);
-                s[i] = fmaf(m.z, x[2], s[i]);
-                s[i] = fmaf(m.w, x[3], s[i]);
+            for (int t = 0; t < 2; ++t) {
+                uint32_t bh2[2], bl[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int o = (k + tq + 4 * e) * kJoinPad + 8 * t + gr;
+                    bh2[e] = m.hi[j & 1][o];
+                    bl[e] = m.lo[j & 1][o];
+                }
+                mma(s[t], ah, bh2);
+                mma(small[t], ah, bl);
+                mma(small[t], al, bh2);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) starts[((size_t)j * bhs + bh) * DK * dv + at + (size_t)i * dv] = s[i];
-        __syncthreads();
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                s[t][2 * hf] += small[t][2 * hf];
+                s[t][2 * hf + 1] += small[t][2 * hf + 1];
+                *reinterpret_cast<float2 *>(starts + j * step + at + (size_t)(8 * hf) * dv + 8 * t) =
+                    make_float2(s[t][2 * hf], s[t][2 * hf + 1]);
+            }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+template <int DK>
+__global__ void __launch_bounds__(2 * DK)
+delta_join_kernel(float *starts, float *back, const float *units, int bhs, int dv, int joins) {
+    if (blockIdx.y) join_states<DK, true>(back, units, bhs, dv, joins);
+    else join_states<DK, false>(starts, units, bhs, dv, joins);
+}
+template <int DK>
+cudaError_t launch_join(float *starts, float *back, const float *units, int bhs, int dv, int joins,
+                        cudaStream_t stream) {
+    constexpr int kBytes = (int)sizeof(DeltaJoinSmem<DK>);
+    cudaError_t e = cudaFuncSetAttribute(delta_join_kernel<DK>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e != cudaSuccess) return e;
+    KernelTimer timer("delta_join", stream);
+    count_launch();
+    return launch_overlapped(delta_join_kernel<DK>, dim3((unsigned)(bhs * (dv / kJoinCols)), back ? 2 : 1),
+                             dim3(2 * DK), kBytes, stream, starts, back, units, bhs, dv, joins);
 }
 
 // ------------------------------------------------------------------ reverse scan
@@ -1898,12 +1963,9 @@ cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, cudaS
 template <int DK>
 cudaError_t launch_segments(const DeltaArgs &a, const DeltaTcLayout &l, uint8_t *ws, cudaStream_t stream) {
     using Smem = DeltaScanSmem<DK, true>;
-    constexpr int kJoinBytes = (2 * DK * DK + DK * kJoinCols) * 4;
     cudaError_t e = cudaFuncSetAttribute(delta_segments_kernel<DK>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Smem::kBytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(delta_join_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kJoinBytes);
     if (e != cudaSuccess) return e;
     CUtensorMap tm_k, tm_v, tm_o;
     if (!scan_maps(a, &tm_k, &tm_v, &tm_o)) return cudaErrorInvalidValue;
@@ -1920,14 +1982,8 @@ cudaError_t launch_segments(const DeltaArgs &a, const DeltaTcLayout &l, uint8_t 
     };
     e = pass(walks * (l.segments - 1) + bhs * (l.segments - 2), 0);
     if (e != cudaSuccess) return e;
-    {
-        KernelTimer timer("delta_join", stream);
-        count_launch();
-        e = launch_overlapped(delta_join_kernel<DK>, dim3((unsigned)(bhs * (a.dv / kJoinCols))),
-                              dim3(2 * DK), kJoinBytes, stream, starts, (const float *)units, bhs,
-                              a.dv, l.segments - 2);
-        if (e != cudaSuccess) return e;
-    }
+    e = launch_join<DK>(starts, nullptr, units, bhs, a.dv, l.segments - 2, stream);
+    if (e != cudaSuccess) return e;
     return pass(walks * (l.segments - 1), 1);
 }
 
@@ -2022,6 +2078,12 @@ cudaError_t launch_forward(const DeltaArgs &a, void *workspace, cudaStream_t str
 }
 
 }  // namespace
+
+cudaError_t launch_delta_join(float *starts, float *back, const float *units, int bhs, int dk, int dv,
+                              int joins, cudaStream_t stream) {
+    return dk == 64 ? launch_join<64>(starts, back, units, bhs, dv, joins, stream)
+                    : launch_join<128>(starts, back, units, bhs, dv, joins, stream);
+}
 
 size_t delta_backward_tc_workspace(int batch, int heads, int key_heads, int seqlen, int dk, int dv) {
     return tc_grad_layout(batch, heads, key_heads, seqlen, dk, dv).total;

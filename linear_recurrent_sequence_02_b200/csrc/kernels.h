@@ -152,6 +152,9 @@ struct DeltaArgs {
 // in place (state_in and state_out the same), and runs of tokens.
 cudaError_t launch_delta_step(const DeltaArgs &a, cudaStream_t stream);
 cudaError_t launch_delta_walk(const DeltaArgs &a, cudaStream_t stream);
+// As launch_delta_walk, in segments where that is faster (dk 64 or 128).
+size_t delta_walk_workspace(int batch, int heads, int seqlen, int dk, int dv);
+cudaError_t launch_delta_walk_segments(const DeltaArgs &a, void *workspace, cudaStream_t stream);
 size_t delta_backward_simt_workspace(int batch, int heads, int key_heads, int seqlen, int dk,
                                      int dv);
 cudaError_t launch_delta_backward_simt(const DeltaArgs &a, void *workspace, cudaStream_t stream);
@@ -161,6 +164,11 @@ size_t delta_tc_workspace(int batch, int heads, int seqlen, int dk, int dv);
 cudaError_t launch_delta_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream);
 size_t delta_backward_tc_workspace(int batch, int heads, int key_heads, int seqlen, int dk, int dv);
 cudaError_t launch_delta_backward_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream);
+// The states between segments, starts[j] += M_j starts[j - 1], j = 1 .. joins,
+// M_j of units [joins][bhs][dk, dk], starts [joins + 1][bhs][dk, dv]; back
+// (may be null): the same with M_{joins + 1 - j}^T.  dk 64 or 128.
+cudaError_t launch_delta_join(float *starts, float *back, const float *units, int bhs, int dk, int dv,
+                              int joins, cudaStream_t stream);
 // dq and dk of key heads shared by several value heads, from float32
 // [B, n, heads, dk] gradients per value head; nothing where none is shared.
 cudaError_t launch_delta_share(const DeltaArgs &a, const float *dq_wide, const float *dk_wide,

@@ -229,6 +229,52 @@ def test_chunkwise_long_with_few_heads(rn, dk, dv, H):
     assert err(S, St, 1) < 3e-5
 
 
+@pytest.mark.parametrize("dk,dv,H,lens", [(128, 64, 2, [1501, 0, 700]), (64, 256, 3, [900, 64, 1500]),
+                                          (128, 128, 1, [1501, 1501, 1])])
+def test_float32_prefill_in_segments(rn, dk, dv, H, lens):
+    """As above in float32 (the walk of single tokens in segments)."""
+    B, n = 3, 1501
+    (q, k, v, g, beta, _), ref = make(24, B, n, 1, H, dk, dv, "f32", decay=0.02)
+    for x, r in zip((q, k, v, g, beta), ref):
+        for b, c in enumerate(lens):
+            x[b, c:] = float("nan")
+            r[b, c:] = 0.0
+    lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    assert rn.retnet_delta_workspace_size(B, H, 1, n, dk, dv, torch.float32) > 0
+    S, S0 = states(25, B, H, dk, dv)
+    whole_S = S.clone()
+    out, whole = torch.full_like(v, 5.0), torch.full_like(v, 5.0)
+    rn.retnet_delta_chunkwise(q, k, v, g, beta, lengths=lengths, state_in=S, state_out=S, out=out)
+    rn.retnet_delta_chunkwise(q, k, v, g, beta, lengths=lengths, state_in=whole_S,
+                              state_out=whole_S, out=whole, algo="simt")
+    done(rn)
+    o, St = oracle.delta_recurrent(*ref[:5], dk ** -0.5, S0, lens)
+    for b, c in enumerate(lens):
+        assert (out[b, c:] == 5).all() and (whole[b, c:] == 5).all()
+        out[b, c:] = whole[b, c:] = 0
+    for got, want, axis in ((out, o, 2), (whole, o, 2), (S, St, 1), (whole_S, St, 1)):
+        assert err(got, want, axis) < bound("f32")
+
+
+@pytest.mark.parametrize("dk,dv,Hk,H,lens", [(64, 128, 1, 2, [1100, 0, 640]), (128, 64, 2, 2, [64, 1100, 65])])
+def test_float32_backward_in_segments(rn, dk, dv, Hk, H, lens):
+    B, n = 3, 1100
+    x, ref = make(26, B, n, Hk, H, dk, dv, "f32", decay=0.02)
+    for t, r in zip(x, ref):
+        for b, c in enumerate(lens):
+            t[b, c:] = float("nan")
+            r[b, c:] = 0.0
+    lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = rn.retnet_delta_backward(*x, lengths=lengths)
+    done(rn)
+    want = oracle.delta_backward(*ref, dk ** -0.5, lens)
+    for name, a, w in zip(("dq", "dk", "dv", "dg", "dbeta"), got, want):
+        for b, c in enumerate(lens):
+            assert not a[b, c:].any(), name
+        w, a = together(w, a)
+        assert err(a, w) < bound("f32"), name
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_chunkwise_gates_at_their_ends(rn, dtype):
     """g: -inf (the state is emptied), 0, and far below what float32 resolves;
