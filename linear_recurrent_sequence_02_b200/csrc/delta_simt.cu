@@ -17,7 +17,7 @@
 //     the latency of the chain product -> reduction -> update from token to
 //     token: a warp owns 4 columns and all rows, so that the chain is nine
 //     shuffles and no barrier (1000 tokens of 128 x 64: 650 us in slabs of 32
-//     columns, 265 us so; four tokens a turn by the triangle between them
+//     columns, 265 us so, 129 in segments; four tokens a turn by the triangle between them
 //     gained a tenth forward and lost it back: one warp a scheduler is then
 //     bound by its instructions).
 #include "delta.cuh"
@@ -990,22 +990,31 @@ static cudaError_t sweep(const DeltaArgs &a, const DeltaSweepOut &o, cudaStream_
 
 // ---- segments of the walks
 // How many segments, and tokens of each (a multiple of `unit`).  Time in
-// tokens behind one another (0.27 us while an SM has no more than four CTAs):
-// both passes, 30 for the further launches, 5 a join of states.  The join
-// holds two transitions in shared memory, so dk 256 walks whole.
+// tokens behind one another (0.26 us): both passes with the waves of CTAs that
+// their registers allow (two CTAs of an SM take 1.2 times as long as one,
+// three 1.5), 30 for the further launches, 10 a join of states (4 for dk 64).
+// Measured: 8 heads, 1000 tokens, 128 x 64: 263 us whole, 129 in 6 segments;
+// 1 head, 8192 tokens, 128 x 128: 2120 and 288 in 24; 64 heads, 512 tokens:
+// 343 and 518 in 3 (whole).  Backward, 1 head, 4096 tokens: 1221 and 302 in
+// 16; 18 heads, 333 tokens: 142 and 173 in 3 (whole).  A join reads whole
+// transitions, for dk 256 four times those of 128, so dk 256 walks whole.
 static DeltaSegments walk_segments(int batch, int heads, int seqlen, int dk, int dv, int unit,
                                    bool backward) {
-    const double walks = (double)batch * heads * (dv / kWalkSlab), units = (double)batch * heads * (dk / kWalkSlab);
-    const int both = backward ? 2 : 1;                       // ways
-    auto load = [](double ctas) { return ctas > 592 ? ctas / 592 : 1; };
     DeltaSegments x = {1, seqlen, nullptr, nullptr, nullptr};
     if (dk > 128) return x;
-    double best = 0.95 * seqlen * load(both * walks);
+    const long long bh = (long long)batch * heads, units = bh * (dk / kWalkSlab);
+    const long long walks = bh * (dv / kWalkSlab) * (backward ? 2 : 1);
+    const int resident = dk == 64 ? 4 : 3;                   // CTAs of an SM
+    auto level = [](long long per_sm) { return per_sm < 2 ? (double)per_sm : 1.2 + 0.3 * (per_sm - 2); };
+    auto load = [&](long long ctas) {
+        return (double)(ctas / (148 * resident)) * level(resident) + level((ctas % (148 * resident) + 147) / 148);
+    };
+    double best = 0.95 * seqlen * load(walks);
     for (int s = 3; s <= 64; ++s) {
         const long long part = ((long long)seqlen + s - 1) / s, tokens = (part + unit - 1) / unit * unit;
         if (tokens * (s - 1) >= seqlen) continue;            // the last would be empty
-        const double cost = 30 + 5 * s +
-            (double)tokens * (load(both * walks * (s - 1) + units * (s - 2)) + load(both * walks * (s - 1)));
+        const double cost = 30 + (dk == 64 ? 4 : 10) * (s - 2) +
+            (double)tokens * (load(walks * (s - 1) + units * (s - 2)) + load(walks * (s - 1)));
         if (cost < best) {
             best = cost;
             x.count = s;

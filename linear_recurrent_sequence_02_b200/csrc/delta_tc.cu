@@ -893,37 +893,41 @@ delta_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
 // starts[j] <- starts[j] + M starts[j - 1], j = 1 .. joins, with M of units
 // [j - 1] (kBack: the transpose of units[joins - j]): a CTA takes 16 columns of
 // a (sequence, head)'s states, a warp 16 rows, in three tf32 products as
-// square_tile; the next M is copied while this one is used.  4 joins for 16
-// heads of 128: @@ us (20 with float32 instructions, bound by their operands
-// from shared memory).
-constexpr int kJoinCols = 16, kJoinPad = 24;
+// square_tile.  A warp's rows of M are its own, so they go from global memory
+// to its registers, the next join's while this one is multiplied; only the
+// state passes through shared memory, [column][k], its two parts.  4 joins for
+// 16 heads of 128: 11 us, most of it the way of M from L2 (8 with every M the
+// first; the products do not show).
+constexpr int kJoinCols = 16;
 template <int DK>
 struct DeltaJoinSmem {
-    static constexpr int pad(bool back) { return DK + (back ? 8 : 4); }   // rows of M: operands in 32 banks
-    float M[2][DK * pad(true)];
-    uint32_t hi[2][DK * kJoinPad], lo[2][DK * kJoinPad];   // the state, [k][column]
+    float hi[2][kJoinCols][DK + 4], lo[2][kJoinCols][DK + 4];
 };
 template <int DK, bool kBack>
-__device__ __forceinline__ void join_states(float *starts, const float *units, int bhs, int dv, int joins) {
-    using Smem = DeltaJoinSmem<DK>;
-    constexpr int kPad = Smem::pad(kBack);
-    extern __shared__ __align__(16) uint8_t join_smem[];
-    Smem &m = *reinterpret_cast<Smem *>(join_smem);
+__device__ __forceinline__ void join_states(DeltaJoinSmem<DK> &m, float *starts, const float *units,
+                                            int bhs, int dv, int joins) {
     const int bh = blockIdx.x / (dv / kJoinCols), col = (blockIdx.x % (dv / kJoinCols)) * kJoinCols;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, gr = lane / 4, tq = lane % 4;
-    // this thread's accumulators: rows r, r + 8, columns 2 tq, + 1 of two tiles
+    // this thread's accumulators: rows r, r + 8, columns 2 tq, + 1 of two tiles;
+    // its columns of M: 16 u + 4 tq .., of which each product takes two
     const int r = 16 * warp + gr;
     const size_t at = (size_t)bh * DK * dv + (size_t)r * dv + col + 2 * tq, step = (size_t)bhs * DK * dv;
     grid_dependency_wait();
-    auto fetch = [&](int j) {
-        if (j <= joins) {
-            const float *src = units + ((size_t)(kBack ? joins - j : j - 1) * bhs + bh) * DK * DK;
-#pragma unroll 8
-            for (int i = threadIdx.x * 4; i < DK * DK; i += 2 * DK * 4)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                 smem_u32(&m.M[j & 1][(i / DK) * kPad + i % DK])), "l"(src + i) : "memory");
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+    auto get_unit = [&](int j, float (&x)[2][DK / 16][4]) {
+        const float *src = units + ((size_t)(kBack ? joins - j : j - 1) * bhs + bh) * DK * DK;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int u = 0; u < DK / 16; ++u) {
+                const int row = r + 8 * hf, k = 16 * u + 4 * tq;
+                if (kBack) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[hf][u][e] = src[(k + e) * DK + row];
+                } else {
+                    const float4 v = *reinterpret_cast<const float4 *>(src + row * DK + k);
+                    x[hf][u][0] = v.x; x[hf][u][1] = v.y; x[hf][u][2] = v.z; x[hf][u][3] = v.w;
+                }
+            }
     };
     auto get = [&](int j, float (&x)[2][4]) {
 #pragma unroll
@@ -933,89 +937,93 @@ __device__ __forceinline__ void join_states(float *starts, const float *units, i
                 *reinterpret_cast<float2 *>(&x[t][2 * hf]) =
                     *reinterpret_cast<const float2 *>(starts + j * step + at + (size_t)(8 * hf) * dv + 8 * t);
     };
-    auto part = [](float x, uint32_t &hi, uint32_t &lo) {
-        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+    // x rounded to 11 bits, and what that leaves (of which the product takes 11)
+    auto part = [](float x, float &hi, float &lo) {
+        const float t = __fmul_rn(x, 8193.f);              // no contraction
+        hi = __fsub_rn(t, __fsub_rn(t, x));
+        lo = __fsub_rn(x, hi);
     };
-    auto mma = [](float (&c)[4], const uint32_t (&x)[4], const uint32_t (&y)[2]) {
+    auto mma = [](float (&c)[4], const float (&x)[4], const float (&y)[2]) {
         asm volatile(
             "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
             "{%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(y[0]), "r"(y[1]));
+            : "r"(__float_as_uint(x[0])), "r"(__float_as_uint(x[1])), "r"(__float_as_uint(x[2])),
+              "r"(__float_as_uint(x[3])), "r"(__float_as_uint(y[0])), "r"(__float_as_uint(y[1])));
     };
-    fetch(1);
-    float s[2][4], next[2][4];
-    get(0, s);
-    for (int j = 1; j <= joins; ++j) {
-        get(j, next);
+    float M[2][2][DK / 16][4], s[2][4], next[2][4];
+    auto join = [&](int j, float (&cur)[2][DK / 16][4], float (&ahead)[2][DK / 16][4]) {
+        if (j < joins) get_unit(j + 1, ahead);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int o = (r + 8 * (e >> 1)) * kJoinPad + 8 * t + 2 * tq + (e & 1);
-                part(s[t][e], m.hi[j & 1][o], m.lo[j & 1][o]);
+                const int c = 8 * t + 2 * tq + (e & 1), k = r + 8 * (e >> 1);
+                part(s[t][e], m.hi[j & 1][c][k], m.lo[j & 1][c][k]);
             }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();                                   // and all are done with the last M
-        fetch(j + 1);
-        const float *M = m.M[j & 1];
-        float small[2][4] = {};                            // products of the low parts
+        __syncthreads();                                   // and all are done with the state before the last
+        float lo1[2][4] = {}, lo2[2][4] = {};              // products of the low parts
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[t][e] = next[t][e];
-#pragma unroll 4
-        for (int k = 0; k < DK; k += 8) {
-            uint32_t ah[4], al[4];
+        if (j < joins) get(j + 1, next);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = r + 8 * (e & 1), c = k + tq + 4 * (e >> 1);
-                part(kBack ? M[c * kPad + row] : M[row * kPad + c], ah[e], al[e]);
-            }
+        for (int u = 0; u < DK / 16; ++u) {
+            float bh4[2][4], bl4[2][4];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                uint32_t bh2[2], bl[2];
+                *reinterpret_cast<float4 *>(bh4[t]) =
+                    *reinterpret_cast<const float4 *>(&m.hi[j & 1][8 * t + gr][16 * u + 4 * tq]);
+                *reinterpret_cast<float4 *>(bl4[t]) =
+                    *reinterpret_cast<const float4 *>(&m.lo[j & 1][8 * t + gr][16 * u + 4 * tq]);
+            }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int o = (k + tq + 4 * e) * kJoinPad + 8 * t + gr;
-                    bh2[e] = m.hi[j & 1][o];
-                    bl[e] = m.lo[j & 1][o];
+            for (int h = 0; h < 4; h += 2) {
+                float ah[4], al[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) part(cur[e & 1][u][h + (e >> 1)], ah[e], al[e]);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const float yh[2] = {bh4[t][h], bh4[t][h + 1]}, yl[2] = {bl4[t][h], bl4[t][h + 1]};
+                    mma(s[t], ah, yh);
+                    mma(lo1[t], ah, yl);
+                    mma(lo2[t], al, yh);
                 }
-                mma(s[t], ah, bh2);
-                mma(small[t], ah, bl);
-                mma(small[t], al, bh2);
             }
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                s[t][2 * hf] += small[t][2 * hf];
-                s[t][2 * hf + 1] += small[t][2 * hf + 1];
+                s[t][2 * hf] += lo1[t][2 * hf] + lo2[t][2 * hf];
+                s[t][2 * hf + 1] += lo1[t][2 * hf + 1] + lo2[t][2 * hf + 1];
                 *reinterpret_cast<float2 *>(starts + j * step + at + (size_t)(8 * hf) * dv + 8 * t) =
                     make_float2(s[t][2 * hf], s[t][2 * hf + 1]);
             }
+    };
+    get_unit(1, M[1]);
+    get(0, s);
+    get(1, next);
+    for (int j = 1; j <= joins; j += 2) {
+        join(j, M[1], M[0]);
+        if (j < joins) join(j + 1, M[0], M[1]);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 template <int DK>
 __global__ void __launch_bounds__(2 * DK)
 delta_join_kernel(float *starts, float *back, const float *units, int bhs, int dv, int joins) {
-    if (blockIdx.y) join_states<DK, true>(back, units, bhs, dv, joins);
-    else join_states<DK, false>(starts, units, bhs, dv, joins);
+    __shared__ __align__(16) DeltaJoinSmem<DK> m;
+    if (blockIdx.y) join_states<DK, true>(m, back, units, bhs, dv, joins);
+    else join_states<DK, false>(m, starts, units, bhs, dv, joins);
 }
 template <int DK>
 cudaError_t launch_join(float *starts, float *back, const float *units, int bhs, int dv, int joins,
                         cudaStream_t stream) {
-    constexpr int kBytes = (int)sizeof(DeltaJoinSmem<DK>);
-    cudaError_t e = cudaFuncSetAttribute(delta_join_kernel<DK>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-    if (e != cudaSuccess) return e;
     KernelTimer timer("delta_join", stream);
     count_launch();
     return launch_overlapped(delta_join_kernel<DK>, dim3((unsigned)(bhs * (dv / kJoinCols)), back ? 2 : 1),
-                             dim3(2 * DK), kBytes, stream, starts, back, units, bhs, dv, joins);
+                             dim3(2 * DK), 0, stream, starts, back, units, bhs, dv, joins);
 }
 
 // ------------------------------------------------------------------ reverse scan
