@@ -528,7 +528,8 @@ __device__ __forceinline__ DeltaWalk whole_walk(const DeltaScanArgs &a, int dk, 
             a.state_out ? a.state_out + at : nullptr, out, false};
 }
 
-template <int DK, bool kSplit, bool kOut, bool kSave>
+// kFine: in two parts; kSplit: the blocks have two.
+template <int DK, bool kSplit, bool kOut, bool kSave, bool kFine>
 __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                              const CUtensorMap &tm_o, const DeltaScanArgs &a,
                                              const DeltaWalk &w) {
@@ -591,8 +592,18 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
             if (elect_one()) {
                 const uint32_t block = out ? Block::kBytes : Block::kQ;
                 const int t0 = (w.first + it) * kC;
-                mbar_expect_tx(&bar.full[s], block + (w.unit ? Smem::kV : Smem::kStage) - Smem::kK);
-                bulk_load(st, blocks + (size_t)it * Block::kBytes, block, &bar.full[s]);
+                const uint8_t *src = blocks + (size_t)it * Block::kBytes;
+                const uint32_t rest = (w.unit ? Smem::kV : Smem::kStage) - Smem::kK;
+                if (kFine || !kSplit) {
+                    mbar_expect_tx(&bar.full[s], block + rest);
+                    bulk_load(st, src, block, &bar.full[s]);
+                } else {                                   // without the second parts
+                    constexpr uint32_t kWBytes = Block::kWlo - Block::kW;
+                    mbar_expect_tx(&bar.full[s], kBox64 + kWBytes + block - Block::kHdr + rest);
+                    bulk_load(st + Block::kT, src + Block::kT, kBox64, &bar.full[s]);
+                    bulk_load(st + Block::kW, src + Block::kW, kWBytes, &bar.full[s]);
+                    bulk_load(st + Block::kHdr, src + Block::kHdr, block - Block::kHdr, &bar.full[s]);
+                }
                 if (!w.unit)
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
@@ -621,7 +632,7 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                 for (int ks = 0; ks < 4; ++ks) {
                     const uint64_t ad = mnmaj + ((Smem::kV + ks * 2048) >> 4);
                     mma_bf16(tmem + Tm::kX, ad, kmaj + ((Block::kT + ks * 32) >> 4), id_tv, ks > 0);
-                    if (kSplit)
+                    if (kFine)
                         mma_bf16(tmem + Tm::kX, ad, kmaj + ((Block::kTlo + ks * 32) >> 4), id_tv, 1);
                 }
             }
@@ -639,7 +650,7 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                         const uint32_t o = p * kBox64 + k4 * 32;
                         const uint64_t wd = kmaj + ((Block::kW + o) >> 4);
                         mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kShi + 8 * ks, wd, id_x, ks > 0 || !w.unit);
-                        if (kSplit) {
+                        if (kFine) {
                             mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kSlo + 8 * ks, wd, id_x, 1);
                             mma_bf16_ts(tmem + Tm::kX, tmem + Tm::kShi + 8 * ks,
                                         kmaj + ((Block::kWlo + o) >> 4), id_x, 1);
@@ -671,7 +682,7 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                     for (int ks = 0; ks < 4; ++ks) {
                         const uint64_t kd = mnmaj + ((Smem::kK + p * kBox64 + ks * 2048) >> 4);
                         mma_bf16_ts(tmem + Tm::kZ + 64 * p, tmem + Tm::kXs + 8 * ks, kd, id_z, ks > 0);
-                        if (kSplit)
+                        if (kFine)
                             mma_bf16_ts(tmem + Tm::kZ + 64 * p, tmem + Tm::kXslo + 8 * ks, kd, id_z, 1);
                     }
                     mma_commit(&bar.z_full[p]);
@@ -708,11 +719,11 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
             uint32_t hi[16], lo[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                if (kSplit) split_pair(S[p][j], hi[j], lo[j]);
+                if (kFine) split_pair(S[p][j], hi[j], lo[j]);
                 else hi[j] = pack_bf16x2(S[p][j].x, S[p][j].y);
             }
             tmem_st16(tl + Tm::kShi + 32 * p + 16 * wg, hi);
-            if (kSplit) tmem_st16(tl + Tm::kSlo + 32 * p + 16 * wg, lo);
+            if (kFine) tmem_st16(tl + Tm::kSlo + 32 * p + 16 * wg, lo);
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&bar.s_ready[p]);
@@ -736,12 +747,12 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                 for (int j = 0; j < 16; ++j) {
                     const float2 r = *reinterpret_cast<const float2 *>(hdr + 32 * wg + 2 * j);
                     const float2 xv = as_pair(x[2 * j], x[2 * j + 1]), xr = mul2(xv, r);
-                    if (kSplit) split_pair(xr, hi[j], lo[j]);
+                    if (kFine) split_pair(xr, hi[j], lo[j]);
                     else hi[j] = pack_bf16x2(xr.x, xr.y);
                     if (kOut || kSave) xb[j] = pack_bf16x2(xv.x, xv.y);
                 }
                 tmem_st16(tl + Tm::kXs + 16 * wg, hi);
-                if (kSplit) tmem_st16(tl + Tm::kXslo + 16 * wg, lo);
+                if (kFine) tmem_st16(tl + Tm::kXslo + 16 * wg, lo);
                 if (kOut) tmem_st16(tl + Tm::kXb + 16 * wg, xb);
                 tmem_wait_st();
                 tc_fence_before();
@@ -837,7 +848,7 @@ template <int DK, bool kSplit>
 __global__ void __launch_bounds__(kScanThreads, 1)
 delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_o, DeltaScanArgs a) {
-    forward_walk<DK, kSplit, true, false>(tm_k, tm_v, tm_o, a, whole_walk(a, DK, blockIdx.x, true));
+    forward_walk<DK, kSplit, true, false, kSplit>(tm_k, tm_v, tm_o, a, whole_walk(a, DK, blockIdx.x, true));
 }
 
 // ---- in segments
@@ -848,18 +859,20 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 // segment as it is; then the states between segments, S_{j+1} = M_j S_j + N_j,
 // in float32; then all other segments' outputs at once.  Each chunk is walked
 // up to three times, but on all SMs: 8192 tokens and 16 heads of 128 in 6
-// segments, walk 274 us whole, 125 us so, and 20 us the join.
+// segments, walk 274 us whole, 103 us so, and 11 us the join.
+// Only what a final state depends on is walked in two parts: not the outputs
+// of the second pass, but its last segment, which is shorter for that.
 // starts [segments - 1][BH][dk, dv]: N_j and then the state before segment
 // j + 1; units [segments - 2][BH][dk, dk]: M of segments 1 ...
-template <int DK>
+template <int DK, bool kSplit, bool kLast>
 __global__ void __launch_bounds__(kScanThreads, 1)
 delta_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const __grid_constant__ CUtensorMap tm_o, DeltaScanArgs a, int bhs, int last) {
+                      const __grid_constant__ CUtensorMap tm_o, DeltaScanArgs a, int bhs) {
     const int slabs = (a.dv + 127) / 128, walks = bhs * slabs;
     const size_t ssize = (size_t)DK * a.dv;
     int cta = blockIdx.x;
     DeltaWalk w;
-    if (last) {                                            // outputs of segments 1 ...
+    if (kLast) {                                           // outputs of segments 1 ...
         const int seg = 1 + cta / walks;
         w = whole_walk(a, DK, cta % walks, true);
         w.from = a.starts + ((size_t)(seg - 1) * bhs + w.bh) * ssize;
@@ -887,7 +900,13 @@ delta_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         w.first = seg * a.segment;
     }
     w.last = w.first + a.segment;
-    forward_walk<DK, true, true, false>(tm_k, tm_v, tm_o, a, w);
+    if constexpr (kSplit && kLast) {
+        if (!w.to) {
+            forward_walk<DK, kSplit, true, false, false>(tm_k, tm_v, tm_o, a, w);
+            return;
+        }
+    }
+    forward_walk<DK, kSplit, true, false, kSplit>(tm_k, tm_v, tm_o, a, w);
 }
 
 // starts[j] <- starts[j] + M starts[j - 1], j = 1 .. joins, with M of units
@@ -1311,7 +1330,7 @@ delta_walks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                    DeltaScanArgs f, DeltaReverseArgs r) {
     const int half = gridDim.x / 2;
     if ((int)blockIdx.x < half)
-        forward_walk<DK, false, false, true>(tm_k, tm_v, tm_v, f, whole_walk(f, DK, blockIdx.x, false));
+        forward_walk<DK, false, false, true, false>(tm_k, tm_v, tm_v, f, whole_walk(f, DK, blockIdx.x, false));
     else reverse_walk<DK>(tm_k, tm_do, tm_dv, r, blockIdx.x - half);
 }
 
@@ -1901,29 +1920,38 @@ cudaError_t launch_prep(const DeltaArgs &a, int nc, uint8_t *blocks, bool backwa
                              sizeof(DeltaPrepSmem<DK, kSplit>), stream, p);
 }
 
-// Segments of the walk over nc chunks: the count with the least time, counted
-// in chunks walked behind one another (a wave of 148 CTAs each, first pass
-// and second).  The two further launches cost 4 of them and a join of states
-// 1.5 (1 for dk 64); without a final state the whole walk has its operands in
-// one part and takes 5/8 of the time (3/4 for dk 64).  Measured with a final state, 128 x 128:
-// 16 heads, 128 chunks: 360 us whole, 212 in 6 segments; 32 chunks: 96 and 79;
-// 48 heads, 32 chunks: 143 and 147 (whole); 64 heads, 128 chunks: 611 and 640
-// (whole).  Without: 16 heads, 128 chunks: 239 and 212; 32 heads: 303 and 377
-// (whole).
-int delta_segments(int batch, int heads, int nc, int dk, int dv, bool final_state) {
+// Segments of the walk over nc chunks, and chunks of each: the count with the
+// least time, counted in chunks walked behind one another in two parts (a wave
+// of 148 CTAs each, first pass and second).  In one part, which is all of it
+// without a final state, a chunk takes 0.6 of that (0.72 for dk 64).  The two
+// further launches cost 7 (5, 4) and a join of states 1.  Measured, 128 x 128,
+// with a final state: 16 heads, 128 chunks: 360 us whole, 198 in 6 segments; 32
+// chunks: 96 and 73; 24 heads, 32 chunks: 110 and 98; 32 heads: 119 and 127
+// (whole); 64 heads, 128 chunks: 611 and 640 (whole).  Without: 16 heads, 128
+// chunks: 239 and 154; 1 head, 32 chunks: 54 and 44; 32 heads, 64 chunks: 158
+// whole.
+struct DeltaCut {
+    int count, chunks;
+};
+DeltaCut delta_segments(int batch, int heads, int nc, int dk, int dv, bool final_state) {
     const long long units = (long long)batch * heads, walks = units * ((dv + 127) / 128);
-    auto waves = [](long long ctas) { return (ctas + 147) / 148; };
-    float best = (float)(waves(walks) * nc) * (final_state ? 0.95f : dk == 64 ? 0.72f : 0.6f);
-    int count = 1;
+    auto waves = [](long long ctas) { return (float)((ctas + 147) / 148); };
+    const float coarse = dk == 64 ? 0.72f : 0.6f, fine = final_state ? 1.f : coarse;
+    const float fixed = !final_state ? 4.f : dk == 64 ? 5.f : 7.f;
+    float best = 0.95f * fine * waves(walks) * nc;
+    DeltaCut cut = {1, nc};
     for (int s = 3; s <= 16 && 4 * s <= nc; ++s) {
-        const long long both = waves(walks + (s - 2) * (walks + units)) + waves(walks * (s - 1));
-        const float cost = (float)(both * ((nc + s - 1) / s)) + 4.f + (dk == 64 ? 1.f : 1.5f) * s;
+        // the last segment in two parts as long as the others in one
+        const int chunks = (int)ceilf(nc / (s - 1 + coarse / fine)), left = nc - (s - 1) * chunks;
+        if (left < 1) continue;
+        const float cost = fine * chunks * waves(walks + (s - 2) * (walks + units)) +
+                           fmaxf(coarse * chunks, fine * left) * waves(walks * (s - 1)) + fixed + s;
         if (cost < best) {
             best = cost;
-            count = s;
+            cut = {s, chunks};
         }
     }
-    return count;
+    return cut;
 }
 
 struct DeltaTcLayout {
@@ -1933,8 +1961,9 @@ struct DeltaTcLayout {
 DeltaTcLayout tc_layout(int batch, int heads, int seqlen, int dk, int dv, bool final_state) {
     DeltaTcLayout l;
     l.nc = (seqlen + kC - 1) / kC;
-    l.segments = delta_segments(batch, heads, l.nc, dk, dv, final_state);
-    l.segment = (l.nc + l.segments - 1) / l.segments;
+    const DeltaCut cut = delta_segments(batch, heads, l.nc, dk, dv, final_state);
+    l.segments = cut.count;
+    l.segment = cut.chunks;
     const size_t bh = (size_t)batch * heads;
     l.starts = bh * l.nc * (dk == 64 ? DeltaBlock<64, true>::kBytes : DeltaBlock<128, true>::kBytes);
     l.units = l.starts + (l.segments > 1 ? (size_t)(l.segments - 1) * bh * dk * dv * 4 : 0);
@@ -1968,13 +1997,9 @@ cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, cudaS
                              Smem::kBytes, stream, tm_k, tm_v, tm_o, s);
 }
 
-template <int DK>
+template <int DK, bool kSplit>
 cudaError_t launch_segments(const DeltaArgs &a, const DeltaTcLayout &l, uint8_t *ws, cudaStream_t stream) {
-    using Smem = DeltaScanSmem<DK, true>;
-    cudaError_t e = cudaFuncSetAttribute(delta_segments_kernel<DK>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Smem::kBytes);
-    if (e != cudaSuccess) return e;
+    using Smem = DeltaScanSmem<DK, kSplit>;
     CUtensorMap tm_k, tm_v, tm_o;
     if (!scan_maps(a, &tm_k, &tm_v, &tm_o)) return cudaErrorInvalidValue;
     float *starts = (float *)(ws + l.starts), *units = (float *)(ws + l.units);
@@ -1982,17 +2007,21 @@ cudaError_t launch_segments(const DeltaArgs &a, const DeltaTcLayout &l, uint8_t 
                        nullptr, a.heads, a.key_heads, a.seqlen, l.nc, a.dv, device_error_word(),
                        l.segments, l.segment, starts, units};
     const int bhs = a.batch * a.heads, walks = bhs * ((a.dv + 127) / 128);
-    auto pass = [&](int ctas, int last) {
-        KernelTimer timer("delta_segments", stream);
+    auto pass = [&](auto kernel, int ctas, const char *name) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)Smem::kBytes);
+        if (e != cudaSuccess) return e;
+        KernelTimer timer(name, stream);
         count_launch();
-        return launch_overlapped(delta_segments_kernel<DK>, dim3((unsigned)ctas), dim3(kScanThreads),
-                                 Smem::kBytes, stream, tm_k, tm_v, tm_o, s, bhs, last);
+        return launch_overlapped(kernel, dim3((unsigned)ctas), dim3(kScanThreads), Smem::kBytes, stream,
+                                 tm_k, tm_v, tm_o, s, bhs);
     };
-    e = pass(walks * (l.segments - 1) + bhs * (l.segments - 2), 0);
+    cudaError_t e = pass(delta_segments_kernel<DK, kSplit, false>,
+                         walks * (l.segments - 1) + bhs * (l.segments - 2), "delta_segments");
     if (e != cudaSuccess) return e;
     e = launch_join<DK>(starts, nullptr, units, bhs, a.dv, l.segments - 2, stream);
     if (e != cudaSuccess) return e;
-    return pass(walks * (l.segments - 1), 1);
+    return pass(delta_segments_kernel<DK, kSplit, true>, walks * (l.segments - 1), "delta_segments_out");
 }
 
 size_t up1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
@@ -2069,20 +2098,20 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
     return launch_delta_share(a, dq_wide, dk_wide, stream);
 }
 
-// The walk in segments carries every state between them in float32, and the
-// products of a segment's transition with it, so it takes operands in two
-// parts whether or not the final state is asked for.
+template <int DK, bool kSplit>
+cudaError_t launch_prefill(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
+    const DeltaTcLayout l = tc_layout(a.batch, a.heads, a.seqlen, DK, a.dv, kSplit);
+    uint8_t *ws = (uint8_t *)workspace;
+    const cudaError_t e = launch_prep<DK, kSplit>(a, l.nc, ws, false, stream);
+    if (e != cudaSuccess) return e;
+    return l.segments > 1 ? launch_segments<DK, kSplit>(a, l, ws, stream)
+                          : launch_scan<DK, kSplit>(a, l.nc, ws, stream);
+}
+// A final state is wanted in float32 precision, and only then operands in two parts.
 template <int DK>
 cudaError_t launch_forward(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
-    const DeltaTcLayout l = tc_layout(a.batch, a.heads, a.seqlen, DK, a.dv, a.state_out != nullptr);
-    uint8_t *ws = (uint8_t *)workspace;
-    const bool split = a.state_out || l.segments > 1;
-    cudaError_t e = split ? launch_prep<DK, true>(a, l.nc, ws, false, stream)
-                          : launch_prep<DK, false>(a, l.nc, ws, false, stream);
-    if (e != cudaSuccess) return e;
-    if (l.segments > 1) return launch_segments<DK>(a, l, ws, stream);
-    return split ? launch_scan<DK, true>(a, l.nc, ws, stream)
-                 : launch_scan<DK, false>(a, l.nc, ws, stream);
+    return a.state_out ? launch_prefill<DK, true>(a, workspace, stream)
+                       : launch_prefill<DK, false>(a, workspace, stream);
 }
 
 }  // namespace
