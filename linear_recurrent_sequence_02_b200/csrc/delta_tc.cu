@@ -514,18 +514,19 @@ struct DeltaScanArgs {
 // What one CTA walks: chunks [first, last) of (sequence, head) bh with the
 // columns v0 .. of the state, from `from` (may be null: zero) to `to` (may be
 // null), both [dk, width].  unit: the state starts as the identity and no
-// values are written, so that it ends as the segment's transition.
+// values are written, so that it ends as the segment's transition.  keep: what
+// the gradients need is kept.
 struct DeltaWalk {
     int bh, v0, first, last, width;
     const float *from;
     float *to;
-    bool out, unit;
+    bool out, unit, keep;
 };
 __device__ __forceinline__ DeltaWalk whole_walk(const DeltaScanArgs &a, int dk, int cta, bool out) {
     const int slabs = (a.dv + 127) / 128, bh = cta / slabs;
     const size_t at = (size_t)bh * dk * a.dv;
     return {bh, (cta % slabs) * 128, 0, a.nc, a.dv, a.state_in ? a.state_in + at : nullptr,
-            a.state_out ? a.state_out + at : nullptr, out, false};
+            a.state_out ? a.state_out + at : nullptr, out, false, true};
 }
 
 // kFine: in two parts; kSplit: the blocks have two.
@@ -727,8 +728,8 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&bar.s_ready[p]);
-            if (kSave && live && c < nc)
-                keep_row(a.s_save, (size_t)bh * a.nc + c, a.dv, v, DK, 64 * p + 32 * wg, hi);
+            if (kSave && w.keep && live && c < nc)
+                keep_row(a.s_save, (size_t)bh * a.nc + w.first + c, a.dv, v, DK, 64 * p + 32 * wg, hi);
         };
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) put_state(p, 0);
@@ -757,8 +758,8 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(&bar.xs_ready);
-                if (kSave && live)
-                    keep_row(a.x_save, (size_t)bh * a.nc + c, a.dv, v, kC, 32 * wg, xb);
+                if (kSave && w.keep && live)
+                    keep_row(a.x_save, (size_t)bh * a.nc + w.first + c, a.dv, v, kC, 32 * wg, xb);
             }
             bool ok = true;
 #pragma unroll
@@ -1075,7 +1076,7 @@ struct DeltaReverseArgs {
 template <int DK>
 __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUtensorMap &tm_do,
                                              const CUtensorMap &tm_dv, const DeltaReverseArgs &a,
-                                             int cta) {
+                                             const DeltaWalk &w) {
     using Smem = DeltaScanSmem<DK, false>;                // V's place holds dO, the output's dV
     using Block = DeltaBlock<DK, false>;
     constexpr int kPieces = DK / 64;
@@ -1086,8 +1087,7 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
     static_assert(sizeof(DeltaReverseBars) <= 256, "barriers");
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    const int slabs = (a.dv + 127) / 128;
-    const int bh = cta / slabs, v0 = (cta % slabs) * 128;
+    const int bh = w.bh, v0 = w.v0;
     const int b = bh / a.heads, h = bh % a.heads;
     unsigned *err = a.err;
     int *abort_flag = &bar.abort_flag;
@@ -1121,14 +1121,14 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
     constexpr uint32_t tmem = 0;                           // all 512 columns, as above
     grid_dependency_wait();
     const int n = delta_tokens_of(a.lengths, b, a.tokens);
-    const int nc = (n + kC - 1) / kC;
+    const int top = min(w.last, (n + kC - 1) / kC), nc = max(0, top - w.first);   // from chunk top - 1 on
 
     int it = 0;                                            // chunks whose copies were issued
     if (warp == 0) {
         const int kh = h / (a.heads / a.key_heads);
         const uint8_t *blocks = a.blocks + (size_t)bh * a.nc * Block::kBytes;
         for (; it < nc; ++it) {
-            const int s = it & 1, c = nc - 1 - it;
+            const int s = it & 1, c = top - 1 - it;
             if (it >= 2 && !warp_spin_wait(&bar.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
             uint8_t *st = smem + s * Smem::kStage;
             if (elect_one()) {
@@ -1148,7 +1148,7 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
         constexpr uint32_t id_k = idesc_bf16(128, 64, 0, 0);    // B: K tile, k contiguous
         constexpr uint32_t id_w = idesc_bf16(128, 64, 0, 1);    // B: W, T^, columns contiguous
         for (int u = 0; u < nc; ++u) {
-            const int s = u & 1, cnt = n - (nc - 1 - u) * kC;
+            const int s = u & 1, cnt = n - (top - 1 - u) * kC;
             uint8_t *st = smem + s * Smem::kStage;
             const uint64_t kmaj = smem_desc_sw128(smem_u32(st), 16, 1024);
             const uint64_t mnmaj = smem_desc_sw128(smem_u32(st), kBox64, 1024);
@@ -1198,17 +1198,21 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
                 }
             }
             __syncwarp();
-            if (u > 0 && !warp_spin_wait(&bar.v_free, (u - 1) & 1, abort_flag, err)) break;
-            if (!warp_spin_wait(&bar.lo_ready, u & 1, abort_flag, err)) break;
-            tc_fence_after();
+            if (w.keep) {
+                if (u > 0 && !warp_spin_wait(&bar.v_free, (u - 1) & 1, abort_flag, err)) break;
+                if (!warp_spin_wait(&bar.lo_ready, u & 1, abort_flag, err)) break;
+                tc_fence_after();
+            }
             if (elect_one()) {
+                if (w.keep) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                    const uint64_t td = mnmaj + ((Block::kT + ks * 2048) >> 4);
-                    mma_bf16_ts(tmem + kDv, tmem + kDx + 8 * ks, td, id_w, ks > 0);
-                    mma_bf16_ts(tmem + kDv, tmem + kDxlo + 8 * ks, td, id_w, 1);
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint64_t td = mnmaj + ((Block::kT + ks * 2048) >> 4);
+                        mma_bf16_ts(tmem + kDv, tmem + kDx + 8 * ks, td, id_w, ks > 0);
+                        mma_bf16_ts(tmem + kDv, tmem + kDxlo + 8 * ks, td, id_w, 1);
+                    }
+                    mma_commit(&bar.v_full);
                 }
-                mma_commit(&bar.v_full);
                 mma_commit(&bar.empty[s]);
             }
             __syncwarp();
@@ -1218,7 +1222,15 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
         const int v = v0 + 32 * (warp % 4) + lane;
         const bool live = v < a.dv;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
-        float2 D[kPieces][16] = {};
+        const size_t sbase = (size_t)(32 * wg) * a.dv + v;
+        float2 D[kPieces][16];
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float *src = w.from + sbase + (size_t)(64 * p + 2 * j) * a.dv;
+                D[p][j] = w.from && live ? make_float2(src[0], src[a.dv]) : both(0.f);
+            }
         // the operand copy of a piece of D, kept for chunk c (the one in front of it)
         auto put_grad = [&](int p, int c) {
             uint32_t hi[16];
@@ -1228,11 +1240,11 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&bar.d_ready[p]);
-            if (live && c >= 0)
+            if (w.keep && live && c >= w.first)
                 keep_row(a.d_save, (size_t)bh * a.nc + c, a.dv, v, DK, 64 * p + 32 * wg, hi);
         };
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) put_grad(p, nc - 1);
+        for (int p = 0; p < kPieces; ++p) put_grad(p, top - 1);
         for (int u = 0; u < nc; ++u) {
             const int s = u & 1;
             const float *hdr = reinterpret_cast<const float *>(smem + s * Smem::kStage + Block::kHdr);
@@ -1272,11 +1284,20 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     D[p][j] = fma2(both(eL), D[p][j], as_pair(z[2 * j], z[2 * j + 1]));
-                put_grad(p, nc - 2 - u);
+                put_grad(p, top - 2 - u);
             }
             if (!ok) break;
         }
-    } else {
+        if (w.to && live)
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float *dst = w.to + sbase + (size_t)(64 * p + 2 * j) * a.dv;
+                    dst[0] = D[p][j].x;
+                    dst[a.dv] = D[p][j].y;
+                }
+    } else if (w.keep) {
         const int col = 32 * (warp % 4) + lane, tid = threadIdx.x - 320;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
         for (int u = 0; u < nc; ++u) {
@@ -1299,7 +1320,7 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
                 for (int x = 0; x < 2; ++x)
                     if (v0 + 64 * x < a.dv)
                         tma_store_4d(&tm_dv, smem + Smem::kOut + x * kBox64, v0 + 64 * x, h,
-                                     (nc - 1 - u) * kC, b);
+                                     (top - 1 - u) * kC, b);
                 tma_store_commit();
             }
         }
@@ -1331,7 +1352,61 @@ delta_walks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int half = gridDim.x / 2;
     if ((int)blockIdx.x < half)
         forward_walk<DK, false, false, true, false>(tm_k, tm_v, tm_v, f, whole_walk(f, DK, blockIdx.x, false));
-    else reverse_walk<DK>(tm_k, tm_do, tm_dv, r, blockIdx.x - half);
+    else reverse_walk<DK>(tm_k, tm_do, tm_dv, r, whole_walk(f, DK, blockIdx.x - half, false));
+}
+
+// Both in segments.  Back through a segment the gradient of the state goes by
+// D -> M^T D + N', so one set of transitions serves both ways.
+// starts [segments - 1][BH][dk, dv] as above; back [segments - 1]: D behind
+// segment segments - 2 first; units [segments - 2][BH][dk, dk].
+struct DeltaBackSegments {
+    int segments, segment;                                   // how many, chunks of each
+    float *starts, *back, *units;
+};
+template <int DK>
+__global__ void __launch_bounds__(kScanThreads, 1)
+delta_walks_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                            const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_dv,
+                            DeltaScanArgs f, DeltaReverseArgs r, DeltaBackSegments x, int bhs, int last) {
+    const int walks = bhs * ((f.dv + 127) / 128), ends = walks * (x.segments - 1);
+    const size_t ssize = (size_t)DK * f.dv;
+    int cta = blockIdx.x;
+    DeltaWalk w;
+    auto cut = [&](int seg) {
+        w.first = seg * x.segment;
+        w.last = w.first + x.segment;
+    };
+    if (cta >= ends && cta < 2 * ends) {                     // back: behind segments .. 1, 0
+        cta -= ends;
+        const int i = cta / walks + last;
+        w = whole_walk(f, DK, cta % walks, false);
+        if (last) w.from = x.back + ((size_t)(i - 1) * bhs + w.bh) * ssize;
+        else w.to = x.back + ((size_t)i * bhs + w.bh) * ssize;
+        w.keep = last || i == 0;
+        cut(x.segments - 1 - i);
+        reverse_walk<DK>(tm_k, tm_do, tm_dv, r, w);
+        return;
+    }
+    if (cta < ends) {
+        const int seg = cta / walks + last;
+        w = whole_walk(f, DK, cta % walks, false);
+        if (last) w.from = x.starts + ((size_t)(seg - 1) * bhs + w.bh) * ssize;
+        else w.to = x.starts + ((size_t)seg * bhs + w.bh) * ssize;
+        w.keep = last || seg == 0;
+        cut(seg);
+    } else {                                                 // M
+        cta -= 2 * ends;
+        const int seg = 1 + cta / bhs;
+        w.bh = cta % bhs;
+        w.v0 = 0;
+        w.width = DK;
+        w.from = nullptr;
+        w.to = x.units + ((size_t)(seg - 1) * bhs + w.bh) * DK * DK;
+        w.out = w.keep = false;
+        w.unit = true;
+        cut(seg);
+    }
+    forward_walk<DK, false, false, true, false>(tm_k, tm_v, tm_v, f, w);
 }
 
 // ------------------------------------------------------------------ gradients
@@ -2026,8 +2101,31 @@ cudaError_t launch_segments(const DeltaArgs &a, const DeltaTcLayout &l, uint8_t 
 
 size_t up1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
 
+// Segments of the backward's walks, as delta_segments, in chunks walked back.
+// Measured, 128 x 128: 1 head, 128 chunks: 280 us whole, 97 in 12 segments; 16
+// heads: 423 and 327 in 4; 24 heads, 64 chunks: 260 and 245 in 3; 32 chunks:
+// 143 and 144 (whole); 32 heads, 64 chunks: 301 and 324 (whole).
+DeltaCut back_segments(int batch, int heads, int nc, int dv) {
+    const long long units = (long long)batch * heads, walks = units * ((dv + 127) / 128);
+    auto waves = [](long long ctas) { return (ctas + 147) / 148; };
+    float best = 0.95f * (float)(waves(2 * walks) * nc);
+    DeltaCut cut = {1, nc};
+    for (int s = 3; s <= 16 && 4 * s <= nc; ++s) {
+        const int chunks = (nc + s - 1) / s;
+        if ((s - 1) * chunks >= nc) continue;
+        const float cost = (float)(chunks * (waves(2 * walks * (s - 1) + units * (s - 2)) +
+                                             waves(2 * walks * (s - 1)))) + 6.f + s;
+        if (cost < best) {
+            best = cost;
+            cut = {s, chunks};
+        }
+    }
+    return cut;
+}
+
 struct DeltaTcGradLayout {
-    size_t blocks, x, s, d, dq, dk, total;
+    size_t blocks, x, s, d, dq, dk, starts, back, units, total;
+    DeltaCut cut;
 };
 DeltaTcGradLayout tc_grad_layout(int batch, int heads, int key_heads, int seqlen, int dk, int dv) {
     const size_t chunks = (size_t)batch * heads * ((seqlen + kC - 1) / kC);
@@ -2039,7 +2137,12 @@ DeltaTcGradLayout tc_grad_layout(int batch, int heads, int key_heads, int seqlen
     l.d = l.s + chunks * dv * dk * 2;
     l.dq = l.d + chunks * dv * dk * 2;
     l.dk = l.dq + wide;
-    l.total = l.dk + wide;
+    l.cut = back_segments(batch, heads, (int)(((size_t)seqlen + kC - 1) / kC), dv);
+    const size_t bh = (size_t)batch * heads, between = l.cut.count - 1;
+    l.starts = l.dk + wide;
+    l.back = l.starts + between * bh * dk * dv * 4;
+    l.units = l.back + between * bh * dk * dv * 4;
+    l.total = l.units + (between ? between - 1 : 0) * bh * dk * dk * 4;
     return l;
 }
 
@@ -2065,17 +2168,32 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
         return cudaErrorInvalidValue;
     {
         using Smem = DeltaScanSmem<DK, false>;
-        e = cudaFuncSetAttribute(delta_walks_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)Smem::kBytes);
-        if (e != cudaSuccess) return e;
-        DeltaScanArgs f = {ws + l.blocks, a.lengths, nullptr, nullptr, nullptr, xs, ss, a.heads,
-                           a.key_heads, a.seqlen, nc, a.dv, device_error_word(), 1, nc, nullptr, nullptr};
-        DeltaReverseArgs r = {ws + l.blocks, a.lengths, ds, a.heads, a.key_heads, a.seqlen, nc, a.dv,
-                              device_error_word()};
-        KernelTimer timer("delta_walks", stream);
-        count_launch();
-        e = launch_overlapped(delta_walks_kernel<DK>, dim3((unsigned)(2 * bh * slabs)),
-                              dim3(kScanThreads), Smem::kBytes, stream, tm_k, tm_v, tm_do, tm_dv, f, r);
+        const DeltaScanArgs f = {ws + l.blocks, a.lengths, nullptr, nullptr, nullptr, xs, ss, a.heads,
+                                 a.key_heads, a.seqlen, nc, a.dv, device_error_word(), 1, nc, nullptr, nullptr};
+        const DeltaReverseArgs r = {ws + l.blocks, a.lengths, ds, a.heads, a.key_heads, a.seqlen, nc, a.dv,
+                                    device_error_word()};
+        const int bhs = (int)bh, walks = bhs * slabs;
+        auto launch = [&](auto kernel, const char *name, int ctas, auto... rest) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)Smem::kBytes);
+            if (e != cudaSuccess) return e;
+            KernelTimer timer(name, stream);
+            count_launch();
+            return launch_overlapped(kernel, dim3((unsigned)ctas), dim3(kScanThreads), Smem::kBytes, stream,
+                                     tm_k, tm_v, tm_do, tm_dv, f, r, rest...);
+        };
+        if (l.cut.count == 1) {
+            e = launch(delta_walks_kernel<DK>, "delta_walks", 2 * walks);
+        } else {
+            const DeltaBackSegments x = {l.cut.count, l.cut.chunks, (float *)(ws + l.starts),
+                                         (float *)(ws + l.back), (float *)(ws + l.units)};
+            const int ends = 2 * walks * (x.segments - 1);
+            e = launch(delta_walks_segments_kernel<DK>, "delta_walks_segments", ends + bhs * (x.segments - 2), x, bhs, 0);
+            if (e != cudaSuccess) return e;
+            e = launch_join<DK>(x.starts, x.back, x.units, bhs, a.dv, x.segments - 2, stream);
+            if (e != cudaSuccess) return e;
+            e = launch(delta_walks_segments_kernel<DK>, "delta_walks_segments", ends, x, bhs, 1);
+        }
         if (e != cudaSuccess) return e;
     }
     {

@@ -390,6 +390,27 @@ def test_backward_lengths_and_gates(rn, dtype):
         assert err(a, w) < bound(dtype, dtype == "bf16"), name
 
 
+@pytest.mark.parametrize("dk,dv,Hk,H,lens", [(128, 64, 1, 2, [2100, 700]), (64, 256, 2, 2, [1, 2100]),
+                                             (64, 64, 8, 16, [2100])])
+def test_backward_long_with_few_heads(rn, dk, dv, Hk, H, lens):
+    """Long enough for walks in segments, of which some may be empty."""
+    B, n = len(lens), 2100
+    x, ref = make(27, B, n, Hk, H, dk, dv, "bf16", decay=0.02)
+    for t, r in zip(x, ref):
+        for b, c in enumerate(lens):
+            t[b, c:] = float("nan")
+            r[b, c:] = 0.0
+    lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = rn.retnet_delta_backward(*x, lengths=lengths)
+    done(rn)
+    want = oracle.delta_backward(*ref, dk ** -0.5, lens)
+    for name, a, w in zip(("dq", "dk", "dv", "dg", "dbeta"), got, want):
+        for b, c in enumerate(lens):
+            assert not a[b, c:].any(), name
+        w, a = together(w, a)
+        assert err(a, w) < bound("bf16", True), name
+
+
 # ------------------------------------------------------------------ as a program uses them
 def test_captured_graph_and_another_stream(rn):
     """A step and a prefill captured into one graph, replayed on new inputs."""
