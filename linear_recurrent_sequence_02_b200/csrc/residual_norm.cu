@@ -31,24 +31,33 @@ struct NormArgs {
     int hidden, post_norm;
 };
 
-// Sum over the TPR threads that own a row; every one of them gets it.
+// Sums over the TPR threads that own a row; every one of them gets them.
 // `red` is this call's own slot, so calls need no barrier between them.
 template <int TPR, int N>
-__device__ __forceinline__ void row_sum(float (&s)[N], float (*red)[N]) {
+__device__ __forceinline__ void row_sum(float (&s)[N], float (*red)[TPR / 32]) {
+    constexpr int W = TPR / 32;
 #pragma unroll
     for (int m = 16; m; m >>= 1)
 #pragma unroll
         for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], m);
-    if (TPR > 32) {
+    if (W > 1) {
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
-            for (int i = 0; i < N; ++i) red[threadIdx.x >> 5][i] = s[i];
+            for (int i = 0; i < N; ++i) red[i][threadIdx.x >> 5] = s[i];
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float a = 0.f;
+            if constexpr (W % 4 == 0) {
 #pragma unroll
-            for (int w = 0; w < TPR / 32; ++w) a += red[w][i];
+                for (int w = 0; w < W; w += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&red[i][w]);
+                    a += (v.x + v.y) + (v.z + v.w);
+                }
+            } else {
+#pragma unroll
+                for (int w = 0; w < W; ++w) a += red[i][w];
+            }
             s[i] = a;
         }
     }
@@ -125,7 +134,7 @@ template <typename T, int TPR, int kVecs>
 __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarpRows : TPR)
 residual_norm_kernel(NormArgs a) {
     constexpr int kRows = TPR == 32 ? kNormWarpRows : 1;
-    __shared__ float red[2][TPR / 32][1];
+    __shared__ __align__(16) float red[2][1][TPR / 32];
     const int lane = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
     const long long row = (long long)blockIdx.x * kRows + (TPR == 32 ? threadIdx.x >> 5 : 0);
     grid_dependency_wait();
@@ -198,9 +207,9 @@ residual_norm_kernel(NormArgs a) {
 // partial row a CTA instead of an atomic a channel and row, and their order
 // does not change from run to run.  With kAhead every thread copies its
 // vectors of the next row to shared memory while it works on this one (8192 x
-// 4096 bf16: 157 us without, 131 with), and reads them again in each pass
-// instead of holding them; without (rows too long for two in shared memory)
-// they come from global memory as they are needed.
+// 4096 bf16: 163 us without, 126 with), and reads them again in each pass
+// instead of holding them; without they come from global memory as they are
+// needed.  A row costs two barriers: the next row's sum of y^2 shares the last.
 template <typename T, int TPR, int kVecs, bool kAhead>
 __global__ void __launch_bounds__(TPR == 32 ? 32 * kNormWarpRows : TPR, TPR <= 256 ? 512 / (TPR == 32 ? 256 : TPR) : 1)
 residual_norm_backward_kernel(NormArgs a) {
@@ -208,7 +217,7 @@ residual_norm_backward_kernel(NormArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int kVecBytes = 8 * sizeof(T), kThreads = TPR == 32 ? 32 * kNormWarpRows : TPR;
     constexpr int kRows = TPR == 32 ? kNormWarpRows : 1;
-    __shared__ float red1[2][TPR / 32][1], red2[2][TPR / 32][2], red3[2][TPR / 32][1];
+    __shared__ __align__(16) float red1[2][2][TPR / 32], red2[2][2][TPR / 32];
     const int lane = TPR == 32 ? threadIdx.x & 31 : threadIdx.x;
     const long long first = (long long)blockIdx.x * kRows + (TPR == 32 ? threadIdx.x >> 5 : 0);
     const int vecs = a.hidden / 8;
@@ -241,32 +250,38 @@ residual_norm_backward_kernel(NormArgs a) {
                                          : "memory");
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    auto load = [&](long long row, int turn, int t, int i) {
+        Packed<T> v;
+        if (kAhead) v.load(place(turn, t, i, 0), 16 * kThreads);
+        else v.load(from[t] + (size_t)row * a.hidden + (lane + i * TPR) * 8);
+        return v;
+    };
+    // this thread's part of the sum of y^2
+    auto squares = [&](long long row, int turn) {
+        float2 q = both(0.f);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            if (lane + i * TPR < vecs) {
+                const Packed<T> y = load(row, turn, kY, i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) q = fma2(y.at(e), y.at(e), q);
+            }
+        return q.x + q.y;
+    };
     int turn = 0;                          // alternating slots
+    float ry = 1.f;
     fetch(first, 0);
+    if (a.post_norm && first < a.rows) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        float s[1] = {squares(first, 0)};
+        row_sum<TPR>(s, red2[1]);          // the first row's own sums go to the other slot
+        ry = rsqrtf(s[0] * inv + a.eps);
+    }
     for (long long row = first; row < a.rows; row += step, turn ^= 1) {
         const size_t base = (size_t)row * a.hidden;
         fetch(row + step, turn ^ 1);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
-        auto get = [&](int t, int i) {
-            Packed<T> v;
-            if (kAhead) v.load(place(turn, t, i, 0), 16 * kThreads);
-            else v.load(from[t] + base + (lane + i * TPR) * 8);
-            return v;
-        };
-        float ry = 1.f;
-        if (a.post_norm) {
-            float2 q = both(0.f);
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i)
-                if (lane + i * TPR < vecs) {
-                    const Packed<T> y = get(kY, i);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) q = fma2(y.at(e), y.at(e), q);
-                }
-            float s[1] = {q.x + q.y};
-            row_sum<TPR>(s, red1[turn]);
-            ry = rsqrtf(s[0] * inv + a.eps);
-        }
+        auto get = [&](int t, int i) { return load(row, turn, t, i); };
         // h, and the sums of h^2 and (dn pre) h
         float2 q0 = both(0.f), q1 = q0, h[kVecs][4], sg[kVecs][4];
 #pragma unroll
@@ -293,7 +308,7 @@ residual_norm_backward_kernel(NormArgs a) {
             }
         }
         float s2[2] = {q0.x + q0.y, q1.x + q1.y};
-        row_sum<TPR>(s2, red2[turn]);
+        row_sum<TPR>(s2, red1[turn]);
         const float rh = rsqrtf(s2[0] * inv + a.eps);
         const float mh = s2[1] * rh * inv;                // mean(t h^)
         float2 q3 = both(0.f);
@@ -331,11 +346,13 @@ residual_norm_backward_kernel(NormArgs a) {
                 if (gated) store8((T *)a.dgate + base + c * 8, dg);
             }
         }
-        float my = 0.f;
-        if (a.post_norm) {
-            float s3[1] = {q3.x + q3.y};
-            row_sum<TPR>(s3, red3[turn]);
+        float my = 0.f, ry_next = 1.f;
+        if (a.post_norm) {                                // with the next row's sum of y^2
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            float s3[2] = {q3.x + q3.y, row + step < a.rows ? squares(row + step, turn ^ 1) : 0.f};
+            row_sum<TPR>(s3, red2[turn]);
             my = s3[0] * inv;                             // mean(u y^)
+            ry_next = rsqrtf(s3[1] * inv + a.eps);
         }
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
@@ -350,6 +367,7 @@ residual_norm_backward_kernel(NormArgs a) {
                 store8((T *)a.dy + base + c * 8, h[i]);
             }
         }
+        ry = ry_next;
     }
     // this CTA's (this warp's) partial sums over its rows
 #pragma unroll
@@ -393,21 +411,30 @@ static int norm_threads(int hidden, int vecs) {
     return t;
 }
 static int rows_per_cta(int tpr) { return tpr == 32 ? kNormWarpRows : 1; }
-constexpr int kForwardVecs = 4, kBackwardVecs = 2;
+constexpr int kForwardVecs = 4;
+// Of the backward: two, but one for shorter float32 rows (16384 x 512: 60 us
+// against 66; 4096 x 2048: 67 against 61).
+static int backward_vecs(int hidden, int size) { return size == 4 && hidden < 2048 ? 1 : 2; }
+// Shared memory of the backward: two rows of five tensors.  Float32 rows come
+// from global memory as they are needed: copied ahead they leave an SM one or
+// two CTAs (8192 x 4096: 345 us ahead, 230 so; bf16: 126 ahead, 163 so).
+constexpr int backward_bytes(int threads, int vecs, int size) { return 2 * 5 * vecs * 8 * size * threads; }
+constexpr bool copies_ahead(int bytes, int size) { return size == 2 && bytes <= 220 * 1024; }
 
-// CTAs of the backward: as many as are resident on 148 SMs, and no more than
-// there are rows for.
-static long long norm_backward_grid(long long rows, int hidden) {
-    const int tpr = norm_threads(hidden, kBackwardVecs), per_cta = rows_per_cta(tpr);
-    const long long resident = 148ll * (tpr <= 256 ? 512 / (tpr == 32 ? 256 : tpr) : 1);
+// CTAs of the backward: as many as registers and shared memory let reside on
+// 148 SMs, and no more than there are rows for.
+static long long norm_backward_grid(long long rows, int hidden, int size) {
+    const int tpr = norm_threads(hidden, backward_vecs(hidden, size)), per_cta = rows_per_cta(tpr);
+    const long long resident = 148ll * (tpr <= 256 ? 512 / (tpr * per_cta) : 1);
     const long long want = (rows + per_cta - 1) / per_cta;
     return want < resident ? want : resident;
 }
-static long long norm_backward_parts(long long rows, int hidden) {
-    return norm_backward_grid(rows, hidden) * rows_per_cta(norm_threads(hidden, kBackwardVecs));
+static long long norm_backward_parts(long long rows, int hidden, int size) {
+    return norm_backward_grid(rows, hidden, size) * rows_per_cta(norm_threads(hidden, backward_vecs(hidden, size)));
 }
 size_t residual_norm_backward_workspace(long long rows, int hidden) {
-    return (size_t)norm_backward_parts(rows, hidden) * hidden * 2 * sizeof(float);
+    const long long b = norm_backward_parts(rows, hidden, 2), f = norm_backward_parts(rows, hidden, 4);
+    return (size_t)(b > f ? b : f) * hidden * 2 * sizeof(float);
 }
 
 template <typename T>
@@ -416,7 +443,10 @@ static cudaError_t launch_forward(const NormArgs &a, cudaStream_t stream) {
     const int tpr = norm_threads(a.hidden, V), per_cta = rows_per_cta(tpr);
     const dim3 g((unsigned)((a.rows + per_cta - 1) / per_cta)), b(tpr * per_cta);
     switch (tpr) {
-        case 32: return launch_overlapped(residual_norm_kernel<T, 32, V>, g, b, 0, stream, a);
+        case 32:                                            // no more registers than a short row needs
+            if (a.hidden <= 256) return launch_overlapped(residual_norm_kernel<T, 32, 1>, g, b, 0, stream, a);
+            if (a.hidden <= 512) return launch_overlapped(residual_norm_kernel<T, 32, 2>, g, b, 0, stream, a);
+            return launch_overlapped(residual_norm_kernel<T, 32, V>, g, b, 0, stream, a);
         case 64: return launch_overlapped(residual_norm_kernel<T, 64, V>, g, b, 0, stream, a);
         case 128: return launch_overlapped(residual_norm_kernel<T, 128, V>, g, b, 0, stream, a);
         case 256: return launch_overlapped(residual_norm_kernel<T, 256, V>, g, b, 0, stream, a);
@@ -424,12 +454,11 @@ static cudaError_t launch_forward(const NormArgs &a, cudaStream_t stream) {
     return launch_overlapped(residual_norm_kernel<T, 512, V>, g, b, 0, stream, a);
 }
 
-template <typename T, int TPR>
+template <typename T, int TPR, int V>
 static cudaError_t launch_backward_tpr(const NormArgs &a, unsigned grid, cudaStream_t stream) {
-    constexpr int V = kBackwardVecs, kThreads = TPR == 32 ? 32 * kNormWarpRows : TPR;
-    // two rows of five tensors; two CTAs of 256 threads share an SM's 227 KB
-    constexpr int kBytes = 2 * 5 * V * 8 * (int)sizeof(T) * kThreads;
-    constexpr bool kAhead = kBytes <= 220 * 1024;
+    constexpr int kThreads = TPR == 32 ? 32 * kNormWarpRows : TPR;
+    constexpr int kBytes = backward_bytes(kThreads, V, (int)sizeof(T));
+    constexpr bool kAhead = copies_ahead(kBytes, (int)sizeof(T));
     auto kernel = residual_norm_backward_kernel<T, TPR, V, kAhead>;
     if (kAhead) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
@@ -438,16 +467,17 @@ static cudaError_t launch_backward_tpr(const NormArgs &a, unsigned grid, cudaStr
     return launch_overlapped(kernel, dim3(grid), dim3(kThreads), kAhead ? kBytes : 0, stream, a);
 }
 
-template <typename T>
+template <typename T, int V>
 static cudaError_t launch_backward(const NormArgs &a, unsigned grid, cudaStream_t stream) {
-    switch (norm_threads(a.hidden, kBackwardVecs)) {
-        case 32: return launch_backward_tpr<T, 32>(a, grid, stream);
-        case 64: return launch_backward_tpr<T, 64>(a, grid, stream);
-        case 128: return launch_backward_tpr<T, 128>(a, grid, stream);
-        case 256: return launch_backward_tpr<T, 256>(a, grid, stream);
-        case 512: return launch_backward_tpr<T, 512>(a, grid, stream);
+    switch (norm_threads(a.hidden, V)) {
+        case 32: return launch_backward_tpr<T, 32, V>(a, grid, stream);
+        case 64: return launch_backward_tpr<T, 64, V>(a, grid, stream);
+        case 128: return launch_backward_tpr<T, 128, V>(a, grid, stream);
+        case 256: return launch_backward_tpr<T, 256, V>(a, grid, stream);
     }
-    return launch_backward_tpr<T, 1024>(a, grid, stream);
+    if constexpr (V == 1) return cudaErrorInvalidValue;      // shorter rows only
+    else return norm_threads(a.hidden, V) == 512 ? launch_backward_tpr<T, 512, V>(a, grid, stream)
+                                                 : launch_backward_tpr<T, 1024, V>(a, grid, stream);
 }
 
 static NormArgs norm_args(const retnet_block_norm &p, long long rows, int hidden) {
@@ -480,8 +510,9 @@ cudaError_t launch_residual_norm_backward(const void *x, const void *y, const vo
                                           long long rows, int hidden, retnet_dtype dtype, void *dx,
                                           void *dy, void *dgate, float *dpost, float *dpre,
                                           void *workspace, cudaStream_t stream) {
-    const long long grid = norm_backward_grid(rows, hidden);
-    const int parts = (int)norm_backward_parts(rows, hidden);
+    const int size = dtype == RETNET_BF16 ? 2 : 4;
+    const long long grid = norm_backward_grid(rows, hidden, size);
+    const int parts = (int)norm_backward_parts(rows, hidden, size);
     float *part_post = (float *)workspace;
     float *part_pre = part_post + (size_t)parts * hidden;
     if (rows > 0) {
@@ -491,9 +522,9 @@ cudaError_t launch_residual_norm_backward(const void *x, const void *y, const vo
         a.part_pre = dpre ? part_pre : nullptr;
         KernelTimer timer("residual_norm_backward", stream);
         count_launch();
-        cudaError_t e = dtype == RETNET_BF16
-                            ? launch_backward<__nv_bfloat16>(a, (unsigned)grid, stream)
-                            : launch_backward<float>(a, (unsigned)grid, stream);
+        cudaError_t e = dtype == RETNET_BF16 ? launch_backward<__nv_bfloat16, 2>(a, (unsigned)grid, stream)
+                        : backward_vecs(hidden, 4) == 1 ? launch_backward<float, 1>(a, (unsigned)grid, stream)
+                                                        : launch_backward<float, 2>(a, (unsigned)grid, stream);
         if (e != cudaSuccess) return e;
     }
     if (!dpost && !dpre) return cudaSuccess;
