@@ -238,13 +238,27 @@ def _stream(t: torch.Tensor):
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
-def _launch(t: torch.Tensor, call, *args) -> int:
-    """call(*args, stream) with t's device current and on its current stream.
-    A decode step's host time is that of its calls, so the device is only
-    switched where it has to be (the raw stream handle and the comparison
-    cost 0.3 us, a device context and a stream object 4 us)."""
-    index = t.get_device()
-    if index == torch.cuda.current_device():
+def _fits(t, dtype, shape, index: int) -> bool:
+    return (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and
+            t.get_device() == index and t.is_contiguous())
+
+
+def _on(t: Optional[torch.Tensor], name: str, dtype, shape, index: int):
+    """As _dev, on the CUDA device of this index (other arguments' device)."""
+    if t is None or _fits(t, dtype, shape, index):
+        return t
+    _dev(t, name, dtype, shape)
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    return t
+
+
+def _launch(index: int, call, *args) -> int:
+    """call(*args, stream) with the device of this index current and on its
+    current stream.  A decode step's host time is that of its calls, so the
+    device is only switched where it has to be (the raw stream handle and the
+    comparison cost 0.3 us, a device context and a stream object 4 us)."""
+    if index == torch._C._cuda_getDevice():
         return call(*args, torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(index):
         return call(*args, torch._C._cuda_getCurrentRawStream(index))
@@ -579,30 +593,26 @@ def retnet_msr_layer(x: torch.Tensor, w_qkvg: torch.Tensor, w_o: torch.Tensor,
 
 
 # ------------------------------------------------------------------ gated delta rule
-def _one_device(x: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
-    index = x.get_device()
-    for t in others:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"all tensors must be on {x.device}, got one on {t.device}")
-
-
-def _delta_shape(q, k, v, g, beta, lengths) -> _DeltaShape:
+def _delta_shape(q, k, v, g, beta, lengths):
+    """(the shape, the device's index)"""
     _dev(q, "q")
     if q.dim() != 4:
         raise ValueError("q must be [batch, seqlen, key_heads, dk]")
-    B, n, Hk, dk = q.shape
-    _dev(k, "k", q.dtype, q.shape)
-    _dev(v, "v", q.dtype)
-    if v.dim() != 4 or v.shape[0] != B or v.shape[1] != n:
-        raise ValueError(f"v must be [{B}, {n}, heads, dv], got {tuple(v.shape)}")
-    H, dv = v.shape[2:]
+    qshape, dtype, index = q.shape, q.dtype, q.get_device()
+    B, n, Hk, dk = qshape
+    _on(k, "k", dtype, qshape, index)
+    if not isinstance(v, torch.Tensor) or v.dim() != 4 or v.shape[:2] != qshape[:2]:
+        raise ValueError(f"v must be a tensor [{B}, {n}, heads, dv]")
+    _, _, H, dv = vshape = v.shape
+    _on(v, "v", dtype, vshape, index)
     if Hk < 1 or H % Hk:
         raise ValueError(f"heads ({H}) must be a multiple of key_heads ({Hk})")
-    _dev(g, "g", q.dtype, (B, n, H))
-    _dev(beta, "beta", q.dtype, (B, n, H))
-    _dev(lengths, "lengths", torch.int32, (B,))
-    _one_device(q, k, v, g, beta, lengths)
-    return _DeltaShape(B, H, Hk, n, dk, dv, _dtype_code(q))
+    gshape = (B, n, H)
+    _on(g, "g", dtype, gshape, index)
+    _on(beta, "beta", dtype, gshape, index)
+    if lengths is not None:
+        _on(lengths, "lengths", torch.int32, (B,), index)
+    return _DeltaShape(B, H, Hk, n, dk, dv, _dtype_code(q)), index
 
 
 def _delta_scale(scale: Optional[float], dk: int) -> float:
@@ -623,11 +633,12 @@ def retnet_delta_recurrent(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
     sequence b has the tokens before lengths[b]; the rows behind them keep
     what `out` held (zeros when it is made here).  Returns out
     [batch, seqlen, heads, dv]."""
-    shape = _delta_shape(q, k, v, g, beta, lengths)
-    _dev(state, "state", torch.float32, (shape.batch, shape.heads, shape.dk, shape.dv))
-    out = _delta_out(v, lengths) if out is None else _dev(out, "out", q.dtype, v.shape)
-    _one_device(q, state, out)
-    st = _launch(q, load_library().retnet_delta_recurrent, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+    shape, index = _delta_shape(q, k, v, g, beta, lengths)
+    if state is None:
+        raise TypeError("state must be a torch.Tensor")
+    _on(state, "state", torch.float32, (shape.batch, shape.heads, shape.dk, shape.dv), index)
+    out = _delta_out(v, lengths) if out is None else _on(out, "out", q.dtype, v.shape, index)
+    st = _launch(index, load_library().retnet_delta_recurrent, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
                  _ptr(beta), _delta_scale(scale, shape.dk), _ptr(lengths), _ptr(state), _ptr(out),
                  ctypes.byref(shape))
     _check("retnet_delta_recurrent", st)
@@ -669,19 +680,18 @@ def retnet_delta_chunkwise(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
     state_in / state_out: float32 [batch, heads, dk, dv] states before the
     first and after the last token.  `workspace` (uint8 CUDA tensor) is
     allocated here when not supplied.  Returns out."""
-    shape = _delta_shape(q, k, v, g, beta, lengths)
+    shape, index = _delta_shape(q, k, v, g, beta, lengths)
     sshape = (shape.batch, shape.heads, shape.dk, shape.dv)
-    _dev(state_in, "state_in", torch.float32, sshape)
-    _dev(state_out, "state_out", torch.float32, sshape)
-    out = _delta_out(v, lengths) if out is None else _dev(out, "out", q.dtype, v.shape)
+    _on(state_in, "state_in", torch.float32, sshape, index)
+    _on(state_out, "state_out", torch.float32, sshape, index)
+    out = _delta_out(v, lengths) if out is None else _on(out, "out", q.dtype, v.shape, index)
     if workspace is None:
         workspace = retnet_workspace(
             retnet_delta_workspace_size(shape.batch, shape.heads, shape.key_heads, shape.seqlen,
                                         shape.dk, shape.dv, q.dtype, algo), q.device)
     else:
-        _dev(workspace, "workspace", torch.uint8)
-    _one_device(q, state_in, state_out, out, workspace)
-    st = _launch(q, load_library().retnet_delta_chunkwise, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+        _on(workspace, "workspace", torch.uint8, workspace.shape, index)
+    st = _launch(index, load_library().retnet_delta_chunkwise, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
                  _ptr(beta), _delta_scale(scale, shape.dk), _ptr(lengths), _ptr(out),
                  ctypes.byref(shape), _ptr(state_in), _ptr(state_out), _ALGOS[algo],
                  _ptr(workspace), workspace.numel())
@@ -699,22 +709,23 @@ def retnet_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
                           workspace: Optional[torch.Tensor] = None):
     """Gradients (dq, dk, dv, dg, dbeta) of retnet_delta_chunkwise's out
     (without initial state) given d_out = dL/dout; shapes as the inputs."""
-    shape = _delta_shape(q, k, v, g, beta, lengths)
-    _dev(d_out, "d_out", q.dtype, v.shape)
+    shape, index = _delta_shape(q, k, v, g, beta, lengths)
+    if d_out is None:
+        raise TypeError("d_out must be a torch.Tensor")
+    _on(d_out, "d_out", q.dtype, v.shape, index)
     grads = []
     for name, given, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dg", dg, g),
                               ("dbeta", dbeta, beta)):
         grads.append(torch.empty_like(like) if given is None else
-                     _dev(given, name, q.dtype, like.shape))
+                     _on(given, name, q.dtype, like.shape, index))
     if workspace is None:
         workspace = retnet_workspace(
             retnet_delta_backward_workspace_size(shape.batch, shape.heads, shape.key_heads,
                                                  shape.seqlen, shape.dk, shape.dv, q.dtype, algo),
             q.device)
     else:
-        _dev(workspace, "workspace", torch.uint8)
-    _one_device(q, d_out, workspace, *grads)
-    st = _launch(q, load_library().retnet_delta_backward, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+        _on(workspace, "workspace", torch.uint8, workspace.shape, index)
+    st = _launch(index, load_library().retnet_delta_backward, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
                  _ptr(beta), _ptr(d_out), _delta_scale(scale, shape.dk), _ptr(lengths),
                  *(_ptr(t) for t in grads), ctypes.byref(shape), _ALGOS[algo], _ptr(workspace),
                  workspace.numel())
@@ -735,20 +746,22 @@ def _block_norm(x, y, gate, post_norm, post_weight, pre_weight, residual_scale, 
     _dev(x, "x")
     if x.dim() < 1:
         raise ValueError("x must be [..., hidden]")
-    hidden = x.shape[-1]
-    _dev(y, "y", x.dtype, x.shape)
-    _dev(gate, "gate", x.dtype, x.shape)
+    xshape, dtype, index = x.shape, x.dtype, x.get_device()
+    hidden = xshape[-1]
+    if y is None:
+        raise TypeError("y must be a torch.Tensor")
+    _on(y, "y", dtype, xshape, index)
+    _on(gate, "gate", dtype, xshape, index)
     if post_weight is not None and not post_norm:
         raise ValueError("post_weight needs post_norm")
-    _dev(post_weight, "post_weight", torch.float32, (hidden,))
-    _dev(pre_weight, "pre_weight", torch.float32, (hidden,))
-    _one_device(x, y, gate, post_weight, pre_weight)
+    _on(post_weight, "post_weight", torch.float32, (hidden,), index)
+    _on(pre_weight, "pre_weight", torch.float32, (hidden,), index)
     rows = x.numel() // hidden if x.numel() else 0
     norm = _BlockNorm(None if gate is None else gate.data_ptr(), int(bool(post_norm)),
                       None if post_weight is None else post_weight.data_ptr(),
                       None if pre_weight is None else pre_weight.data_ptr(),
                       float(residual_scale), float(eps))
-    return norm, rows, hidden
+    return norm, rows, hidden, (dtype, xshape, index)
 
 
 def retnet_residual_norm(x: torch.Tensor, y: torch.Tensor, *, gate: Optional[torch.Tensor] = None,
@@ -762,12 +775,11 @@ def retnet_residual_norm(x: torch.Tensor, y: torch.Tensor, *, gate: Optional[tor
         h = x + residual_scale * swish(gate) * z;  n = rms(h) * pre_weight
     with float32 weights [hidden] (None: 1).  Returns (h, n); h may be x and
     n may be y."""
-    norm, rows, hidden = _block_norm(x, y, gate, post_norm, post_weight, pre_weight,
-                                     residual_scale, eps)
-    h = torch.empty_like(x) if h is None else _dev(h, "h", x.dtype, x.shape)
-    n = torch.empty_like(x) if n is None else _dev(n, "n", x.dtype, x.shape)
-    _one_device(x, h, n)
-    st = _launch(x, load_library().retnet_residual_norm, _ptr(x), _ptr(y), ctypes.byref(norm),
+    norm, rows, hidden, like = _block_norm(x, y, gate, post_norm, post_weight, pre_weight,
+                                           residual_scale, eps)
+    h = torch.empty_like(x) if h is None else _on(h, "h", *like)
+    n = torch.empty_like(x) if n is None else _on(n, "n", *like)
+    st = _launch(like[2], load_library().retnet_residual_norm, _ptr(x), _ptr(y), ctypes.byref(norm),
                  rows, hidden, _dtype_code(x), _ptr(h), _ptr(n))
     _check("retnet_residual_norm", st)
     return h, n
@@ -794,26 +806,27 @@ def retnet_residual_norm_backward(x: torch.Tensor, y: torch.Tensor, dn: torch.Te
     """Gradients of retnet_residual_norm given dn and dh, the gradients of n
     and h (dh None: 0).  dgate is None without a gate, and a weight's gradient
     (float32 [hidden], summed over the rows) is None where the weight is."""
-    norm, rows, hidden = _block_norm(x, y, gate, post_norm, post_weight, pre_weight,
-                                     residual_scale, eps)
-    _dev(dn, "dn", x.dtype, x.shape)
-    _dev(dh, "dh", x.dtype, x.shape)
-    dx = torch.empty_like(x) if dx is None else _dev(dx, "dx", x.dtype, x.shape)
-    dy = torch.empty_like(x) if dy is None else _dev(dy, "dy", x.dtype, x.shape)
+    norm, rows, hidden, like = _block_norm(x, y, gate, post_norm, post_weight, pre_weight,
+                                           residual_scale, eps)
+    if dn is None:
+        raise TypeError("dn must be a torch.Tensor")
+    _on(dn, "dn", *like)
+    _on(dh, "dh", *like)
+    dx = torch.empty_like(x) if dx is None else _on(dx, "dx", *like)
+    dy = torch.empty_like(x) if dy is None else _on(dy, "dy", *like)
     if gate is None:
         if dgate is not None:
             raise ValueError("dgate needs a gate")
     else:
-        dgate = torch.empty_like(x) if dgate is None else _dev(dgate, "dgate", x.dtype, x.shape)
+        dgate = torch.empty_like(x) if dgate is None else _on(dgate, "dgate", *like)
     dpost = None if post_weight is None else torch.empty_like(post_weight)
     dpre = None if pre_weight is None else torch.empty_like(pre_weight)
     if workspace is None:              # the allocator's 512-byte alignment is enough here
         workspace = torch.empty(retnet_residual_norm_backward_workspace_size(rows, hidden),
                                 dtype=torch.uint8, device=x.device)
     else:
-        _dev(workspace, "workspace", torch.uint8)
-    _one_device(x, dn, dh, dx, dy, dgate, workspace)
-    st = _launch(x, load_library().retnet_residual_norm_backward, _ptr(x), _ptr(y), _ptr(dn),
+        _on(workspace, "workspace", torch.uint8, workspace.shape, like[2])
+    st = _launch(like[2], load_library().retnet_residual_norm_backward, _ptr(x), _ptr(y), _ptr(dn),
                  _ptr(dh), ctypes.byref(norm), rows, hidden, _dtype_code(x), _ptr(dx), _ptr(dy),
                  _ptr(dgate), _ptr(dpost), _ptr(dpre), _ptr(workspace), workspace.numel())
     _check("retnet_residual_norm_backward", st)

@@ -256,23 +256,26 @@ def test_float32_prefill_in_segments(rn, dk, dv, H, lens):
         assert err(got, want, axis) < bound("f32")
 
 
-@pytest.mark.parametrize("dk,dv,Hk,H,lens", [(64, 128, 1, 2, [1100, 0, 640]), (128, 64, 2, 2, [64, 1100, 65])])
-def test_float32_backward_in_segments(rn, dk, dv, Hk, H, lens):
+@pytest.mark.parametrize("dtype,dk,dv,Hk,H,lens", [
+    ("f32", 64, 128, 1, 2, [1100, 0, 640]), ("f32", 128, 64, 2, 2, [64, 1100, 65]),
+    ("bf16", 128, 128, 1, 1, [700, 1100, 1])])
+def test_float32_backward_in_segments(rn, dtype, dk, dv, Hk, H, lens):
+    """Float32 arithmetic, on either type."""
     B, n = 3, 1100
-    x, ref = make(26, B, n, Hk, H, dk, dv, "f32", decay=0.02)
+    x, ref = make(26, B, n, Hk, H, dk, dv, dtype, decay=0.02)
     for t, r in zip(x, ref):
         for b, c in enumerate(lens):
             t[b, c:] = float("nan")
             r[b, c:] = 0.0
     lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
-    got = rn.retnet_delta_backward(*x, lengths=lengths)
+    got = rn.retnet_delta_backward(*x, lengths=lengths, algo="simt")
     done(rn)
     want = oracle.delta_backward(*ref, dk ** -0.5, lens)
     for name, a, w in zip(("dq", "dk", "dv", "dg", "dbeta"), got, want):
         for b, c in enumerate(lens):
             assert not a[b, c:].any(), name
         w, a = together(w, a)
-        assert err(a, w) < bound("f32"), name
+        assert err(a, w) < bound(dtype), name
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -586,3 +589,29 @@ def test_states_and_workspaces_beyond_32_bits(rn):
     done(rn)
     for a, b in zip(grads, alone):
         assert torch.isfinite(b).all() and torch.equal(a[-16:], b)
+
+
+def test_arguments_that_do_not_fit(rn):
+    """The bindings name the argument that does not fit the others."""
+    (q, k, v, g, beta, do), _ = make(28, 2, 5, 2, 4, 64, 128, "bf16")
+    S = torch.zeros(2, 4, 64, 128, device="cuda")
+    for kw, kind in ((dict(k=k[:1]), ValueError), (dict(k=k.float()), TypeError),
+                     (dict(v=v[:, :4]), ValueError), (dict(g=g.cpu()), ValueError),
+                     (dict(beta=beta[:, :, :2]), ValueError), (dict(state=S.double()), TypeError),
+                     (dict(state=None), TypeError), (dict(out=v.transpose(1, 2)), ValueError),
+                     (dict(lengths=torch.ones(2, device="cuda")), TypeError),
+                     (dict(lengths=torch.ones(3, device="cuda", dtype=torch.int32)), ValueError)):
+        args = dict(q=q, k=k, v=v, g=g, beta=beta, state=S)
+        args.update(kw)
+        with pytest.raises(kind):
+            rn.retnet_delta_recurrent(**args)
+    with pytest.raises(TypeError):
+        rn.retnet_delta_backward(q, k, v, g, beta, None)
+    for kw in (dict(dq=k.float()), dict(workspace=S)):
+        with pytest.raises(TypeError):
+            rn.retnet_delta_backward(q, k, v, g, beta, do, **kw)
+    # a parameter is a tensor
+    p = torch.nn.Parameter(q)
+    assert torch.equal(rn.retnet_delta_chunkwise(p, k, v, g, beta),
+                       rn.retnet_delta_chunkwise(q, k, v, g, beta))
+    done(rn)
