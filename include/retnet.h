@@ -411,7 +411,9 @@ RETNET_API retnet_status retnet_delta_recurrent(const void *q, const void *k, co
  * operands are rounded to bf16 on the way to `out`, and a final state keeps
  * float32 accuracy.  out must not overlap the inputs, the states or the
  * workspace.
- *   workspace  retnet_delta_workspace_size() bytes, 1024-byte aligned.
+ *   workspace  retnet_delta_workspace_size() bytes, 1024-byte aligned.  They
+ *              follow from the whole shape and need not grow with seqlen:
+ *              for one workspace over several lengths take the largest.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 RETNET_API retnet_status retnet_delta_workspace_size(const retnet_delta_shape *shape,
                                                      retnet_algo algo, size_t *bytes);
@@ -427,7 +429,8 @@ RETNET_API retnet_status retnet_delta_chunkwise(const void *q, const void *k, co
  * d_out = dL/dout, writes dq, dk, dv, dg, dbeta, shaped and typed as q, k,
  * v, g, beta; a key head's dq and dk are the sums over its value heads, in
  * head order.  The gradients must not overlap the inputs or each other.
- *   workspace  retnet_delta_backward_workspace_size() bytes, 1024-byte aligned.
+ *   workspace  retnet_delta_backward_workspace_size() bytes, 1024-byte aligned
+ *              (as above).
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 RETNET_API retnet_status retnet_delta_backward_workspace_size(const retnet_delta_shape *shape,
                                                               retnet_algo algo, size_t *bytes);
