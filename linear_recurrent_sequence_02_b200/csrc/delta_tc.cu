@@ -741,16 +741,21 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
             if (!warp_spin_wait(&bar.x_full, c & 1, abort_flag, err)) break;
             tc_fence_after();
             {
-                uint32_t x[32], hi[16], lo[16], xb[16];
-                tmem_ld32(tl + Tm::kX + 32 * wg, x);
-                tmem_wait_ld();
+                uint32_t hi[16], lo[16], xb[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float2 r = *reinterpret_cast<const float2 *>(hdr + 32 * wg + 2 * j);
-                    const float2 xv = as_pair(x[2 * j], x[2 * j + 1]), xr = mul2(xv, r);
-                    if (kFine) split_pair(xr, hi[j], lo[j]);
-                    else hi[j] = pack_bf16x2(xr.x, xr.y);
-                    if (kOut || kSave) xb[j] = pack_bf16x2(xv.x, xv.y);
+                for (int hf = 0; hf < 2; ++hf) {           // 16 columns at a time, for the registers
+                    uint32_t x[16];
+                    tmem_ld16(tl + Tm::kX + 32 * wg + 16 * hf, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int i = 8 * hf + j;
+                        const float2 r = *reinterpret_cast<const float2 *>(hdr + 32 * wg + 2 * i);
+                        const float2 xv = as_pair(x[2 * j], x[2 * j + 1]), xr = mul2(xv, r);
+                        if (kFine) split_pair(xr, hi[i], lo[i]);
+                        else hi[i] = pack_bf16x2(xr.x, xr.y);
+                        if (kOut || kSave) xb[i] = pack_bf16x2(xv.x, xv.y);
+                    }
                 }
                 tmem_st16(tl + Tm::kXs + 16 * wg, hi);
                 if (kFine) tmem_st16(tl + Tm::kXslo + 16 * wg, lo);
@@ -767,12 +772,15 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                 ok = ok && warp_spin_wait(&bar.z_full[p], c & 1, abort_flag, err);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t z[32];
-                tmem_ld32(tl + Tm::kZ + 64 * p + 32 * wg, z);
-                tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    S[p][j] = fma2(both(eL), S[p][j], as_pair(z[2 * j], z[2 * j + 1]));
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t z[16];
+                    tmem_ld16(tl + Tm::kZ + 64 * p + 32 * wg + 16 * hf, z);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        S[p][8 * hf + j] = fma2(both(eL), S[p][8 * hf + j], as_pair(z[2 * j], z[2 * j + 1]));
+                }
                 put_state(p, c + 1);
             }
             if (!ok) break;
@@ -1253,15 +1261,19 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
             if (!warp_spin_wait(&bar.y_full, u & 1, abort_flag, err)) break;
             tc_fence_after();
             {
-                uint32_t y1[32], y2[32], dx[16], lo[16];
-                tmem_ld32(tl + kY1 + 32 * wg, y1);
-                tmem_ld32(tl + kY2 + 32 * wg, y2);
-                tmem_wait_ld();
+                uint32_t dx[16], lo[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float2 r = *reinterpret_cast<const float2 *>(hdr + 32 * wg + 2 * j);
-                    split_pair(fma2(r, as_pair(y2[2 * j], y2[2 * j + 1]), as_pair(y1[2 * j], y1[2 * j + 1])),
-                               dx[j], lo[j]);
+                for (int hf = 0; hf < 2; ++hf) {           // 16 columns at a time, for the registers
+                    uint32_t y1[16], y2[16];
+                    tmem_ld16(tl + kY1 + 32 * wg + 16 * hf, y1);
+                    tmem_ld16(tl + kY2 + 32 * wg + 16 * hf, y2);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 r = *reinterpret_cast<const float2 *>(hdr + 32 * wg + 16 * hf + 2 * j);
+                        split_pair(fma2(r, as_pair(y2[2 * j], y2[2 * j + 1]), as_pair(y1[2 * j], y1[2 * j + 1])),
+                                   dx[8 * hf + j], lo[8 * hf + j]);
+                    }
                 }
                 tmem_st16(tl + kDx + 16 * wg, dx);
                 tmem_wait_st();
@@ -1278,12 +1290,15 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
                 ok = ok && warp_spin_wait(&bar.z_full[p], u & 1, abort_flag, err);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t z[32];
-                tmem_ld32(tl + kZ + 64 * p + 32 * wg, z);
-                tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    D[p][j] = fma2(both(eL), D[p][j], as_pair(z[2 * j], z[2 * j + 1]));
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t z[16];
+                    tmem_ld16(tl + kZ + 64 * p + 32 * wg + 16 * hf, z);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        D[p][8 * hf + j] = fma2(both(eL), D[p][8 * hf + j], as_pair(z[2 * j], z[2 * j + 1]));
+                }
                 put_grad(p, top - 2 - u);
             }
             if (!ok) break;
