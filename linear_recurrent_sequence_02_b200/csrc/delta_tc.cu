@@ -463,7 +463,7 @@ delta_prep_kernel(DeltaPrepArgs a) {
 // S_hi (W_hi + W_lo) + S_lo W_hi, Z takes both parts of Xs against the exact
 // K, so each product carries 16 bits (the lowest parts' product, 2^-18, is
 // left out) and the state keeps float32 accuracy over the walk (measured
-// 3e-6 after 8192 tokens); without it S is only ever seen through bf16
+// 3e-6 to 6e-6 after 8192 tokens); without it S is only ever seen through bf16
 // outputs and one part is enough.
 constexpr int kScanThreads = 448;
 constexpr int kChainWarps = 8;
