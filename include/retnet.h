@@ -495,11 +495,13 @@ RETNET_API retnet_status retnet_check_device_errors(retnet_stream_t stream);
 #ifdef RETNET_TEST_HOOKS
 /* Debug build only (compiled with RETNET_TEST_HOOKS; absent from the
  * default library).  No counterpart on the pages: a way to exercise the
- * timeout path without a GPU fault.  Sets, for the tensor-core prefill
- * kernels on the current device, the wall-time limit of every pipeline
- * wait (wait_limit_ns > 0; the default build uses about 2 s), and whether
- * the state pass's first CTA skips its first TMA load (skip = 1), so that
- * its MMA warp's wait runs out and the CTA takes the timeout path.
+ * timeout path without a GPU fault.  Sets, for the tensor-core kernels of
+ * the retention prefill and of the gated delta rule on the current device,
+ * the wall-time limit of every pipeline wait (wait_limit_ns > 0; the default
+ * build uses about 2 s), and whether (skip = 1) the state pass's first CTA
+ * skips its first TMA load, and the delta rule's walks over the first
+ * (sequence, head) and its gradients' first CTA their second, so that a wait
+ * runs out and the CTA takes the timeout path.
  * Errors: INVALID_ARG, CUDA. */
 RETNET_API retnet_status retnet_test_set_hooks(unsigned long long wait_limit_ns,
                                                int skip_first_state_load);

@@ -1880,7 +1880,7 @@ cudaError_t launch_chunkwise_tc(const ChunkwiseArgs &a, const float *gammas, cud
 
 #ifdef RETNET_TEST_HOOKS
 // Debug build only: lowers the wall-time limit of the pipeline waits in this
-// file's kernels, and makes the state pass's first CTA skip its first load.
+// file's kernels and the delta rule's, and makes first CTAs skip a load.
 extern "C" RETNET_API retnet_status retnet_test_set_hooks(unsigned long long wait_limit_ns,
                                                           int skip_first_state_load) {
     if (wait_limit_ns == 0 || (skip_first_state_load != 0 && skip_first_state_load != 1))
@@ -1888,7 +1888,8 @@ extern "C" RETNET_API retnet_status retnet_test_set_hooks(unsigned long long wai
     if (cudaMemcpyToSymbol(retnet::sm100::g_hook_wait_limit_ns, &wait_limit_ns,
                            sizeof(wait_limit_ns)) != cudaSuccess ||
         cudaMemcpyToSymbol(retnet::g_hook_skip_first_load, &skip_first_state_load,
-                           sizeof(int)) != cudaSuccess)
+                           sizeof(int)) != cudaSuccess ||
+        retnet::set_delta_hooks(wait_limit_ns, skip_first_state_load) != cudaSuccess)
         return RETNET_ERR_CUDA;
     return RETNET_OK;
 }

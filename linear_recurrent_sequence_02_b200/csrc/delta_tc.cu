@@ -30,6 +30,18 @@ using namespace sm100;
 constexpr int kC = kDeltaChunk;
 constexpr uint32_t kBox64 = 8192;          // 64 rows x 64 bf16, 128-byte swizzled
 
+#ifdef RETNET_TEST_HOOKS
+// Test hook (debug build only): when set, the walks of the first (sequence,
+// head)'s first columns and the gradient kernel's first CTA never issue their
+// second stage's copies, so that waits run out with MMAs of the first issued.
+static __device__ int g_hook_skip_second_load = 0;
+__device__ __forceinline__ bool hook_skips(bool first, int it) {
+    return first && it == 1 && *(volatile int *)&g_hook_skip_second_load;
+}
+#else
+__device__ __forceinline__ constexpr bool hook_skips(bool, int) { return false; }
+#endif
+
 // One chunk's prepared operands, in shared-memory order.  Every tile is
 // boxes of 64 rows (tokens) of 64 columns, 128-byte swizzled.
 // kSplit: T^ and W in two bf16 parts (16 bits together), which the final
@@ -66,6 +78,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// Waits (bounded) for the MMAs that this warp has in flight.  A commit only
+// tracks what its own thread issued, and elect.sync chooses the same lane for
+// the same mask each time, so it is issued as the MMAs were.
+__device__ __forceinline__ void drain_mmas(uint64_t *bar, unsigned *err) {
+    __syncwarp();
+    if (elect_one()) mma_commit(bar);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_drain(bar, 0, err);
+    __syncwarp();
 }
 // Two bf16 parts of a pair: hi the rounding, lo the rounding of what it left.
 __device__ __forceinline__ void split_pair(float2 x, uint32_t &hi, uint32_t &lo) {
@@ -589,6 +611,7 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
         for (; it < nc; ++it) {
             const int s = it & 1;
             if (it >= 2 && !warp_spin_wait(&bar.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
+            if (hook_skips(bh == 0 && v0 == 0, it)) continue;
             uint8_t *st = smem + s * Smem::kStage;
             if (elect_one()) {
                 const uint32_t block = out ? Block::kBytes : Block::kQ;
@@ -841,13 +864,10 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
     // After an abort, wait (bounded) for the copies still in flight before
     // shared memory goes away and for the MMAs before tensor memory is freed.
     if (*abort_flag && warp == 0 && lane == 0)
-        for (int j = max(0, it - 2); j < it; ++j) mbar_drain(&bar.full[j & 1], (j >> 1) & 1, err);
+        for (int j = max(0, it - 2); j < it; ++j)
+            if (!hook_skips(bh == 0 && v0 == 0, j)) mbar_drain(&bar.full[j & 1], (j >> 1) & 1, err);
     if (warp == 1) {
-        if (*abort_flag && lane == 0) {
-            mma_commit(&bar.drain);
-            mbar_drain(&bar.drain, 0, err);
-        }
-        __syncwarp();
+        if (*abort_flag) drain_mmas(&bar.drain, err);
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -1138,6 +1158,7 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
         for (; it < nc; ++it) {
             const int s = it & 1, c = top - 1 - it;
             if (it >= 2 && !warp_spin_wait(&bar.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
+            if (hook_skips(bh == 0 && v0 == 0, it)) continue;
             uint8_t *st = smem + s * Smem::kStage;
             if (elect_one()) {
                 mbar_expect_tx(&bar.full[s], Smem::kStage);
@@ -1344,13 +1365,10 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
     tc_fence_before();
     __syncthreads();
     if (*abort_flag && warp == 0 && lane == 0)             // as in the forward walk
-        for (int j = max(0, it - 2); j < it; ++j) mbar_drain(&bar.full[j & 1], (j >> 1) & 1, err);
+        for (int j = max(0, it - 2); j < it; ++j)
+            if (!hook_skips(bh == 0 && v0 == 0, j)) mbar_drain(&bar.full[j & 1], (j >> 1) & 1, err);
     if (warp == 1) {
-        if (*abort_flag && lane == 0) {
-            mma_commit(&bar.drain);
-            mbar_drain(&bar.drain, 0, err);
-        }
-        __syncwarp();
+        if (*abort_flag) drain_mmas(&bar.drain, err);
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -1581,6 +1599,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 const int s = it & 1;
                 if (it >= 2) ok = warp_spin_wait(&m.empty[s], ((it >> 1) - 1) & 1, abort_flag, err);
                 if (!ok) break;
+                if (hook_skips(blockIdx.x == 0, it)) continue;
                 uint8_t *st = smem + Smem::kStage0 + s * Smem::kStage;
                 if (elect_one()) {
                     mbar_expect_tx(&m.full[s], Smem::kStage);
@@ -1971,14 +1990,11 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     __syncthreads();
     if (*abort_flag && warp == 8 && lane == 0) {           // as in the walks
         for (int j = max(0, kit - 2); j < kit; ++j) mbar_drain(&m.keys[j & 1], (j >> 1) & 1, err);
-        for (int j = max(0, it - 2); j < it; ++j) mbar_drain(&m.full[j & 1], (j >> 1) & 1, err);
+        for (int j = max(0, it - 2); j < it; ++j)
+            if (!hook_skips(blockIdx.x == 0, j)) mbar_drain(&m.full[j & 1], (j >> 1) & 1, err);
     }
     if (warp == 9) {
-        if (*abort_flag && lane == 0) {
-            mma_commit(&m.drain);
-            mbar_drain(&m.drain, 0, err);
-        }
-        __syncwarp();
+        if (*abort_flag) drain_mmas(&m.drain, err);
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -2273,6 +2289,14 @@ size_t delta_tc_workspace(int batch, int heads, int seqlen, int dk, int dv) {
     const size_t without = tc_layout(batch, heads, seqlen, dk, dv, false).total;
     return with > without ? with : without;
 }
+
+#ifdef RETNET_TEST_HOOKS
+cudaError_t set_delta_hooks(unsigned long long wait_limit_ns, int skip_load) {
+    const cudaError_t e = cudaMemcpyToSymbol(sm100::g_hook_wait_limit_ns, &wait_limit_ns,
+                                             sizeof(wait_limit_ns));
+    return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_hook_skip_second_load, &skip_load, sizeof(int));
+}
+#endif
 
 cudaError_t launch_delta_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream) {
     return a.dk == 64 ? launch_forward<64>(a, workspace, stream)

@@ -164,6 +164,9 @@ size_t delta_tc_workspace(int batch, int heads, int seqlen, int dk, int dv);
 cudaError_t launch_delta_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream);
 size_t delta_backward_tc_workspace(int batch, int heads, int key_heads, int seqlen, int dk, int dv);
 cudaError_t launch_delta_backward_tc(const DeltaArgs &a, void *workspace, cudaStream_t stream);
+#ifdef RETNET_TEST_HOOKS
+cudaError_t set_delta_hooks(unsigned long long wait_limit_ns, int skip_load);
+#endif
 // The states between segments, starts[j] += M_j starts[j - 1], j = 1 .. joins,
 // M_j of units [joins][bhs][dk, dk], starts [joins + 1][bhs][dk, dv]; back
 // (may be null): the same with M_{joins + 1 - j}^T.  dk 64 or 128.
