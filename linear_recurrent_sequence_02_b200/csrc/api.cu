@@ -171,11 +171,11 @@ static retnet_status check_delta_shape(const retnet_delta_shape *s) {
         !dtype_ok(s->dtype) || s->dk <= 0 || s->dv <= 0)
         return RETNET_ERR_INVALID_ARG;
     if (!head_dim_ok(s->dk) || !head_dim_ok(s->dv)) return RETNET_ERR_UNSUPPORTED;
-    // a CTA per (sequence, head) and slab of columns or chunk of tokens
+    // at most 2^23 chunks: the largest grid, 32 CTAs a (sequence, head) of the
+    // backward's sweeps, is then 2^28, and a tensor's largest stride 2^38 bytes
     const long long bh = (long long)(s->batch > 0 ? s->batch : 1) * s->heads;
     const long long chunks = (s->seqlen + (long long)kDeltaChunk - 1) / kDeltaChunk;
-    // (and a row of the saved operands per value channel of each)
-    if (bh > 0x7fffffffll / 256 / (chunks > 0 ? chunks : 1)) return RETNET_ERR_UNSUPPORTED;
+    if (bh > (1ll << 23) / (chunks > 0 ? chunks : 1)) return RETNET_ERR_UNSUPPORTED;
     return RETNET_OK;
 }
 static bool algo_ok(retnet_algo a) {

@@ -55,6 +55,23 @@ def test_shapes(lib, bad, status):
         assert size(ctypes.byref(shape(**bad)), 0, ctypes.byref(n)) == status
 
 
+@pytest.mark.parametrize("B,H,n,fits", [
+    (1 << 23, 1, 1, True), ((1 << 23) + 1, 1, 1, False), (1 << 23, 1, 0, True),
+    (1 << 15, 256, 64, True), (1 << 15, 256, 65, False), (1 << 17, 1, 4096, True),
+    (1 << 17, 1, 4097, False), (1, 1, 1 << 29, True), (1, 1, (1 << 29) + 1, False),
+    (3, 5, 64 * (2 ** 23 // 15), True), (3, 5, 64 * (2 ** 23 // 15) + 1, False),
+])
+def test_largest_shapes(lib, B, H, n, fits):
+    """2^23 chunks of 64 tokens over all sequences and heads, and one more
+    (workspace sizes only: nothing is launched)."""
+    size = ctypes.c_size_t(0)
+    for dk in (64, 256):
+        for dtype in (0, 1):
+            s = ctypes.byref(shape(B, H, H, n, dk, 256, dtype))
+            for f in (lib.retnet_delta_workspace_size, lib.retnet_delta_backward_workspace_size):
+                assert f(s, 0, ctypes.byref(size)) == (OK if fits else UNSUPPORTED)
+
+
 def test_arguments(lib):
     s = shape()
     assert calls(lib, None) == (INVALID,) * 3
