@@ -615,6 +615,16 @@ def _delta_shape(q, k, v, g, beta, lengths):
     return _DeltaShape(B, H, Hk, n, dk, dv, _dtype_code(q)), index
 
 
+def _gates(g, beta, lengths):
+    """g, beta and lengths for a call.  The library reads from 16-byte aligned
+    addresses; contiguous slices of these (one token of one sequence, the
+    lengths of the later sequences) start anywhere, and such are copied."""
+    if (g.data_ptr() | beta.data_ptr() | (0 if lengths is None else lengths.data_ptr())) & 15:
+        g, beta, lengths = (t if t is None or not t.data_ptr() & 15 else t.clone()
+                            for t in (g, beta, lengths))
+    return g, beta, lengths
+
+
 def _delta_scale(scale: Optional[float], dk: int) -> float:
     return dk ** -0.5 if scale is None else float(scale)
 
@@ -638,6 +648,7 @@ def retnet_delta_recurrent(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
         raise TypeError("state must be a torch.Tensor")
     _on(state, "state", torch.float32, (shape.batch, shape.heads, shape.dk, shape.dv), index)
     out = _delta_out(v, lengths) if out is None else _on(out, "out", q.dtype, v.shape, index)
+    g, beta, lengths = _gates(g, beta, lengths)
     st = _launch(index, load_library().retnet_delta_recurrent, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
                  _ptr(beta), _delta_scale(scale, shape.dk), _ptr(lengths), _ptr(state), _ptr(out),
                  ctypes.byref(shape))
@@ -685,6 +696,7 @@ def retnet_delta_chunkwise(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
     _on(state_in, "state_in", torch.float32, sshape, index)
     _on(state_out, "state_out", torch.float32, sshape, index)
     out = _delta_out(v, lengths) if out is None else _on(out, "out", q.dtype, v.shape, index)
+    g, beta, lengths = _gates(g, beta, lengths)
     if workspace is None:
         workspace = retnet_workspace(
             retnet_delta_workspace_size(shape.batch, shape.heads, shape.key_heads, shape.seqlen,
@@ -718,6 +730,9 @@ def retnet_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
                               ("dbeta", dbeta, beta)):
         grads.append(torch.empty_like(like) if given is None else
                      _on(given, name, q.dtype, like.shape, index))
+    # dg and dbeta as g and beta, written beside and copied
+    to = [t if not t.data_ptr() & 15 or i < 3 else torch.empty_like(t) for i, t in enumerate(grads)]
+    g, beta, lengths = _gates(g, beta, lengths)
     if workspace is None:
         workspace = retnet_workspace(
             retnet_delta_backward_workspace_size(shape.batch, shape.heads, shape.key_heads,
@@ -727,9 +742,12 @@ def retnet_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
         _on(workspace, "workspace", torch.uint8, workspace.shape, index)
     st = _launch(index, load_library().retnet_delta_backward, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
                  _ptr(beta), _ptr(d_out), _delta_scale(scale, shape.dk), _ptr(lengths),
-                 *(_ptr(t) for t in grads), ctypes.byref(shape), _ALGOS[algo], _ptr(workspace),
+                 *(_ptr(t) for t in to), ctypes.byref(shape), _ALGOS[algo], _ptr(workspace),
                  workspace.numel())
     _check("retnet_delta_backward", st)
+    for given, t in zip(grads, to):
+        if given is not t:
+            given.copy_(t)
     return tuple(grads)
 
 
