@@ -18,7 +18,8 @@ __device__ __forceinline__ int delta_tokens_of(const int *lengths, int b, int se
 // x is linear in b, and dbeta is (gradient of x) . x / b.  Where b is 0 the
 // backward takes a b of this size instead: x keeps all its digits, the
 // quotient is the limit, and what it writes to the state is nothing beside it.
-__device__ __forceinline__ float nonzero_beta(float b) { return fabsf(b) < 1e-15f ? 1e-15f : b; }
+constexpr float kBetaFloor = 1e-15f;
+__device__ __forceinline__ float nonzero_beta(float b) { return fabsf(b) < kBetaFloor ? kBetaFloor : b; }
 
 // g where sums of it are formed: e^g is 0 in float32 from here on, and
 // differences of sums stay finite when g is -inf.

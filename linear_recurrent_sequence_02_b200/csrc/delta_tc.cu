@@ -1804,6 +1804,15 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     a.dbeta[r] = from_f32<__nv_bfloat16>(t < w.cnt ? S.db[t] / (G.beta[t] * G.beta[t]) : 0.f);
                 }
             }
+            // where b counts as 0 (nonzero_beta), v has no part in x: what dV held
+            // for dbeta's sake, and this CTA alone has read, goes
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+                for (unsigned none = __ballot_sync(0xffffffffu, G.beta[lane + 32 * v] == kBetaFloor); none; none &= none - 1) {
+                    const int t = 32 * v + __ffs(none) - 1;
+                    __nv_bfloat16 *row = a.dv_ + ((row0 + t) * a.heads + w.h) * a.dv;
+                    for (int j = lane; j < a.dv; j += 32) row[j] = from_f32<__nv_bfloat16>(0.f);
+                }
             __syncwarp();
             prepare();                                     // this item's turn is free
             if (elect_one()) {

@@ -1,5 +1,6 @@
 """The gated delta rule as its documentation allows it, where
 test_delta_gpu.py does not go."""
+import numpy as np
 import pytest
 import torch
 
@@ -54,3 +55,28 @@ def test_prefill_and_backward_of_later_tokens_and_sequences(rn, dtype):
                     rn.retnet_delta_backward(*part, lengths=lengths[1:].clone())):
         assert torch.equal(a, b)
     done(rn)
+
+
+# ------------------------------------------------------------------ gates
+@pytest.mark.parametrize("dtype,algo", [("bf16", "auto"), ("bf16", "simt"), ("f32", "auto")])
+@pytest.mark.parametrize("Hk,H,dk,dv", [(2, 2, 64, 64), (1, 2, 128, 256)])
+def test_values_of_tokens_that_write_nothing_have_no_gradient(rn, dtype, algo, Hk, H, dk, dv):
+    """dv = beta r: exactly 0 where beta is."""
+    B, n = 2, 200
+    x, _ = make(54, B, n, Hk, H, dk, dv, dtype)
+    off = torch.rand(B, n, H, device="cuda", generator=torch.Generator("cuda").manual_seed(1)) < 0.3
+    off[:, 64:128], off[1, :, 0], off[:, 5], off[:, 70] = True, True, False, False
+    x[4][off] = 0.0
+    lengths = torch.tensor([200, 170], dtype=torch.int32, device="cuda")
+    got = rn.retnet_delta_backward(*x, lengths=lengths, algo=algo)
+    done(rn)
+    assert not got[2][off].any()
+    on = ~off
+    on[1, 170:] = False
+    assert got[2][on].any(-1).all() and got[4][:, :170][off[:, :170]].abs().max() > 0
+    want = oracle.delta_backward(*(t.double().cpu().numpy() for t in x), dk ** -0.5, [200, 170])
+    for b in range(B):
+        for h in range(H):
+            if want[2][b, :, h].any():
+                e = np.linalg.norm(got[2][b, :, h].double().cpu().numpy() - want[2][b, :, h])
+                assert e < bound(dtype, dtype == "bf16" and algo == "auto") * np.linalg.norm(want[2][b, :, h])
