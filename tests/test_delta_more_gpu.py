@@ -80,3 +80,29 @@ def test_values_of_tokens_that_write_nothing_have_no_gradient(rn, dtype, algo, H
             if want[2][b, :, h].any():
                 e = np.linalg.norm(got[2][b, :, h].double().cpu().numpy() - want[2][b, :, h])
                 assert e < bound(dtype, dtype == "bf16" and algo == "auto") * np.linalg.norm(want[2][b, :, h])
+
+
+# ------------------------------------------------------------------ many sequences
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hk,H,dk,dv", [(1, 4, 64, 256), (2, 4, 128, 256), (4, 4, 256, 256),
+                                        (8, 24, 128, 64)])
+def test_step_of_many_sequences_of_which_some_are_over(rn, dtype, Hk, H, dk, dv):
+    """A step's CTAs (444) take several (sequence, head, 32 columns) each, and
+    pass over those of a sequence that is over."""
+    B = 71
+    assert B * H * dv // 32 > 3 * 444
+    (q, k, v, g, beta, _), ref = make(55, B, 1, Hk, H, dk, dv, dtype)
+    lens = np.random.default_rng(56).integers(-1, 3, B)
+    lens[:4] = 0, 1, 0, 0
+    over = torch.from_numpy(lens < 1).cuda()
+    for x, r in zip((q, k, v, g, beta), ref):
+        x[over], r[lens < 1] = float("nan"), 0.0
+    S, S0 = states(57, B, H, dk, dv)
+    out = torch.full_like(v, 7.0)
+    lengths = torch.from_numpy(lens.astype(np.int32)).cuda()
+    rn.retnet_delta_recurrent(q, k, v, g, beta, S, lengths=lengths, out=out)
+    done(rn)
+    o, St = oracle.delta_recurrent(*ref[:5], dk ** -0.5, S0, lens.tolist())
+    assert (out[over] == 7).all() and torch.equal(S[over].cpu(), torch.from_numpy(S0[lens < 1]).float())
+    assert err(out[~over], o[lens > 0]) < bound(dtype)
+    assert err(S, St, 1) < 2e-5
