@@ -376,6 +376,13 @@ RETNET_API retnet_status retnet_msr_layer(const void *x, const void *w_qkvg, con
  *           not read, their rows of `out` are left as they were, and their
  *           gradients are zero.
  *   state   device float32 [batch, heads, dk, dv], as for retention.
+ * A value that is not finite: one of q reaches its own token's output; one of
+ * v its channel of its value head's outputs from its token on; one of k, beta or
+ * g (NaN; -inf is a decay) all of them.  On the tensor-core path k, v, g and beta also reach the
+ * earlier tokens of their chunk of 64 (tokens 64 c .. 64 c + 63), whose zeros
+ * meet them in the products.  Other sequences, other heads and, for v, other
+ * channels keep their bits; the gradients of the key head's value heads, in
+ * that sequence, are then of no use.
  * Sizes: batch, seqlen >= 0; 1 <= key_heads <= heads <= 256 with heads a
  * multiple of key_heads; dk, dv in {64, 128, 256}; at most 2^23 chunks of 64
  * tokens over all sequences and heads (UNSUPPORTED beyond); scale finite. */

@@ -106,3 +106,50 @@ def test_step_of_many_sequences_of_which_some_are_over(rn, dtype, Hk, H, dk, dv)
     assert (out[over] == 7).all() and torch.equal(S[over].cpu(), torch.from_numpy(S0[lens < 1]).float())
     assert err(out[~over], o[lens > 0]) < bound(dtype)
     assert err(S, St, 1) < 2e-5
+
+
+# ------------------------------------------------------------------ infinities and NaN
+@pytest.mark.parametrize("dtype,algo,chunk", [("bf16", "tensor", 64), ("bf16", "simt", 1),
+                                              ("f32", "auto", 1)])
+@pytest.mark.parametrize("which", ["v", "k", "g"])
+def test_where_a_value_that_is_not_finite_goes(rn, dtype, algo, chunk, which):
+    """To the outputs from its token on, of its head (of its channel, for v);
+    on the tensor cores also to the earlier tokens of its chunk of 64.  Other
+    sequences, heads, channels and chunks before keep their bits, and the
+    gradients of other sequences and heads theirs."""
+    B, n, H, d, at = 2, 200, 2, 64, 100
+    x, _ = make(58, B, n, H, H, d, d, dtype)
+    clean = rn.retnet_delta_chunkwise(*x[:5], algo=algo)
+    grads = rn.retnet_delta_backward(*x, algo=algo)
+    bad = [t.clone() for t in x]
+    if which == "v":
+        bad[2][0, at, 1, 5] = float("inf")
+    elif which == "k":
+        bad[1][0, at, 1, 5] = float("nan")
+    else:
+        bad[3][0, at, 1] = float("nan")
+    out = rn.retnet_delta_chunkwise(*bad[:5], algo=algo)
+    bad_grads = rn.retnet_delta_backward(*bad, algo=algo)
+    done(rn)
+    for a, b in zip((out, *bad_grads), (clean, *grads)):
+        assert torch.equal(a[1], b[1]) and torch.equal(a[0, :, 0], b[0, :, 0])
+    start = at // chunk * chunk
+    assert torch.equal(out[0, :start, 1], clean[0, :start, 1])
+    mine = out[0, at:, 1, 5:6] if which == "v" else out[0, at:, 1]
+    assert not torch.isfinite(mine).any()
+    if which == "v":
+        rest = [c for c in range(d) if c != 5]
+        assert torch.equal(out[0, :, 1, rest], clean[0, :, 1, rest])
+
+
+@pytest.mark.parametrize("dtype,algo", [("bf16", "tensor"), ("bf16", "simt"), ("f32", "auto")])
+def test_a_query_that_is_not_finite_spoils_its_own_output_alone(rn, dtype, algo):
+    B, n, H, d, at = 2, 200, 2, 64, 100
+    x, _ = make(59, B, n, 1, H, d, d, dtype)
+    clean = rn.retnet_delta_chunkwise(*x[:5], algo=algo)
+    x[0][0, at, 0, 5] = float("nan")
+    out = rn.retnet_delta_chunkwise(*x[:5], algo=algo)
+    done(rn)
+    assert torch.isnan(out[0, at]).all()
+    out[0, at] = clean[0, at]
+    assert torch.equal(out, clean)
