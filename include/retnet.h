@@ -414,8 +414,11 @@ RETNET_API retnet_status retnet_delta_recurrent(const void *q, const void *k, co
  * state_in).  RETNET_ALGO_SIMT runs the recurrent form (AUTO does so for
  * float32 too, in segments of a long sequence beside one another); the
  * tensor-core path works in chunks of 64 tokens, for bf16 with dk 64 or 128;
- * AUTO takes it there for all but a few tokens.  On the tensor-core path
- * operands are rounded to bf16 on the way to `out`, and a final state keeps
+ * AUTO takes it there for all but a few tokens.  Its products take bf16
+ * operands: on the way to `out` what a chunk forms from q, k, g and beta, the
+ * state and x are rounded to bf16 (together with the result's rounding 2.9e-3
+ * of the norm, up to 4.4e-3 with decays near 0 over thousands of tokens; the
+ * result's alone is 1.7e-3, which is all that SIMT has); a final state keeps
  * float32 accuracy.  out must not overlap the inputs, the states or the
  * workspace.
  *   workspace  retnet_delta_workspace_size() bytes, 1024-byte aligned.  They
@@ -435,7 +438,11 @@ RETNET_API retnet_status retnet_delta_chunkwise(const void *q, const void *k, co
 /* Gradients of the prefill without initial state (as for retention): given
  * d_out = dL/dout, writes dq, dk, dv, dg, dbeta, shaped and typed as q, k,
  * v, g, beta; a key head's dq and dk are the sums over its value heads, in
- * head order.  The gradients must not overlap the inputs or each other.
+ * head order.  On the tensor-core path (bf16 with dk 64 or 128, but for SIMT)
+ * the operands are rounded to bf16 as in the prefill, the states, the
+ * gradients of the states and x are kept in bf16, and dq, dk, dg and dbeta are
+ * formed from dv as it leaves: 2.4e-3 to 4.9e-3 of a gradient's norm.  A beta
+ * of less than 1e-15 in size counts as 0; dbeta is then the limit.  The gradients must not overlap the inputs or each other.
  *   workspace  retnet_delta_backward_workspace_size() bytes, 1024-byte aligned
  *              (as above).
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */

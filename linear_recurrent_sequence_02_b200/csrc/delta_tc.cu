@@ -18,6 +18,21 @@
 // A operand in tensor memory that the thread writes where it read its
 // accumulator.  Nothing but the prepared tiles, K and V goes through shared
 // memory, all of it by bulk copies one chunk ahead.
+//
+// Roundings.  Accumulators, states, sums and decays are float32; the operands
+// of a product are bf16, each rounded once where it is formed, since a second
+// part doubles the product's MMAs.  What each moves an output by (2-norm, 400
+// tokens of 128 x 128, mean log decay -0.02; made one at a time by
+// oracle/delta_chunks.py, and the kernels' errors are those of all of them
+// within 0.5 %): P 1.6e-3, X as the output's operand 1.5e-3, the result
+// 1.7e-3, S, Q~ and e^{G_L - G} X 0.8 to 0.9e-3, T^ 0.3e-3, W 0.2e-3;
+// together 3.1e-3 (2.9e-3 at -0.2, 3.5e-3 at -0.002).  With P and X in two
+// parts it would be 2.2e-3, for twice the output's MMAs.  In the backward: the
+// pairs A and B 1.5e-3 of dq and dk, X 1.4 to 1.7e-3 of all but dv, dV 1.7e-3
+// of dv and dbeta (0.4e-3 of dk), D 0.8e-3, dX 0.2e-3 of dk (dV takes it in
+// two parts, or it would add 1.7e-3), the results 1.7e-3; together 2.6e-3 (dv)
+// to 3.5e-3 (dbeta).  A final state has no rounding of a result behind it, so
+// all that it depends on goes in two parts (kSplit): 2.6e-6 instead of 1.8e-3.
 #include "delta.cuh"
 #include "pairs.cuh"
 #include "sm100_chain.cuh"
@@ -126,7 +141,8 @@ __device__ __forceinline__ void put_channel(uint8_t *tile, int col, const uint32
 }
 
 // What the walks keep for the gradients (X^T, S^T, D^T: a row of `cols`
-// values per v channel and chunk) lies as [chunk][block of 64 channels][group
+// values per v channel and chunk; in bf16, as the operands that they have just
+// been and will be again) lies as [chunk][block of 64 channels][group
 // of 8 columns][channel][8]: a warp, whose lanes are channels, writes 512
 // consecutive bytes at a time, and a block is one copy and, as it is, an
 // MN-major operand without swizzle (columns by channels).  Offset, in
@@ -375,7 +391,7 @@ delta_prep_kernel(DeltaPrepArgs a) {
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 16; ++i) m.M[o + i][o + col] = x[i];
-    } else {                                               // Q~ where Q was
+    } else {                                               // Q~ where Q was, bf16 as its operand
         constexpr int kVecs = DK / 8;
 #pragma unroll 2
         for (int i = tid - 128; i < kC * kVecs; i += 128) {
@@ -738,7 +754,8 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                 S[p][j] = w.unit ? make_float2(k == v ? 1.f : 0.f, k + 1 == v ? 1.f : 0.f)
                           : w.from && live ? make_float2(src[0], src[w.width]) : both(0.f);
             }
-        // the operand copies of a piece of S; c: the chunk that starts with it
+        // the operand copies of a piece of S, which itself stays float32; the
+        // gradients keep the first.  c: the chunk that starts with it
         auto put_state = [&](int p, int c) {
             uint32_t hi[16], lo[16];
 #pragma unroll
@@ -890,7 +907,8 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 // up to three times, but on all SMs: 8192 tokens and 16 heads of 128 in 6
 // segments, walk 274 us whole, 103 us so, and 11 us the join.
 // Only what a final state depends on is walked in two parts: not the outputs
-// of the second pass, but its last segment, which is shorter for that.
+// of the second pass (it would take 0.1e-3 off their 3.1e-3), but its last
+// segment, which is shorter for that.
 // starts [segments - 1][BH][dk, dv]: N_j and then the state before segment
 // j + 1; units [segments - 2][BH][dk, dk]: M of segments 1 ...
 template <int DK, bool kSplit, bool kLast>
@@ -1389,7 +1407,8 @@ delta_walks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 }
 
 // Both in segments.  Back through a segment the gradient of the state goes by
-// D -> M^T D + N', so one set of transitions serves both ways.
+// D -> M^T D + N', so one set of transitions serves both ways, in one bf16
+// part as the walks that go on from them (the joins between are float32).
 // starts [segments - 1][BH][dk, dv] as above; back [segments - 1]: D behind
 // segment segments - 2 first; units [segments - 2][BH][dk, dk].
 struct DeltaBackSegments {
@@ -1450,6 +1469,8 @@ delta_walks_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __gr
 //   dq = scale e^G (dO S^T) + A K
 //   dk = -e^G (dV S^T) + e^{G_L - G} (X D^T) + A^T Q + (B + B^T) K
 //   dbeta = (dv . x) / b^2;  dg as in delta_simt.cu.
+// dV is read as it left, in bf16, so that it is written once; A and B are
+// rounded as operands, but E, from which dg is summed, takes them before that.
 // A chunk's 64 rows fill half of a tcgen05 tile, so two operands share one:
 // rows 0-63 belong to the queries (dO, Q, A), rows 64-127 to the keys
 // (dV, K, B), and a thread of the epilogue owns a row of dq or of dk:

@@ -27,3 +27,7 @@ from .delta import (  # noqa: F401,E402
     residual_norm,
     residual_norm_backward,
 )
+from .delta_chunks import (  # noqa: F401,E402
+    delta_chunks,
+    delta_chunks_backward,
+)

@@ -1,0 +1,101 @@
+"""The tensor-core path's bf16 roundings: no more of them than documented.
+
+The oracle's chunk form (oracle/delta_chunks.py) makes exactly the documented
+roundings, in float64 between them.  Kernel and oracle are each compared with
+the definition, and the kernel may not be further from it, for any (batch,
+head), than the oracle is.
+
+How close the two errors are: a kernel's float32 noise puts a value on the
+other side of a border between two bf16 numbers only where it is about as far
+from both, so its error keeps its size.  An error over a (batch, head) is then
+a norm of N independent roundings of given sizes, N at least 64 for each token
+(a row of X, of dV, of P or A, of the result; for dg and dbeta one number a
+token).  Even if all of them were drawn anew, the ratio of two such norms has
+a standard deviation of at most 1 / sqrt(N); the bound is three of them.  A
+further rounding of a main operand, 1.5e-3 and more of its output beside 2.4e-3
+to 3.1e-3, raises the error by 11 % and more; 64 tokens allow 4.7 %.
+Short enough for walks of whole sequences: 11 chunks."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from helpers import record
+from test_delta_gpu import bound, done, err, make, rn, states  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [  # n, Hk, H, dk, dv, lengths
+    (704, 2, 2, 128, 128, [704, 500]), (300, 1, 3, 64, 256, [300, 0, 129]),
+    (321, 1, 2, 128, 64, [64, 321]), (448, 2, 4, 64, 64, [447, 300]),
+]
+
+
+def ragged(seed, n, Hk, H, dk, dv, lens, dtype="bf16", decay=0.2):
+    x, ref = make(seed, len(lens), n, Hk, H, dk, dv, dtype, decay)
+    for t, r in zip(x, ref):
+        for b, c in enumerate(lens):
+            t[b, c:] = float("nan")
+            r[b, c:] = 0.0
+    return x, ref, torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def per_head(x):
+    """dg, dbeta [B, n, H] with their tokens as the values of a (batch, head)"""
+    return x[..., None] if x.ndim == 3 else x
+
+
+def no_further(got, rounded, want, lens, what):
+    """Both against want, [B, n, heads, d] (a key head's gradients by key heads)
+    or [B, n, heads]."""
+    got = per_head(got.double().cpu().numpy())
+    rounded, want = per_head(rounded), per_head(want)
+    assert np.isfinite(got).all() and got.shape == rounded.shape == want.shape
+    for b, tokens in enumerate(lens):
+        assert not got[b, tokens:].any()
+        for h in range(got.shape[2] if tokens else 0):
+            size = np.linalg.norm(want[b, :, h])
+            mine, theirs = (np.linalg.norm(x[b, :, h] - want[b, :, h]) / size for x in (got, rounded))
+            record(mine, what)
+            record(mine / theirs, what + " / rounded oracle")
+            values = tokens * (64 if want.shape[3] > 1 else 1)
+            assert mine < (1 + 3 / np.sqrt(values)) * theirs, (what, b, h)
+
+
+@pytest.mark.parametrize("decay", [0.2, 0.02])
+@pytest.mark.parametrize("n,Hk,H,dk,dv,lens", SHAPES)
+def test_prefill(rn, n, Hk, H, dk, dv, lens, decay):
+    x, ref, lengths = ragged(60 + n, n, Hk, H, dk, dv, lens, decay=decay)
+    S, S0 = states(61, len(lens), H, dk, dv)
+    want, _ = oracle.delta_recurrent(*ref[:5], dk ** -0.5, S0, lens)
+    for final in (False, True):
+        end = torch.empty_like(S) if final else None
+        out = rn.retnet_delta_chunkwise(*x[:5], lengths=lengths, state_in=S, state_out=end, algo="tensor")
+        done(rn)
+        o, _ = oracle.delta_chunks(*ref[:5], dk ** -0.5, S0, lens, final_state=final)
+        no_further(out, o, want, lens, "out")
+
+
+@pytest.mark.parametrize("decay", [0.2, 0.02])
+@pytest.mark.parametrize("n,Hk,H,dk,dv,lens", SHAPES)
+def test_backward(rn, n, Hk, H, dk, dv, lens, decay):
+    x, ref, lengths = ragged(62 + n, n, Hk, H, dk, dv, lens, decay=decay)
+    got = rn.retnet_delta_backward(*x, lengths=lengths, algo="tensor")
+    done(rn)
+    rounded = oracle.delta_chunks_backward(*ref, dk ** -0.5, lens)
+    want = oracle.delta_backward(*ref, dk ** -0.5, lens)
+    for name, a, r, w in zip(("dq", "dk", "dv", "dg", "dbeta"), got, rounded, want):
+        no_further(a, r, w, lens, name)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,Hk,H,dk,dv,lens", SHAPES + [(150, 1, 2, 256, 64, [150, 77]),
+                                                        (1100, 1, 1, 128, 64, [1100, 300, 640])])
+def test_gates_gradients_of_every_head(rn, dtype, n, Hk, H, dk, dv, lens):
+    """In float32 arithmetic, for each (batch, head) by itself: with 64 tokens
+    and more, a head's dg and dbeta together have the size of their terms."""
+    x, ref, lengths = ragged(64 + n, n, Hk, H, dk, dv, lens, dtype)
+    got = rn.retnet_delta_backward(*x, lengths=lengths, algo="simt")[3:]
+    done(rn)
+    for a, w in zip(got, oracle.delta_backward(*ref, dk ** -0.5, lens)[3:]):
+        assert err(per_head(a), per_head(w)) < bound(dtype)
