@@ -419,8 +419,13 @@ RETNET_API retnet_status retnet_delta_recurrent(const void *q, const void *k, co
  * state and x are rounded to bf16 (together with the result's rounding 2.9e-3
  * of the norm, up to 4.4e-3 with decays near 0 over thousands of tokens; the
  * result's alone is 1.7e-3, which is all that SIMT has); a final state keeps
- * float32 accuracy.  out must not overlap the inputs, the states or the
- * workspace.
+ * float32 accuracy.  Equal calls give equal bits, whatever the workspace
+ * held.  Between calls that differ the bits of a sequence's `out` may differ,
+ * inside these roundings: with state_out operands go in two bf16 parts; which
+ * path AUTO takes for up to 16 tokens, and whether and where a long sequence is
+ * cut into segments (on either path), follow from batch, heads, seqlen, dk, dv
+ * and state_out.  The recurrent form and SIMT give a sequence the same bits in
+ * any batch.  out must not overlap the inputs, the states or the workspace.
  *   workspace  retnet_delta_workspace_size() bytes, 1024-byte aligned.  They
  *              follow from the whole shape and need not grow with seqlen:
  *              for one workspace over several lengths take the largest.

@@ -689,7 +689,9 @@ def retnet_delta_chunkwise(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
                            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gated delta rule, prefill (tensors as for retnet_delta_recurrent).
     state_in / state_out: float32 [batch, heads, dk, dv] states before the
-    first and after the last token.  `workspace` (uint8 CUDA tensor) is
+    first and after the last token.  Equal calls give equal bits; asking for a
+    state, or another batch, may change those of a sequence's out inside its
+    roundings (algo="simt" does not).  `workspace` (uint8 CUDA tensor) is
     allocated here when not supplied.  Returns out."""
     shape, index = _delta_shape(q, k, v, g, beta, lengths)
     sshape = (shape.batch, shape.heads, shape.dk, shape.dv)

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle
-from test_delta_gpu import bound, done, err, make, rn, states  # noqa: F401
+from test_delta_gpu import DT, bound, done, err, make, rn, states  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -153,3 +153,47 @@ def test_a_query_that_is_not_finite_spoils_its_own_output_alone(rn, dtype, algo)
     assert torch.isnan(out[0, at]).all()
     out[0, at] = clean[0, at]
     assert torch.equal(out, clean)
+
+
+# ------------------------------------------------------------------ what the bits follow from
+@pytest.mark.parametrize("dtype,B,n,Hk,H,dk,dv", [("bf16", 2, 200, 1, 2, 128, 128),
+                                                  ("bf16", 1, 2000, 1, 1, 64, 256),
+                                                  ("f32", 1, 1500, 1, 2, 128, 64)])
+def test_equal_calls_give_equal_bits_whatever_the_workspace_held(rn, dtype, B, n, Hk, H, dk, dv):
+    """Whole walks and walks in segments; workspaces of zeros, of NaN (all
+    bits set) and of large numbers."""
+    x, _ = make(65, B, n, Hk, H, dk, dv, dtype)
+    lengths = torch.tensor([n - 70, n][-B:], dtype=torch.int32, device="cuda")
+    shape = (B, H, Hk, n, dk, dv, DT[dtype])
+    room = [rn.retnet_workspace(size(*shape), "cuda") for size in (
+        rn.retnet_delta_workspace_size, rn.retnet_delta_backward_workspace_size)]
+    seen = []
+    for fill in (0x00, 0xFF, 0x7E):
+        for ws in room:
+            ws.fill_(fill)
+        S = torch.full((B, H, dk, dv), float("nan"), device="cuda")
+        seen.append((rn.retnet_delta_chunkwise(*x[:5], lengths=lengths, state_out=S, workspace=room[0]),
+                     rn.retnet_delta_chunkwise(*x[:5], lengths=lengths, workspace=room[0].fill_(fill)), S,
+                     *rn.retnet_delta_backward(*x, lengths=lengths, workspace=room[1])))
+    done(rn)
+    for a, *others in zip(*seen):
+        assert torch.isfinite(a).all() and all(torch.equal(a, b) for b in others)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_recurrent_forms_give_a_sequence_the_same_bits_in_any_batch(rn, dtype):
+    B, n, H, dk, dv = 5, 90, 2, 128, 64
+    x, _ = make(66, B, n, H, H, dk, dv, dtype)
+    S, _ = states(67, B, H, dk, dv)
+    many = S.clone()
+    one = torch.empty_like(S)
+    out = rn.retnet_delta_recurrent(*x[:5], many)
+    simt = rn.retnet_delta_chunkwise(*x[:5], state_in=S, state_out=one, algo="simt")
+    for b in range(B):
+        alone, s = [t[b:b + 1] for t in x[:5]], S[b:b + 1].clone()
+        assert torch.equal(rn.retnet_delta_recurrent(*alone, s), out[b:b + 1])
+        assert torch.equal(s, many[b:b + 1])
+        assert torch.equal(rn.retnet_delta_chunkwise(*alone, state_in=S[b:b + 1], algo="simt"),
+                           simt[b:b + 1])
+    assert torch.equal(simt, out) and torch.equal(one, many)
+    done(rn)
