@@ -8,12 +8,18 @@
 //   dx  = dh + r_h (t - h^ mean(t h^)),  t = dn pre,       dpre  = sum_rows dn h^
 //   dg  = s dx z swish'(g),  dz = s dx swish(g),           dpost = sum_rows dz y^
 //   dy  = r_y (u - y^ mean(u y^)),       u = dz post.
-// Every row is read once and written once: an HBM stream of 5 tensors
-// forward (x, y, g; h, n) and 8 backward (x, y, g, dh, dn; dx, dy, dg).  A
-// row stays in the registers of the threads that own it (vectors of 8
-// channels, up to 4 each forward and 2 backward), so the two (three) sums over the row cost
-// shuffles and one barrier each and nothing is read twice; h is formed from
-// x, y and g again in the backward, which reads no more than a stored h would.
+// Every row comes from HBM once and is written once: a stream of 5 tensors
+// forward (x, y, g; h, n) and 8 backward (x, y, g, dh, dn; dx, dy, dg); h is
+// formed from x, y and g again in the backward, which reads no more than a
+// stored h would.
+// Forward a row stays in the registers of the threads that own it (up to 4
+// vectors of 8 channels each), so that nothing is read twice and its two sums
+// cost shuffles and one barrier each.  Backward a thread owns up to 2 vectors
+// and keeps h; the other tensors are read again in each of the three passes
+// over the row (y in up to four, dn and g in two), from the copies in shared
+// memory or, where there are none (float32, and bf16 above 8192 channels),
+// through L1 and L2.  Its sums share two barriers a row: h^2 with t h, and u y^
+// with the next row's y^2.
 #include "kernels.h"
 #include "pairs.cuh"
 
