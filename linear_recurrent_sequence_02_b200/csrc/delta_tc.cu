@@ -159,10 +159,13 @@ __device__ __forceinline__ void keep_row(__nv_bfloat16 *kept, size_t chunk, int 
 
 // ------------------------------------------------------------------ prep
 // One CTA of eight warps per chunk of a (sequence, value head): the products
-// by mma.sync (a 64 x 64 x dk product has too few rows to fill a tcgen05
-// tile, and a grid of thousands of chunks hides its latency), the inverse in
-// float32: four 16 x 16 triangles by substitution, a column a lane, then the
-// squares below them by products, 16 and then 32 rows at a time.
+// by mma.sync, whose accumulators are in the registers that apply the decays
+// and split the results; the inverse in float32: four 16 x 16 triangles by
+// substitution, a column a lane, then the squares below them by products, 16
+// and then 32 rows at a time.  69 us for 2048 chunks of 128 x 256, of which
+// its copies take 33; what bounds it is half the issue slots and its barriers.
+// [Q; K] K^T as one tcgen05 product of 128 rows, as delta_grad_tc_kernel forms
+// it, and CTAs that stay for several chunks have not been built here.
 // The chunk's block is put together in shared memory, K and Q first where W
 // and Q~ replace them, and leaves by one copy.
 // Decays e^{G_i - G_j}: of rows and columns in different 16-row blocks as
