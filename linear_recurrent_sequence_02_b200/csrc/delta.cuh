@@ -15,11 +15,11 @@ __device__ __forceinline__ int delta_tokens_of(const int *lengths, int b, int se
     return lengths ? min(max(lengths[b], 0), seqlen) : seqlen;
 }
 
-// x is linear in b, and dbeta is (gradient of x) . x / b.  Where b is 0 the
-// backward takes a b of this size instead: x keeps all its digits, the
-// quotient is the limit, and what it writes to the state is nothing beside it.
-constexpr float kBetaFloor = 1e-15f;
-__device__ __forceinline__ float nonzero_beta(float b) { return fabsf(b) < kBetaFloor ? kBetaFloor : b; }
+// Tokens that write nothing: b of 0, or too small for quotients by it.  dbeta
+// is (gradient of x) . (v - k S), which for the others is taken from x as
+// (gradient of x) . x / b; for these x is 0, whatever v and k hold, and the
+// backward forms v - k S beside it.
+__device__ __forceinline__ bool writes_nothing(float b) { return fabsf(b) < 1e-15f; }
 
 // g where sums of it are formed: e^g is 0 in float32 from here on, and
 // differences of sums stay finite when g is -inf.

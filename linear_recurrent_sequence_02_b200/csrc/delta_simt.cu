@@ -270,7 +270,8 @@ struct DeltaSpan {
     bool unit;
 };
 // v: the values (forward) or the output's gradient (reverse).
-// save: x (kSweepSave) or r (kSweepReverse), float32 [B, n, H, dv];
+// save: x (kSweepSave; v - k S of tokens that write nothing) or r
+// (kSweepReverse), float32 [B, n, H, dv];
 // marks: the state before (D behind) every chunk of kDeltaChunk tokens,
 // float32 [B, H, chunks, dk, dv].
 template <typename T, int DK, DeltaSweep kSweep>
@@ -357,8 +358,7 @@ __device__ __forceinline__ void delta_walk(const T *__restrict__ q, const T *__r
             }
             const float2 v0 = unit ? both(0.f) : make_float2(to_f32(ahead[u].v[0]), to_f32(ahead[u].v[1]));
             const float2 v1 = unit ? both(0.f) : make_float2(to_f32(ahead[u].v[2]), to_f32(ahead[u].v[3]));
-            const float a = expf(to_f32(ahead[u].g)), bt0 = to_f32(ahead[u].b);
-            const float bt = kSweep == kSweepSave ? nonzero_beta(bt0) : bt0;
+            const float a = expf(to_f32(ahead[u].g)), bt = to_f32(ahead[u].b);
             load(ahead[u], step + kWalkAhead < n);
             if (kKeep) {
                 const int t = kRev ? end - 1 - step : begin + step;
@@ -412,12 +412,17 @@ __device__ __forceinline__ void delta_walk(const T *__restrict__ q, const T *__r
                     s[i][1] = mul2(both(a), fma2(both(wk[i]), b1, fma2(both(wq[i]), o1, s[i][1])));
                 }
             } else {
-                x0 = mul2(both(bt), fma2(both(-a), y0, v0));
-                x1 = mul2(both(bt), fma2(both(-a), y1, v1));
+                const float2 u0 = fma2(both(-a), y0, v0), u1 = fma2(both(-a), y1, v1);
+                x0 = mul2(both(bt), u0);
+                x1 = mul2(both(bt), u1);
 #pragma unroll
                 for (int i = 0; i < RPL; ++i) {
                     s[i][0] = fma2(both(wk[i]), x0, mul2(both(a), s[i][0]));
                     s[i][1] = fma2(both(wk[i]), x1, mul2(both(a), s[i][1]));
+                }
+                if (kSweep == kSweepSave && writes_nothing(bt)) {
+                    x0 = u0;                         // v - k S is kept in the place of x
+                    x1 = u1;
                 }
             }
             if (kFwd) {
@@ -588,7 +593,8 @@ delta_sweeps_segments_kernel(const T *__restrict__ q, const T *__restrict__ k,
 //   B_ij = -b_i (r_i . x_j) e^{G_i - G_j},    i > j
 //   dq = scale e^G (do S^T) + A K
 //   dk = e^{G_L - G} (X D^T) - b e^G (R S^T) + A^T Q + (B + B^T) K
-//   dv = b R,   dbeta = R . X / b
+//   dv = b R,   dbeta = R . X / b  (R . X of tokens that write nothing: the
+//   walk has left v - k S in X for them, which A, B and dk leave out)
 // dg_t is the sum of everything that crosses token t, each term formed once
 // and added to the tokens it crosses: the pairs E = A (.) QK^T + B (.) KK^T
 // with j < t <= i (rows minus columns of E summed from t on: the same float
@@ -755,8 +761,9 @@ delta_grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
             if (ri >= cj && ri < cnt)
                 dec = expf(ri / 16 == cj / 16 ? m.G.within(ri, cj)
                                               : m.G.until(cj, ri / 16 - 1) + (m.G.in[ri].x + m.G.in[ri].y));
-            const float va = scale * dec * pa[i][l];
-            const float vb = ri > cj ? -m.beta[ri] * dec * pb[i][l] : 0.f;
+            const bool none = writes_nothing(m.beta[cj]);
+            const float va = none ? 0.f : scale * dec * pa[i][l];
+            const float vb = ri > cj && !none ? -m.beta[ri] * dec * pb[i][l] : 0.f;
             m.A[ri][cj] = va;
             m.B[ri][cj] = vb;
             fq[i][l] = ri == cj ? 0.f : fmaf(va, fq[i][l], vb * fk[i][l]);   // E off the diagonal
@@ -814,7 +821,7 @@ delta_grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
                 const int cj = c0 + 16 * l;
                 aq[i][l] *= scale * e;
                 ar[i][l] *= -bt * e;
-                ax[i][l] *= rest;
+                ax[i][l] = writes_nothing(bt) ? 0.f : ax[i][l] * rest;
                 inter = fmaf(m.Qs[ri][cj], aq[i][l], inter);
                 inter = fmaf(m.Ks[ri][cj], ar[i][l], inter);
                 ahead = fmaf(m.Ks[ri][cj], ax[i][l], ahead);
@@ -882,7 +889,7 @@ delta_grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
         for (int i = cnt - 1; i >= tid; --i) s += (m.rowsum[i] - m.colsum[i]) + m.inter[i];
         for (int i = 0; i < tid; ++i) s += m.ahead[i];
         dg[(row0 + tid) * heads + h] = from_f32<T>(s);
-        dbeta[(row0 + tid) * heads + h] = from_f32<T>(m.db[tid] / nonzero_beta(m.beta[tid]));
+        dbeta[(row0 + tid) * heads + h] = from_f32<T>(writes_nothing(m.beta[tid]) ? m.db[tid] : m.db[tid] / m.beta[tid]);
     }
 }
 

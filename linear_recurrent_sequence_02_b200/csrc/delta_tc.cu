@@ -68,7 +68,9 @@ struct DeltaBlock {
     static constexpr uint32_t kTlo = kBox64;
     static constexpr uint32_t kW = kSplit ? 2 * kBox64 : kBox64;
     static constexpr uint32_t kWlo = kW + kKB * kBox64;
-    // float rest[64] = e^{G_L - G}, then e^{G_L}; a walk without output stops here
+    // float rest[64] = e^{G_L - G}, then e^{G_L}; a walk without output stops
+    // here.  Of the backward: whether any token writes nothing, at 65, and
+    // which do, at 128.
     static constexpr uint32_t kHdr = kSplit ? kWlo + kKB * kBox64 : kWlo;
     static constexpr uint32_t kQ = kHdr + 1024;
     static constexpr uint32_t kP = kQ + kKB * kBox64;
@@ -130,6 +132,14 @@ __device__ __forceinline__ void clear_rows(uint8_t *box, int boxes, int cnt, int
     fence_async_shared();
     __syncwarp();
 }
+// Rows of the tokens that write nothing (flags[row] != 0) as zeros, likewise.
+__device__ __forceinline__ void clear_flagged(uint8_t *box, int boxes, const float *flags, int lane) {
+    for (int r = 0; r < kC; ++r)
+        if (flags[r] != 0.f && lane < 8 * boxes)
+            *reinterpret_cast<uint4 *>(box + (lane / 8) * kBox64 + r * 128 + (lane % 8) * 16) = make_uint4(0, 0, 0, 0);
+    fence_async_shared();
+    __syncwarp();
+}
 // 64 tokens of a v channel's accumulator into a tile of token rows (two
 // boxes of 64 channels), bf16: col is the channel in the tile.
 __device__ __forceinline__ void put_channel(uint8_t *tile, int col, const uint32_t (&o)[2][32]) {
@@ -179,7 +189,8 @@ struct DeltaPrepSmem {
     uint8_t block[DeltaBlock<DK, kSplit>::kBytes];
     float M[kC][kMPad];                    // M, then T in its place
     DecaySums G;
-    float beta[kC], e[kC], in[kC];         // e^G; e^{G_i - G_r}
+    float beta[kC], own[kC];               // b; 1 where a token of the backward writes nothing
+    float e[kC], in[kC];                   // e^G; e^{G_i - G_r}
     float across[3][kC];                   // [block - 1][j]: e^{G_r - G_j}
     float diag[kC][20];                    // [i][j - r - 1]: e^{G_i - G_j} in a block, 0 above
 };
@@ -321,15 +332,18 @@ delta_prep_kernel(DeltaPrepArgs a) {
             const float hi = lane + 32 < cnt ? log_decay(to_f32(a.g[at + (size_t)(lane + 32) * a.heads])) : 0.f;
             sum_decays(m.G, lane, lo, hi);
         } else if (warp == 1) {
+            float *hdr = reinterpret_cast<float *>(m.block + Block::kHdr);
+            unsigned any = 0;
 #pragma unroll
             for (int i = lane; i < kC; i += 32) {
-                float bt = 0.f;
-                if (i < cnt) {
-                    bt = to_f32(a.beta[(row0 + i) * a.heads + h]);
-                    if (a.backward) bt = nonzero_beta(bt);
-                }
-                m.beta[i] = bt;
+                const float bt = i < cnt ? to_f32(a.beta[(row0 + i) * a.heads + h]) : 0.f;
+                const bool none = a.backward && i < cnt && writes_nothing(bt);
+                m.beta[i] = none ? 0.f : bt;
+                m.own[i] = none ? 1.f : bt;
+                hdr[128 + i] = none ? 1.f : 0.f;
+                any |= __ballot_sync(0xffffffffu, none);
             }
+            if (lane == 0) hdr[65] = any ? 1.f : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < kEach; ++u) {
@@ -426,7 +440,10 @@ delta_prep_kernel(DeltaPrepArgs a) {
         __syncthreads();
     }
     // T^ = T diag(b) in its tiles; W = T^ diag(e^G) K in two parts of T^, K
-    // being exact: warp w the rows 16 (w % 4) and a half of the columns
+    // being exact: warp w the rows 16 (w % 4) and a half of the columns.
+    // Where a token of the backward writes nothing, T^ has T itself in the
+    // tiles: dV = T^^T dX is then the gradient of x, and the forward walk
+    // meets a row of zeros there instead of V's.
     {
         constexpr int kTiles = DK / 16;                    // of 8 columns
         const int rb = warp & 3, half = warp >> 2, r = 16 * rb + gr;
@@ -444,7 +461,8 @@ delta_prep_kernel(DeltaPrepArgs a) {
                     const float t0 = t.x * bt.x, t1 = t.y * bt.y;
                     if (half == 0) {
                         uint32_t th, tl;
-                        split_pair(t0, t1, th, tl);
+                        const float2 own = *reinterpret_cast<const float2 *>(&m.own[j]);
+                        split_pair(t.x * own.x, t.y * own.y, th, tl);
                         *reinterpret_cast<uint32_t *>(m.block + Block::kT + tile_off(i, j)) = th;
                         if (kSplit) *reinterpret_cast<uint32_t *>(m.block + Block::kTlo + tile_off(i, j)) = tl;
                     }
@@ -669,6 +687,10 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
             const uint64_t mnmaj = smem_desc_sw128(smem_u32(st), kBox64, 1024);
             if (!warp_spin_wait(&bar.full[s], (c >> 1) & 1, abort_flag, err)) break;
             if (n - c * kC < kC) clear_rows(st + Smem::kK, DK / 64 + 2, n - c * kC, lane);
+            if (kSave && !w.unit) {
+                const float *hdr = reinterpret_cast<const float *>(st + Block::kHdr);
+                if (hdr[65] != 0.f) clear_flagged(st + Smem::kV, 2, hdr + 128, lane);
+            }
             tc_fence_after();
             if (!w.unit && elect_one()) {
 #pragma unroll
@@ -1472,6 +1494,9 @@ delta_walks_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __gr
 //   dq = scale e^G (dO S^T) + A K
 //   dk = -e^G (dV S^T) + e^{G_L - G} (X D^T) + A^T Q + (B + B^T) K
 //   dbeta = (dv . x) / b^2;  dg as in delta_simt.cu.
+// Of a token that writes nothing x is 0 and dV the gradient of x, r, which B
+// and dk leave out (b r is 0); dbeta = r . (v - k S before it), of which
+// r . k S are that row's sums of E and of k (r S^T) (S.none), and dv is 0.
 // dV is read as it left, in bf16, so that it is written once; A and B are
 // rounded as operands, but E, from which dg is summed, takes them before that.
 // A chunk's 64 rows fill half of a tcgen05 tile, so two operands share one:
@@ -1502,6 +1527,7 @@ struct DeltaGradTcBars {
         float row[2][2][kC];               // of E: [queries, keys][column half]
         float col[8][32];                  // by warp: its column half
         float inter[2][2][kC], ahead[2][kC], db[kC], sd[8];
+        float none[2][kC];                 // [column half]: - r . k S, where nothing is written
     } sum[2];
     float decay[kC][kC + 1];                               // e^{G_i - G_j}, i >= j
 };
@@ -1528,7 +1554,7 @@ struct DeltaGradTcSmem {
 };
 
 struct DeltaGradTcArgs {
-    const __nv_bfloat16 *g, *beta, *x, *s, *d;             // X^T, S^T, D^T of every chunk
+    const __nv_bfloat16 *v, *g, *beta, *x, *s, *d;         // X^T, S^T, D^T of every chunk
     const int *lengths;
     __nv_bfloat16 *dq, *dk_, *dv_, *dg, *dbeta;
     float *dq_wide, *dk_wide;
@@ -1747,7 +1773,8 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 for (int v = 0; v < 2; ++v) {
                     const int t = lane + 32 * v;
                     g[v] = t < w.cnt ? log_decay(to_f32(a.g[at + (size_t)t * a.heads])) : 0.f;
-                    bt[v] = t < w.cnt ? nonzero_beta(to_f32(a.beta[at + (size_t)t * a.heads])) : 1.f;
+                    bt[v] = t < w.cnt ? to_f32(a.beta[at + (size_t)t * a.heads]) : 1.f;
+                    if (writes_nothing(bt[v])) bt[v] = 0.f;
                 }
                 sum_decays(G.G, lane, g[0], g[1]);
                 __syncwarp();
@@ -1825,17 +1852,25 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     const size_t r = (row0 + t) * a.heads + w.h;
                     const float dg = s + back[v] + (front[v] - own[v]);
                     a.dg[r] = from_f32<__nv_bfloat16>(t < w.cnt ? dg : 0.f);
-                    a.dbeta[r] = from_f32<__nv_bfloat16>(t < w.cnt ? S.db[t] / (G.beta[t] * G.beta[t]) : 0.f);
+                    if (G.beta[t] != 0.f)
+                        a.dbeta[r] = from_f32<__nv_bfloat16>(t < w.cnt ? S.db[t] / (G.beta[t] * G.beta[t]) : 0.f);
                 }
             }
-            // where b counts as 0 (nonzero_beta), v has no part in x: what dV held
-            // for dbeta's sake, and this CTA alone has read, goes
+            // tokens that write nothing: r lies in dV, which only this CTA has read
 #pragma unroll
             for (int v = 0; v < 2; ++v)
-                for (unsigned none = __ballot_sync(0xffffffffu, G.beta[lane + 32 * v] == kBetaFloor); none; none &= none - 1) {
-                    const int t = 32 * v + __ffs(none) - 1;
-                    __nv_bfloat16 *row = a.dv_ + ((row0 + t) * a.heads + w.h) * a.dv;
-                    for (int j = lane; j < a.dv; j += 32) row[j] = from_f32<__nv_bfloat16>(0.f);
+                for (unsigned left = __ballot_sync(0xffffffffu, G.beta[lane + 32 * v] == 0.f); left; left &= left - 1) {
+                    const int t = 32 * v + __ffs(left) - 1;
+                    const size_t r = (row0 + t) * a.heads + w.h;
+                    __nv_bfloat16 *dv = a.dv_ + r * a.dv;
+                    float d = 0.f;
+                    for (int j = lane; j < a.dv; j += 32) {
+                        d = fmaf(to_f32(dv[j]), to_f32(a.v[r * a.dv + j]), d);
+                        dv[j] = from_f32<__nv_bfloat16>(0.f);
+                    }
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+                    if (lane == 0) a.dbeta[r] = from_f32<__nv_bfloat16>(d + (S.none[0][t] + S.none[1][t]));
                 }
             __syncwarp();
             prepare();                                     // this item's turn is free
@@ -1908,6 +1943,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 tmem_ld32(tl + kPk + 32 * hf, pk);
                 tmem_wait_ld();
                 const float f = key ? -1.f : a.scale;
+                const bool none = key && G.beta[i] == 0.f;
                 float e[32], rs = 0.f, mid = 0.f;
                 uint8_t *tile = smem + (key ? Smem::kB : Smem::kA);
 #pragma unroll
@@ -1925,6 +1961,15 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         rs += e[jl];
                     }
                     store8(reinterpret_cast<__nv_bfloat16 *>(tile + tile_off(i, 32 * hf + 8 * j8)), w8);
+                }
+                if (none) {
+                    S.none[hf][i] = rs;
+                    rs = 0.f;
+#pragma unroll
+                    for (int j8 = 0; j8 < 4; ++j8)
+                        *reinterpret_cast<uint4 *>(tile + tile_off(i, 32 * hf + 8 * j8)) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) e[j] = 0.f;
                 }
                 fence_async_shared();
                 tc_fence_before();
@@ -1951,7 +1996,8 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             ok = ok && warp_spin_wait(&m.c_full, n & 1, abort_flag, err);
             if (ok) {
                 tc_fence_after();
-                const float f1 = key ? -G.e[i] : a.scale * G.e[i], f2 = G.rest[i];
+                const bool none = key && G.beta[i] == 0.f;
+                const float f0 = key ? -G.e[i] : a.scale * G.e[i], f1 = none ? 0.f : f0, f2 = G.rest[i];
                 uint8_t *mine = ks + (key ? Smem::kK : Smem::kQ);
                 float2 inter = both(0.f), ahead = both(0.f);
                 float *wide = (key ? a.dk_wide : a.dq_wide) + ((row0 + i) * a.heads + w.h) * (size_t)DK;
@@ -1973,9 +2019,9 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         for (int jj = 0; jj < 4; ++jj) {
                             const int j = 4 * j8 + jj;
                             const float2 o2 = as_pair(own[jj] << 16, own[jj] & 0xffff0000u);
-                            const float2 z = mul2(both(f1), as_pair(c1[2 * j], c1[2 * j + 1]));
+                            const float2 z = as_pair(c1[2 * j], c1[2 * j + 1]);
                             inter = fma2(o2, z, inter);
-                            r[j] = add2(z, as_pair(c3[2 * j], c3[2 * j + 1]));
+                            r[j] = fma2(both(f1), z, as_pair(c3[2 * j], c3[2 * j + 1]));
                             if (key) {
                                 const float2 x = mul2(both(f2), as_pair(c2[2 * j], c2[2 * j + 1]));
                                 ahead = fma2(o2, x, ahead);
@@ -2011,7 +2057,8 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         }
                     }
                 }
-                S.inter[key][hf][i] = in ? inter.x + inter.y : 0.f;
+                S.inter[key][hf][i] = in ? f1 * (inter.x + inter.y) : 0.f;
+                if (none) S.none[hf][i] += f0 * (inter.x + inter.y);
                 if (key) S.ahead[hf][i] = in ? ahead.x + ahead.y : 0.f;
                 fence_async_shared();
                 warp_arrive(&m.done[n & 1]);
@@ -2265,7 +2312,7 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
         e = cudaFuncSetAttribute(delta_grad_tc_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Smem::kBytes);
         if (e != cudaSuccess) return e;
-        DeltaGradTcArgs g = {(const __nv_bfloat16 *)a.g, (const __nv_bfloat16 *)a.beta, xs, ss, ds, a.lengths,
+        DeltaGradTcArgs g = {(const __nv_bfloat16 *)a.v, (const __nv_bfloat16 *)a.g, (const __nv_bfloat16 *)a.beta, xs, ss, ds, a.lengths,
                              (__nv_bfloat16 *)a.dq, (__nv_bfloat16 *)a.dk_grad,
                              (__nv_bfloat16 *)a.dv_grad, (__nv_bfloat16 *)a.dg,
                              (__nv_bfloat16 *)a.dbeta, dq_wide, dk_wide, a.scale, a.heads,

@@ -35,7 +35,7 @@ def bf16(x):
 class _Chunk:
     """What a chunk's products take of its tokens, for a (sequence, head)."""
 
-    def __init__(self, q, k, g, b, scale, rounds, two_parts, f):
+    def __init__(self, q, k, g, b, scale, rounds, two_parts, f, none=False):
         self.f, self.rounds, self.two = f, rounds, two_parts
         self.q, self.k, self.b, self.scale = q, k, b, f(scale)
         n = len(g)
@@ -46,9 +46,10 @@ class _Chunk:
         self.rest = self.decay[-1].copy()
         self.eL = self.e[-1]
         M = np.tril(k @ k.T, -1) * self.decay * b[:, None]
-        T = np.linalg.inv(np.eye(n, dtype=f) + M) * b
-        self.T, self.Tlo = self.part("T", T)
-        W = (T * self.e) @ k
+        T = np.linalg.inv(np.eye(n, dtype=f) + M)
+        # in the backward T itself where a token writes nothing (b of 0)
+        self.T, self.Tlo = self.part("T", T * np.where(none, f(1), b))
+        W = (T * b * self.e) @ k
         self.W, self.Wlo = self.part("W", W)
         self.Q = self.round("Q", q * (self.scale * self.e)[:, None])
         self.P = self.round("P", self.scale * (q @ k.T) * self.decay)
@@ -101,14 +102,16 @@ def delta_chunks_backward(q, k, v, g, beta, d_out, scale, lengths=None, rounds=A
     """Gradients (dq, dk, dv, dg, dbeta) of sum(o * d_out) without initial state."""
     f = dtype
     q, k, v, g, beta, d_out = (_f64(x).astype(f) for x in (q, k, v, g, beta, d_out))
-    beta = np.where(np.abs(beta) < 1e-15, f(1e-15), beta)
+    none = np.abs(beta) < 1e-15            # tokens that write nothing
+    beta = np.where(none, f(0), beta)
     dq, dk, dv_ = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
     dg, db = np.zeros_like(g), np.zeros_like(beta)
     for b, h, kh, chunks in _walks(q, k, v, g, beta, lengths):
         made, s = [], np.zeros((q.shape[-1], v.shape[-1]), f)
         for c in chunks:
-            w = _Chunk(q[b, c, kh], k[b, c, kh], g[b, c, h], beta[b, c, h], scale, rounds, False, f)
-            X, s, hi = w.step(s, v[b, c, h])
+            off = none[b, c, h]
+            w = _Chunk(q[b, c, kh], k[b, c, kh], g[b, c, h], beta[b, c, h], scale, rounds, False, f, off)
+            X, s, hi = w.step(s, np.where(off[:, None], f(0), v[b, c, h]))
             made.append((c, w, w.round("X", X), hi))
         D = np.zeros_like(s)
         for c, w, X, S in reversed(made):
@@ -118,20 +121,23 @@ def delta_chunks_backward(q, k, v, g, beta, d_out, scale, lengths=None, rounds=A
             hi = w.round("dX", dX)
             D = w.eL * D + w.Q.T @ do - w.W.T @ hi
             dV = w.round("dV", w.T.T @ (hi + w.round("dX", dX - hi)))
+            off = none[b, c, h][:, None]                   # there dV is the gradient of x
             A = w.scale * (do @ X.T) * w.decay
             B = -np.tril(dV @ X.T, -1) * w.decay
-            E = np.tril(A * (w.q @ w.k.T) + B * (w.k @ w.k.T), -1)
-            A, B = w.round("AB", A), w.round("AB", B)
             from_q = w.scale * w.e[:, None] * (do @ S.T)
             from_k = -w.e[:, None] * (dV @ S.T)
+            missed = (dV * v[b, c, h]).sum(1) + (w.k * from_k).sum(1) + (B * (w.k @ w.k.T)).sum(1)
+            B, from_k = np.where(off, 0.0, B), np.where(off, 0.0, from_k)
+            E = np.tril(A * (w.q @ w.k.T) + B * (w.k @ w.k.T), -1)
+            A, B = w.round("AB", A), w.round("AB", B)
             to_D = w.rest[:, None] * (X @ Dh.T)
             dq[b, c, kh] += from_q + A @ w.k
             dk[b, c, kh] += from_k + to_D + A.T @ w.q + (B + B.T) @ w.k
             inter = (w.q * from_q).sum(1) + (w.k * from_k).sum(1) + E.sum(1) - E.sum(0)
             ahead = (w.k * to_D).sum(1)
             dg[b, c, h] = np.cumsum(inter[::-1])[::-1] + np.cumsum(ahead) - ahead + w.eL * (S * Dh).sum()
-            db[b, c, h] = (dV * X).sum(1) / (w.b * w.b)
-            dv_[b, c, h] = np.where((w.b == f(1e-15))[:, None], 0.0, dV)
+            db[b, c, h] = np.where(off[:, 0], missed, (dV * X).sum(1) / np.where(off[:, 0], 1.0, w.b * w.b))
+            dv_[b, c, h] = np.where(off, 0.0, dV)
     if "grads" in rounds:
         dq, dk, dg, db = (bf16(x) for x in (dq, dk, dg, db))
     return dq, dk, dv_, dg, db

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import oracle
+from helpers import record
 from test_delta_gpu import DT, bound, done, err, make, rn, states  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -80,6 +81,43 @@ def test_values_of_tokens_that_write_nothing_have_no_gradient(rn, dtype, algo, H
             if want[2][b, :, h].any():
                 e = np.linalg.norm(got[2][b, :, h].double().cpu().numpy() - want[2][b, :, h])
                 assert e < bound(dtype, dtype == "bf16" and algo == "auto") * np.linalg.norm(want[2][b, :, h])
+
+
+@pytest.mark.parametrize("dtype,algo", [("bf16", "tensor"), ("bf16", "simt"), ("f32", "auto")])
+@pytest.mark.parametrize("n,Hk,H,dk,dv", [(200, 2, 2, 64, 64), (130, 1, 2, 128, 256), (1500, 1, 1, 128, 64)])
+def test_backward_past_tokens_that_write_nothing_whatever_they_hold(rn, dtype, algo, n, Hk, H, dk, dv):
+    """beta = 0 at tokens whose v (and, for some, k) is far beyond the others':
+    x is 0 there, so no other token's gradient sees it."""
+    B = 2
+    (q, k, v, g, beta, do), _ = make(68, B, n, Hk, H, dk, dv, dtype, decay=0.05)
+    rng = np.random.default_rng(69)
+    off = torch.from_numpy(rng.random((B, n)) < 0.2).cuda()
+    off[:, :3], off[:, 64:70] = torch.tensor([True, False, False], device="cuda"), True
+    beta[off] = 0.0
+    v[off] *= 1e30
+    k[off] *= 100.0
+    x = [q, k, v, g, beta, do]
+    got = rn.retnet_delta_backward(*x, algo=algo)
+    v2 = v.clone()
+    v2[off] = torch.finfo(v.dtype).min
+    lowest = rn.retnet_delta_backward(q, k, v2, g, beta, do, algo=algo)
+    done(rn)
+    tol = bound(dtype, dtype == "bf16" and algo == "tensor")
+    ref = [t.double().cpu().numpy() for t in x]
+    want = oracle.delta_backward(*ref, dk ** -0.5)
+    at = off.cpu().numpy()
+    for i, (name, a, b, w) in enumerate(zip(("dq", "dk", "dv", "dg", "dbeta"), got, lowest, want)):
+        if name != "dbeta":
+            assert torch.equal(a, b), name
+        for here in (at, ~at):
+            a_, w_ = a.double().cpu().numpy()[here], w[here]
+            assert np.isfinite(a_).all(), name
+            e, size = np.linalg.norm(a_ - w_), np.linalg.norm(w_)
+            if name in ("dk", "dv") and here is at:        # nothing is written: nothing to change
+                assert e == size == 0, name
+            else:
+                assert record(e / size, name) < tol, name
+    assert torch.equal(got[4][~off], lowest[4][~off])
 
 
 # ------------------------------------------------------------------ many sequences
