@@ -99,3 +99,24 @@ def test_gates_gradients_of_every_head(rn, dtype, n, Hk, H, dk, dv, lens):
     done(rn)
     for a, w in zip(got, oracle.delta_backward(*ref, dk ** -0.5, lens)[3:]):
         assert err(per_head(a), per_head(w)) < bound(dtype)
+
+
+@pytest.mark.parametrize("n,Hk,H,dk,dv,lens", [(2100, 1, 2, 128, 64, [2100, 700]), (2100, 1, 1, 128, 256, [64, 2100]),
+                                               (1800, 2, 2, 64, 128, [1800, 0, 1000])])
+def test_segments_for_every_head(rn, n, Hk, H, dk, dv, lens):
+    """Walks in segments, where a state has also passed a segment's transition
+    (one more S and X of the same sizes each way): at most twelve roundings of
+    a norm's 2^-8 / sqrt(3) each, were none of them weakened on its way,
+    sqrt(12 / 3) * 2^-8 = 7.8e-3, for each (batch, head) of 64 tokens or more."""
+    x, ref, lengths = ragged(70 + n, n, Hk, H, dk, dv, lens, decay=0.02)
+    out = rn.retnet_delta_chunkwise(*x[:5], lengths=lengths, algo="tensor")
+    end = torch.empty(len(lens), H, dk, dv, device="cuda")
+    with_state = rn.retnet_delta_chunkwise(*x[:5], lengths=lengths, state_out=end, algo="tensor")
+    got = rn.retnet_delta_backward(*x, lengths=lengths, algo="tensor")
+    done(rn)
+    o, _ = oracle.delta_recurrent(*ref[:5], dk ** -0.5, None, lens)
+    tol = 2 * 2.0 ** -8
+    assert err(out, o) < tol and err(with_state, o) < tol
+    for name, a, w in zip(("dq", "dk", "dv", "dg", "dbeta"), got,
+                          oracle.delta_backward(*ref, dk ** -0.5, lens)):
+        assert err(per_head(a), per_head(w)) < tol, name
