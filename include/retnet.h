@@ -443,8 +443,9 @@ RETNET_API retnet_status retnet_delta_chunkwise(const void *q, const void *k, co
 /* Gradients of the prefill without initial state (as for retention): given
  * d_out = dL/dout, writes dq, dk, dv, dg, dbeta, shaped and typed as q, k,
  * v, g, beta; a key head's dq and dk are the sums over its value heads, in
- * head order.  On the tensor-core path (bf16 with dk 64 or 128, but for SIMT)
- * the operands are rounded to bf16 as in the prefill, the states, the
+ * head order.  On the tensor-core path (bf16 with dk 64 or 128; AUTO takes it
+ * but for calls of at most 16 tokens and 256 in all sequences and heads) the
+ * operands are rounded to bf16 as in the prefill, the states, the
  * gradients of the states and x are kept in bf16, and dq, dk, dg and dbeta are
  * formed from dv as it leaves: 2.4e-3 to 4.9e-3 of a gradient's norm.  A beta
  * of less than 1e-15 in size counts as 0; dbeta is then the limit.  The gradients must not overlap the inputs or each other.

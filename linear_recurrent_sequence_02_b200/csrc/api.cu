@@ -189,10 +189,22 @@ static bool delta_tensor(const retnet_delta_shape *s, retnet_algo algo) {
 // about 0.4 us a token while the GPU has room for all columns at once, where
 // the chunks' two take 12 us and more (64 heads of 128, 16 tokens: 11.6
 // against 16.3 us, 32: 19.8 against 16.4; 512 heads, 8: 46 against 57, 16: 75
-// against 58).  The backward's chunks win at every length (20 against 25 us).
+// against 58).
 static bool delta_prefill_tensor(const retnet_delta_shape *s, retnet_algo algo) {
     const bool few = s->seqlen <= 16 &&
                      (long long)s->batch * s->heads * s->dv * s->seqlen <= (1 << 19);
+    return delta_tensor(s, algo) && !(algo == RETNET_ALGO_AUTO && few);
+}
+// A backward of a few tokens in all goes token by token in float32, though
+// that takes longer (16 heads of 128, 4 tokens: 62 against 25 us): dg and
+// dbeta are a dot product each, whose roundings on the tensor cores are
+// relative to its terms, and a handful of such sums may all come out near 0
+// beside them.  Drawn calls of up to 64 tokens whose dq, dk, dg or dbeta was
+// more than 5e-3 of its norm off there: 537 of 2492 with up to 16 tokens in all
+// sequences and heads, 224 of 5130 with up to 64, 28 of 7499 with up to 256,
+// none of 12058 with more.
+static bool delta_backward_tensor(const retnet_delta_shape *s, retnet_algo algo) {
+    const bool few = s->seqlen <= 16 && (long long)s->batch * s->heads * s->seqlen <= 256;
     return delta_tensor(s, algo) && !(algo == RETNET_ALGO_AUTO && few);
 }
 // A float32 prefill walks in segments, which need a workspace.
@@ -654,7 +666,7 @@ retnet_status retnet_delta_backward_workspace_size(const retnet_delta_shape *sha
     if (!bytes || !algo_ok(algo)) return RETNET_ERR_INVALID_ARG;
     retnet_status st = check_delta_shape(shape);
     if (st != RETNET_OK) return st;
-    const bool tensor = delta_tensor(shape, algo);
+    const bool tensor = delta_backward_tensor(shape, algo);
     if (algo == RETNET_ALGO_TENSOR && !tensor) return RETNET_ERR_UNSUPPORTED;
     *bytes = (tensor ? delta_backward_tc_workspace : delta_backward_simt_workspace)(
         shape->batch, shape->heads, shape->key_heads, shape->seqlen, shape->dk, shape->dv);
@@ -681,7 +693,7 @@ retnet_status retnet_delta_backward(const void *q, const void *k, const void *v,
         return RETNET_ERR_WORKSPACE;
     a.d_out = d_out;
     a.dq = dq; a.dk_grad = dk; a.dv_grad = dv; a.dg = dg; a.dbeta = dbeta;
-    if (delta_tensor(shape, algo))
+    if (delta_backward_tensor(shape, algo))
         RETNET_CUDA_TRY(launch_delta_backward_tc(a, workspace, (cudaStream_t)stream));
     else
         RETNET_CUDA_TRY(launch_delta_backward_simt(a, workspace, (cudaStream_t)stream));

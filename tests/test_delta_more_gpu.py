@@ -235,3 +235,19 @@ def test_recurrent_forms_give_a_sequence_the_same_bits_in_any_batch(rn, dtype):
                            simt[b:b + 1])
     assert torch.equal(simt, out) and torch.equal(one, many)
     done(rn)
+
+
+@pytest.mark.parametrize("B,n,Hk,H,dk,dv", [(4, 1, 1, 1, 128, 256), (1, 2, 1, 1, 64, 64), (2, 1, 1, 1, 128, 128),
+                                            (2, 3, 2, 4, 64, 128), (1, 16, 2, 16, 128, 64), (5, 4, 1, 3, 64, 256)])
+def test_backward_of_a_few_tokens_is_rounded_once(rn, B, n, Hk, H, dk, dv):
+    """A handful of dg and dbeta may all be near 0 beside their terms, so these
+    calls go in float32 arithmetic: every gradient of every token to one
+    rounding of the result (2^-8 of a value at most) and float32's own, 2e-5 of
+    terms up to five times the sum's norm, in each of several draws."""
+    for seed in range(12):
+        x, ref = make(100 + seed, B, n, Hk, H, dk, dv, "bf16")
+        got = rn.retnet_delta_backward(*x)
+        done(rn)
+        for name, a, w in zip(("dq", "dk", "dv", "dg", "dbeta"), got, oracle.delta_backward(*ref, dk ** -0.5)):
+            a, size = a.double().cpu().numpy(), np.linalg.norm(w)
+            assert np.linalg.norm(a - w) <= (2.0 ** -8 + 1e-4) * size, (name, seed)
