@@ -415,11 +415,11 @@ RETNET_API retnet_status retnet_delta_recurrent(const void *q, const void *k, co
  * float32 too, in segments of a long sequence beside one another); the
  * tensor-core path works in chunks of 64 tokens, for bf16 with dk 64 or 128;
  * AUTO takes it there for all but a few tokens.  Its products take bf16
- * operands: on the way to `out` what a chunk forms from q, k, g and beta, the
- * state and x are rounded to bf16 (together with the result's rounding 2.9e-3
- * of the norm, up to 4.4e-3 with decays near 0 over thousands of tokens; the
- * result's alone is 1.7e-3, which is all that SIMT has); a final state keeps
- * float32 accuracy.  Equal calls give equal bits, whatever the workspace
+ * operands, some in two parts: on the way to `out` what a chunk forms from k, g
+ * and beta for its inverse, the decayed q and the state are rounded to bf16
+ * (together with the result's rounding 1.7e-3 to 2.1e-3 of the norm, up to 3e-3
+ * with decays near 0 over thousands of tokens; the result's alone is 1.7e-3,
+ * which is all that SIMT has); a final state is within 5e-6 of its norm.  Equal calls give equal bits, whatever the workspace
  * held.  Between calls that differ the bits of a sequence's `out` may differ,
  * inside these roundings: with state_out operands go in two bf16 parts; which
  * path AUTO takes for up to 16 tokens, and whether and where a long sequence is
@@ -444,11 +444,12 @@ RETNET_API retnet_status retnet_delta_chunkwise(const void *q, const void *k, co
  * d_out = dL/dout, writes dq, dk, dv, dg, dbeta, shaped and typed as q, k,
  * v, g, beta; a key head's dq and dk are the sums over its value heads, in
  * head order.  On the tensor-core path (bf16 with dk 64 or 128; AUTO takes it
- * but for calls of at most 16 tokens and 256 in all sequences and heads) the
- * operands are rounded to bf16 as in the prefill, the states, the
- * gradients of the states and x are kept in bf16, and dq, dk, dg and dbeta are
- * formed from dv as it leaves: 2.4e-3 to 4.9e-3 of a gradient's norm.  A beta
- * of less than 1e-15 in size counts as 0; dbeta is then the limit.  The gradients must not overlap the inputs or each other.
+ * but for calls of at most 16 tokens and 256 in all sequences and heads)
+ * operands are rounded to bf16 as in the prefill, and the states and their
+ * gradients are kept in bf16: 1.7e-3 to 2.2e-3 of a gradient's norm, with
+ * decays near 0 up to 3e-3 and, of dg, where few heads leave few independent
+ * terms, 4e-3.  A beta of less than 1e-15 in size counts as 0; dbeta is then
+ * the limit.  The gradients must not overlap the inputs or each other.
  *   workspace  retnet_delta_backward_workspace_size() bytes, 1024-byte aligned
  *              (as above).
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */

@@ -17,22 +17,26 @@
 // channel of S, X and O, and what passes between products (S^T, X^T) is an
 // A operand in tensor memory that the thread writes where it read its
 // accumulator.  Nothing but the prepared tiles, K and V goes through shared
-// memory, all of it by bulk copies one chunk ahead.
+// memory, all of it by bulk copies one chunk ahead; outputs go from registers
+// to global memory, 64 bytes a warp and token.
 //
 // Roundings.  Accumulators, states, sums and decays are float32; the operands
-// of a product are bf16, each rounded once where it is formed, since a second
-// part doubles the product's MMAs.  What each moves an output by (2-norm, 400
-// tokens of 128 x 128, mean log decay -0.02; made one at a time by
-// oracle/delta_chunks.py, and the kernels' errors are those of all of them
-// within 0.5 %): P 1.6e-3, X as the output's operand 1.5e-3, the result
-// 1.7e-3, S, Q~ and e^{G_L - G} X 0.8 to 0.9e-3, T^ 0.3e-3, W 0.2e-3;
-// together 3.1e-3 (2.9e-3 at -0.2, 3.5e-3 at -0.002).  With P and X in two
-// parts it would be 2.2e-3, for twice the output's MMAs.  In the backward: the
-// pairs A and B 1.5e-3 of dq and dk, X 1.4 to 1.7e-3 of all but dv, dV 1.7e-3
-// of dv and dbeta (0.4e-3 of dk), D 0.8e-3, dX 0.2e-3 of dk (dV takes it in
-// two parts, or it would add 1.7e-3), the results 1.7e-3; together 2.6e-3 (dv)
-// to 3.5e-3 (dbeta).  A final state has no rounding of a result behind it, so
-// all that it depends on goes in two parts (kSplit): 2.6e-6 instead of 1.8e-3.
+// of a product are bf16, in one part or, where one moved a result by more than
+// its own rounding and a second costs little, in two (2^-17; each part more is
+// a product more).  In two: P and X, which alone made an output's error 3.1e-3
+// instead of 2.1e-3; X, A, B and dV where the gradients are formed of them
+// (dq 3.0 to 1.9e-3, dbeta 3.5 to 1.8e-3); e^{G_L - G} X and, in the backward,
+// Q~, whose errors stay in the state and its gradient while decays are slow
+// (dg with mean log decays of -0.002: 4.6 to 2.8e-3); dX for dV.  With these
+// in one part calls of the backward of few heads were up to 6e-3 off in dg.
+// What the others move a result by (2-norm, 400 tokens of 128 x 128, mean log
+// decay -0.02; made one at a time by oracle/delta_chunks.py, and the kernels'
+// errors are those of all of them within 1 %): the result 1.7e-3, Q~ of an
+// output and S 0.8e-3, D 0.8e-3, T^ 0.3e-3, W 0.2e-3, dX 0.2e-3, dV as it left
+// 0.4e-3 of dk; together 2.1e-3 of an output, 1.8 to 2.2e-3 of the gradients
+// (1.7e-3 and 1.7 to 1.8e-3 at -0.2, 2.7e-3 and 2.3 to 2.8e-3 at -0.002).  A
+// final state has no rounding of a result behind it, so all that it depends on
+// goes in two parts (kSplit): 3.4e-6 instead of 0.4e-3.
 #include "delta.cuh"
 #include "pairs.cuh"
 #include "sm100_chain.cuh"
@@ -60,7 +64,7 @@ __device__ __forceinline__ constexpr bool hook_skips(bool, int) { return false; 
 // One chunk's prepared operands, in shared-memory order.  Every tile is
 // boxes of 64 rows (tokens) of 64 columns, 128-byte swizzled.
 // kSplit: T^ and W in two bf16 parts (16 bits together), which the final
-// state's float32 precision needs.
+// state's float32 precision needs.  P is in two in any case.
 template <int DK, bool kSplit>
 struct DeltaBlock {
     static constexpr uint32_t kKB = DK / 64;
@@ -73,8 +77,13 @@ struct DeltaBlock {
     // which do, at 128.
     static constexpr uint32_t kHdr = kSplit ? kWlo + kKB * kBox64 : kWlo;
     static constexpr uint32_t kQ = kHdr + 1024;
+    // P in two parts; the prep's copy in shared memory ends with the first
     static constexpr uint32_t kP = kQ + kKB * kBox64;
-    static constexpr uint32_t kBytes = kP + kBox64;
+    static constexpr uint32_t kPlo = kP + kBox64;
+    static constexpr uint32_t kBytes = kPlo + kBox64;
+    // the backward's blocks, with Q~'s second part
+    static constexpr uint32_t kQlo = kBytes;
+    static constexpr uint32_t kBack = kQlo + kKB * kBox64;
 };
 
 // Byte offset of element (row, col) of a 64-row tile of boxes.
@@ -141,13 +150,18 @@ __device__ __forceinline__ void clear_flagged(uint8_t *box, int boxes, const flo
     __syncwarp();
 }
 // 64 tokens of a v channel's accumulator into a tile of token rows (two
-// boxes of 64 channels), bf16: col is the channel in the tile.
-__device__ __forceinline__ void put_channel(uint8_t *tile, int col, const uint32_t (&o)[2][32]) {
+// boxes of 64 channels), bf16: col is the channel in the tile.  x becomes the
+// pairs' second parts, in its first half.
+__device__ __forceinline__ void put_channel(uint8_t *tile, int col, uint32_t (&x)[64]) {
     uint8_t *box = tile + (col / 64) * kBox64 + (col & 7) * 2;
+    const int seg = (col & 63) >> 3;
 #pragma unroll
-    for (int i = 0; i < kC; ++i)
-        *reinterpret_cast<__nv_bfloat16 *>(box + i * 128 + ((((col & 63) >> 3) ^ (i & 7)) << 4)) =
-            __float2bfloat16_rn(__uint_as_float(o[i / 32][i % 32]));
+    for (int i = 0; i < kC; i += 2) {
+        uint32_t hi;
+        split_pair(as_pair(x[i], x[i + 1]), hi, x[i / 2]);
+        *reinterpret_cast<uint16_t *>(box + i * 128 + ((seg ^ (i & 7)) << 4)) = (uint16_t)hi;
+        *reinterpret_cast<uint16_t *>(box + (i + 1) * 128 + ((seg ^ ((i + 1) & 7)) << 4)) = (uint16_t)(hi >> 16);
+    }
 }
 
 // What the walks keep for the gradients (X^T, S^T, D^T: a row of `cols`
@@ -186,7 +200,7 @@ constexpr int kMPad = 68;
 
 template <int DK, bool kSplit>
 struct DeltaPrepSmem {
-    uint8_t block[DeltaBlock<DK, kSplit>::kBytes];
+    uint8_t block[DeltaBlock<DK, kSplit>::kPlo];
     float M[kC][kMPad];                    // M, then T in its place
     DecaySums G;
     float beta[kC], own[kC];               // b; 1 where a token of the backward writes nothing
@@ -214,9 +228,12 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], const void *
                  : "r"(smem_u32(p)));
 }
 
-// Rows 16 RB .. and 16-column tiles T0 .. T0 + NT - 1 of M or P.
+// Rows 16 RB .. and 16-column tiles T0 .. T0 + NT - 1 of M or P.  P's second
+// part goes straight to the block in global memory: there is no room for it
+// beside three CTAs an SM.
 template <int DK, bool kSplit, int RB, int T0, int NT>
-__device__ __forceinline__ void pair_tiles(DeltaPrepSmem<DK, kSplit> &m, bool isP, float scale, int lane) {
+__device__ __forceinline__ void pair_tiles(DeltaPrepSmem<DK, kSplit> &m, uint8_t *plo, bool isP, float scale,
+                                           int lane) {
     using Block = DeltaBlock<DK, kSplit>;
     const uint8_t *Kt = m.block + Block::kW, *At = isP ? m.block + Block::kQ : Kt;
     const int gr = lane / 4, tq = lane % 4;
@@ -249,9 +266,12 @@ __device__ __forceinline__ void pair_tiles(DeltaPrepSmem<DK, kSplit> &m, bool is
                 if (!isP && i == j) w.x = 0.f;
                 if (!isP && i == j + 1) w.y = 0.f;
             }
-            if (isP)
-                *reinterpret_cast<uint32_t *>(m.block + Block::kP + tile_off(i, j)) = pack_bf16x2(w.x, w.y);
-            else
+            if (isP) {
+                uint32_t hi, lo;
+                split_pair(w, hi, lo);
+                *reinterpret_cast<uint32_t *>(m.block + Block::kP + tile_off(i, j)) = hi;
+                *reinterpret_cast<uint32_t *>(plo + tile_off(i, j)) = lo;
+            } else
                 *reinterpret_cast<float2 *>(&m.M[i][j]) = w;
         }
     }
@@ -365,6 +385,13 @@ delta_prep_kernel(DeltaPrepArgs a) {
         const int j = t - (blk == 1 ? 0 : blk == 2 ? 16 : 48);
         m.across[blk - 1][j] = expf(m.G.until(j, blk - 1));
     }
+    uint8_t *block = a.blocks + (size_t)blockIdx.x * (a.backward ? Block::kBack : Block::kBytes);
+    uint8_t *plo = block + Block::kPlo;
+    if (tid < 192) {                                       // of P's second part: six squares above the diagonal
+        const int q = tid / 32, rb = q < 3 ? 0 : q < 5 ? 1 : 2, cb = q < 3 ? 1 + q : q < 5 ? q - 1 : 3;
+        *reinterpret_cast<uint4 *>(plo + tile_off(16 * rb + (tid & 31) / 2, 16 * cb + 8 * (tid & 1))) =
+            make_uint4(0, 0, 0, 0);
+    }
     {   // above the diagonal: P, and M where its triangles' inverses are multiplied
         const int r = tid / 4;
 #pragma unroll
@@ -382,12 +409,12 @@ delta_prep_kernel(DeltaPrepArgs a) {
     // warps 0-3: M from K K^T, warps 4-7: P from Q K^T, two or three of the ten
     // 16 x 16 tiles up to the diagonal each
     switch (warp & 3) {
-        case 0: pair_tiles<DK, kSplit, 3, 0, 2>(m, warp >= 4, a.scale, lane); break;
-        case 1: pair_tiles<DK, kSplit, 3, 2, 2>(m, warp >= 4, a.scale, lane); break;
-        case 2: pair_tiles<DK, kSplit, 2, 0, 3>(m, warp >= 4, a.scale, lane); break;
+        case 0: pair_tiles<DK, kSplit, 3, 0, 2>(m, plo, warp >= 4, a.scale, lane); break;
+        case 1: pair_tiles<DK, kSplit, 3, 2, 2>(m, plo, warp >= 4, a.scale, lane); break;
+        case 2: pair_tiles<DK, kSplit, 2, 0, 3>(m, plo, warp >= 4, a.scale, lane); break;
         default:
-            pair_tiles<DK, kSplit, 1, 0, 2>(m, warp >= 4, a.scale, lane);
-            pair_tiles<DK, kSplit, 0, 0, 1>(m, warp >= 4, a.scale, lane);
+            pair_tiles<DK, kSplit, 1, 0, 2>(m, plo, warp >= 4, a.scale, lane);
+            pair_tiles<DK, kSplit, 0, 0, 1>(m, plo, warp >= 4, a.scale, lane);
     }
     __syncthreads();
     if (warp < 4) {
@@ -416,10 +443,13 @@ delta_prep_kernel(DeltaPrepArgs a) {
             __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(Qt + tile_off(r, j));
             float qv[8];
             load8(p, qv);
-            const float s = a.scale * m.e[r];
+            const float f = a.scale * m.e[r];
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) qv[e] *= s;
-            store8(p, qv);
+            for (int e = 0; e < 4; ++e) split_pair(qv[2 * e] * f, qv[2 * e + 1] * f, hi[e], lo[e]);
+            *reinterpret_cast<uint4 *>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (a.backward)
+                *reinterpret_cast<uint4 *>(block + Block::kQlo + tile_off(r, j)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     }
     __syncthreads();
@@ -501,7 +531,7 @@ delta_prep_kernel(DeltaPrepArgs a) {
     fence_async_shared();
     __syncthreads();
     if (tid == 0) {
-        bulk_store(a.blocks + (size_t)blockIdx.x * Block::kBytes, m.block, Block::kBytes);
+        bulk_store(block, m.block, Block::kPlo);
         tma_store_commit();
         tma_store_wait_read();
     }
@@ -512,23 +542,23 @@ delta_prep_kernel(DeltaPrepArgs a) {
 // Warps: 0 copies, 1 MMAs, 2-9 two warpgroups of the chain (the columns of
 // an accumulator, tokens or k, split between them), 10-13 the output.
 // Per chunk, in the order the MMAs are issued:
-//   X^T  = V^T T^^T + S^T (-W)^T    [needs S]       -> chain: X, Xs = e^{G_L-G} X
+//   X^T  = V^T T^^T + S^T (-W)^T    [needs S]       -> chain: Xs = e^{G_L-G} X, then X
 //   O^T  = S^T Q~^T                 (while the chain rounds X)
-//   Z^T  = Xs^T K                   [needs X]       -> chain: S = e^{G_L} S + Z
+//   Z^T  = Xs^T K                   [needs Xs]      -> chain: S = e^{G_L} S + Z
 //   O^T += X^T P^T                  (while the chain rounds S)
 // S and Z go 64 rows of S at a time, so that the chain's work on one piece
 // runs beside the MMAs of the other.  S itself stays in the chain's registers
-// in float32.  With kSplit its operand copies are two bf16 parts: X^T takes
-// S_hi (W_hi + W_lo) + S_lo W_hi, Z takes both parts of Xs against the exact
-// K, so each product carries 16 bits (the lowest parts' product, 2^-18, is
-// left out) and the state keeps float32 accuracy over the walk (measured
-// 3e-6 to 6e-6 after 8192 tokens); without it S is only ever seen through bf16
-// outputs and one part is enough.
+// in float32.  Z takes both bf16 parts of Xs against the exact K.  With kSplit
+// S's operand copies have two parts too: X^T takes S_hi (W_hi + W_lo) + S_lo
+// W_hi, so each product carries 16 bits (the lowest parts' product, 2^-18, is
+// left out) and the state keeps float32 accuracy over the walk (measured 3e-6
+// to 4e-6 after 8192 tokens); without it S is only ever seen through bf16
+// outputs, and one part of it and of T^ and W is enough.
 constexpr int kScanThreads = 448;
 constexpr int kChainWarps = 8;
 
 struct DeltaScanBars {
-    uint64_t full[2], empty[2], s_ready[2], z_full[2], x_full, xs_ready, o_full, o_free, drain;
+    uint64_t full[2], empty[2], s_ready[2], z_full[2], x_full, xs_ready, xb_ready, o_full, o_free, drain;
     uint32_t tmem_slot;
     int abort_flag;
 };
@@ -538,8 +568,7 @@ struct DeltaScanSmem {
     static constexpr uint32_t kK = Block::kBytes;
     static constexpr uint32_t kV = kK + Block::kKB * kBox64;
     static constexpr uint32_t kStage = kV + 2 * kBox64;
-    static constexpr uint32_t kOut = 2 * kStage;          // 64 tokens x 128 channels
-    static constexpr uint32_t kBars = kOut + 2 * kBox64;
+    static constexpr uint32_t kBars = 2 * kStage;
     static constexpr uint32_t kBytes = kBars + 256;
     static_assert(sizeof(DeltaScanBars) <= 256 && kBytes <= 227 * 1024, "shared memory");
 };
@@ -552,8 +581,9 @@ struct DeltaScanTmem {
     static constexpr uint32_t kX = kZ + DK;
     static constexpr uint32_t kXs = kX + 64;              // Xs hi, lo
     static constexpr uint32_t kXslo = kXs + 32;
-    static constexpr uint32_t kXb = kXslo + 32;           // X
-    static constexpr uint32_t kO = kXb + 32;
+    static constexpr uint32_t kXb = kXslo + 32;           // X hi, lo
+    static constexpr uint32_t kXblo = kXb + 32;
+    static constexpr uint32_t kO = kXblo + 32;
     static_assert(kO + 64 <= 512, "tensor memory");
 };
 
@@ -591,7 +621,7 @@ __device__ __forceinline__ DeltaWalk whole_walk(const DeltaScanArgs &a, int dk, 
 // kFine: in two parts; kSplit: the blocks have two.
 template <int DK, bool kSplit, bool kOut, bool kSave, bool kFine>
 __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                                             const CUtensorMap &tm_o, const DeltaScanArgs &a,
+                                             const DeltaScanArgs &a,
                                              const DeltaWalk &w) {
     using Smem = DeltaScanSmem<DK, kSplit>;
     using Block = DeltaBlock<DK, kSplit>;
@@ -605,7 +635,7 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int bh = w.bh, v0 = w.v0;
     const int b = bh / a.heads, h = bh % a.heads;
-    const bool out = kOut && w.out;
+    const bool out = kOut && w.out, again = out || (kSave && w.keep);   // X itself is used
     unsigned *err = a.err;
     int *abort_flag = &bar.abort_flag;
 
@@ -618,6 +648,7 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
         }
         mbar_init(&bar.x_full, 1);
         mbar_init(&bar.xs_ready, kChainWarps);
+        mbar_init(&bar.xb_ready, kOut ? kChainWarps : 4);
         mbar_init(&bar.o_full, 1);
         mbar_init(&bar.o_free, 4);
         mbar_init(&bar.drain, 1);
@@ -625,7 +656,6 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
         fence_barrier_init();
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
-        if (kOut) tma_prefetch_desc(&tm_o);
     }
     if (warp == 1) {
         tmem_alloc(&bar.tmem_slot, 512);
@@ -644,7 +674,8 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
     int it = 0;                                            // chunks whose copies were issued
     if (warp == 0) {
         const int kh = h / (a.heads / a.key_heads);
-        const uint8_t *blocks = a.blocks + ((size_t)bh * a.nc + w.first) * Block::kBytes;
+        constexpr uint32_t kStep = kSave ? Block::kBack : Block::kBytes;
+        const uint8_t *blocks = a.blocks + ((size_t)bh * a.nc + w.first) * kStep;
         for (; it < nc; ++it) {
             const int s = it & 1;
             if (it >= 2 && !warp_spin_wait(&bar.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
@@ -653,7 +684,7 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
             if (elect_one()) {
                 const uint32_t block = out ? Block::kBytes : Block::kQ;
                 const int t0 = (w.first + it) * kC;
-                const uint8_t *src = blocks + (size_t)it * Block::kBytes;
+                const uint8_t *src = blocks + (size_t)it * kStep;
                 const uint32_t rest = (w.unit ? Smem::kV : Smem::kStage) - Smem::kK;
                 if (kFine || !kSplit) {
                     mbar_expect_tx(&bar.full[s], block + rest);
@@ -731,10 +762,11 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < DK / 16; ++ks)
-                        mma_bf16_ts(tmem + Tm::kO, tmem + Tm::kShi + 8 * ks,
-                                    kmaj + ((Block::kQ + (ks / 4) * kBox64 + (ks % 4) * 32) >> 4),
-                                    id_x, ks > 0);
+                    for (int ks = 0; ks < DK / 16; ++ks) {
+                        const uint64_t qd = kmaj + ((Block::kQ + (ks / 4) * kBox64 + (ks % 4) * 32) >> 4);
+                        mma_bf16_ts(tmem + Tm::kO, tmem + Tm::kShi + 8 * ks, qd, id_x, ks > 0);
+                        if (kFine) mma_bf16_ts(tmem + Tm::kO, tmem + Tm::kSlo + 8 * ks, qd, id_x, 1);
+                    }
                 }
                 __syncwarp();
             }
@@ -747,16 +779,27 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                     for (int ks = 0; ks < 4; ++ks) {
                         const uint64_t kd = mnmaj + ((Smem::kK + p * kBox64 + ks * 2048) >> 4);
                         mma_bf16_ts(tmem + Tm::kZ + 64 * p, tmem + Tm::kXs + 8 * ks, kd, id_z, ks > 0);
-                        if (kFine)
-                            mma_bf16_ts(tmem + Tm::kZ + 64 * p, tmem + Tm::kXslo + 8 * ks, kd, id_z, 1);
+                        mma_bf16_ts(tmem + Tm::kZ + 64 * p, tmem + Tm::kXslo + 8 * ks, kd, id_z, 1);
                     }
                     mma_commit(&bar.z_full[p]);
                 }
+            }
+            __syncwarp();
+            // (X has been read for this, before the next chunk's takes its place)
+            if (again) {
+                if (!warp_spin_wait(&bar.xb_ready, c & 1, abort_flag, err)) break;
+                tc_fence_after();
+            }
+            if (elect_one()) {
                 if (out) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint64_t pd = kmaj + ((Block::kP + ks * 32) >> 4);
+                        mma_bf16_ts(tmem + Tm::kO, tmem + Tm::kXb + 8 * ks, pd, id_x, 1);
+                        mma_bf16_ts(tmem + Tm::kO, tmem + Tm::kXblo + 8 * ks, pd, id_x, 1);
                         mma_bf16_ts(tmem + Tm::kO, tmem + Tm::kXb + 8 * ks,
-                                    kmaj + ((Block::kP + ks * 32) >> 4), id_x, 1);
+                                    kmaj + ((Block::kPlo + ks * 32) >> 4), id_x, 1);
+                    }
                     mma_commit(&bar.o_full);
                 }
                 mma_commit(&bar.empty[s]);
@@ -806,30 +849,38 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
             if (!warp_spin_wait(&bar.x_full, c & 1, abort_flag, err)) break;
             tc_fence_after();
             {
-                uint32_t hi[16], lo[16], xb[16];
+                uint32_t x[16], hi[16], lo[16];
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {           // 16 columns at a time, for the registers
-                    uint32_t x[16];
                     tmem_ld16(tl + Tm::kX + 32 * wg + 16 * hf, x);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int i = 8 * hf + j;
                         const float2 r = *reinterpret_cast<const float2 *>(hdr + 32 * wg + 2 * i);
-                        const float2 xv = as_pair(x[2 * j], x[2 * j + 1]), xr = mul2(xv, r);
-                        if (kFine) split_pair(xr, hi[i], lo[i]);
-                        else hi[i] = pack_bf16x2(xr.x, xr.y);
-                        if (kOut || kSave) xb[i] = pack_bf16x2(xv.x, xv.y);
+                        split_pair(mul2(as_pair(x[2 * j], x[2 * j + 1]), r), hi[i], lo[i]);
                     }
                 }
                 tmem_st16(tl + Tm::kXs + 16 * wg, hi);
-                if (kFine) tmem_st16(tl + Tm::kXslo + 16 * wg, lo);
-                if (kOut) tmem_st16(tl + Tm::kXb + 16 * wg, xb);
+                tmem_st16(tl + Tm::kXslo + 16 * wg, lo);
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(&bar.xs_ready);
-                if (kSave && w.keep && live)
-                    keep_row(a.x_save, (size_t)bh * a.nc + w.first + c, a.dv, v, kC, 32 * wg, xb);
+                if (out) {                                 // X in two parts, beside the MMAs on Xs
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        tmem_ld16(tl + Tm::kX + 32 * wg + 16 * hf, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            split_pair(as_pair(x[2 * j], x[2 * j + 1]), hi[8 * hf + j], lo[8 * hf + j]);
+                    }
+                    tmem_st16(tl + Tm::kXb + 16 * wg, hi);
+                    tmem_st16(tl + Tm::kXblo + 16 * wg, lo);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    warp_arrive(&bar.xb_ready);
+                }
             }
             bool ok = true;
 #pragma unroll
@@ -859,47 +910,54 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
                     dst[0] = S[p][j].x;
                     dst[w.width] = S[p][j].y;
                 }
-    } else if (out) {
-        // O through shared memory, token rows of 64 channels (the swizzle of
-        // the copy out), so that global memory sees whole lines
-        const int col = 32 * (warp % 4) + lane, tid = threadIdx.x - 320;
+    } else if (again) {
+        const int v = v0 + 32 * (warp % 4) + lane;
+        const bool live = v < a.dv;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
-        for (int c = 0; c < nc; ++c) {
-            const bool ok = warp_spin_wait(&bar.o_full, c & 1, abort_flag, err);
-            uint32_t o[2][32];
-            if (ok) {
+        if (kSave) {                                       // X in two parts for the gradients
+            for (int c = 0; c < nc; ++c) {
+                if (!warp_spin_wait(&bar.x_full, c & 1, abort_flag, err)) break;
                 tc_fence_after();
+                uint32_t hi[2][16], lo[2][16];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {              // 16 tokens at a time
+                    uint32_t x[16];
+                    tmem_ld16(tl + Tm::kX + 16 * q, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        split_pair(as_pair(x[2 * j], x[2 * j + 1]), hi[q / 2][8 * (q & 1) + j],
+                                   lo[q / 2][8 * (q & 1) + j]);
+                }
+                tc_fence_before();
+                warp_arrive(&bar.xb_ready);
+                if (live)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const size_t chunk = (size_t)bh * a.nc + w.first + c;
+                        keep_row(a.x_save, chunk, a.dv, v, 2 * kC, 32 * hf, hi[hf]);
+                        keep_row(a.x_save, chunk, a.dv, v, 2 * kC, kC + 32 * hf, lo[hf]);
+                    }
+            }
+        } else {                                           // a thread's tokens of its channel
+            const size_t step = (size_t)a.heads * a.dv;
+            __nv_bfloat16 *dst = a.out + (((size_t)b * a.tokens + (size_t)w.first * kC) * a.heads + h) * a.dv + v;
+            for (int c = 0; c < nc; ++c, dst += kC * step) {
+                if (!warp_spin_wait(&bar.o_full, c & 1, abort_flag, err)) break;
+                tc_fence_after();
+                uint32_t o[2][32];
                 tmem_ld32(tl + Tm::kO, o[0]);
                 tmem_ld32(tl + Tm::kO + 32, o[1]);
                 tmem_wait_ld();
                 tc_fence_before();
                 warp_arrive(&bar.o_free);
-            }
-            if (tid == 0) tma_store_wait_read();           // the last tile has left
-            if (named_barrier_or(1, 128, !ok)) break;
-            put_channel(smem + Smem::kOut, col, o);
-            const int cnt = n - c * kC;
-            if (cnt >= kC) fence_async_shared();
-            named_barrier(1, 128);
-            if (cnt >= kC) {
-                if (tid == 0) {
-                    for (int x = 0; x < 2; ++x)
-                        if (v0 + 64 * x < a.dv)
-                            tma_store_4d(&tm_o, smem + Smem::kOut + x * kBox64, v0 + 64 * x, h, (w.first + c) * kC, b);
-                    tma_store_commit();
-                }
-            } else {                                       // rows behind the sequence stay
-                for (int i = tid; i < cnt * 16; i += 128) {
-                    const int r = i / 16, ch = i % 16;
-                    if (v0 + ch * 8 < a.dv)
-                        *reinterpret_cast<uint4 *>(
-                            a.out + (((size_t)b * a.tokens + (w.first + c) * kC + r) * a.heads + h) * a.dv + v0 + ch * 8) =
-                            *reinterpret_cast<const uint4 *>(smem + Smem::kOut + (ch / 8) * kBox64 + r * 128 +
-                                                             (((ch & 7) ^ (r & 7)) << 4));
-                }
+                const int cnt = live ? n - c * kC : 0;     // rows behind the sequence stay
+                __nv_bfloat16 *p = dst;
+#pragma unroll
+                for (int i = 0; i < kC; ++i, p += step)
+                    if (i < cnt) *p = __float2bfloat16_rn(__uint_as_float(o[i / 32][i % 32]));
             }
         }
-        if (tid == 0) tma_store_wait_read();
     }
     tc_fence_before();
     __syncthreads();
@@ -918,8 +976,8 @@ __device__ __forceinline__ void forward_walk(const CUtensorMap &tm_k, const CUte
 template <int DK, bool kSplit>
 __global__ void __launch_bounds__(kScanThreads, 1)
 delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const __grid_constant__ CUtensorMap tm_o, DeltaScanArgs a) {
-    forward_walk<DK, kSplit, true, false, kSplit>(tm_k, tm_v, tm_o, a, whole_walk(a, DK, blockIdx.x, true));
+                  DeltaScanArgs a) {
+    forward_walk<DK, kSplit, true, false, kSplit>(tm_k, tm_v, a, whole_walk(a, DK, blockIdx.x, true));
 }
 
 // ---- in segments
@@ -932,14 +990,14 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 // up to three times, but on all SMs: 8192 tokens and 16 heads of 128 in 6
 // segments, walk 274 us whole, 103 us so, and 11 us the join.
 // Only what a final state depends on is walked in two parts: not the outputs
-// of the second pass (it would take 0.1e-3 off their 3.1e-3), but its last
+// of the second pass (it would take 0.2e-3 off their 2.1e-3), but its last
 // segment, which is shorter for that.
 // starts [segments - 1][BH][dk, dv]: N_j and then the state before segment
 // j + 1; units [segments - 2][BH][dk, dk]: M of segments 1 ...
 template <int DK, bool kSplit, bool kLast>
 __global__ void __launch_bounds__(kScanThreads, 1)
 delta_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const __grid_constant__ CUtensorMap tm_o, DeltaScanArgs a, int bhs) {
+                      DeltaScanArgs a, int bhs) {
     const int slabs = (a.dv + 127) / 128, walks = bhs * slabs;
     const size_t ssize = (size_t)DK * a.dv;
     int cta = blockIdx.x;
@@ -974,11 +1032,11 @@ delta_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     w.last = w.first + a.segment;
     if constexpr (kSplit && kLast) {
         if (!w.to) {
-            forward_walk<DK, kSplit, true, false, false>(tm_k, tm_v, tm_o, a, w);
+            forward_walk<DK, kSplit, true, false, false>(tm_k, tm_v, a, w);
             return;
         }
     }
-    forward_walk<DK, kSplit, true, false, kSplit>(tm_k, tm_v, tm_o, a, w);
+    forward_walk<DK, kSplit, true, false, kSplit>(tm_k, tm_v, a, w);
 }
 
 // starts[j] <- starts[j] + M starts[j - 1], j = 1 .. joins, with M of units
@@ -1123,23 +1181,36 @@ cudaError_t launch_join(float *starts, float *back, const float *units, int bhs,
 //   dX = P^T dO + diag(e^{G_L - G}) K D,   dV = T^^T dX,
 //   D <- e^{G_L} D + Q~^T dO - W^T dX,
 // transposed and laid out as in the forward walk (v channels as lanes, D in
-// the chain's registers in float32, its operand copy and dX rounded to bf16:
-// gradients leave in bf16).  Per chunk, in the order of the MMAs:
+// the chain's registers in float32, its operand copy and, for W, dX in one
+// bf16 part, P and Q~ in two).  Per chunk, in the order of the MMAs:
 //   Y1^T = dO^T P;  Y2^T = D^T K^T       [needs D]   -> chain: dX = Y1 + rest Y2
 //   Z^T  = dO^T Q~                       (while the chain rounds dX)
 //   Z^T += dX^T (-W)                     [needs dX]  -> chain: D = e^{G_L} D + Z
 //   dV^T = dX^T T^                       (while the chain rounds D)
-// D is kept for every chunk (d_save, as S^T in the forward walk).
+// D is kept for every chunk (d_save, as S^T in the forward walk), and what dV
+// leaves behind its bf16 result (v_lo), for dbeta.
 struct DeltaReverseBars {
     uint64_t full[2], empty[2], d_ready[2], z_full[2], y_full, dx_ready, lo_ready, v_full, v_free, drain;
     uint32_t tmem_slot;
     int abort_flag;
 };
 
+template <int DK>
+struct DeltaReverseSmem {
+    using Block = DeltaBlock<DK, false>;
+    static constexpr uint32_t kK = Block::kBack;
+    static constexpr uint32_t kDo = kK + Block::kKB * kBox64;
+    static constexpr uint32_t kStage = kDo + 2 * kBox64;
+    static constexpr uint32_t kOut = 2 * kStage;          // dV, 64 tokens x 128 channels
+    static constexpr uint32_t kBars = kOut + 2 * kBox64;
+    static constexpr uint32_t kBytes = kBars + 256;
+    static_assert(sizeof(DeltaReverseBars) <= 256 && kBytes <= 227 * 1024, "shared memory");
+};
+
 struct DeltaReverseArgs {
     const uint8_t *blocks;
     const int *lengths;
-    __nv_bfloat16 *d_save;
+    __nv_bfloat16 *d_save, *v_lo;          // D^T of every chunk; dV^T's second part (keep_row)
     int heads, key_heads, tokens, nc, dv;
     unsigned *err;
 };
@@ -1148,14 +1219,13 @@ template <int DK>
 __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUtensorMap &tm_do,
                                              const CUtensorMap &tm_dv, const DeltaReverseArgs &a,
                                              const DeltaWalk &w) {
-    using Smem = DeltaScanSmem<DK, false>;                // V's place holds dO, the output's dV
+    using Smem = DeltaReverseSmem<DK>;
     using Block = DeltaBlock<DK, false>;
     constexpr int kPieces = DK / 64;
     constexpr uint32_t kD = 0, kZ = DK / 2, kY1 = kZ + DK, kY2 = kY1 + 64, kDx = kY2 + 64, kDxlo = kDx + 32, kDv = kDxlo + 32;
     static_assert(kDv + 64 <= 512, "tensor memory");
     extern __shared__ __align__(1024) uint8_t smem[];
     DeltaReverseBars &bar = *reinterpret_cast<DeltaReverseBars *>(smem + Smem::kBars);
-    static_assert(sizeof(DeltaReverseBars) <= 256, "barriers");
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int bh = w.bh, v0 = w.v0;
@@ -1197,7 +1267,7 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
     int it = 0;                                            // chunks whose copies were issued
     if (warp == 0) {
         const int kh = h / (a.heads / a.key_heads);
-        const uint8_t *blocks = a.blocks + (size_t)bh * a.nc * Block::kBytes;
+        const uint8_t *blocks = a.blocks + (size_t)bh * a.nc * Block::kBack;
         for (; it < nc; ++it) {
             const int s = it & 1, c = top - 1 - it;
             if (it >= 2 && !warp_spin_wait(&bar.empty[s], ((it >> 1) - 1) & 1, abort_flag, err)) break;
@@ -1205,10 +1275,10 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
             uint8_t *st = smem + s * Smem::kStage;
             if (elect_one()) {
                 mbar_expect_tx(&bar.full[s], Smem::kStage);
-                bulk_load(st, blocks + (size_t)c * Block::kBytes, Block::kBytes, &bar.full[s]);
+                bulk_load(st, blocks + (size_t)c * Block::kBack, Block::kBack, &bar.full[s]);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                    tma_load_4d(st + Smem::kV + x * kBox64, &tm_do, &bar.full[s], v0 + 64 * x, h, c * kC, b);
+                    tma_load_4d(st + Smem::kDo + x * kBox64, &tm_do, &bar.full[s], v0 + 64 * x, h, c * kC, b);
 #pragma unroll
                 for (int x = 0; x < DK / 64; ++x)
                     tma_load_4d(st + Smem::kK + x * kBox64, &tm_k, &bar.full[s], 64 * x, kh, c * kC, b);
@@ -1229,9 +1299,11 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16(tmem + kY1, mnmaj + ((Smem::kV + ks * 2048) >> 4),
-                             mnmaj + ((Block::kP + ks * 2048) >> 4), id_do, ks > 0);
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint64_t ad = mnmaj + ((Smem::kDo + ks * 2048) >> 4);
+                    mma_bf16(tmem + kY1, ad, mnmaj + ((Block::kP + ks * 2048) >> 4), id_do, ks > 0);
+                    mma_bf16(tmem + kY1, ad, mnmaj + ((Block::kPlo + ks * 2048) >> 4), id_do, 1);
+                }
             }
             __syncwarp();
             bool ok = true;
@@ -1245,14 +1317,15 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
                     for (int k4 = 0; k4 < 4; ++k4)
                         mma_bf16_ts(tmem + kY2, tmem + kD + 32 * p + 8 * k4,
                                     kmaj + ((Smem::kK + p * kBox64 + k4 * 32) >> 4), id_k, p + k4 > 0);
-                    if (p == kPieces - 1) {
-                        mma_commit(&bar.y_full);
+                    if (p == kPieces - 1) mma_commit(&bar.y_full);
+                    // (a piece of D that is ready has been read from Z)
 #pragma unroll
-                        for (int q = 0; q < kPieces; ++q)
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_bf16(tmem + kZ + 64 * q, mnmaj + ((Smem::kV + ks * 2048) >> 4),
-                                         mnmaj + ((Block::kQ + q * kBox64 + ks * 2048) >> 4), id_do, ks > 0);
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint64_t ad = mnmaj + ((Smem::kDo + ks * 2048) >> 4);
+                        mma_bf16(tmem + kZ + 64 * p, ad,
+                                 mnmaj + ((Block::kQ + p * kBox64 + ks * 2048) >> 4), id_do, ks > 0);
+                        mma_bf16(tmem + kZ + 64 * p, ad,
+                                 mnmaj + ((Block::kQlo + p * kBox64 + ks * 2048) >> 4), id_do, 1);
                     }
                 }
                 __syncwarp();
@@ -1381,11 +1454,11 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp % 4)) << 16);
         for (int u = 0; u < nc; ++u) {
             const bool ok = warp_spin_wait(&bar.v_full, u & 1, abort_flag, err);
-            uint32_t o[2][32];
+            uint32_t o[64];
             if (ok) {
                 tc_fence_after();
-                tmem_ld32(tl + kDv, o[0]);
-                tmem_ld32(tl + kDv + 32, o[1]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld16(tl + kDv + 16 * q, *reinterpret_cast<uint32_t (*)[16]>(&o[16 * q]));
                 tmem_wait_ld();
                 tc_fence_before();
                 warp_arrive(&bar.v_free);
@@ -1395,6 +1468,11 @@ __device__ __forceinline__ void reverse_walk(const CUtensorMap &tm_k, const CUte
             put_channel(smem + Smem::kOut, col, o);        // zeros behind the sequence
             fence_async_shared();
             named_barrier(1, 128);
+            if (v0 + col < a.dv)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                    keep_row(a.v_lo, (size_t)bh * a.nc + top - 1 - u, a.dv, v0 + col, kC, 32 * hf,
+                             *reinterpret_cast<const uint32_t (*)[16]>(&o[16 * hf]));
             if (tid == 0) {
                 for (int x = 0; x < 2; ++x)
                     if (v0 + 64 * x < a.dv)
@@ -1427,7 +1505,7 @@ delta_walks_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                    DeltaScanArgs f, DeltaReverseArgs r) {
     const int half = gridDim.x / 2;
     if ((int)blockIdx.x < half)
-        forward_walk<DK, false, false, true, false>(tm_k, tm_v, tm_v, f, whole_walk(f, DK, blockIdx.x, false));
+        forward_walk<DK, false, false, true, false>(tm_k, tm_v, f, whole_walk(f, DK, blockIdx.x, false));
     else reverse_walk<DK>(tm_k, tm_do, tm_dv, r, whole_walk(f, DK, blockIdx.x - half, false));
 }
 
@@ -1483,7 +1561,7 @@ delta_walks_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __gr
         w.unit = true;
         cut(seg);
     }
-    forward_walk<DK, false, false, true, false>(tm_k, tm_v, tm_v, f, w);
+    forward_walk<DK, false, false, true, false>(tm_k, tm_v, f, w);
 }
 
 // ------------------------------------------------------------------ gradients
@@ -1497,12 +1575,13 @@ delta_walks_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __gr
 // Of a token that writes nothing x is 0 and dV the gradient of x, r, which B
 // and dk leave out (b r is 0); dbeta = r . (v - k S before it), of which
 // r . k S are that row's sums of E and of k (r S^T) (S.none), and dv is 0.
-// dV is read as it left, in bf16, so that it is written once; A and B are
-// rounded as operands, but E, from which dg is summed, takes them before that.
+// X comes in two parts, A and B are made two; dV is read as it left and, for
+// dbeta, with its second part (dot products by the row warps: there is no room
+// for another tile).  E, from which dg is summed, takes A and B in float32.
 // A chunk's 64 rows fill half of a tcgen05 tile, so two operands share one:
 // rows 0-63 belong to the queries (dO, Q, A), rows 64-127 to the keys
 // (dV, K, B), and a thread of the epilogue owns a row of dq or of dk:
-//   pair columns  [dO; dV] X^T and [Q; K] K^T        (64 each)
+//   pair columns  [dO; dV] X^T and [Q; K] K^T        (64 each; X, A, B by parts)
 //   C1 = [dO; dV] S^T,  C2 = [*; X] D^T              (summed over v, 64 at a time)
 //   C3 = [A; B] K,      C4 = [*; A^T] Q + [*; B^T] K (C4 where the pairs were)
 // (*: whatever precedes the operand in shared memory; those rows are not read.)
@@ -1512,7 +1591,7 @@ delta_walks_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __gr
 constexpr int kGradTcThreads = 352;        // warps 0-7 rows, 8 copies, 9 MMAs, 10 gates and sums
 
 struct DeltaGradTcBars {
-    uint64_t full[2], empty[2], keys[2], keys_free[2], gates[2], done[2];
+    uint64_t full[2], lo_full[2], empty[2], keys[2], keys_free[2], gates[2], done[2];
     uint64_t pair_full, ab_ready, c_full, acc_free, drain;
     uint32_t tmem_slot;
     int abort_flag;
@@ -1528,15 +1607,16 @@ struct DeltaGradTcBars {
         float col[8][32];                  // by warp: its column half
         float inter[2][2][kC], ahead[2][kC], db[kC], sd[8];
         float none[2][kC];                 // [column half]: - r . k S, where nothing is written
+        float lo[2][kC];                   // [channel half]: dV's second part . x
     } sum[2];
-    float decay[kC][kC + 1];                               // e^{G_i - G_j}, i >= j
 };
 template <int DK>
 struct DeltaGradTcSmem {
     static constexpr uint32_t kKB = DK / 64;
     // two buffers of keys: a Q and a K box by turns ([Q; K] is 128 rows of one
     // operand, and each alone has its column blocks two boxes apart; dq and dk
-    // leave from where a thread read its row of them), then the tiles A, B
+    // leave from where a thread read its row of them), then the tiles A, B;
+    // the second parts of X by stages while A and B are not yet formed
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kK = kBox64;
     static constexpr uint32_t kKeyStep = 2 * kBox64;
@@ -1548,13 +1628,17 @@ struct DeltaGradTcSmem {
     static constexpr uint32_t kDo = 0, kDv = kBox64, kX = 2 * kBox64, kS = 3 * kBox64;
     static constexpr uint32_t kD = kS + kKB * kBox64;
     static constexpr uint32_t kStage = kD + kKB * kBox64;
-    static constexpr uint32_t kBars = kStage0 + 2 * kStage;
+    // float decay[64][65] = e^{G_i - G_j}, i >= j; the second parts of A and B
+    // once they have been formed with it
+    static constexpr uint32_t kDecay = kStage0 + 2 * kStage;
+    static constexpr uint32_t kBars = kDecay + 16640;
     static constexpr uint32_t kBytes = kBars + ((sizeof(DeltaGradTcBars) + 127) & ~127u);
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
 struct DeltaGradTcArgs {
-    const __nv_bfloat16 *v, *g, *beta, *x, *s, *d;         // X^T, S^T, D^T of every chunk
+    const __nv_bfloat16 *v, *g, *beta;
+    const __nv_bfloat16 *x, *s, *d, *v_lo;                 // X^T (two parts), S^T, D^T, dV^T's second part
     const int *lengths;
     __nv_bfloat16 *dq, *dk_, *dv_, *dg, *dbeta;
     float *dq_wide, *dk_wide;
@@ -1583,6 +1667,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&m.full[s], 1);
+            mbar_init(&m.lo_full[s], 1);
             mbar_init(&m.empty[s], 9);                     // the MMAs and 8 warps
             mbar_init(&m.keys[s], 1);
             mbar_init(&m.keys_free[s], 1);
@@ -1624,7 +1709,8 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         return w;
     };
 
-    int it = 0, kit = 0;                                   // stages and keys issued
+    float (*decay)[kC + 1] = reinterpret_cast<float (*)[kC + 1]>(smem + Smem::kDecay);
+    int it = 0, kit = 0, lit = 0;                          // stages, keys and second parts issued
     if (warp == 8) {
         bool ok = true;
         for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
@@ -1655,10 +1741,23 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     mbar_expect_tx(&m.full[s], Smem::kStage);
                     tma_load_4d(st + Smem::kDo, &tm_do, &m.full[s], 64 * u, w.h, w.t0, w.b);
                     tma_load_4d(st + Smem::kDv, &tm_dv, &m.full[s], 64 * u, w.h, w.t0, w.b);
-                    bulk_load(st + Smem::kX, a.x + (first + u) * (64 * kC), kBox64, &m.full[s]);
+                    bulk_load(st + Smem::kX, a.x + (first + u) * (2 * 64 * kC), kBox64, &m.full[s]);
                     bulk_load(st + Smem::kS, a.s + (first + u) * (64 * DK), kKB * kBox64, &m.full[s]);
                     bulk_load(st + Smem::kD, a.d + (first + u) * (64 * DK), kKB * kBox64, &m.full[s]);
                 }
+                __syncwarp();
+                // X's second parts of an item's first stages go where A and B
+                // of the last item were, once they have been read
+                if (u < min(nv, 2) - 1) continue;
+                if (u < 2 && kit > 1) ok = warp_spin_wait(&m.c_full, kit & 1, abort_flag, err);
+                if (!ok) break;
+                for (; lit <= it; ++lit)
+                    if (elect_one()) {
+                        uint64_t *bar = &m.lo_full[lit & 1];
+                        mbar_expect_tx(bar, kBox64);
+                        bulk_load(smem + Smem::kA + (lit & 1) * kBox64,
+                                  a.x + ((first + u - (it - lit)) * 2 + 1) * (64 * kC), kBox64, bar);
+                    }
                 __syncwarp();
             }
         }
@@ -1698,14 +1797,22 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 const int s = g & 1;
                 const uint32_t so = (Smem::kStage0 + s * Smem::kStage) >> 4;
                 const uint64_t kst = akm + so, kept = plain + so;
-                ok = warp_spin_wait(&m.full[s], (g >> 1) & 1, abort_flag, err);
+                const uint64_t xlo = plain + ((Smem::kA + s * kBox64) >> 4);
+                ok = warp_spin_wait(&m.full[s], (g >> 1) & 1, abort_flag, err) &&
+                     warp_spin_wait(&m.lo_full[s], (g >> 1) & 1, abort_flag, err);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16(tmem + kPd, kst + ((Smem::kDo + ks * 32) >> 4),
-                                 kept + ((Smem::kX + ks * 256) >> 4), id_px, u + ks > 0);
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint64_t dd = kst + ((Smem::kDo + ks * 32) >> 4);
+                        mma_bf16(tmem + kPd, dd, kept + ((Smem::kX + ks * 256) >> 4), id_px, u + ks > 0);
+                        mma_bf16(tmem + kPd, dd, xlo + ((ks * 256) >> 4), id_px, 1);
+                    }
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)         // the box in front fills the rows that are not read
+                        mma_bf16(tmem + kC2, xlo - (kBox64 >> 4) + ((ks * 256) >> 4),
+                                 kept + ((Smem::kD + ks * 256) >> 4), id_c2, u + ks > 0);
                     if (u == nv - 1) mma_commit(&m.pair_full);
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
@@ -1714,7 +1821,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)         // dV fills the rows that are not read
                         mma_bf16(tmem + kC2, kept + ((Smem::kDv + ks * 256) >> 4),
-                                 kept + ((Smem::kD + ks * 256) >> 4), id_c2, u + ks > 0);
+                                 kept + ((Smem::kD + ks * 256) >> 4), id_c2, 1);
                     mma_commit(&m.empty[s]);
                 }
                 __syncwarp();
@@ -1728,9 +1835,12 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     const uint64_t qb = keymn + ((Smem::kQ + ks * 2048) >> 4);
                     const uint64_t kb = keymn + ((Smem::kK + ks * 2048) >> 4);
                     mma_bf16(tmem + kC3, akm + ((Smem::kA + ks * 32) >> 4), kb, id_c1, ks > 0);
+                    mma_bf16(tmem + kC3, akm + ((Smem::kDecay + ks * 32) >> 4), kb, id_c1, 1);
                     // the box in front of A (of B) fills the rows that are not read
                     mma_bf16(tmem + kC4, amn + ((Smem::kA - kBox64 + ks * 2048) >> 4), qb, id_c2, ks > 0);
                     mma_bf16(tmem + kC4, amn + ((Smem::kA + ks * 2048) >> 4), kb, id_c2, 1);
+                    mma_bf16(tmem + kC4, amn + ((Smem::kDecay - kBox64 + ks * 2048) >> 4), qb, id_c2, 1);
+                    mma_bf16(tmem + kC4, amn + ((Smem::kDecay + ks * 2048) >> 4), kb, id_c2, 1);
                 }
                 mma_commit(&m.c_full);
             }
@@ -1853,7 +1963,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     const float dg = s + back[v] + (front[v] - own[v]);
                     a.dg[r] = from_f32<__nv_bfloat16>(t < w.cnt ? dg : 0.f);
                     if (G.beta[t] != 0.f)
-                        a.dbeta[r] = from_f32<__nv_bfloat16>(t < w.cnt ? S.db[t] / (G.beta[t] * G.beta[t]) : 0.f);
+                        a.dbeta[r] = from_f32<__nv_bfloat16>(t < w.cnt ? (S.db[t] + (S.lo[0][t] + S.lo[1][t])) / (G.beta[t] * G.beta[t]) : 0.f);
                 }
             }
             // tokens that write nothing: r lies in dV, which only this CTA has read
@@ -1904,10 +2014,10 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     const float f = G.since[t];
 #pragma unroll
                     for (int cb = 0; cb < rb; ++cb)
-                        m.decay[t][16 * cb + q] = f * G.across[rb - 1][16 * cb + q];
-                    m.decay[t][16 * rb + q] = r >= q ? expf(G.G.within(t, 16 * rb + q)) : 0.f;
+                        decay[t][16 * cb + q] = f * G.across[rb - 1][16 * cb + q];
+                    decay[t][16 * rb + q] = r >= q ? expf(G.G.within(t, 16 * rb + q)) : 0.f;
 #pragma unroll
-                    for (int cb = rb + 1; cb < 4; ++cb) m.decay[t][16 * cb + q] = 0.f;
+                    for (int cb = rb + 1; cb < 4; ++cb) decay[t][16 * cb + q] = 0.f;
                 }
             }
             if (named_barrier_or(1, 256, !ok)) break;      // all eight warps
@@ -1915,7 +2025,18 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             // MMAs on A and B, of those before them at once, for the pairs
             // wait for all
             float2 sd = both(0.f);
-            auto dot_states = [&]() {
+            // dV's second part times x, 8 tokens of a channel twice a stage: of
+            // the last two stages read while A and B are on their way
+            int stage = 0;
+            uint4 vl[2][2];
+            auto get_lo = [&](uint4 (&to)[2], int u) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    to[e] = reinterpret_cast<const uint4 *>(a.v_lo)[((size_t)item * nv + u) * (64 * kC / 8) + tid + 256 * e];
+            };
+            if (tid < 64 * nv)                             // 128 bytes each, the item's
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(a.v_lo + (size_t)item * nv * (64 * kC) + tid * 64));
+            auto dot_states = [&](const uint4 (&vl)[2]) {
                 const int s = g & 1;
                 ok = ok && warp_spin_wait(&m.full[s], (g >> 1) & 1, abort_flag, err);
                 ++g;
@@ -1931,24 +2052,58 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     sd = fma2(as_pair(x.z << 16, x.z & 0xffff0000u), as_pair(y.z << 16, y.z & 0xffff0000u), sd);
                     sd = fma2(as_pair(x.w << 16, x.w & 0xffff0000u), as_pair(y.w << 16, y.w & 0xffff0000u), sd);
                 }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(st + Smem::kX + (tid + 256 * e) * 16);
+                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, lw[4] = {vl[e].x, vl[e].y, vl[e].z, vl[e].w};
+                    float p[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 t = mul2(as_pair(xw[j] << 16, xw[j] & 0xffff0000u),
+                                              as_pair(lw[j] << 16, lw[j] & 0xffff0000u));
+                        p[2 * j] = t.x;
+                        p[2 * j + 1] = t.y;
+                    }
+                    // summed over the warp's 32 channels, as the columns of E below
+#pragma unroll
+                    for (int o = 4; o; o >>= 1)
+#pragma unroll
+                        for (int j = 0; j < o; ++j) {
+                            const float give = lane & (4 * o) ? p[j] : p[j + o];
+                            const float keep = lane & (4 * o) ? p[j + o] : p[j];
+                            p[j] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * o);
+                        }
+                    p[0] += __shfl_xor_sync(0xffffffffu, p[0], 2);
+                    p[0] += __shfl_xor_sync(0xffffffffu, p[0], 1);
+                    if ((lane & 3) == 0) {
+                        float &sum = S.lo[warp & 1][8 * (warp / 2 + 4 * e) + lane / 4];
+                        sum = stage ? sum + p[0] : p[0];
+                    }
+                }
+                ++stage;
                 warp_arrive(&m.empty[s]);
             };
-            for (int u = 0; u < nv - 2; ++u) dot_states();
+            for (int u = 0; u < nv - 2; ++u) {
+                get_lo(vl[0], u);
+                dot_states(vl[0]);
+            }
             ok = ok && warp_spin_wait(&m.keys[n & 1], (n >> 1) & 1, abort_flag, err) &&
                  warp_spin_wait(&m.pair_full, n & 1, abort_flag, err);
-            if (ok) {                                      // A, B, and the sums of E
+            float e[32], rs = 0.f, mid = 0.f;
+            uint32_t low[16];                              // A's, B's second parts
+            const bool none = key && G.beta[i] == 0.f;
+            if (ok) {                                      // A, B, and the terms of E
                 tc_fence_after();
                 uint32_t pd[32], pk[32];
                 tmem_ld32(tl + kPd + 32 * hf, pd);
                 tmem_ld32(tl + kPk + 32 * hf, pk);
                 tmem_wait_ld();
                 const float f = key ? -1.f : a.scale;
-                const bool none = key && G.beta[i] == 0.f;
-                float e[32], rs = 0.f, mid = 0.f;
                 uint8_t *tile = smem + (key ? Smem::kB : Smem::kA);
 #pragma unroll
                 for (int j8 = 0; j8 < 4; ++j8) {
                     float w8[8];
+                    uint32_t hi[4];
 #pragma unroll
                     for (int jj = 0; jj < 8; ++jj) {
                         const int jl = 8 * j8 + jj, j = 32 * hf + jl;
@@ -1956,11 +2111,13 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         // a row behind the sequence may be NaN: chosen, not multiplied
                         const float p = in ? __uint_as_float(pd[jl]) : 0.f;
                         if (diag) mid = p;
-                        w8[jj] = diag && key ? 0.f : f * p * m.decay[i][j];
+                        w8[jj] = diag && key ? 0.f : f * p * decay[i][j];
                         e[jl] = diag ? 0.f : w8[jj] * __uint_as_float(pk[jl]);
                         rs += e[jl];
                     }
-                    store8(reinterpret_cast<__nv_bfloat16 *>(tile + tile_off(i, 32 * hf + 8 * j8)), w8);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) split_pair(w8[2 * q], w8[2 * q + 1], hi[q], low[4 * j8 + q]);
+                    *reinterpret_cast<uint4 *>(tile + tile_off(i, 32 * hf + 8 * j8)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 }
                 if (none) {
                     S.none[hf][i] = rs;
@@ -1969,11 +2126,23 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     for (int j8 = 0; j8 < 4; ++j8)
                         *reinterpret_cast<uint4 *>(tile + tile_off(i, 32 * hf + 8 * j8)) = make_uint4(0, 0, 0, 0);
 #pragma unroll
+                    for (int j = 0; j < 16; ++j) low[j] = 0u;
+#pragma unroll
                     for (int j = 0; j < 32; ++j) e[j] = 0.f;
                 }
+            }
+            if (named_barrier_or(2, 256, !ok)) break;      // the decays have been read
+            {
+                uint8_t *tile = smem + Smem::kDecay + (key ? kBox64 : 0);
+#pragma unroll
+                for (int j8 = 0; j8 < 4; ++j8)
+                    *reinterpret_cast<uint4 *>(tile + tile_off(i, 32 * hf + 8 * j8)) =
+                        make_uint4(low[4 * j8], low[4 * j8 + 1], low[4 * j8 + 2], low[4 * j8 + 3]);
                 fence_async_shared();
                 tc_fence_before();
                 warp_arrive(&m.ab_ready);
+                get_lo(vl[0], max(0, nv - 2));
+                if (nv > 1) get_lo(vl[1], nv - 1);
                 if (key && (warp & 1) == hf) S.db[i] = mid;
                 S.row[key][hf][i] = rs;
                 // column sums over the warp's rows: halves swapped and added
@@ -1988,7 +2157,8 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     }
                 S.col[warp][lane] = e[0];
             }
-            for (int u = max(0, nv - 2); u < nv; ++u) dot_states();
+            dot_states(vl[0]);
+            if (nv > 1) dot_states(vl[1]);
             float sd1 = sd.x + sd.y;
 #pragma unroll
             for (int o = 16; o; o >>= 1) sd1 += __shfl_xor_sync(0xffffffffu, sd1, o);
@@ -1996,7 +2166,6 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             ok = ok && warp_spin_wait(&m.c_full, n & 1, abort_flag, err);
             if (ok) {
                 tc_fence_after();
-                const bool none = key && G.beta[i] == 0.f;
                 const float f0 = key ? -G.e[i] : a.scale * G.e[i], f1 = none ? 0.f : f0, f2 = G.rest[i];
                 uint8_t *mine = ks + (key ? Smem::kK : Smem::kQ);
                 float2 inter = both(0.f), ahead = both(0.f);
@@ -2072,6 +2241,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         for (int j = max(0, kit - 2); j < kit; ++j) mbar_drain(&m.keys[j & 1], (j >> 1) & 1, err);
         for (int j = max(0, it - 2); j < it; ++j)
             if (!hook_skips(blockIdx.x == 0, j)) mbar_drain(&m.full[j & 1], (j >> 1) & 1, err);
+        for (int j = max(0, lit - 2); j < lit; ++j) mbar_drain(&m.lo_full[j & 1], (j >> 1) & 1, err);
     }
     if (warp == 9) {
         if (*abort_flag) drain_mmas(&m.drain, err);
@@ -2157,10 +2327,9 @@ DeltaTcLayout tc_layout(int batch, int heads, int seqlen, int dk, int dv, bool f
     return l;
 }
 
-bool scan_maps(const DeltaArgs &a, CUtensorMap *k, CUtensorMap *v, CUtensorMap *o) {
+bool scan_maps(const DeltaArgs &a, CUtensorMap *k, CUtensorMap *v) {
     return token_map(k, a.k, a.batch, a.seqlen, a.key_heads, a.dk) &&
-           token_map(v, a.v, a.batch, a.seqlen, a.heads, a.dv) &&
-           token_map(o, a.out, a.batch, a.seqlen, a.heads, a.dv);
+           token_map(v, a.v, a.batch, a.seqlen, a.heads, a.dv);
 }
 
 template <int DK, bool kSplit>
@@ -2170,8 +2339,8 @@ cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, cudaS
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Smem::kBytes);
     if (e != cudaSuccess) return e;
-    CUtensorMap tm_k, tm_v, tm_o;
-    if (!scan_maps(a, &tm_k, &tm_v, &tm_o)) return cudaErrorInvalidValue;
+    CUtensorMap tm_k, tm_v;
+    if (!scan_maps(a, &tm_k, &tm_v)) return cudaErrorInvalidValue;
     DeltaScanArgs s = {blocks, a.lengths, a.state_in, a.state_out, (__nv_bfloat16 *)a.out, nullptr,
                        nullptr, a.heads, a.key_heads, a.seqlen, nc, a.dv, device_error_word(),
                        1, nc, nullptr, nullptr};
@@ -2180,14 +2349,14 @@ cudaError_t launch_scan(const DeltaArgs &a, int nc, const uint8_t *blocks, cudaS
     count_launch();
     return launch_overlapped(delta_scan_kernel<DK, kSplit>,
                              dim3((unsigned)(a.batch * a.heads * slabs)), dim3(kScanThreads),
-                             Smem::kBytes, stream, tm_k, tm_v, tm_o, s);
+                             Smem::kBytes, stream, tm_k, tm_v, s);
 }
 
 template <int DK, bool kSplit>
 cudaError_t launch_segments(const DeltaArgs &a, const DeltaTcLayout &l, uint8_t *ws, cudaStream_t stream) {
     using Smem = DeltaScanSmem<DK, kSplit>;
-    CUtensorMap tm_k, tm_v, tm_o;
-    if (!scan_maps(a, &tm_k, &tm_v, &tm_o)) return cudaErrorInvalidValue;
+    CUtensorMap tm_k, tm_v;
+    if (!scan_maps(a, &tm_k, &tm_v)) return cudaErrorInvalidValue;
     float *starts = (float *)(ws + l.starts), *units = (float *)(ws + l.units);
     DeltaScanArgs s = {ws, a.lengths, a.state_in, a.state_out, (__nv_bfloat16 *)a.out, nullptr,
                        nullptr, a.heads, a.key_heads, a.seqlen, l.nc, a.dv, device_error_word(),
@@ -2200,7 +2369,7 @@ cudaError_t launch_segments(const DeltaArgs &a, const DeltaTcLayout &l, uint8_t 
         KernelTimer timer(name, stream);
         count_launch();
         return launch_overlapped(kernel, dim3((unsigned)ctas), dim3(kScanThreads), Smem::kBytes, stream,
-                                 tm_k, tm_v, tm_o, s, bhs);
+                                 tm_k, tm_v, s, bhs);
     };
     cudaError_t e = pass(delta_segments_kernel<DK, kSplit, false>,
                          walks * (l.segments - 1) + bhs * (l.segments - 2), "delta_segments");
@@ -2235,7 +2404,7 @@ DeltaCut back_segments(int batch, int heads, int nc, int dv) {
 }
 
 struct DeltaTcGradLayout {
-    size_t blocks, x, s, d, dq, dk, starts, back, units, total;
+    size_t blocks, x, s, d, vlo, dq, dk, starts, back, units, total;
     DeltaCut cut;
 };
 DeltaTcGradLayout tc_grad_layout(int batch, int heads, int key_heads, int seqlen, int dk, int dv) {
@@ -2243,10 +2412,11 @@ DeltaTcGradLayout tc_grad_layout(int batch, int heads, int key_heads, int seqlen
     const size_t wide = heads != key_heads ? up1k((size_t)batch * seqlen * heads * dk * 4) : 0;
     DeltaTcGradLayout l;
     l.blocks = 0;
-    l.x = chunks * (dk == 64 ? DeltaBlock<64, false>::kBytes : DeltaBlock<128, false>::kBytes);
-    l.s = l.x + chunks * dv * kC * 2;
+    l.x = chunks * (dk == 64 ? DeltaBlock<64, false>::kBack : DeltaBlock<128, false>::kBack);
+    l.s = l.x + chunks * dv * kC * 4;
     l.d = l.s + chunks * dv * dk * 2;
-    l.dq = l.d + chunks * dv * dk * 2;
+    l.vlo = l.d + chunks * dv * dk * 2;
+    l.dq = l.vlo + chunks * dv * kC * 2;
     l.dk = l.dq + wide;
     l.cut = back_segments(batch, heads, (int)(((size_t)seqlen + kC - 1) / kC), dv);
     const size_t bh = (size_t)batch * heads, between = l.cut.count - 1;
@@ -2264,7 +2434,7 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
     const DeltaTcGradLayout l = tc_grad_layout(a.batch, a.heads, a.key_heads, a.seqlen, a.dk, a.dv);
     uint8_t *ws = (uint8_t *)workspace;
     __nv_bfloat16 *xs = (__nv_bfloat16 *)(ws + l.x), *ss = (__nv_bfloat16 *)(ws + l.s),
-                  *ds = (__nv_bfloat16 *)(ws + l.d);
+                  *ds = (__nv_bfloat16 *)(ws + l.d), *vlo = (__nv_bfloat16 *)(ws + l.vlo);
     float *dq_wide = (float *)(ws + l.dq), *dk_wide = (float *)(ws + l.dk);
     cudaError_t e = launch_prep<DK, false>(a, nc, ws + l.blocks, true, stream);
     if (e != cudaSuccess) return e;
@@ -2278,10 +2448,10 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
         !token_map(&tm_dk, a.dk_grad, a.batch, a.seqlen, a.key_heads, DK))
         return cudaErrorInvalidValue;
     {
-        using Smem = DeltaScanSmem<DK, false>;
+        using Smem = DeltaReverseSmem<DK>;                 // the larger of the two walks'
         const DeltaScanArgs f = {ws + l.blocks, a.lengths, nullptr, nullptr, nullptr, xs, ss, a.heads,
                                  a.key_heads, a.seqlen, nc, a.dv, device_error_word(), 1, nc, nullptr, nullptr};
-        const DeltaReverseArgs r = {ws + l.blocks, a.lengths, ds, a.heads, a.key_heads, a.seqlen, nc, a.dv,
+        const DeltaReverseArgs r = {ws + l.blocks, a.lengths, ds, vlo, a.heads, a.key_heads, a.seqlen, nc, a.dv,
                                     device_error_word()};
         const int bhs = (int)bh, walks = bhs * slabs;
         auto launch = [&](auto kernel, const char *name, int ctas, auto... rest) {
@@ -2312,7 +2482,7 @@ cudaError_t launch_backward(const DeltaArgs &a, void *workspace, cudaStream_t st
         e = cudaFuncSetAttribute(delta_grad_tc_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)Smem::kBytes);
         if (e != cudaSuccess) return e;
-        DeltaGradTcArgs g = {(const __nv_bfloat16 *)a.v, (const __nv_bfloat16 *)a.g, (const __nv_bfloat16 *)a.beta, xs, ss, ds, a.lengths,
+        DeltaGradTcArgs g = {(const __nv_bfloat16 *)a.v, (const __nv_bfloat16 *)a.g, (const __nv_bfloat16 *)a.beta, xs, ss, ds, vlo, a.lengths,
                              (__nv_bfloat16 *)a.dq, (__nv_bfloat16 *)a.dk_grad,
                              (__nv_bfloat16 *)a.dv_grad, (__nv_bfloat16 *)a.dg,
                              (__nv_bfloat16 *)a.dbeta, dq_wide, dk_wide, a.scale, a.heads,

@@ -3,7 +3,8 @@ to bf16 of the tensor-core path and none besides (test infrastructure).
 
 Between the roundings everything is float64, so that a kernel differs from
 this by its float32 arithmetic alone: where that moves a value across the
-border between two bf16 numbers, by one step of it.  `rounds` names the
+border between two bf16 numbers, by one step of it.  What the kernels hold in
+two bf16 parts (2^-17 of it) is not rounded here.  `rounds` names the
 roundings that are made (ALL of them by default); without any this is the
 chunk form itself and equals oracle.delta_recurrent and delta_backward.
 
@@ -16,12 +17,13 @@ import numpy as np
 from .delta import _f64, _lengths
 
 CHUNK = 64
-# forward: T^, W, Q~ and P as the chunks' operands; the state as an operand, X
-# for the output and e^{G_L - G} X for the state; the output itself
-FORWARD = ("T", "W", "Q", "P", "S", "X", "Xs", "out")
-# backward: those of its forward walk, D and dX as operands (dV takes dX in two
-# parts), dV as it leaves, the pairs A and B, the gradients that leave
-BACKWARD = ("T", "W", "Q", "P", "S", "X", "Xs", "D", "dX", "dV", "AB", "grads")
+# forward: T^, W and Q~ as the chunks' operands, the state as an operand, the
+# output itself; P and both uses of X are in two parts
+FORWARD = ("T", "W", "Q", "S", "out")
+# backward: T^ and W, the state and its gradient D as operands and as they are
+# kept, dX where it meets W (dV takes it in two parts), dV as it leaves (dbeta
+# takes it in two), the gradients that leave; Q~, P, X and the pairs are in two
+BACKWARD = ("T", "W", "S", "D", "dX", "dV", "grads")
 ALL = FORWARD + BACKWARD
 
 
@@ -51,8 +53,8 @@ class _Chunk:
         self.T, self.Tlo = self.part("T", T * np.where(none, f(1), b))
         W = (T * b * self.e) @ k
         self.W, self.Wlo = self.part("W", W)
-        self.Q = self.round("Q", q * (self.scale * self.e)[:, None])
-        self.P = self.round("P", self.scale * (q @ k.T) * self.decay)
+        self.Q = q * (self.scale * self.e)[:, None]
+        self.P = self.scale * (q @ k.T) * self.decay
 
     def round(self, name, x):
         return bf16(x) if name in self.rounds else x
@@ -63,11 +65,10 @@ class _Chunk:
         return hi, self.round(name, x - hi) if self.two else 0.0 * x
 
     def step(self, S, v):
-        """(X, the state behind the chunk, the state as an operand)"""
+        """(X, the state behind the chunk, the state as an operand: its parts)"""
         hi, lo = self.part("S", S)
         X = (self.T + self.Tlo) @ v - ((self.W + self.Wlo) @ hi + self.W @ lo)
-        Xs = sum(self.part("Xs", self.rest[:, None] * X))
-        return X, self.eL * S + self.k.T @ Xs, hi
+        return X, self.eL * S + self.k.T @ (self.rest[:, None] * X), hi, lo
 
 
 def _walks(q, k, v, g, beta, lengths):
@@ -82,7 +83,7 @@ def _walks(q, k, v, g, beta, lengths):
 def delta_chunks(q, k, v, g, beta, scale, state=None, lengths=None, final_state=False, rounds=ALL,
                  dtype=np.float64):
     """(o, S after the last token).  final_state: as where one is asked for,
-    with T^, W, the state and e^{G_L - G} X in two bf16 parts."""
+    with T^, W and the state in two bf16 parts."""
     f = dtype
     q, k, v, g, beta = (_f64(x).astype(f) for x in (q, k, v, g, beta))
     B, n, H, dv = v.shape
@@ -92,8 +93,8 @@ def delta_chunks(q, k, v, g, beta, scale, state=None, lengths=None, final_state=
         s = S[b, h]
         for c in chunks:
             w = _Chunk(q[b, c, kh], k[b, c, kh], g[b, c, h], beta[b, c, h], scale, rounds, final_state, f)
-            X, s, hi = w.step(s, v[b, c, h])
-            o[b, c, h] = w.round("out", w.Q @ hi + w.P @ w.round("X", X))
+            X, s, hi, lo = w.step(s, v[b, c, h])
+            o[b, c, h] = w.round("out", w.round("Q", w.Q) @ (hi + lo) + w.P @ X)
         S[b, h] = s
     return o, S
 
@@ -111,8 +112,8 @@ def delta_chunks_backward(q, k, v, g, beta, d_out, scale, lengths=None, rounds=A
         for c in chunks:
             off = none[b, c, h]
             w = _Chunk(q[b, c, kh], k[b, c, kh], g[b, c, h], beta[b, c, h], scale, rounds, False, f, off)
-            X, s, hi = w.step(s, np.where(off[:, None], f(0), v[b, c, h]))
-            made.append((c, w, w.round("X", X), hi))
+            X, s, hi, _ = w.step(s, np.where(off[:, None], f(0), v[b, c, h]))
+            made.append((c, w, X, hi))
         D = np.zeros_like(s)
         for c, w, X, S in reversed(made):
             do = d_out[b, c, h]
@@ -120,7 +121,8 @@ def delta_chunks_backward(q, k, v, g, beta, d_out, scale, lengths=None, rounds=A
             dX = w.P.T @ do + w.rest[:, None] * (w.k @ Dh)
             hi = w.round("dX", dX)
             D = w.eL * D + w.Q.T @ do - w.W.T @ hi
-            dV = w.round("dV", w.T.T @ (hi + w.round("dX", dX - hi)))
+            full = w.T.T @ dX
+            dV = w.round("dV", full)
             off = none[b, c, h][:, None]                   # there dV is the gradient of x
             A = w.scale * (do @ X.T) * w.decay
             B = -np.tril(dV @ X.T, -1) * w.decay
@@ -129,14 +131,13 @@ def delta_chunks_backward(q, k, v, g, beta, d_out, scale, lengths=None, rounds=A
             missed = (dV * v[b, c, h]).sum(1) + (w.k * from_k).sum(1) + (B * (w.k @ w.k.T)).sum(1)
             B, from_k = np.where(off, 0.0, B), np.where(off, 0.0, from_k)
             E = np.tril(A * (w.q @ w.k.T) + B * (w.k @ w.k.T), -1)
-            A, B = w.round("AB", A), w.round("AB", B)
             to_D = w.rest[:, None] * (X @ Dh.T)
             dq[b, c, kh] += from_q + A @ w.k
             dk[b, c, kh] += from_k + to_D + A.T @ w.q + (B + B.T) @ w.k
             inter = (w.q * from_q).sum(1) + (w.k * from_k).sum(1) + E.sum(1) - E.sum(0)
             ahead = (w.k * to_D).sum(1)
             dg[b, c, h] = np.cumsum(inter[::-1])[::-1] + np.cumsum(ahead) - ahead + w.eL * (S * Dh).sum()
-            db[b, c, h] = np.where(off[:, 0], missed, (dV * X).sum(1) / np.where(off[:, 0], 1.0, w.b * w.b))
+            db[b, c, h] = np.where(off[:, 0], missed, (full * X).sum(1) / np.where(off[:, 0], 1.0, w.b * w.b))
             dv_[b, c, h] = np.where(off, 0.0, dV)
     if "grads" in rounds:
         dq, dk, dg, db = (bf16(x) for x in (dq, dk, dg, db))

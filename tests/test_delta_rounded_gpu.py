@@ -12,8 +12,9 @@ a norm of N independent roundings of given sizes, N at least 64 for each token
 (a row of X, of dV, of P or A, of the result; for dg and dbeta one number a
 token).  Even if all of them were drawn anew, the ratio of two such norms has
 a standard deviation of at most 1 / sqrt(N); the bound is three of them.  A
-further rounding of a main operand, 1.5e-3 and more of its output beside 2.4e-3
-to 3.1e-3, raises the error by 11 % and more; 64 tokens allow 4.7 %.
+further rounding of a main operand (P, X, A or B, dV: 1.5e-3 and more of its
+output, beside 1.7e-3 to 2.2e-3) raises the error by 20 % and more; 64 tokens
+allow 4.7 %.
 Short enough for walks of whole sequences: 11 chunks."""
 import numpy as np
 import pytest
