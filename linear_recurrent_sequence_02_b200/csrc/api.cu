@@ -187,9 +187,9 @@ static bool delta_tensor(const retnet_delta_shape *s, retnet_algo algo) {
 }
 // A prefill of a few tokens goes token by token: its one launch takes 2 us and
 // about 0.4 us a token while the GPU has room for all columns at once, where
-// the chunks' two take 12 us and more (64 heads of 128, 16 tokens: 11.6
-// against 16.3 us, 32: 19.8 against 16.4; 512 heads, 8: 46 against 57, 16: 75
-// against 58).
+// the chunks' two take 15 us and more (64 heads of 128, 16 tokens: 10.5
+// against 15.2 us, 32: 18.8 against 15.2; 512 heads, 8: 36 against 43, 16: 64
+// against 43).
 static bool delta_prefill_tensor(const retnet_delta_shape *s, retnet_algo algo) {
     const bool few = s->seqlen <= 16 &&
                      (long long)s->batch * s->heads * s->dv * s->seqlen <= (1 << 19);

@@ -186,8 +186,9 @@ __device__ __forceinline__ void keep_row(__nv_bfloat16 *kept, size_t chunk, int 
 // by mma.sync, whose accumulators are in the registers that apply the decays
 // and split the results; the inverse in float32: four 16 x 16 triangles by
 // substitution, a column a lane, then the squares below them by products, 16
-// and then 32 rows at a time.  69 us for 2048 chunks of 128 x 256, of which
-// its copies take 33; what bounds it is half the issue slots and its barriers.
+// and then 32 rows at a time.  77 us for 2048 chunks of 128 x 256 (69 before
+// P's second part, of which its copies took 33); what bounds it is half the
+// issue slots and its barriers.
 // [Q; K] K^T as one tcgen05 product of 128 rows, as delta_grad_tc_kernel forms
 // it, and CTAs that stay for several chunks have not been built here.
 // The chunk's block is put together in shared memory, K and Q first where W
@@ -988,7 +989,7 @@ delta_scan_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 // segment as it is; then the states between segments, S_{j+1} = M_j S_j + N_j,
 // in float32; then all other segments' outputs at once.  Each chunk is walked
 // up to three times, but on all SMs: 8192 tokens and 16 heads of 128 in 6
-// segments, walk 274 us whole, 103 us so, and 11 us the join.
+// segments, 431 us a call whole and 231 so, of which the join takes 11.
 // Only what a final state depends on is walked in two parts: not the outputs
 // of the second pass (it would take 0.2e-3 off their 2.1e-3), but its last
 // segment, which is shorter for that.
@@ -1587,7 +1588,7 @@ delta_walks_segments_kernel(const __grid_constant__ CUtensorMap tm_k, const __gr
 // (*: whatever precedes the operand in shared memory; those rows are not read.)
 // Persistent, a CTA an SM: the copies of the next chunk run beside the pairs
 // and the epilogue of this one (a CTA a chunk, 2048 chunks of 128 x 128: 175
-// us, persistent 100 us).
+// us, persistent 100; 131 with the second parts: A's and B's 13, X's 11, dV's 5).
 constexpr int kGradTcThreads = 352;        // warps 0-7 rows, 8 copies, 9 MMAs, 10 gates and sums
 
 struct DeltaGradTcBars {
@@ -2281,11 +2282,11 @@ cudaError_t launch_prep(const DeltaArgs &a, int nc, uint8_t *blocks, bool backwa
 // of 148 CTAs each, first pass and second).  In one part, which is all of it
 // without a final state, a chunk takes 0.6 of that (0.72 for dk 64).  The two
 // further launches cost 7 (5, 4) and a join of states 1.  Measured, 128 x 128,
-// with a final state: 16 heads, 128 chunks: 360 us whole, 198 in 6 segments; 32
-// chunks: 96 and 73; 24 heads, 32 chunks: 110 and 98; 32 heads: 119 and 127
-// (whole); 64 heads, 128 chunks: 611 and 640 (whole).  Without: 16 heads, 128
-// chunks: 239 and 154; 1 head, 32 chunks: 54 and 44; 32 heads, 64 chunks: 158
-// whole.
+// with a final state, a call: 16 heads, 128 chunks: 431 us whole, 231 in 6
+// segments; 32 chunks: 114 and 80; 24 heads, 32 chunks: 129 and 107; 32 heads:
+// 140 and 136; 64 heads, 128 chunks: 720 and 726 (whole).  Without: 16 heads,
+// 128 chunks: 333 and 187; 1 head, 32 chunks: 76 and 48; 32 heads, 64 chunks:
+// 206 and 176.
 struct DeltaCut {
     int count, chunks;
 };
@@ -2382,9 +2383,9 @@ cudaError_t launch_segments(const DeltaArgs &a, const DeltaTcLayout &l, uint8_t 
 size_t up1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
 
 // Segments of the backward's walks, as delta_segments, in chunks walked back.
-// Measured, 128 x 128: 1 head, 128 chunks: 280 us whole, 97 in 12 segments; 16
-// heads: 423 and 327 in 4; 24 heads, 64 chunks: 260 and 245 in 3; 32 chunks:
-// 143 and 144 (whole); 32 heads, 64 chunks: 301 and 324 (whole).
+// Measured, 128 x 128, a call: 1 head, 128 chunks: 347 us whole, 113 in 12
+// segments; 16 heads: 501 and 396 in 4; 24 heads, 64 chunks: 314 and 303 in 3;
+// 32 chunks: 177 and 183 (whole); 32 heads, 64 chunks: 359 and 411 (whole).
 DeltaCut back_segments(int batch, int heads, int nc, int dv) {
     const long long units = (long long)batch * heads, walks = units * ((dv + 127) / 128);
     auto waves = [](long long ctas) { return (ctas + 147) / 148; };
