@@ -27,8 +27,8 @@ __device__ __forceinline__ float log_decay(float g) { return g < -105.f ? -105.f
 
 // Sums of a chunk's log decays, so that a difference of two keeps float32
 // accuracy behind any decays before it: each is an unevaluated sum of two
-// floats (the second what the first rounded away), and they start anew every
-// 16 tokens.
+// floats (the second what the first rounded away, by Knuth's two-sum), and
+// they start anew every 16 tokens.
 struct DecaySums {
     float2 in[64];                         // from the 16-token block's start, inclusive
     float total[4];                        // of a block

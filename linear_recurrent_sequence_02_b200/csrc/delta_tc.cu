@@ -192,7 +192,8 @@ __device__ __forceinline__ void keep_row(__nv_bfloat16 *kept, size_t chunk, int 
 // [Q; K] K^T as one tcgen05 product of 128 rows, as delta_grad_tc_kernel forms
 // it, and CTAs that stay for several chunks have not been built here.
 // The chunk's block is put together in shared memory, K and Q first where W
-// and Q~ replace them, and leaves by one copy.
+// and Q~ replace them, and leaves by one copy; second parts of P and Q~, for
+// which three CTAs leave no room there, go from registers to global memory.
 // Decays e^{G_i - G_j}: of rows and columns in different 16-row blocks as
 // e^{G_i - G_r} e^{G_r - G_j} with r the row before the block of i, so that
 // both factors are at most 1 and 160 exponentials replace 2000.
@@ -1087,7 +1088,8 @@ __device__ __forceinline__ void join_states(DeltaJoinSmem<DK> &m, float *starts,
                 *reinterpret_cast<float2 *>(&x[t][2 * hf]) =
                     *reinterpret_cast<const float2 *>(starts + j * step + at + (size_t)(8 * hf) * dv + 8 * t);
     };
-    // x rounded to 11 bits, and what that leaves (of which the product takes 11)
+    // x rounded to 11 bits (the split of Veltkamp and Dekker), and what that
+    // leaves (of which the product takes 11)
     auto part = [](float x, float &hi, float &lo) {
         const float t = __fmul_rn(x, 8193.f);              // no contraction
         hi = __fsub_rn(t, __fsub_rn(t, x));
@@ -1593,7 +1595,7 @@ constexpr int kGradTcThreads = 352;        // warps 0-7 rows, 8 copies, 9 MMAs, 
 
 struct DeltaGradTcBars {
     uint64_t full[2], lo_full[2], empty[2], keys[2], keys_free[2], gates[2], done[2];
-    uint64_t pair_full, ab_ready, c_full, acc_free, drain;
+    uint64_t pair_full, ab_ready, ablo_ready, c_full, acc_free, drain;
     uint32_t tmem_slot;
     int abort_flag;
     // By turns of two items, so that warp 10 prepares the one after next and
@@ -1679,6 +1681,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         mbar_init(&m.pair_full, 1);
         mbar_init(&m.ab_ready, 8);
+        mbar_init(&m.ablo_ready, 8);
         mbar_init(&m.c_full, 1);
         mbar_init(&m.acc_free, 8);
         mbar_init(&m.drain, 1);
@@ -1830,19 +1833,25 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             ok = ok && warp_spin_wait(&m.ab_ready, n & 1, abort_flag, err);
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {
+            // first and second parts of A and B; the box in front of A (of B)
+            // fills the rows that are not read
+            auto chunk_products = [&](uint32_t tiles, bool first) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
                     const uint64_t qb = keymn + ((Smem::kQ + ks * 2048) >> 4);
                     const uint64_t kb = keymn + ((Smem::kK + ks * 2048) >> 4);
-                    mma_bf16(tmem + kC3, akm + ((Smem::kA + ks * 32) >> 4), kb, id_c1, ks > 0);
-                    mma_bf16(tmem + kC3, akm + ((Smem::kDecay + ks * 32) >> 4), kb, id_c1, 1);
-                    // the box in front of A (of B) fills the rows that are not read
-                    mma_bf16(tmem + kC4, amn + ((Smem::kA - kBox64 + ks * 2048) >> 4), qb, id_c2, ks > 0);
-                    mma_bf16(tmem + kC4, amn + ((Smem::kA + ks * 2048) >> 4), kb, id_c2, 1);
-                    mma_bf16(tmem + kC4, amn + ((Smem::kDecay - kBox64 + ks * 2048) >> 4), qb, id_c2, 1);
-                    mma_bf16(tmem + kC4, amn + ((Smem::kDecay + ks * 2048) >> 4), kb, id_c2, 1);
+                    mma_bf16(tmem + kC3, akm + ((tiles + ks * 32) >> 4), kb, id_c1, !first || ks > 0);
+                    mma_bf16(tmem + kC4, amn + ((tiles - kBox64 + ks * 2048) >> 4), qb, id_c2, !first || ks > 0);
+                    mma_bf16(tmem + kC4, amn + ((tiles + ks * 2048) >> 4), kb, id_c2, 1);
                 }
+            };
+            if (elect_one()) chunk_products(Smem::kA, true);
+            __syncwarp();
+            ok = warp_spin_wait(&m.ablo_ready, n & 1, abort_flag, err);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+                chunk_products(Smem::kDecay, false);
                 mma_commit(&m.c_full);
             }
             __syncwarp();
@@ -2131,6 +2140,9 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
                     for (int j = 0; j < 32; ++j) e[j] = 0.f;
                 }
+                fence_async_shared();
+                tc_fence_before();
+                warp_arrive(&m.ab_ready);
             }
             if (named_barrier_or(2, 256, !ok)) break;      // the decays have been read
             {
@@ -2140,8 +2152,7 @@ delta_grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     *reinterpret_cast<uint4 *>(tile + tile_off(i, 32 * hf + 8 * j8)) =
                         make_uint4(low[4 * j8], low[4 * j8 + 1], low[4 * j8 + 2], low[4 * j8 + 3]);
                 fence_async_shared();
-                tc_fence_before();
-                warp_arrive(&m.ab_ready);
+                warp_arrive(&m.ablo_ready);
                 get_lo(vl[0], max(0, nv - 2));
                 if (nv > 1) get_lo(vl[1], nv - 1);
                 if (key && (warp & 1) == hf) S.db[i] = mid;
