@@ -419,7 +419,10 @@ RETNET_API retnet_status retnet_delta_recurrent(const void *q, const void *k, co
  * and beta for its inverse, the decayed q and the state are rounded to bf16
  * (together with the result's rounding 1.7e-3 to 2.1e-3 of the norm, up to 3e-3
  * with decays near 0 over thousands of tokens; the result's alone is 1.7e-3,
- * which is all that SIMT has); a final state is within 5e-6 of its norm.  Equal calls give equal bits, whatever the workspace
+ * which is all that SIMT has); a final state is within 5e-6 of its norm.  These
+ * are errors of the writes x, so with keys that nearly repeat, whose writes
+ * mostly cancel, they are a larger part of what is left: up to 8e-3, and 4e-5
+ * of a state, with one key for all tokens (with state_out 2.3e-3).  Equal calls give equal bits, whatever the workspace
  * held.  Between calls that differ the bits of a sequence's `out` may differ,
  * inside these roundings: with state_out operands go in two bf16 parts; which
  * path AUTO takes for up to 16 tokens, and whether and where a long sequence is

@@ -121,3 +121,48 @@ def test_segments_for_every_head(rn, n, Hk, H, dk, dv, lens):
     for name, a, w in zip(("dq", "dk", "dv", "dg", "dbeta"), got,
                           oracle.delta_backward(*ref, dk ** -0.5, lens)):
         assert err(per_head(a), per_head(w)) < tol, name
+
+
+def alike(seed, n, H, dk, dv, cos, decay):
+    """As make, every key near one of its head (all the same: cos None)."""
+    x, ref = make(seed, 1, n, H, H, dk, dv, "bf16", decay)
+    rng = np.random.default_rng(seed)
+    one = rng.standard_normal((1, 1, H, dk))
+    k = one / np.linalg.norm(one, axis=-1, keepdims=True) + np.zeros((1, n, 1, 1))
+    if cos is not None:
+        k = cos * k + np.sqrt(1 - cos ** 2) * ref[1]
+    x[1] = torch.from_numpy(k).bfloat16().cuda()
+    ref[1] = x[1].double().cpu().numpy()
+    return x, ref
+
+
+@pytest.mark.parametrize("cos", [0.7, 0.95, None])
+@pytest.mark.parametrize("n,H,dk,dv,decay", [(300, 2, 64, 64, 0.02), (500, 1, 128, 128, 0.002)])
+def test_keys_that_nearly_repeat(rn, n, H, dk, dv, decay, cos):
+    """Writes that mostly cancel: the rounded oracle's errors, no more (the
+    roundings are independent as before).  A state's own, of writes that are
+    kept to 2^-17 of themselves, from operands kept to as much (T^, W, S: as
+    much again), against the norm of the writes that reach it: 2^-16."""
+    x, ref = alike(80 + n, n, H, dk, dv, cos, decay)
+    want, S = oracle.delta_recurrent(*ref[:5], dk ** -0.5)
+    for final in (False, True):
+        end = torch.empty(1, H, dk, dv, device="cuda") if final else None
+        out = rn.retnet_delta_chunkwise(*x[:5], state_out=end, algo="tensor")
+        done(rn)
+        o, _ = oracle.delta_chunks(*ref[:5], dk ** -0.5, final_state=final)
+        no_further(out, o, want, [n], "out")
+    for h in range(H):
+        writes, s = 0.0, np.zeros((dk, dv))
+        for t in range(n):
+            a = np.exp(ref[3][0, t, h])
+            w = ref[4][0, t, h] * (ref[2][0, t, h] - a * ref[1][0, t, h] @ s)
+            s = a * s + np.outer(ref[1][0, t, h], w)
+            writes = a * a * writes + (ref[1][0, t, h] ** 2).sum() * (w ** 2).sum()
+        e = np.linalg.norm(end[0, h].double().cpu().numpy() - S[0, h])
+        assert record(e / np.sqrt(writes), "state / writes") < 2.0 ** -16
+    got = rn.retnet_delta_backward(*x, algo="tensor")
+    done(rn)
+    for name, a, r, w in zip(("dq", "dk", "dv", "dg", "dbeta"), got,
+                             oracle.delta_chunks_backward(*ref, dk ** -0.5),
+                             oracle.delta_backward(*ref, dk ** -0.5)):
+        no_further(a, r, w, [n], name)
